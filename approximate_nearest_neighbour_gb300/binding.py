@@ -28,9 +28,11 @@ IVFPQ_ERR_TIMEOUT = -6
 LUT_FP32, LUT_FP16, LUT_FP8 = 0, 1, 2
 LUT_TYPES = {"fp32": LUT_FP32, "fp16": LUT_FP16, "fp8": LUT_FP8}
 MAX_K = 2048
+MXFP4, NVFP4 = 0, 1
+FP4_FORMATS = {"mxfp4": MXFP4, "nvfp4": NVFP4}
 
 # name -> (restype, argtypes); mirrors include/ivfpq.h
-_VP, _I, _I64 = C.c_void_p, C.c_int, C.c_int64
+_VP, _I, _I64, _F = C.c_void_p, C.c_int, C.c_int64, C.c_float
 SIGNATURES = {
     "ivfpq_index_create": (_I, [_I, _I, _I, _I, _VP, _VP, C.POINTER(_VP)]),
     "ivfpq_index_destroy": (_I, [_VP]),
@@ -59,6 +61,18 @@ SIGNATURES = {
     "ivfpq_encode_hinted": (_I, [_VP, _VP, _I64, _VP, _VP, _VP, C.POINTER(_I64), _VP]),
     "ivfpq_repaired_queries": (_I, [_VP, C.POINTER(_I64), _VP]),
     "ivfpq_knn_graph": (_I, [_VP, _VP, _VP, _I64, _I, _I, _VP, _VP, _VP]),
+    "fp4_quantize": (_I, [_VP, _I, _I64, _I64, _I64, _I, _VP, _VP, _VP, _VP]),
+    "fp4_dequantize": (_I, [_VP, _VP, _I64, _I64, _I, _VP, _VP, _I, _VP]),
+    "fp4_product": (_I, [_VP, _VP, _I64, _VP, _VP, _I64, _I64, _I, _VP, _VP, _VP, _I, _VP]),
+    "fp4_linear": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _I64, _I64, _I, _VP, _VP, _VP, _I, _VP]),
+    "score_adjust": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _VP,
+                          _VP, _VP, _I64, _VP, _VP, _I64, _I, _VP, _I, _I64, _VP]),
+    "topk_distill_forward": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _F, _I, _VP, _VP,
+                                  _VP]),
+    "topk_distill_backward": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _F, _I, _VP, _VP,
+                                   _VP, _I64, _VP]),
+    "topk_distill": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _F, _I, _VP, _VP, _VP, _I64,
+                          _VP]),
     "ivfpq_device_check": (_I, [_VP]),
     "ivfpq_selftest_wait_timeout": (_I, [_I, _VP]),
     "ivfpq_last_error": (C.c_char_p, []),
@@ -513,3 +527,354 @@ def kselect_noalloc(vals, k, out_vals, out_idx, stream=None):
     _check("kselect_noalloc", lib().kselect_noalloc(_ptr(vals), rows, cols, k, _ptr(out_vals),
                                                      _ptr(out_idx), _stream(stream)))
     return out_vals, out_idx
+
+
+# ---- 4-bit vectors, score rows and distillation ------------------------------
+_dtypes = None
+
+
+def _dtype_code(t, name):
+    """ivfpq_dtype of a torch dtype."""
+    global _dtypes
+    if _dtypes is None:
+        torch = _torch()
+        _dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    code = _dtypes.get(t)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t}")
+    return code
+
+
+def _rows(t, name):
+    """(dtype code, rows, cols, row stride) of a floating 2-d CUDA matrix whose
+    rows are dense; the rows themselves may be strided or repeated."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    code = _dtype_code(t.dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{name} must have dense rows (stride 1 along columns)")
+    if rows <= 1:
+        ld = cols
+    elif 0 < ld < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return code, rows, cols, ld
+
+
+def _out_rows(t, shape, dtype, name, device):
+    """As _out, for an output whose rows may be strided: (tensor, row stride)."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    _, rows, cols, ld = _rows(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if (rows, cols) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (the inputs' device), got {t.device}")
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name} must not repeat rows")
+    return t, ld
+
+
+def _vector(t, dtype, n, name, device):
+    """Checks an optional 1-d contiguous argument of n entries."""
+    if t is None:
+        return None
+    _need(t, dtype, name, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+class _on:
+    """Runs a call on `stream`: outputs made inside belong to it, and the
+    allocator keeps the given tensors until its work is done."""
+
+    def __init__(self, stream, device, *tensors):
+        torch = _torch()
+        cur = torch.cuda.current_stream(device)
+        self.ctx = None
+        if stream is not None and stream != cur:
+            self.ctx = torch.cuda.stream(stream)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.device(device)
+        self.handle = (stream if stream is not None else cur).cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _fp4_format(fmt):
+    if isinstance(fmt, str):
+        if fmt not in FP4_FORMATS:
+            raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(FP4_FORMATS)}")
+        return FP4_FORMATS[fmt]
+    if fmt not in (MXFP4, NVFP4):
+        raise ValueError(f"unknown 4-bit format {fmt!r}")
+    return fmt
+
+
+def fp4_shapes(rows, cols, fmt="mxfp4"):
+    """Shapes of the packed codes and of the scale tiles of a [rows, cols] matrix."""
+    kp = (cols + 31) // 32 * 32
+    span = 128 if _fp4_format(fmt) == MXFP4 else 64  # columns of a scale tile
+    return (rows, kp // 2), ((rows + 127) // 128, (kp + span - 1) // span, 512)
+
+
+def _packed(codes, scales, fmt, name, cols=None):
+    """(rows, cols) of packed rows, with the scales' shape checked against the codes'."""
+    torch = _torch()
+    _need(codes, torch.uint8, f"{name} codes", 2)
+    _need(scales, torch.uint8, f"{name} scales", 3)
+    rows, pitch = codes.shape
+    if pitch == 0 or pitch % 16:
+        raise ValueError(f"{name} codes must have a multiple of 16 bytes per row, got {pitch}")
+    if cols is None:
+        cols = 2 * pitch
+    elif not 2 * pitch - 32 < cols <= 2 * pitch:
+        raise ValueError(f"{name}: {cols} columns do not match codes of {pitch} bytes per row")
+    want = fp4_shapes(rows, cols, fmt)[1]
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{name} scales must have shape {want}, got {tuple(scales.shape)}")
+    if scales.device != codes.device:
+        raise ValueError(f"{name}: codes and scales on several devices")
+    return rows, cols
+
+
+def fp4_quantize(x, fmt="mxfp4", tensor_scale=None, codes=None, scales=None, stream=None):
+    """(codes, scales) of the rows of x in a 4-bit block-scaled format:
+    "mxfp4" (a power-of-two scale per 32 columns) or "nvfp4" (an E4M3 scale per
+    16 columns beside tensor_scale, fp32 [1] on the device, 1 if not given)."""
+    torch = _torch()
+    f = _fp4_format(fmt)
+    code, rows, cols, ld = _rows(x, "x")
+    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", x.device)
+    cs, ss = fp4_shapes(rows, cols, f)
+    with _on(stream, x.device, x, tensor_scale, codes, scales) as h:
+        codes = _out(codes, cs, torch.uint8, "codes", x.device)
+        scales = _out(scales, ss, torch.uint8, "scales", x.device)
+        _check("fp4_quantize", lib().fp4_quantize(x.data_ptr(), code, rows, cols, ld, f, g,
+                                                  codes.data_ptr(), scales.data_ptr(), h))
+    return codes, scales
+
+
+def fp4_dequantize(codes, scales, cols=None, fmt="mxfp4", tensor_scale=None, dtype=None, out=None,
+                   stream=None):
+    """The values packed rows stand for, [rows, cols] (cols: all packed columns
+    if not given) of dtype (float32 if not given)."""
+    torch = _torch()
+    f = _fp4_format(fmt)
+    rows, cols = _packed(codes, scales, f, "fp4_dequantize:", cols)
+    dtype = out.dtype if dtype is None and out is not None else dtype or torch.float32
+    code = _dtype_code(dtype, "dtype")
+    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", codes.device)
+    with _on(stream, codes.device, codes, scales, tensor_scale, out) as h:
+        out = _out(out, (rows, cols), dtype, "out", codes.device)
+        _check("fp4_dequantize", lib().fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows,
+                                                      cols, f, g, out.data_ptr(), code, h))
+    return out
+
+
+def fp4_product(a_codes, a_scales, b_codes, b_scales, fmt="mxfp4", a_tensor_scale=None,
+                b_tensor_scale=None, dtype=None, out=None, stream=None):
+    """Inner products [m, n] of packed rows a [m, cols] and b [n, cols], in
+    dtype (float32 if not given: score rows for kselect, once negated)."""
+    torch = _torch()
+    f = _fp4_format(fmt)
+    m, cols = _packed(a_codes, a_scales, f, "fp4_product: a")
+    n, bcols = _packed(b_codes, b_scales, f, "fp4_product: b")
+    if cols != bcols:
+        raise ValueError(f"fp4_product: a has {cols} packed columns and b {bcols}")
+    dev = a_codes.device
+    _same_device("fp4_product", a_codes, b_codes)
+    dtype = out.dtype if dtype is None and out is not None else dtype or torch.float32
+    code = _dtype_code(dtype, "dtype")
+    ga = _vector(a_tensor_scale, torch.float32, 1, "a_tensor_scale", dev)
+    gb = _vector(b_tensor_scale, torch.float32, 1, "b_tensor_scale", dev)
+    with _on(stream, dev, a_codes, a_scales, b_codes, b_scales, a_tensor_scale, b_tensor_scale,
+             out) as h:
+        out = _out(out, (m, n), dtype, "out", dev)
+        _check("fp4_product", lib().fp4_product(
+            a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(),
+            n, cols, f, ga, gb, out.data_ptr(), code, h))
+    return out
+
+
+def fp4_linear(x, w_codes, w_scales, fmt="mxfp4", x_tensor_scale=None, w_tensor_scale=None,
+               dtype=None, out=None, stream=None):
+    """x [m, cols] quantized row by row, times packed weights w [n, cols]:
+    [m, n] in dtype (x's if not given)."""
+    torch = _torch()
+    f = _fp4_format(fmt)
+    xcode, m, cols, ld = _rows(x, "x")
+    n, _ = _packed(w_codes, w_scales, f, "fp4_linear: w", cols)
+    dev = x.device
+    _same_device("fp4_linear", x, w_codes)
+    dtype = out.dtype if dtype is None and out is not None else dtype or x.dtype
+    code = _dtype_code(dtype, "dtype")
+    gx = _vector(x_tensor_scale, torch.float32, 1, "x_tensor_scale", dev)
+    gw = _vector(w_tensor_scale, torch.float32, 1, "w_tensor_scale", dev)
+    with _on(stream, dev, x, w_codes, w_scales, x_tensor_scale, w_tensor_scale, out) as h:
+        out = _out(out, (m, n), dtype, "out", dev)
+        _check("fp4_linear", lib().fp4_linear(
+            x.data_ptr(), xcode, m, ld, w_codes.data_ptr(), w_scales.data_ptr(), n, cols, f, gx,
+            gw, out.data_ptr(), code, h))
+    return out
+
+
+def score_adjust(scores, history=None, history_len=None, prompt_len=None, repetition=None,
+                 presence=None, frequency=None, bias_ids=None, bias_vals=None, temperature=None,
+                 mask=None, negate=False, out=None, dtype=None, stream=None):
+    """Score rows with penalties for repeated tokens, biases, temperature and a
+    bit mask applied (include/ivfpq.h states the order). history: int32
+    [rows, length] (rows may be strided) with history_len and prompt_len int32
+    [rows]; repetition, presence, frequency, temperature: fp32 [rows];
+    bias_ids / bias_vals: int32 / fp32 [rows, nb]; mask: int32 [rows or 1,
+    ceil(cols / 32)], set bits are allowed. out (scores itself, or the scores'
+    type or float32) is made if not given."""
+    torch = _torch()
+    code, rows, cols, lds = _rows(scores, "scores")
+    dev = scores.device
+    hist_cols = ldh = nb = ldm = 0
+    if history is not None:
+        if not isinstance(history, torch.Tensor) or history.dtype != torch.int32:
+            raise TypeError("history must be an int32 tensor")
+        if history.dim() != 2 or history.shape[0] != rows or history.device != dev:
+            raise ValueError(f"history must be [{rows}, length] on {dev}")
+        hist_cols = history.shape[1]
+        ldh, inner = history.stride()
+        if hist_cols > 1 and inner != 1:
+            raise ValueError("history must have dense rows (stride 1 along its length)")
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    if (bias_ids is None) != (bias_vals is None):
+        raise ValueError("bias_ids and bias_vals go together")
+    if bias_ids is not None:
+        _need(bias_ids, torch.int32, "bias_ids", 2)
+        _need(bias_vals, torch.float32, "bias_vals", 2)
+        nb = bias_ids.shape[1]
+        if bias_ids.shape[0] != rows or bias_vals.shape != bias_ids.shape:
+            raise ValueError(f"bias_ids and bias_vals must both be [{rows}, nb]")
+        _same_device("score_adjust", scores, bias_ids, bias_vals)
+    if mask is not None:
+        _need(mask, torch.int32, "mask", 2)
+        words = (cols + 31) // 32
+        if mask.shape[0] not in (1, rows) or mask.shape[1] != words or mask.device != dev:
+            raise ValueError(f"mask must be [{rows} or 1, {words}] on {dev}, got "
+                             f"{tuple(mask.shape)}")
+        ldm = words if mask.shape[0] == rows else 0
+    i32, f32 = torch.int32, torch.float32
+    hl = _vector(history_len, i32, rows, "history_len", dev)
+    pl = _vector(prompt_len, i32, rows, "prompt_len", dev)
+    rep = _vector(repetition, f32, rows, "repetition", dev)
+    pres = _vector(presence, f32, rows, "presence", dev)
+    freq = _vector(frequency, f32, rows, "frequency", dev)
+    temp = _vector(temperature, f32, rows, "temperature", dev)
+    dtype = out.dtype if dtype is None and out is not None else dtype or scores.dtype
+    ocode = _dtype_code(dtype, "dtype")
+    with _on(stream, dev, scores, history, history_len, prompt_len, repetition, presence,
+             frequency, bias_ids, bias_vals, temperature, mask, out) as h:
+        out, ldo = _out_rows(out, (rows, cols), dtype, "out", dev)
+        _check("score_adjust", lib().score_adjust(
+            scores.data_ptr(), code, rows, cols, lds,
+            history.data_ptr() if hist_cols else None, hist_cols, ldh, hl if hist_cols else None,
+            pl if hist_cols else None, rep, pres, freq,
+            bias_ids.data_ptr() if nb else None, bias_vals.data_ptr() if nb else None, nb, temp,
+            mask.data_ptr() if mask is not None else None, ldm, int(bool(negate)),
+            out.data_ptr(), ocode, ldo, h))
+    return out
+
+
+def _teacher(fn, scores, vals, ids):
+    """Checks of a distillation call's inputs: (dtype code, rows, cols, stride, k)."""
+    torch = _torch()
+    code, rows, cols, ld = _rows(scores, "scores")
+    _need(vals, torch.float32, "teacher_vals", 2)
+    _need(ids, torch.int64, "teacher_ids", 2)
+    k = vals.shape[1]
+    if vals.shape[0] != rows or ids.shape != vals.shape:
+        raise ValueError(f"{fn}: teacher_vals and teacher_ids must both be [{rows}, k], got "
+                         f"{tuple(vals.shape)} and {tuple(ids.shape)}")
+    _same_device(fn, scores, vals, ids)
+    return code, rows, cols, ld, k
+
+
+def topk_distill_forward(scores, teacher_vals, teacher_ids, temperature=1.0, negated=False,
+                         stream=None):
+    """(loss fp32 [rows], stats fp32 [rows, 2]) of the student's score rows
+    against a teacher's top list, as kselect or a search returns it (fp32
+    values and int64 ids, [rows, k]); negated: smaller values are better, as in
+    distances. stats is for topk_distill_backward."""
+    torch = _torch()
+    code, rows, cols, ld, k = _teacher("topk_distill_forward", scores, teacher_vals, teacher_ids)
+    dev = scores.device
+    with _on(stream, dev, scores, teacher_vals, teacher_ids) as h:
+        loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        _check("topk_distill_forward", lib().topk_distill_forward(
+            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
+            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), loss.data_ptr(),
+            stats.data_ptr(), h))
+    return loss, stats
+
+
+def topk_distill_backward(scores, teacher_vals, teacher_ids, stats, row_grad, temperature=1.0,
+                          negated=False, grad=None, stream=None):
+    """Gradient of sum(row_grad * loss) with respect to the scores, in their
+    type; grad may be scores itself. A row whose row_grad is 0 gets zeros."""
+    torch = _torch()
+    code, rows, cols, ld, k = _teacher("topk_distill_backward", scores, teacher_vals, teacher_ids)
+    dev = scores.device
+    _need(stats, torch.float32, "stats", 2)
+    if tuple(stats.shape) != (rows, 2) or stats.device != dev:
+        raise ValueError(f"stats must be [{rows}, 2] on {dev}")
+    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
+    if w is None:
+        raise TypeError("row_grad must be a torch tensor")
+    with _on(stream, dev, scores, teacher_vals, teacher_ids, stats, row_grad, grad) as h:
+        grad, ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
+        _check("topk_distill_backward", lib().topk_distill_backward(
+            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
+            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), stats.data_ptr(),
+            w, grad.data_ptr(), ldg, h))
+    return grad
+
+
+def topk_distill(scores, teacher_vals, teacher_ids, row_grad, temperature=1.0, negated=False,
+                 grad=None, stream=None):
+    """(loss fp32 [rows], gradient of sum(row_grad * loss)) in one call, as a
+    training step needs them; grad may be scores itself."""
+    torch = _torch()
+    code, rows, cols, ld, k = _teacher("topk_distill", scores, teacher_vals, teacher_ids)
+    dev = scores.device
+    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
+    if w is None:
+        raise TypeError("row_grad must be a torch tensor")
+    with _on(stream, dev, scores, teacher_vals, teacher_ids, row_grad, grad) as h:
+        loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+        grad, ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
+        _check("topk_distill", lib().topk_distill(
+            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
+            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), w,
+            loss.data_ptr(), grad.data_ptr(), ldg, h))
+    return loss, grad

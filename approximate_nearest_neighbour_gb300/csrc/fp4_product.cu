@@ -1,0 +1,454 @@
+// fp4_product / fp4_linear: out[i, j] = ga gb sum_t a[i, t] b[j, t] over packed
+// 4-bit block-scaled rows (layout: fp4.cuh), on the block-scaled tensor-core
+// product of the 5th generation (tcgen05.mma, kind::mxf4nvf4: E2M1 elements
+// with an E8M0 scale per 32 or an E4M3 scale per 16, fp32 accumulation).
+//
+// The table b is the instruction's 128-row operand and the rows of a its
+// columns, so an accumulator lane holds one column of out and a warp's store
+// covers 32 consecutive columns of one row of out, whatever their alignment;
+// and a few rows of a cost a narrow instruction instead of a padded one.
+//
+// One CTA per (128 columns of out, T rows of out, slice of K), 6 warps:
+//  * warp 0, one thread: TMA producer. A stage is 256 columns of K: 128 rows
+//    of b and T rows of a (128 bytes each, 128-byte swizzle) and their scale
+//    tiles, which are contiguous;
+//  * warp 1: TMEM; one thread copies a stage's scale tiles to TMEM and issues
+//    one product per 64 columns. Each stage has TMEM columns of its own for
+//    its scales: they are rewritten only after the stage's products committed;
+//  * warps 2..5: epilogue, a TMEM lane each.
+// A cluster splits K between its CTAs when there are few tiles; the partial
+// sums are joined in rank order through distributed shared memory. Shared
+// memory lets at most two CTAs of any variant share an SM, and two always fit
+// its 512 TMEM columns: no CTA of a cluster waits for TMEM that another
+// cluster holds while it waits itself.
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace ivfpq {
+
+int fp4_quantize_device(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt,
+                        const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                        cudaStream_t s);
+
+namespace {
+
+constexpr int BN = 128;            // columns of out (rows of b) per CTA
+constexpr int KB = 128;            // bytes of K per stage and row
+constexpr int KE = 2 * KB;         // K columns per stage
+constexpr int kThreads = 192;
+
+struct ProdArgs {
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  const float* a_ts;
+  const float* b_ts;
+  void* out;
+  int64_t ldo;
+  int64_t m, n;
+  int kp;       // padded K
+  int ntile;    // scale tiles along K
+  int dtype;
+  int* err;
+};
+
+template <int FMT, int T>
+struct Cfg {
+  static constexpr int kTilesPerStage = FMT == IVFPQ_MXFP4 ? 2 : 4;  // scale tiles of 256 columns
+  static constexpr int kSf = kTilesPerStage * 512;
+  static constexpr int kB = BN * KB;
+  static constexpr int kA = T * KB;
+  static constexpr int kStage = kB + kA + 2 * kSf;
+  static constexpr int kStages = T <= 32 ? 4 : 3;
+  static constexpr int kBars = 256;
+  static constexpr int kTotal = kStages * kStage + kBars + 1024;
+  // TMEM: the accumulator, then each stage's scales of b and of a
+  static constexpr int kSfCols = 2 * 4 * kTilesPerStage;
+  static constexpr int kAccCols = T < 32 ? 32 : T;
+  static constexpr int kUsed = kAccCols + kStages * kSfCols;
+  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256 && kTotal > 76 * 1024, "two CTAs per SM, and their TMEM fits");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Scale tile in shared memory: 32 rows of 16 bytes, no swizzle, 8-row groups
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// One scale tile to four TMEM columns of all four lane groups.
+__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+               : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, uint32_t acc) {
+  if (FMT == IVFPQ_MXFP4)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        : "memory");
+}
+// Instruction descriptor: E2M1 operands, K-major, M = 128, N = T, the scale
+// type, and (MXFP4) which half of a TMEM column's four scales this product
+// uses.
+template <int FMT, int T>
+__device__ __forceinline__ uint32_t fp4_idesc(uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(T >> 3) << 17) |
+         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(BN >> 7) << 27) | (sf_id << 29);
+}
+__device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, float v) {
+  if (dtype == IVFPQ_F32)
+    static_cast<float*>(out)[at] = v;
+  else if (dtype == IVFPQ_BF16)
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(out)[at] = __float2half_rn(v);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
+                   "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// grid (column tiles, row tiles, K slices); the cluster is the K slices.
+template <int FMT, int T>
+__global__ void __launch_bounds__(kThreads)
+fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_a, const ProdArgs p) {
+  using C = Cfg<FMT, T>;
+  extern __shared__ uint8_t fp4_smem_raw[];
+  const uint32_t raw = smem_u32(fp4_smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = fp4_smem_raw + (base - raw);
+  const uint32_t bars = base + C::kStages * C::kStage;
+  auto s_b = [&](int s) { return base + s * (C::kB + C::kA); };
+  auto s_a = [&](int s) { return base + s * (C::kB + C::kA) + C::kB; };
+  const uint32_t sf0 = base + C::kStages * (C::kB + C::kA);
+  auto s_sfb = [&](int s) { return sf0 + s * 2 * C::kSf; };
+  auto s_sfa = [&](int s) { return sf0 + s * 2 * C::kSf + C::kSf; };
+  auto bar_full = [&](int s) { return bars + 8 * s; };
+  auto bar_empty = [&](int s) { return bars + 8 * (C::kStages + s); };
+  const uint32_t bar_acc = bars + 16 * C::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 16 * C::kStages + 8);
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(gbase + (bars - base) + 16 * C::kStages + 16);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nslice = gridDim.z;
+  const int nk = (p.kp + KE - 1) / KE;
+  const int k_lo = int(int64_t(nk) * blockIdx.z / nslice);
+  const int k_hi = int(int64_t(nk) * (blockIdx.z + 1) / nslice);
+  const int n0 = blockIdx.x * BN;
+  const int m0 = blockIdx.y * T;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    mbar_init(bar_acc, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(C::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    atomicExch(p.err, 1);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---- TMA producer ----
+    const uint8_t* sb = p.b_scales + int64_t(blockIdx.x) * p.ntile * 512;
+    const uint8_t* sa = p.a_scales + int64_t(m0 >> 7) * p.ntile * 512;
+    int it = 0;
+    for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc, ++it) {
+      const int s = it % C::kStages;
+      if (!mbar_wait(bar_empty(s), ((it / C::kStages) & 1) ^ 1)) {
+        fail();
+        break;
+      }
+      const int t0 = kc * C::kTilesPerStage;
+      const uint32_t sf_bytes = uint32_t(min(C::kTilesPerStage, p.ntile - t0)) * 512;
+      mbar_expect_tx(bar_full(s), C::kB + C::kA + 2 * sf_bytes);
+      tma_load_2d(s_b(s), &map_b, kc * KB, n0, bar_full(s));
+      tma_load_2d(s_a(s), &map_a, kc * KB, m0, bar_full(s));
+      bulk_load(s_sfb(s), sb + int64_t(t0) * 512, sf_bytes, bar_full(s));
+      bulk_load(s_sfa(s), sa + int64_t(t0) * 512, sf_bytes, bar_full(s));
+    }
+    // copies still in flight land before the CTA ends
+    for (int j = max(0, it - C::kStages); j < it; ++j)
+      mbar_wait(bar_full(j % C::kStages), (j / C::kStages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    // ---- scale copies and products ----
+    int it = 0;
+    for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc, ++it) {
+      const int s = it % C::kStages;
+      if (!mbar_wait(bar_full(s), (it / C::kStages) & 1)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      const int tiles = min(C::kTilesPerStage, p.ntile - kc * C::kTilesPerStage);
+      const uint32_t tsb = tmem + C::kAccCols + s * C::kSfCols;
+      const uint32_t tsa = tsb + C::kSfCols / 2;
+      for (int t = 0; t < tiles; ++t) {
+        scale_copy(tsb + 4 * t, scale_desc(s_sfb(s) + 512 * t));
+        scale_copy(tsa + 4 * t, scale_desc(s_sfa(s) + 512 * t));
+      }
+      const uint64_t db = smem_desc(s_b(s)), da = smem_desc(s_a(s));
+      const int steps = min(4, (p.kp - kc * KE + 63) / 64);
+      for (int j = 0; j < steps; ++j) {
+        const uint64_t adv = uint64_t(j * 32) >> 4;  // 64 columns = 32 bytes
+        const int t = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
+        const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
+        mma_fp4<FMT>(tmem, db + adv, da + adv, fp4_idesc<FMT, T>(id), tsb + 4 * t, tsa + 4 * t,
+                     it > 0 || j > 0);
+      }
+      mma_commit(bar_empty(s));
+    }
+    // also the end of every product issued before an early exit
+    mma_commit(bar_acc);
+    if (!mbar_wait(bar_acc, 0)) fail();
+  } else if (warp >= 2) {
+    if (!mbar_wait(bar_acc, 0)) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const float alpha = (p.a_ts ? __ldg(p.a_ts) : 1.f) * (p.b_ts ? __ldg(p.b_ts) : 1.f);
+  const bool ok = !*abort_flag;
+  // ---- epilogue: warp w of 2..5 reads TMEM lanes 32 * (w % 4) .. +32 ----
+  if (nslice == 1) {
+    if (warp >= 2 && ok) {
+      const int lg = warp & 3;
+      const int64_t col = n0 + 32 * lg + lane;
+#pragma unroll 1
+      for (int c = 0; c < C::kAccCols; c += 32) {
+        float v[32];
+        tmem_ld32(tmem + (uint32_t(32 * lg) << 16) + uint32_t(c), v);
+        if (col < p.n) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < T && m0 + c + j < p.m)
+              store_out(p.out, (m0 + c + j) * p.ldo + col, p.dtype, v[j] * alpha);
+        }
+      }
+    }
+  } else {
+    // partial sums to this CTA's shared memory ([T][128]; every stage has been
+    // consumed), then each rank joins its share of the rows
+    float* part = reinterpret_cast<float*>(gbase);
+    if (warp >= 2) {
+      const int lg = warp & 3;
+#pragma unroll 1
+      for (int c = 0; c < C::kAccCols; c += 32) {
+        float v[32];
+        tmem_ld32(tmem + (uint32_t(32 * lg) << 16) + uint32_t(c), v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < T) part[(c + j) * BN + 32 * lg + lane] = v[j];
+      }
+    }
+    cluster_sync();
+    const int rank = int(cluster_rank());
+    const int rows = int(min(int64_t(T), p.m - m0));
+    for (int i = rank * kThreads + threadIdx.x; i < rows * BN; i += nslice * kThreads) {
+      float sum = 0.f;
+      for (int r = 0; r < nslice; ++r) sum += ld_cluster(base + 4u * uint32_t(i), uint32_t(r));
+      const int64_t col = n0 + i % BN;
+      if (col < p.n && ok) store_out(p.out, (m0 + i / BN) * p.ldo + col, p.dtype, sum * alpha);
+    }
+    cluster_sync();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(C::kTmem)
+                 : "memory");
+  }
+}
+
+int code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  IVFPQ_TRY(tensor_map_encoder(&enc));
+  cuuint64_t dims[2] = {cuuint64_t(pitch), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(pitch)};
+  cuuint32_t box[2] = {KB, cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld code bytes", int(r),
+              (long long)rows, (long long)pitch);
+    return IVFPQ_ERR_CUDA;
+  }
+  return IVFPQ_OK;
+}
+
+template <int FMT, int T>
+int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
+  using C = Cfg<FMT, T>;
+  CUtensorMap mb, ma;
+  IVFPQ_TRY(code_map(&mb, b, p.n, p.kp / 2, BN));
+  IVFPQ_TRY(code_map(&ma, a, p.m, p.kp / 2, T));
+  auto kern = fp4_product_kernel<FMT, T>;
+  IVFPQ_TRY(set_dynamic_smem(kern, C::kTotal));
+  const int64_t tiles_n = ceil_div(p.n, BN), tiles_m = ceil_div(p.m, T);
+  const int64_t nk = ceil_div(p.kp, KE);
+  // K slices while the tiles alone leave SMs idle and a slice keeps two stages
+  int slices = 1;
+  while (slices < 8 && tiles_n * tiles_m * slices * 2 <= 2 * num_sms() && nk >= 4 * slices)
+    slices *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(tiles_n), unsigned(tiles_m), unsigned(slices));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kTotal;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = unsigned(slices);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, mb, ma, p));
+  IVFPQ_LAUNCHED_K(kern, C::kTotal, kThreads);
+  return IVFPQ_OK;
+}
+
+template <int FMT>
+int launch_fmt(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
+  // the narrowest instruction that holds all rows; a narrow one starts at row
+  // 0 of its scale tile, so it is only taken where one row tile covers m
+  if (p.m <= 16) return launch<FMT, 16>(a, b, p, s);
+  if (p.m <= 32) return launch<FMT, 32>(a, b, p, s);
+  if (p.m <= 64) return launch<FMT, 64>(a, b, p, s);
+  return launch<FMT, 128>(a, b, p, s);
+}
+
+int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
+                   const uint8_t* b_scales, int64_t n, int64_t cols, int fmt, const float* a_ts,
+                   const float* b_ts, void* out, int dtype, cudaStream_t s) {
+  ProdArgs p{};
+  p.a_scales = a_scales;
+  p.b_scales = b_scales;
+  p.a_ts = fmt == IVFPQ_NVFP4 ? a_ts : nullptr;
+  p.b_ts = fmt == IVFPQ_NVFP4 ? b_ts : nullptr;
+  p.out = out;
+  p.ldo = n;
+  p.m = m;
+  p.n = n;
+  p.kp = int(fp4_padded_cols(cols));
+  p.ntile = int(fp4_scale_tiles(cols, fmt));
+  p.dtype = dtype;
+  IVFPQ_TRY(device_status_word(&p.err));
+  return fmt == IVFPQ_MXFP4 ? launch_fmt<IVFPQ_MXFP4>(a, b, p, s)
+                            : launch_fmt<IVFPQ_NVFP4>(a, b, p, s);
+}
+
+int check_product(const char* fn, int64_t m, int64_t n, int64_t cols, int fmt, int dtype) {
+  IVFPQ_REQUIRE(m >= 0 && m <= 65535 * int64_t(128), "%s: m=%lld outside [0, 8388480]", fn,
+                (long long)m);
+  IVFPQ_REQUIRE(n >= 0 && n < (int64_t(1) << 31) - 128, "%s: n=%lld outside [0, 2^31 - 128)", fn,
+                (long long)n);
+  IVFPQ_REQUIRE(cols >= 1 && cols <= (int64_t(1) << 24), "%s: cols=%lld outside [1, 2^24]", fn,
+                (long long)cols);
+  IVFPQ_REQUIRE(fmt == IVFPQ_MXFP4 || fmt == IVFPQ_NVFP4, "%s: unknown format %d", fn, fmt);
+  IVFPQ_REQUIRE(known_dtype(dtype), "%s: unknown element type %d", fn, dtype);
+  return IVFPQ_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace ivfpq
+
+using namespace ivfpq;
+
+extern "C" int fp4_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                           const uint8_t* b_codes, const uint8_t* b_scales, int64_t n,
+                           int64_t cols, int fmt, const float* a_tensor_scale,
+                           const float* b_tensor_scale, void* out, int dtype, void* stream) {
+  clear_error();
+  IVFPQ_TRY(check_product("fp4_product", m, n, cols, fmt, dtype));
+  if (m == 0 || n == 0) return IVFPQ_OK;
+  IVFPQ_REQUIRE(a_codes && a_scales && b_codes && b_scales && out, "fp4_product: null pointer");
+  IVFPQ_REQUIRE(aligned16(a_codes) && aligned16(a_scales) && aligned16(b_codes) &&
+                    aligned16(b_scales),
+                "fp4_product: codes and scales must be 16-byte aligned");
+  return product_device(a_codes, a_scales, m, b_codes, b_scales, n, cols, fmt, a_tensor_scale,
+                        b_tensor_scale, out, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ldx,
+                          const uint8_t* w_codes, const uint8_t* w_scales, int64_t n, int64_t cols,
+                          int fmt, const float* x_tensor_scale, const float* w_tensor_scale,
+                          void* out, int dtype, void* stream) {
+  clear_error();
+  IVFPQ_TRY(check_product("fp4_linear", m, n, cols, fmt, dtype));
+  IVFPQ_REQUIRE(known_dtype(x_dtype), "fp4_linear: unknown element type %d", x_dtype);
+  IVFPQ_REQUIRE(ldx >= cols || m <= 1 || ldx == 0, "fp4_linear: row stride %lld below cols=%lld",
+                (long long)ldx, (long long)cols);
+  if (m == 0 || n == 0) return IVFPQ_OK;
+  IVFPQ_REQUIRE(x && w_codes && w_scales && out, "fp4_linear: null pointer");
+  IVFPQ_REQUIRE(aligned16(w_codes) && aligned16(w_scales),
+                "fp4_linear: codes and scales must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Workspace ws(s);
+  uint8_t* codes = nullptr;
+  const int64_t code_bytes = m * (fp4_padded_cols(cols) / 2);
+  const int64_t scale_bytes = ceil_div(m, 128) * fp4_scale_tiles(cols, fmt) * 512;
+  IVFPQ_TRY(ws.alloc(&codes, size_t(ceil_div(code_bytes, 512) * 512 + scale_bytes)));
+  uint8_t* scales = codes + ceil_div(code_bytes, 512) * 512;
+  IVFPQ_TRY(fp4_quantize_device(x, x_dtype, m, cols, ldx, fmt, x_tensor_scale, codes, scales, s));
+  return product_device(codes, scales, m, w_codes, w_scales, n, cols, fmt, x_tensor_scale,
+                        w_tensor_scale, out, dtype, s);
+}

@@ -431,6 +431,155 @@ int ivfpq_repaired_queries(const ivfpq_index* index, int64_t* count, void* strea
 int knn_merge(const float* dists, const int64_t* ids, int64_t nq, int nshards, int k_in, int k,
               float* out_dist, int64_t* out_ids, void* stream);
 
+/* Element types of score rows and floating vectors. */
+typedef enum { IVFPQ_F32 = 0, IVFPQ_F16 = 1, IVFPQ_BF16 = 2 } ivfpq_dtype;
+
+/* 4-bit block-scaled formats (OCP microscaling formats specification v1.0 for
+ * MXFP4). Elements are E2M1: 0, .5, 1, 1.5, 2, 3, 4, 6 in magnitude. */
+typedef enum {
+  IVFPQ_MXFP4 = 0, /* one E8M0 scale (a power of two) per 32 columns */
+  IVFPQ_NVFP4 = 1  /* one E4M3 scale per 16 columns, one fp32 scale per matrix */
+} ivfpq_fp4_format;
+
+/*
+ * fp4_quantize -- rows to 4-bit block-scaled form.
+ * MXFP4: block scale 2^e, e = floor(log2(amax)) - 2 clamped to [-127, 127].
+ * NVFP4: block scale s = E4M3(min(448, amax / (6 g))), g = *tensor_scale, and
+ * a value stands for element * s * g. Elements are x / scale rounded to
+ * nearest (ties to the even code), saturating at 6. A block that holds an
+ * infinity or a NaN gets a NaN scale and reads back as NaN.
+ *  x       device [rows, cols] of dtype, row stride ldx elements (>= cols, or
+ *          0 to repeat one row); cols need not be a multiple of the block:
+ *          the last block is short
+ *  tensor_scale  device fp32 [1], > 0 (NVFP4; NULL = 1); ignored for MXFP4
+ *  codes   device uint8 [rows, kp / 2] (out), kp = cols rounded up to 32: two
+ *          codes per byte, the even column in the low half, zero past cols
+ *  scales  device uint8 (out), tiles of 128 rows x 4 blocks, 512 bytes each,
+ *          [ceil(rows / 128)][ceil(kp / (4 * block))]: row r, block c is byte
+ *          (r % 32) * 16 + (r / 32 % 4) * 4 + c % 4 of its tile; bytes of rows
+ *          and blocks beyond the matrix are zero, and must be where a caller
+ *          lays scales out
+ * codes and scales start on 16-byte boundaries. Errors: INVALID_ARG, CUDA.
+ */
+int fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt,
+                 const float* tensor_scale, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * fp4_dequantize -- the values that packed rows stand for, [rows, cols] of
+ * dtype (densely packed): element * block scale in fp32 (exact), times
+ * *tensor_scale (NVFP4), rounded once to dtype. Errors: INVALID_ARG, CUDA.
+ */
+int fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                   int fmt, const float* tensor_scale, void* out, int dtype, void* stream);
+
+/*
+ * fp4_product -- inner products of packed rows:
+ *   out[i, j] = ga gb sum_t a[i, t] b[j, t]
+ * on the block-scaled tensor-core product, accumulated in fp32, rounded once
+ * to dtype. Both operands have the same format and cols (layout as written by
+ * fp4_quantize); ga, gb are the matrices' fp32 scales (device fp32 [1], NULL =
+ * 1; NVFP4 only). Many rows or a single one: the narrow case reads b once.
+ * The sum over cols is split in an order fixed by the sizes, so results
+ * repeat bit for bit.
+ *  out  device [m, n] of dtype, densely packed
+ * m <= 8,388,480 rows. Errors: INVALID_ARG, CUDA.
+ */
+int fp4_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t cols, int fmt,
+                const float* a_tensor_scale, const float* b_tensor_scale, void* out, int dtype,
+                void* stream);
+
+/*
+ * fp4_linear -- floating rows through a packed weight matrix: x is quantized
+ * as by fp4_quantize, then multiplied as by fp4_product; the result is that
+ * of the two calls. Errors: INVALID_ARG, OOM, CUDA.
+ *  x  device [m, cols] of x_dtype, row stride ldx elements
+ *  w  packed [n, cols]; out device [m, n] of dtype
+ */
+int fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const uint8_t* w_codes,
+               const uint8_t* w_scales, int64_t n, int64_t cols, int fmt,
+               const float* x_tensor_scale, const float* w_tensor_scale, void* out, int dtype,
+               void* stream);
+
+/*
+ * score_adjust -- the changes of score rows between the product that makes
+ * them and the selection that reads them, in this order, for row r, column c:
+ *   c in the row's history:     x = x > 0 ? x / repetition : x * repetition
+ *   n occurrences past the prompt, n > 0:  x -= n * frequency + presence
+ *   c in the row's bias list:   x += its bias (the last entry of an id holds)
+ *   x /= temperature
+ *   c not allowed by the mask:  x = -inf (whatever the score was)
+ *   negate != 0:                x = -x (kselect selects the smallest)
+ * computed in fp32 and rounded once.
+ *  scores        device [rows, cols] of dtype, row stride lds (0 repeats a row)
+ *  history       device int32 [rows, hist_cols], row stride ldh, or NULL;
+ *                entries outside [0, cols) are ignored
+ *  history_len   device int32 [rows], entries of each row in use (NULL: all)
+ *  prompt_len    device int32 [rows], how many of them are the prompt's, which
+ *                only the repetition factor looks at (NULL: none)
+ *  repetition, presence, frequency, temperature  device fp32 [rows] or NULL
+ *                (1, 0, 0, 1)
+ *  bias_ids, bias_vals  device int32 / fp32 [rows, nb] or NULL; ids outside
+ *                [0, cols) are ignored
+ *  mask          device int32 words, bit c % 32 of word c / 32 set = allowed,
+ *                row stride ldm words (0: one mask for all rows), or NULL. A
+ *                row that its mask leaves nothing is -inf throughout
+ *  out           device [rows, cols] of out_dtype (dtype or IVFPQ_F32), row
+ *                stride ldo; may be scores itself (same type and stride)
+ * Errors: INVALID_ARG, CUDA.
+ */
+int score_adjust(const void* scores, int dtype, int64_t rows, int64_t cols, int64_t lds,
+                 const int32_t* history, int64_t hist_cols, int64_t ldh,
+                 const int32_t* history_len, const int32_t* prompt_len, const float* repetition,
+                 const float* presence, const float* frequency, const int32_t* bias_ids,
+                 const float* bias_vals, int64_t nb, const float* temperature,
+                 const int32_t* mask, int64_t ldm, int negate, void* out, int out_dtype,
+                 int64_t ldo, void* stream);
+
+/*
+ * topk_distill_forward -- a student's loss against a teacher's top list, per
+ * row, with tau = temperature:
+ *   p_i = softmax_i(t_i / tau) over the row's valid list entries,
+ *   q_j = softmax_j(s_j / tau) over all columns of the student's row,
+ *   loss = tau^2 sum_i p_i (log p_i - log q_id(i))
+ *  scores        device [rows, cols] of dtype, row stride lds (0 repeats a row)
+ *  teacher_vals  device fp32 [rows, k], teacher_ids device int64 [rows, k]: as
+ *                kselect or a search returns them; an entry whose id is outside
+ *                [0, cols) or whose t is -inf (the padding of a short list) is
+ *                not valid. A repeated id stands for the sum of its entries
+ *  negated       nonzero: t = -value (distances, or kselect of negated scores)
+ *  loss          device fp32 [rows] (out); 0 for a row without valid entries,
+ *                +inf where a valid entry's score is -inf
+ *  stats         device fp32 [rows, 2] (out): the row's largest score m and
+ *                sum_j exp((s_j - m) / tau), for topk_distill_backward
+ * 1 <= k <= IVFPQ_MAX_K. A score of -inf has q = 0. Errors: INVALID_ARG, CUDA.
+ */
+int topk_distill_forward(const void* scores, int dtype, int64_t rows, int64_t cols, int64_t lds,
+                         const float* teacher_vals, const int64_t* teacher_ids, int k,
+                         float temperature, int negated, float* loss, float* stats, void* stream);
+
+/*
+ * topk_distill_backward -- the loss's gradient with respect to the scores:
+ *   grad[r, j] = row_grad[r] tau (q_j - sum of p_i over the entries with id j)
+ * (0 for a row without valid entries, and for a row whose row_grad is 0,
+ * whatever its scores hold). stats as topk_distill_forward wrote them;
+ * row_grad device fp32 [rows]; grad device [rows, cols] of dtype (out), row
+ * stride ldg; may be scores itself (same stride). Errors: INVALID_ARG, CUDA.
+ */
+int topk_distill_backward(const void* scores, int dtype, int64_t rows, int64_t cols, int64_t lds,
+                          const float* teacher_vals, const int64_t* teacher_ids, int k,
+                          float temperature, int negated, const float* stats,
+                          const float* row_grad, void* grad, int64_t ldg, void* stream);
+
+/*
+ * topk_distill -- loss and gradient in one call (arguments as above).
+ * Errors: INVALID_ARG, OOM, CUDA.
+ */
+int topk_distill(const void* scores, int dtype, int64_t rows, int64_t cols, int64_t lds,
+                 const float* teacher_vals, const int64_t* teacher_ids, int k, float temperature,
+                 int negated, const float* row_grad, float* loss, void* grad, int64_t ldg,
+                 void* stream);
+
 /* ivfpq_device_check -- synchronises `stream` and reports whether any kernel
  * of this library on the current device gave up a bounded wait since the
  * last check (the tensor-core distance pipeline waits on its own copies and
