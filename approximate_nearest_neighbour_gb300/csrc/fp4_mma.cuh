@@ -1,0 +1,108 @@
+// Block-scaled 4-bit tensor-core products: operand copies, scale tiles, the
+// instruction and the arguments shared by the narrow and the wide kernel.
+#pragma once
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace ivfpq {
+
+constexpr int BN = 128;            // columns of out (rows of b) per CTA
+constexpr int KB = 128;            // bytes of K per stage and row
+constexpr int KE = 2 * KB;         // K columns per stage
+
+struct ProdArgs {
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  const float* a_ts;
+  const float* b_ts;
+  void* out;
+  int64_t ldo;
+  int64_t m, n;
+  int kp;       // padded K
+  int ntile;    // scale tiles along K
+  int dtype;
+  int* err;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Scale tile in shared memory: 32 rows of 16 bytes, no swizzle, 8-row groups
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// One scale tile to four TMEM columns of all four lane groups.
+__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+               : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, uint32_t acc) {
+  if (FMT == IVFPQ_MXFP4)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        : "memory");
+}
+// Instruction descriptor: E2M1 operands, K-major, M = 128, N = T, the scale
+// type, and (MXFP4) which half of a TMEM column's four scales this product
+// uses.
+template <int FMT, int T>
+__device__ __forceinline__ uint32_t fp4_idesc(uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(T >> 3) << 17) |
+         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(BN >> 7) << 27) | (sf_id << 29);
+}
+__device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, float v) {
+  if (dtype == IVFPQ_F32)
+    static_cast<float*>(out)[at] = v;
+  else if (dtype == IVFPQ_BF16)
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(out)[at] = __float2half_rn(v);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
+                   "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// Tensor map over packed code rows; a box is 128 bytes of K by box_rows rows.
+int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows);
+
+// The wide kernel (fp4_wide.cu).
+int fp4_product_wide(const uint8_t* a, const uint8_t* b, const ProdArgs& p, int fmt,
+                     cudaStream_t s);
+
+}  // namespace ivfpq

@@ -23,9 +23,7 @@
 // cluster holds while it waits itself.
 #include <algorithm>
 
-#include "fp4.cuh"
-#include "internal.h"
-#include "tc_ptx.cuh"
+#include "fp4_mma.cuh"
 
 namespace ivfpq {
 
@@ -33,26 +31,27 @@ int fp4_quantize_device(const void* x, int dtype, int64_t rows, int64_t cols, in
                         const float* tensor_scale, uint8_t* codes, uint8_t* scales,
                         cudaStream_t s);
 
+int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  IVFPQ_TRY(tensor_map_encoder(&enc));
+  cuuint64_t dims[2] = {cuuint64_t(pitch), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(pitch)};
+  cuuint32_t box[2] = {KB, cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld code bytes", int(r),
+              (long long)rows, (long long)pitch);
+    return IVFPQ_ERR_CUDA;
+  }
+  return IVFPQ_OK;
+}
+
 namespace {
 
-constexpr int BN = 128;            // columns of out (rows of b) per CTA
-constexpr int KB = 128;            // bytes of K per stage and row
-constexpr int KE = 2 * KB;         // K columns per stage
 constexpr int kThreads = 192;
-
-struct ProdArgs {
-  const uint8_t* a_scales;
-  const uint8_t* b_scales;
-  const float* a_ts;
-  const float* b_ts;
-  void* out;
-  int64_t ldo;
-  int64_t m, n;
-  int kp;       // padded K
-  int ntile;    // scale tiles along K
-  int dtype;
-  int* err;
-};
 
 template <int FMT, int T>
 struct Cfg {
@@ -71,78 +70,6 @@ struct Cfg {
   static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
   static_assert(kUsed <= 256 && kTotal > 76 * 1024, "two CTAs per SM, and their TMEM fits");
 };
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-// Scale tile in shared memory: 32 rows of 16 bytes, no swizzle, 8-row groups
-// 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
-}
-// One scale tile to four TMEM columns of all four lane groups.
-__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
-}
-template <int FMT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t sa, uint32_t sb, uint32_t acc) {
-  if (FMT == IVFPQ_MXFP4)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
-        : "memory");
-}
-// Instruction descriptor: E2M1 operands, K-major, M = 128, N = T, the scale
-// type, and (MXFP4) which half of a TMEM column's four scales this product
-// uses.
-template <int FMT, int T>
-__device__ __forceinline__ uint32_t fp4_idesc(uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(T >> 3) << 17) |
-         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(BN >> 7) << 27) | (sf_id << 29);
-}
-__device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, float v) {
-  if (dtype == IVFPQ_F32)
-    static_cast<float*>(out)[at] = v;
-  else if (dtype == IVFPQ_BF16)
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(out)[at] = __float2half_rn(v);
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
-      : "=f"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
 
 // grid (column tiles, row tiles, K slices); the cluster is the K slices.
 template <int FMT, int T>
@@ -315,30 +242,12 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   }
 }
 
-int code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc;
-  IVFPQ_TRY(tensor_map_encoder(&enc));
-  cuuint64_t dims[2] = {cuuint64_t(pitch), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(pitch)};
-  cuuint32_t box[2] = {KB, cuuint32_t(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    set_error("cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld code bytes", int(r),
-              (long long)rows, (long long)pitch);
-    return IVFPQ_ERR_CUDA;
-  }
-  return IVFPQ_OK;
-}
-
 template <int FMT, int T>
 int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
   using C = Cfg<FMT, T>;
   CUtensorMap mb, ma;
-  IVFPQ_TRY(code_map(&mb, b, p.n, p.kp / 2, BN));
-  IVFPQ_TRY(code_map(&ma, a, p.m, p.kp / 2, T));
+  IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, BN));
+  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, T));
   auto kern = fp4_product_kernel<FMT, T>;
   IVFPQ_TRY(set_dynamic_smem(kern, C::kTotal));
   const int64_t tiles_n = ceil_div(p.n, BN), tiles_m = ceil_div(p.m, T);
@@ -390,6 +299,9 @@ int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const u
   p.ntile = int(fp4_scale_tiles(cols, fmt));
   p.dtype = dtype;
   IVFPQ_TRY(device_status_word(&p.err));
+  // enough 128 x 128 tiles to keep every SM busy without splitting K
+  if (m > 64 && ceil_div(n, BN) * ceil_div(m, 128) >= num_sms())
+    return fp4_product_wide(a, b, p, fmt, s);
   return fmt == IVFPQ_MXFP4 ? launch_fmt<IVFPQ_MXFP4>(a, b, p, s)
                             : launch_fmt<IVFPQ_NVFP4>(a, b, p, s);
 }
@@ -397,7 +309,7 @@ int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const u
 int check_product(const char* fn, int64_t m, int64_t n, int64_t cols, int fmt, int dtype) {
   IVFPQ_REQUIRE(m >= 0 && m <= 65535 * int64_t(128), "%s: m=%lld outside [0, 8388480]", fn,
                 (long long)m);
-  IVFPQ_REQUIRE(n >= 0 && n < (int64_t(1) << 31) - 128, "%s: n=%lld outside [0, 2^31 - 128)", fn,
+  IVFPQ_REQUIRE(n >= 0 && n < (int64_t(1) << 31) - 1024, "%s: n=%lld outside [0, 2^31 - 1024)", fn,
                 (long long)n);
   IVFPQ_REQUIRE(cols >= 1 && cols <= (int64_t(1) << 24), "%s: cols=%lld outside [1, 2^24]", fn,
                 (long long)cols);

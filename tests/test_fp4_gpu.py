@@ -157,9 +157,12 @@ def _operands(B, fmt, m, n, cols, seed):
 @pytest.mark.parametrize("m,n,cols", [
     (1, 1, 1), (1, 128, 32), (2, 129, 96), (16, 1000, 64), (17, 257, 128), (33, 300, 300),
     (64, 128, 256), (65, 4099, 96), (128, 128, 512), (129, 1, 1000), (300, 515, 777),
-    (1, 4096, 4096), (5, 333, 8200), (37, 2048, 2304), (130, 640, 4097), (513, 1283, 96)])
+    (1, 4096, 4096), (5, 333, 8200), (37, 2048, 2304), (130, 640, 4097), (513, 1283, 96),
+    (100, 20000, 64), (100, 40000, 700), (1100, 2100, 1000), (130, 20000, 300), (300, 20000, 96),
+    (1500, 20001, 160), (2500, 2500, 520), (257, 9999, 2050)])
 def test_product(B, fmt, m, n, cols):
-    """One row to many, ragged tiles and K, one and several K slices."""
+    """One row to many, ragged tiles and K, one and several K slices, few and
+    many tiles per CTA."""
     import torch
     qa, qb, ga, gb, va, vb = _operands(B, fmt, m, n, cols, m + n + cols)
     alpha = 1.0 if ga is None else float(ga) * float(gb)
