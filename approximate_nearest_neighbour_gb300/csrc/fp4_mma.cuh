@@ -39,36 +39,63 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
 }
-// One scale tile to four TMEM columns of all four lane groups.
-__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
+// The issuing warp runs its loops converged, so that descriptors and addresses
+// stay uniform, and one lane (el != 0) issues: a lane branching off alone made
+// each scale copy cost 61 clocks and an empty step 800 (the operands move from
+// vector registers one by one).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(e));
+  return e;
 }
-template <int FMT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t sa, uint32_t sb, uint32_t acc) {
-  if (FMT == IVFPQ_MXFP4)
+// One scale tile to four TMEM columns of all four lane groups.
+template <int CG>
+__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc, uint32_t el) {
+  if (CG == 2)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+        " @q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(tmem),
+        "l"(desc), "r"(el)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
-        : "memory");
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(tmem),
+      "l"(desc), "r"(el)
+      : "memory");
 }
-// Instruction descriptor: E2M1 operands, K-major, M = 128, N = T, the scale
+#define IVFPQ_MMA_FP4(GROUP, KIND)                                                               \
+  asm volatile(                                                                                  \
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 q, %7, 0;\n"                    \
+      " @q tcgen05.mma.cta_group::" GROUP ".kind::" KIND                                         \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),                                           \
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(el)                            \
+      : "memory")
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sa, uint32_t sb, uint32_t acc, uint32_t el) {
+  if (FMT == IVFPQ_MXFP4 && CG == 1) IVFPQ_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+  if (FMT == IVFPQ_NVFP4 && CG == 1) IVFPQ_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  if (FMT == IVFPQ_MXFP4 && CG == 2) IVFPQ_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+  if (FMT == IVFPQ_NVFP4 && CG == 2) IVFPQ_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+}
+#undef IVFPQ_MMA_FP4
+__device__ __forceinline__ void mma_commit_el(uint32_t bar, uint32_t el) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          bar),
+      "r"(el)
+      : "memory");
+}
+// Instruction descriptor: E2M1 operands, K-major, M = 128 per CTA, N = T, the scale
 // type, and (MXFP4) which half of a TMEM column's four scales this product
 // uses.
-template <int FMT, int T>
+template <int FMT, int T, int CG>
 __device__ __forceinline__ uint32_t fp4_idesc(uint32_t sf_id) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(T >> 3) << 17) |
-         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(BN >> 7) << 27) | (sf_id << 29);
+         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(CG * BN >> 7) << 27) | (sf_id << 29);
 }
 __device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, float v) {
   if (dtype == IVFPQ_F32)

@@ -94,7 +94,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(gbase + (bars - base) + 16 * C::kStages + 16);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFullMask, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int nslice = gridDim.z;
   const int nk = (p.kp + KE - 1) / KE;
   const int k_lo = int(int64_t(nk) * blockIdx.z / nslice);
@@ -149,12 +149,13 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
     // copies still in flight land before the CTA ends
     for (int j = max(0, it - C::kStages); j < it; ++j)
       mbar_wait(bar_full(j % C::kStages), (j / C::kStages) & 1);
-  } else if (warp == 1 && lane == 0) {
-    // ---- scale copies and products ----
-    int it = 0;
-    for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc, ++it) {
-      const int s = it % C::kStages;
-      if (!mbar_wait(bar_full(s), (it / C::kStages) & 1)) {
+  } else if (warp == 1) {
+    // ---- scale copies and products: the whole warp runs, one lane issues ----
+    const uint32_t el = elect_one();
+    const uint64_t d_b = smem_desc(s_b(0)), d_a = smem_desc(s_a(0)), d_sf = scale_desc(s_sfb(0));
+    uint32_t s = 0, phase = 0;
+    for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc) {
+      if (!mbar_wait(bar_full(s), phase)) {
         fail();
         break;
       }
@@ -162,23 +163,34 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
       const int tiles = min(C::kTilesPerStage, p.ntile - kc * C::kTilesPerStage);
       const uint32_t tsb = tmem + C::kAccCols + s * C::kSfCols;
       const uint32_t tsa = tsb + C::kSfCols / 2;
-      for (int t = 0; t < tiles; ++t) {
-        scale_copy(tsb + 4 * t, scale_desc(s_sfb(s) + 512 * t));
-        scale_copy(tsa + 4 * t, scale_desc(s_sfa(s) + 512 * t));
+      const uint64_t sd = d_sf + s * uint32_t((2 * C::kSf) >> 4);
+#pragma unroll
+      for (int t = 0; t < C::kTilesPerStage; ++t) {
+        if (t < tiles) {
+          scale_copy<1>(tsb + 4 * t, sd + 32 * t, el);
+          scale_copy<1>(tsa + 4 * t, sd + 32 * t + C::kSf / 16, el);
+        }
       }
-      const uint64_t db = smem_desc(s_b(s)), da = smem_desc(s_a(s));
+      const uint64_t db = d_b + s * uint32_t((C::kB + C::kA) >> 4);
+      const uint64_t da = d_a + s * uint32_t((C::kB + C::kA) >> 4);
       const int steps = min(4, (p.kp - kc * KE + 63) / 64);
-      for (int j = 0; j < steps; ++j) {
-        const uint64_t adv = uint64_t(j * 32) >> 4;  // 64 columns = 32 bytes
-        const int t = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
-        const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
-        mma_fp4<FMT>(tmem, db + adv, da + adv, fp4_idesc<FMT, T>(id), tsb + 4 * t, tsa + 4 * t,
-                     it > 0 || j > 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < steps) {
+          const int t = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
+          const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
+          mma_fp4<FMT, 1>(tmem, db + 2 * j, da + 2 * j, fp4_idesc<FMT, T, 1>(id), tsb + 4 * t,
+                       tsa + 4 * t, kc > k_lo || j > 0, el);
+        }
       }
-      mma_commit(bar_empty(s));
+      mma_commit_el(bar_empty(s), el);
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
     }
     // also the end of every product issued before an early exit
-    mma_commit(bar_acc);
+    mma_commit_el(bar_acc, el);
     if (!mbar_wait(bar_acc, 0)) fail();
   } else if (warp >= 2) {
     if (!mbar_wait(bar_acc, 0)) fail();
