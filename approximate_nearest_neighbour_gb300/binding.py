@@ -530,6 +530,9 @@ def kselect_noalloc(vals, k, out_vals, out_idx, stream=None):
 
 
 # ---- 4-bit vectors, score rows and distillation ------------------------------
+# These calls take a few microseconds on the device for small inputs, so their
+# marshalling stays short: one look-up of the stream, no context managers, and
+# the general checks (_need, _out) only where a cheap test does not settle them.
 _dtypes = None
 
 
@@ -548,17 +551,17 @@ def _dtype_code(t, name):
 def _rows(t, name):
     """(dtype code, rows, cols, row stride) of a floating 2-d CUDA matrix whose
     rows are dense; the rows themselves may be strided or repeated."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    code = _dtype_code(t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions")
+    try:
+        code = _dtype_code(t.dtype, name)
+        rows, cols = t.shape
+        ld, inner = t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    except ValueError:
+        raise ValueError(f"{name} must have 2 dimensions") from None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    rows, cols = t.shape
-    ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have dense rows (stride 1 along columns)")
     if rows <= 1:
         ld = cols
@@ -567,11 +570,34 @@ def _rows(t, name):
     return code, rows, cols, ld
 
 
-def _out_rows(t, shape, dtype, name, device):
-    """As _out, for an output whose rows may be strided: (tensor, row stride)."""
-    torch = _torch()
+def _matrix(t, dtype, rows, cols, name, dev):
+    """Address of a contiguous [rows, cols] matrix of dtype on dev."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _vector(t, dtype, n, name, dev):
+    """Address of an optional contiguous vector of n entries of dtype on dev."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+        return None
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have {n} entries, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _out_rows(t, shape, dtype, name, device):
+    """A caller-given output whose rows may be strided: its row stride."""
     _, rows, cols, ld = _rows(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -581,57 +607,34 @@ def _out_rows(t, shape, dtype, name, device):
         raise ValueError(f"{name} must be on {device} (the inputs' device), got {t.device}")
     if rows > 1 and ld < cols:
         raise ValueError(f"{name} must not repeat rows")
-    return t, ld
+    return ld
 
 
-def _vector(t, dtype, n, name, device):
-    """Checks an optional 1-d contiguous argument of n entries."""
-    if t is None:
-        return None
-    _need(t, dtype, name, 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t.data_ptr()
+def _current(dev):
+    """Handle of the current stream of a tensor's device, which must be the
+    current device (kernels are launched there)."""
+    C_ = _torch()._C
+    if C_._cuda_getDevice() != dev.index:
+        raise ValueError(f"the tensors are on {dev} and the current device is another")
+    return C_._cuda_getCurrentRawStream(dev.index)
 
 
-class _on:
-    """Runs a call on `stream`: outputs made inside belong to it, and the
-    allocator keeps the given tensors until its work is done."""
-
-    def __init__(self, stream, device, *tensors):
-        torch = _torch()
-        cur = torch.cuda.current_stream(device)
-        self.ctx = None
-        if stream is not None and stream != cur:
-            self.ctx = torch.cuda.stream(stream)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.device(device)
-        self.handle = (stream if stream is not None else cur).cuda_stream
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+def _on_stream(fn, stream, args, kwargs):
+    """fn(*args, **kwargs) with `stream` current: its outputs belong to that
+    stream, and the allocator keeps the given tensors until its work is done."""
+    torch = _torch()
+    for t in (*args, *kwargs.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
 
 
 def _fp4_format(fmt):
-    if isinstance(fmt, str):
-        if fmt not in FP4_FORMATS:
-            raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(FP4_FORMATS)}")
-        return FP4_FORMATS[fmt]
-    if fmt not in (MXFP4, NVFP4):
-        raise ValueError(f"unknown 4-bit format {fmt!r}")
-    return fmt
+    f = FP4_FORMATS.get(fmt) if isinstance(fmt, str) else fmt
+    if f != MXFP4 and f != NVFP4:
+        raise ValueError(f"unknown 4-bit format {fmt!r}: one of {sorted(FP4_FORMATS)}")
+    return f
 
 
 def fp4_shapes(rows, cols, fmt="mxfp4"):
@@ -641,23 +644,34 @@ def fp4_shapes(rows, cols, fmt="mxfp4"):
     return (rows, kp // 2), ((rows + 127) // 128, (kp + span - 1) // span, 512)
 
 
-def _packed(codes, scales, fmt, name, cols=None):
-    """(rows, cols) of packed rows, with the scales' shape checked against the codes'."""
+def _packed(codes, scales, f, name, cols=None):
+    """(rows, columns) of packed rows, with the scales' shape checked against the codes'."""
     torch = _torch()
-    _need(codes, torch.uint8, f"{name} codes", 2)
-    _need(scales, torch.uint8, f"{name} scales", 3)
-    rows, pitch = codes.shape
+    u8 = torch.uint8
+    try:
+        rows, pitch = codes.shape
+        shape = scales.shape
+    except (AttributeError, ValueError):
+        _need(codes, u8, f"{name} codes", 2)
+        _need(scales, u8, f"{name} scales", 3)
+        raise
+    if (codes.dtype != u8 or scales.dtype != u8 or not codes.is_cuda
+            or not codes.is_contiguous() or not scales.is_contiguous()
+            or scales.device != codes.device):
+        _need(codes, u8, f"{name} codes", 2)
+        _need(scales, u8, f"{name} scales", 3)
+        raise ValueError(f"{name}: codes and scales on several devices")
     if pitch == 0 or pitch % 16:
         raise ValueError(f"{name} codes must have a multiple of 16 bytes per row, got {pitch}")
+    kp = 2 * pitch
     if cols is None:
-        cols = 2 * pitch
-    elif not 2 * pitch - 32 < cols <= 2 * pitch:
+        cols = kp
+    elif not kp - 32 < cols <= kp:
         raise ValueError(f"{name}: {cols} columns do not match codes of {pitch} bytes per row")
-    want = fp4_shapes(rows, cols, fmt)[1]
-    if tuple(scales.shape) != want:
-        raise ValueError(f"{name} scales must have shape {want}, got {tuple(scales.shape)}")
-    if scales.device != codes.device:
-        raise ValueError(f"{name}: codes and scales on several devices")
+    span = 128 if f == MXFP4 else 64
+    if shape != ((rows + 127) // 128, (kp + span - 1) // span, 512):
+        raise ValueError(f"{name} scales must have shape {fp4_shapes(rows, cols, f)[1]}, got "
+                         f"{tuple(shape)}")
     return rows, cols
 
 
@@ -665,16 +679,23 @@ def fp4_quantize(x, fmt="mxfp4", tensor_scale=None, codes=None, scales=None, str
     """(codes, scales) of the rows of x in a 4-bit block-scaled format:
     "mxfp4" (a power-of-two scale per 32 columns) or "nvfp4" (an E4M3 scale per
     16 columns beside tensor_scale, fp32 [1] on the device, 1 if not given)."""
+    if stream is not None:
+        return _on_stream(fp4_quantize, stream, (x, fmt, tensor_scale, codes, scales), {})
     torch = _torch()
     f = _fp4_format(fmt)
     code, rows, cols, ld = _rows(x, "x")
-    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", x.device)
+    dev = x.device
+    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", dev)
     cs, ss = fp4_shapes(rows, cols, f)
-    with _on(stream, x.device, x, tensor_scale, codes, scales) as h:
-        codes = _out(codes, cs, torch.uint8, "codes", x.device)
-        scales = _out(scales, ss, torch.uint8, "scales", x.device)
-        _check("fp4_quantize", lib().fp4_quantize(x.data_ptr(), code, rows, cols, ld, f, g,
-                                                  codes.data_ptr(), scales.data_ptr(), h))
+    u8 = torch.uint8
+    codes = (torch.empty(cs, dtype=u8, device=dev) if codes is None
+             else _out(codes, cs, u8, "codes", dev))
+    scales = (torch.empty(ss, dtype=u8, device=dev) if scales is None
+              else _out(scales, ss, u8, "scales", dev))
+    rc = (_lib or lib()).fp4_quantize(x.data_ptr(), code, rows, cols, ld, f, g, codes.data_ptr(),
+                                      scales.data_ptr(), _current(dev))
+    if rc:
+        _check("fp4_quantize", rc)
     return codes, scales
 
 
@@ -682,16 +703,23 @@ def fp4_dequantize(codes, scales, cols=None, fmt="mxfp4", tensor_scale=None, dty
                    stream=None):
     """The values packed rows stand for, [rows, cols] (cols: all packed columns
     if not given) of dtype (float32 if not given)."""
+    if stream is not None:
+        return _on_stream(fp4_dequantize, stream,
+                          (codes, scales, cols, fmt, tensor_scale, dtype, out), {})
     torch = _torch()
     f = _fp4_format(fmt)
     rows, cols = _packed(codes, scales, f, "fp4_dequantize:", cols)
-    dtype = out.dtype if dtype is None and out is not None else dtype or torch.float32
+    dev = codes.device
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
-    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", codes.device)
-    with _on(stream, codes.device, codes, scales, tensor_scale, out) as h:
-        out = _out(out, (rows, cols), dtype, "out", codes.device)
-        _check("fp4_dequantize", lib().fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows,
-                                                      cols, f, g, out.data_ptr(), code, h))
+    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", dev)
+    out = (torch.empty((rows, cols), dtype=dtype, device=dev) if out is None
+           else _out(out, (rows, cols), dtype, "out", dev))
+    rc = (_lib or lib()).fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, f, g,
+                                        out.data_ptr(), code, _current(dev))
+    if rc:
+        _check("fp4_dequantize", rc)
     return out
 
 
@@ -699,6 +727,9 @@ def fp4_product(a_codes, a_scales, b_codes, b_scales, fmt="mxfp4", a_tensor_scal
                 b_tensor_scale=None, dtype=None, out=None, stream=None):
     """Inner products [m, n] of packed rows a [m, cols] and b [n, cols], in
     dtype (float32 if not given: score rows for kselect, once negated)."""
+    if stream is not None:
+        return _on_stream(fp4_product, stream, (a_codes, a_scales, b_codes, b_scales, fmt,
+                                                a_tensor_scale, b_tensor_scale, dtype, out), {})
     torch = _torch()
     f = _fp4_format(fmt)
     m, cols = _packed(a_codes, a_scales, f, "fp4_product: a")
@@ -706,17 +737,20 @@ def fp4_product(a_codes, a_scales, b_codes, b_scales, fmt="mxfp4", a_tensor_scal
     if cols != bcols:
         raise ValueError(f"fp4_product: a has {cols} packed columns and b {bcols}")
     dev = a_codes.device
-    _same_device("fp4_product", a_codes, b_codes)
-    dtype = out.dtype if dtype is None and out is not None else dtype or torch.float32
+    if b_codes.device != dev:
+        _same_device("fp4_product", a_codes, b_codes)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
     ga = _vector(a_tensor_scale, torch.float32, 1, "a_tensor_scale", dev)
     gb = _vector(b_tensor_scale, torch.float32, 1, "b_tensor_scale", dev)
-    with _on(stream, dev, a_codes, a_scales, b_codes, b_scales, a_tensor_scale, b_tensor_scale,
-             out) as h:
-        out = _out(out, (m, n), dtype, "out", dev)
-        _check("fp4_product", lib().fp4_product(
-            a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(),
-            n, cols, f, ga, gb, out.data_ptr(), code, h))
+    out = (torch.empty((m, n), dtype=dtype, device=dev) if out is None
+           else _out(out, (m, n), dtype, "out", dev))
+    rc = (_lib or lib()).fp4_product(
+        a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n,
+        cols, f, ga, gb, out.data_ptr(), code, _current(dev))
+    if rc:
+        _check("fp4_product", rc)
     return out
 
 
@@ -724,21 +758,28 @@ def fp4_linear(x, w_codes, w_scales, fmt="mxfp4", x_tensor_scale=None, w_tensor_
                dtype=None, out=None, stream=None):
     """x [m, cols] quantized row by row, times packed weights w [n, cols]:
     [m, n] in dtype (x's if not given)."""
+    if stream is not None:
+        return _on_stream(fp4_linear, stream, (x, w_codes, w_scales, fmt, x_tensor_scale,
+                                               w_tensor_scale, dtype, out), {})
     torch = _torch()
     f = _fp4_format(fmt)
     xcode, m, cols, ld = _rows(x, "x")
     n, _ = _packed(w_codes, w_scales, f, "fp4_linear: w", cols)
     dev = x.device
-    _same_device("fp4_linear", x, w_codes)
-    dtype = out.dtype if dtype is None and out is not None else dtype or x.dtype
+    if w_codes.device != dev:
+        _same_device("fp4_linear", x, w_codes)
+    if dtype is None:
+        dtype = x.dtype if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
     gx = _vector(x_tensor_scale, torch.float32, 1, "x_tensor_scale", dev)
     gw = _vector(w_tensor_scale, torch.float32, 1, "w_tensor_scale", dev)
-    with _on(stream, dev, x, w_codes, w_scales, x_tensor_scale, w_tensor_scale, out) as h:
-        out = _out(out, (m, n), dtype, "out", dev)
-        _check("fp4_linear", lib().fp4_linear(
-            x.data_ptr(), xcode, m, ld, w_codes.data_ptr(), w_scales.data_ptr(), n, cols, f, gx,
-            gw, out.data_ptr(), code, h))
+    out = (torch.empty((m, n), dtype=dtype, device=dev) if out is None
+           else _out(out, (m, n), dtype, "out", dev))
+    rc = (_lib or lib()).fp4_linear(x.data_ptr(), xcode, m, ld, w_codes.data_ptr(),
+                                    w_scales.data_ptr(), n, cols, f, gx, gw, out.data_ptr(), code,
+                                    _current(dev))
+    if rc:
+        _check("fp4_linear", rc)
     return out
 
 
@@ -752,12 +793,19 @@ def score_adjust(scores, history=None, history_len=None, prompt_len=None, repeti
     bias_ids / bias_vals: int32 / fp32 [rows, nb]; mask: int32 [rows or 1,
     ceil(cols / 32)], set bits are allowed. out (scores itself, or the scores'
     type or float32) is made if not given."""
+    if stream is not None:
+        return _on_stream(score_adjust, stream,
+                          (scores, history, history_len, prompt_len, repetition, presence,
+                           frequency, bias_ids, bias_vals, temperature, mask, negate, out, dtype),
+                          {})
     torch = _torch()
+    i32, f32 = torch.int32, torch.float32
     code, rows, cols, lds = _rows(scores, "scores")
     dev = scores.device
+    hist = hl = pl = bi = bv = mk = None
     hist_cols = ldh = nb = ldm = 0
     if history is not None:
-        if not isinstance(history, torch.Tensor) or history.dtype != torch.int32:
+        if not isinstance(history, torch.Tensor) or history.dtype != i32:
             raise TypeError("history must be an int32 tensor")
         if history.dim() != 2 or history.shape[0] != rows or history.device != dev:
             raise ValueError(f"history must be [{rows}, length] on {dev}")
@@ -765,58 +813,64 @@ def score_adjust(scores, history=None, history_len=None, prompt_len=None, repeti
         ldh, inner = history.stride()
         if hist_cols > 1 and inner != 1:
             raise ValueError("history must have dense rows (stride 1 along its length)")
+        hl = _vector(history_len, i32, rows, "history_len", dev)
+        pl = _vector(prompt_len, i32, rows, "prompt_len", dev)
+        hist = history.data_ptr()
+        if hist_cols == 0:
+            hist = hl = pl = None
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len need a history")
     if (bias_ids is None) != (bias_vals is None):
         raise ValueError("bias_ids and bias_vals go together")
     if bias_ids is not None:
-        _need(bias_ids, torch.int32, "bias_ids", 2)
-        _need(bias_vals, torch.float32, "bias_vals", 2)
-        nb = bias_ids.shape[1]
-        if bias_ids.shape[0] != rows or bias_vals.shape != bias_ids.shape:
+        if not isinstance(bias_ids, torch.Tensor):
+            raise TypeError("bias_ids must be a torch tensor")
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != rows:
             raise ValueError(f"bias_ids and bias_vals must both be [{rows}, nb]")
-        _same_device("score_adjust", scores, bias_ids, bias_vals)
+        nb = bias_ids.shape[1]
+        bi = _matrix(bias_ids, i32, rows, nb, "bias_ids", dev)
+        bv = _matrix(bias_vals, f32, rows, nb, "bias_vals", dev)
+        if nb == 0:
+            bi = bv = None
     if mask is not None:
-        _need(mask, torch.int32, "mask", 2)
         words = (cols + 31) // 32
-        if mask.shape[0] not in (1, rows) or mask.shape[1] != words or mask.device != dev:
-            raise ValueError(f"mask must be [{rows} or 1, {words}] on {dev}, got "
-                             f"{tuple(mask.shape)}")
-        ldm = words if mask.shape[0] == rows else 0
-    i32, f32 = torch.int32, torch.float32
-    hl = _vector(history_len, i32, rows, "history_len", dev)
-    pl = _vector(prompt_len, i32, rows, "prompt_len", dev)
+        if not isinstance(mask, torch.Tensor):
+            raise TypeError("mask must be a torch tensor")
+        mrows = rows if mask.dim() == 2 and mask.shape[0] == rows else 1
+        mk = _matrix(mask, i32, mrows, words, "mask", dev)
+        ldm = words if mrows == rows else 0
     rep = _vector(repetition, f32, rows, "repetition", dev)
     pres = _vector(presence, f32, rows, "presence", dev)
     freq = _vector(frequency, f32, rows, "frequency", dev)
     temp = _vector(temperature, f32, rows, "temperature", dev)
-    dtype = out.dtype if dtype is None and out is not None else dtype or scores.dtype
-    ocode = _dtype_code(dtype, "dtype")
-    with _on(stream, dev, scores, history, history_len, prompt_len, repetition, presence,
-             frequency, bias_ids, bias_vals, temperature, mask, out) as h:
-        out, ldo = _out_rows(out, (rows, cols), dtype, "out", dev)
-        _check("score_adjust", lib().score_adjust(
-            scores.data_ptr(), code, rows, cols, lds,
-            history.data_ptr() if hist_cols else None, hist_cols, ldh, hl if hist_cols else None,
-            pl if hist_cols else None, rep, pres, freq,
-            bias_ids.data_ptr() if nb else None, bias_vals.data_ptr() if nb else None, nb, temp,
-            mask.data_ptr() if mask is not None else None, ldm, int(bool(negate)),
-            out.data_ptr(), ocode, ldo, h))
+    if dtype is None:
+        dtype = scores.dtype if out is None else out.dtype
+    ocode = code if dtype is scores.dtype else _dtype_code(dtype, "dtype")
+    if out is None:
+        out, ldo = torch.empty((rows, cols), dtype=dtype, device=dev), cols
+    else:
+        ldo = _out_rows(out, (rows, cols), dtype, "out", dev)
+    rc = (_lib or lib()).score_adjust(
+        scores.data_ptr(), code, rows, cols, lds, hist, hist_cols, ldh, hl, pl, rep, pres, freq,
+        bi, bv, nb, temp, mk, ldm, 1 if negate else 0, out.data_ptr(), ocode, ldo, _current(dev))
+    if rc:
+        _check("score_adjust", rc)
     return out
 
 
-def _teacher(fn, scores, vals, ids):
-    """Checks of a distillation call's inputs: (dtype code, rows, cols, stride, k)."""
+def _teacher(scores, vals, ids):
+    """Checks of a distillation call's inputs: (dtype code, rows, cols, row
+    stride, k, addresses of the teacher's values and ids)."""
     torch = _torch()
     code, rows, cols, ld = _rows(scores, "scores")
-    _need(vals, torch.float32, "teacher_vals", 2)
-    _need(ids, torch.int64, "teacher_ids", 2)
-    k = vals.shape[1]
-    if vals.shape[0] != rows or ids.shape != vals.shape:
-        raise ValueError(f"{fn}: teacher_vals and teacher_ids must both be [{rows}, k], got "
-                         f"{tuple(vals.shape)} and {tuple(ids.shape)}")
-    _same_device(fn, scores, vals, ids)
-    return code, rows, cols, ld, k
+    try:
+        k = vals.shape[1]
+    except (AttributeError, IndexError):
+        _need(vals, torch.float32, "teacher_vals", 2)
+        raise
+    dev = scores.device
+    return (code, rows, cols, ld, k, _matrix(vals, torch.float32, rows, k, "teacher_vals", dev),
+            _matrix(ids, torch.int64, rows, k, "teacher_ids", dev))
 
 
 def topk_distill_forward(scores, teacher_vals, teacher_ids, temperature=1.0, negated=False,
@@ -825,16 +879,19 @@ def topk_distill_forward(scores, teacher_vals, teacher_ids, temperature=1.0, neg
     against a teacher's top list, as kselect or a search returns it (fp32
     values and int64 ids, [rows, k]); negated: smaller values are better, as in
     distances. stats is for topk_distill_backward."""
+    if stream is not None:
+        return _on_stream(topk_distill_forward, stream,
+                          (scores, teacher_vals, teacher_ids, temperature, negated), {})
     torch = _torch()
-    code, rows, cols, ld, k = _teacher("topk_distill_forward", scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    with _on(stream, dev, scores, teacher_vals, teacher_ids) as h:
-        loss = torch.empty((rows,), dtype=torch.float32, device=dev)
-        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        _check("topk_distill_forward", lib().topk_distill_forward(
-            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
-            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), loss.data_ptr(),
-            stats.data_ptr(), h))
+    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    rc = (_lib or lib()).topk_distill_forward(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
+                                              temperature, 1 if negated else 0, loss.data_ptr(),
+                                              stats.data_ptr(), _current(dev))
+    if rc:
+        _check("topk_distill_forward", rc)
     return loss, stats
 
 
@@ -842,21 +899,26 @@ def topk_distill_backward(scores, teacher_vals, teacher_ids, stats, row_grad, te
                           negated=False, grad=None, stream=None):
     """Gradient of sum(row_grad * loss) with respect to the scores, in their
     type; grad may be scores itself. A row whose row_grad is 0 gets zeros."""
+    if stream is not None:
+        return _on_stream(topk_distill_backward, stream,
+                          (scores, teacher_vals, teacher_ids, stats, row_grad, temperature,
+                           negated, grad), {})
     torch = _torch()
-    code, rows, cols, ld, k = _teacher("topk_distill_backward", scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    _need(stats, torch.float32, "stats", 2)
-    if tuple(stats.shape) != (rows, 2) or stats.device != dev:
-        raise ValueError(f"stats must be [{rows}, 2] on {dev}")
-    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
-    if w is None:
+    st = _matrix(stats, torch.float32, rows, 2, "stats", dev)
+    if row_grad is None:
         raise TypeError("row_grad must be a torch tensor")
-    with _on(stream, dev, scores, teacher_vals, teacher_ids, stats, row_grad, grad) as h:
-        grad, ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
-        _check("topk_distill_backward", lib().topk_distill_backward(
-            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
-            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), stats.data_ptr(),
-            w, grad.data_ptr(), ldg, h))
+    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
+    if grad is None:
+        grad, ldg = torch.empty((rows, cols), dtype=scores.dtype, device=dev), cols
+    else:
+        ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
+    rc = (_lib or lib()).topk_distill_backward(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
+                                               temperature, 1 if negated else 0, st, w,
+                                               grad.data_ptr(), ldg, _current(dev))
+    if rc:
+        _check("topk_distill_backward", rc)
     return grad
 
 
@@ -864,17 +926,24 @@ def topk_distill(scores, teacher_vals, teacher_ids, row_grad, temperature=1.0, n
                  grad=None, stream=None):
     """(loss fp32 [rows], gradient of sum(row_grad * loss)) in one call, as a
     training step needs them; grad may be scores itself."""
+    if stream is not None:
+        return _on_stream(topk_distill, stream,
+                          (scores, teacher_vals, teacher_ids, row_grad, temperature, negated,
+                           grad), {})
     torch = _torch()
-    code, rows, cols, ld, k = _teacher("topk_distill", scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
-    if w is None:
+    if row_grad is None:
         raise TypeError("row_grad must be a torch tensor")
-    with _on(stream, dev, scores, teacher_vals, teacher_ids, row_grad, grad) as h:
-        loss = torch.empty((rows,), dtype=torch.float32, device=dev)
-        grad, ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
-        _check("topk_distill", lib().topk_distill(
-            scores.data_ptr(), code, rows, cols, ld, teacher_vals.data_ptr(),
-            teacher_ids.data_ptr(), k, float(temperature), int(bool(negated)), w,
-            loss.data_ptr(), grad.data_ptr(), ldg, h))
+    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
+    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if grad is None:
+        grad, ldg = torch.empty((rows, cols), dtype=scores.dtype, device=dev), cols
+    else:
+        ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
+    rc = (_lib or lib()).topk_distill(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
+                                      temperature, 1 if negated else 0, w, loss.data_ptr(),
+                                      grad.data_ptr(), ldg, _current(dev))
+    if rc:
+        _check("topk_distill", rc)
     return loss, grad

@@ -105,26 +105,6 @@ __device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, floa
   else
     static_cast<__half*>(out)[at] = __float2half_rn(v);
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
-      : "=f"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // Tensor map over packed code rows; a box is 128 bytes of K by box_rows rows.
 int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows);
 

@@ -1,19 +1,19 @@
 // The wide product of packed 4-bit rows (fp4_product.cu has the narrow one and
 // the entry points): many rows on both sides.
 //
-// Pairs of CTAs (cta_group::2), one CTA per SM, persistent: a pair computes 256
-// columns of out (rows of b) x T rows of out, T = 128 or 256. Each CTA holds
-// 128 rows of b and T / 2 rows of a and accumulates its 128 columns over all T
-// rows, so an SM takes in 38 KB per 256 columns of K where a CTA on its own
-// took 54 KB: filling shared memory was the limit (8192 x 16384 x 4096 nvfp4:
-// loads alone 157 us, products alone 146 us, together 198 us on single CTAs).
+// Persistent CTAs, one per SM, of 128 columns of out (rows of b) x T rows of
+// out, T = 128 or 256, alone (CG = 1) or in pairs (cta_group::2): a pair shares
+// the T rows of a, half in each CTA, so an SM takes in 38 KB per 256 columns
+// of K instead of 54 KB. Filling shared memory is close to a limit: 8192 x
+// 16384 x 4096 nvfp4 takes 157 us for the loads alone, 146 us for the products
+// alone and 194 us together on single CTAs, 183 us in pairs.
 //
 // 10 warps: warp 0 loads; warp 1 of the pair's first CTA copies scales to TMEM
 // and issues products for both; warps 2..9 store (two per TMEM lane group, half
-// of the rows each). While a tile is stored the next one is computed: with T =
-// 256 the two accumulators overlap (TMEM columns 0..255 and 160..415), so the
-// storing warps first empty the 96 shared columns and release them. Columns
-// 416..511 hold two buffers of scales, each reused when the products two
+// of the rows each). While a tile is stored the next ones are computed: T = 128
+// has three accumulators; with T = 256 two overlap (TMEM columns 0..255 and
+// 160..415), so the storing warps first empty the 96 shared columns and
+// release them. Columns 416..511 hold two buffers of scales, each reused when the products two
 // stages back have finished.
 #include <algorithm>
 
@@ -26,33 +26,45 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kSfBase = 416;  // first TMEM column of the scales
 
-template <int FMT, int T>
+template <int FMT, int T, int CG>
 struct WideCfg {
   static constexpr int kTiles = FMT == IVFPQ_MXFP4 ? 2 : 4;  // scale tiles per stage and 128 rows
   static constexpr int kRt = T / 128;
   static constexpr int kSfTile = kTiles * 512;
   static constexpr int kB = BN * KB;
-  static constexpr int kA = T / 2 * KB;
+  static constexpr int kA = T / CG * KB;
   static constexpr int kSf = (1 + kRt) * kSfTile;  // b's scales, then all T rows' of a
   static constexpr int kStage = kB + kA + kSf;
   static constexpr int kStages = (226 * 1024 - 1536) / kStage < 8 ? (226 * 1024 - 1536) / kStage : 8;
   static constexpr int kTotal = kStages * kStage + 512 + 1024;
   static constexpr int kSfCols = 4 * kTiles * (1 + kRt);  // TMEM columns of one scale buffer
-  static constexpr int kAcc1 = T == 256 ? 160 : T;        // first column of the second accumulator
-  static_assert(kSfBase + 2 * kSfCols <= 512 && kAcc1 + T <= kSfBase, "TMEM columns");
+  // accumulators and the columns between their starts
+  static constexpr int kAccs = T == 256 ? 2 : 3;
+  static constexpr int kAccStep = T == 256 ? 160 : T;
+  static_assert(kSfBase + 2 * kSfCols <= 512 && (kAccs - 1) * kAccStep + T <= kSfBase,
+                "TMEM columns");
   static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
-// A copy into this CTA's shared memory that completes on a barrier of either
-// CTA of the pair (bar is a cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                                 uint32_t bar, uint32_t el) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
-      " @q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(el)
-      : "memory");
+// A copy into this CTA's shared memory; in a pair it completes on a barrier of
+// either CTA (bar is then a cluster address).
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar, uint32_t el) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q cp.async.bulk.tensor.2d.cta_group::2"
+        ".shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(el)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n @q cp.async.bulk.tensor.2d"
+        ".shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(el)
+        : "memory");
 }
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t a;
@@ -63,22 +75,30 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
-__device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t el) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
-          bar),
-      "r"(el)
-      : "memory");
+// Completes on this CTA's barrier ...
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t el) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+            bar),
+        "r"(el)
+        : "memory");
+  else
+    mma_commit_el(bar, el);
 }
-// Completes on the barrier of both CTAs.
-__device__ __forceinline__ void pair_commit_both(uint32_t bar, uint32_t el) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
-      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n}" ::"r"(bar),
-      "h"(uint16_t(3)), "r"(el)
-      : "memory");
+// ... or on the barrier of every CTA of the group.
+template <int CG>
+__device__ __forceinline__ void commit_all(uint32_t bar, uint32_t el) {
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q tcgen05.commit.cta_group::2"
+        ".mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
+        "h"(uint16_t(3)), "r"(el)
+        : "memory");
+  else
+    mma_commit_el(bar, el);
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -90,35 +110,69 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// 16 accumulator columns (rows r0 .. r0 + 15 of out) of this lane's column.
+// All of the SM's TMEM; in a pair both CTAs take part.
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
+        "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(slot)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n"
+        "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::"r"(slot)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t tmem) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// 16 accumulator columns (rows r0 .. r0 + 15 of out) of this lane's column. With
+// 16-bit outputs and even row lengths two lanes exchange halves, so that each
+// stores two neighbouring columns of one of two rows: half the store
+// instructions, each of 128 bytes.
 template <class O>
-__device__ __forceinline__ void store16(O* out, int64_t ldo, int64_t r0, int64_t m, bool live,
-                                        const uint32_t (&r)[16], float alpha) {
+__device__ __forceinline__ void store16(O* out, int64_t ldo, int r0, int64_t m, bool live,
+                                        bool pairs, const uint32_t (&r)[16], float alpha) {
+  if constexpr (sizeof(O) == 2) {
+    if (pairs) {
+      const int odd = threadIdx.x & 1;
+      uint32_t* p = reinterpret_cast<uint32_t*>(out + (r0 + odd) * ldo - odd);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2, p += ldo) {
+        const float v0 = __uint_as_float(r[j]) * alpha, v1 = __uint_as_float(r[j + 1]) * alpha;
+        const float got = __shfl_xor_sync(kFullMask, odd ? v0 : v1, 1);
+        O w[2] = {from_f32<O>(odd ? got : v0), from_f32<O>(odd ? v1 : got)};
+        if (live && r0 + j + odd < m) *p = *reinterpret_cast<const uint32_t*>(w);
+      }
+      return;
+    }
+  }
   O* p = out + r0 * ldo;
   if (live) {
-    if (r0 + 16 <= m) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j, p += ldo) *p = from_f32<O>(__uint_as_float(r[j]) * alpha);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j, p += ldo)
-        if (r0 + j < m) *p = from_f32<O>(__uint_as_float(r[j]) * alpha);
-    }
+    for (int j = 0; j < 16; ++j, p += ldo)
+      if (r0 + j < m) *p = from_f32<O>(__uint_as_float(r[j]) * alpha);
   }
 }
 
 struct Tiling {
-  int tn, tm;   // pair tiles along n and m
+  int tn, tm;   // tiles along n and m
   int m_fast;   // consecutive tiles go along m
 };
 
-template <int FMT, int T, class O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int FMT, int T, int CG, class O>
+__global__ void __launch_bounds__(kThreads, 1)
 fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_a,
                 const __grid_constant__ CUtensorMap map_sb,
                 const __grid_constant__ CUtensorMap map_sa, const ProdArgs p, const Tiling tl) {
-  using C = WideCfg<FMT, T>;
+  using C = WideCfg<FMT, T, CG>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t fp4_wide_smem[];
   const uint32_t raw = smem_u32(fp4_wide_smem);
@@ -132,19 +186,21 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
   auto bar_full = [&](int s) { return bars + 8 * s; };          // first CTA's: both CTAs' copies
   auto bar_empty = [&](int s) { return bars + 8 * (NS + s); };  // each CTA's
   auto bar_sf = [&](int b) { return bars + 16 * NS + 8 * b; };
-  const uint32_t bar_acc = bars + 16 * NS + 16;   // each CTA's: a tile is computed
-  const uint32_t bar_free = bars + 16 * NS + 24;  // first CTA's: both CTAs' shared columns are read
-  const uint32_t bar_end = bars + 16 * NS + 32;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 16 * NS + 40);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (bars - base) + 16 * NS + 48);
+  // per accumulator: each CTA's, a tile is computed; the first CTA's, what the
+  // next product overwrites has been read in all CTAs
+  auto bar_acc = [&](int b) { return bars + 16 * NS + 16 + 8 * b; };
+  auto bar_free = [&](int b) { return bars + 16 * NS + 40 + 8 * b; };
+  const uint32_t bar_end = bars + 16 * NS + 64;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 16 * NS + 72);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (bars - base) + 16 * NS + 80);
 
   const int warp = __shfl_sync(kFullMask, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int rank = int(cluster_rank());
-  const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+  const int rank = CG == 2 ? int(cluster_rank()) : 0;
+  const int group = blockIdx.x / CG, ngroups = gridDim.x / CG;
   const int ntiles = tl.tn * tl.tm;
   const int nk = (p.kp + KE - 1) / KE;
-  // first column of this CTA and first row of pair tile t
-  auto col0 = [&](int t) { return ((tl.m_fast ? t / tl.tm : t % tl.tn) * 2 + rank) * BN; };
+  // first column of this CTA and first row of tile t
+  auto col0 = [&](int t) { return ((tl.m_fast ? t / tl.tm : t % tl.tn) * CG + rank) * BN; };
   auto row0 = [&](int t) { return (tl.m_fast ? t % tl.tm : t / tl.tn) * T; };
 
   if (threadIdx.x == 0) {
@@ -154,22 +210,18 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
     }
     mbar_init(bar_sf(0), 1);
     mbar_init(bar_sf(1), 1);
-    mbar_init(bar_acc, 1);
-    mbar_init(bar_free, 2 * kEpiWarps);
+    for (int b = 0; b < C::kAccs; ++b) {
+      mbar_init(bar_acc(b), 1);
+      mbar_init(bar_free(b), CG * kEpiWarps);
+    }
     mbar_init(bar_end, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot));
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto fail = [&]() {
@@ -183,7 +235,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
     uint32_t s = 0, phase = 1;
     int used = 0;
     bool ok = true;
-    for (int t = pair; t < ntiles && ok && !*abort_flag; t += npairs) {
+    for (int t = group; t < ntiles && ok && !*abort_flag; t += ngroups) {
       const int n0 = col0(t), m0 = row0(t);
       const int sb = n0 / BN * p.ntile, sa = m0 / 128 * p.ntile;
       for (int kc = 0; kc < nk; ++kc) {
@@ -192,15 +244,15 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
           ok = false;
           break;
         }
-        if (rank == 0 && el) mbar_expect_tx(bar_full(s), 2 * C::kStage);
-        const uint32_t bar = map_rank(bar_full(s), 0);
-        tma_load_2d_pair(s_b(s), &map_b, kc * KB, n0, bar, el);
-        tma_load_2d_pair(s_a(s), &map_a, kc * KB, m0 + rank * (T / 2), bar, el);
+        if (rank == 0 && el) mbar_expect_tx(bar_full(s), CG * C::kStage);
+        const uint32_t bar = CG == 2 ? map_rank(bar_full(s), 0) : bar_full(s);
+        tma_load<CG>(s_b(s), &map_b, kc * KB, n0, bar, el);
+        tma_load<CG>(s_a(s), &map_a, kc * KB, m0 + rank * (T / CG), bar, el);
         // scale tiles past the row's (or the matrix's) end are read and not used
-        tma_load_2d_pair(s_sf(s), &map_sb, 0, sb + kc * C::kTiles, bar, el);
+        tma_load<CG>(s_sf(s), &map_sb, 0, sb + kc * C::kTiles, bar, el);
 #pragma unroll
         for (int r = 0; r < C::kRt; ++r)
-          tma_load_2d_pair(s_sf(s) + (1 + r) * C::kSfTile, &map_sa, 0,
+          tma_load<CG>(s_sf(s) + (1 + r) * C::kSfTile, &map_sa, 0,
                            sa + r * p.ntile + kc * C::kTiles, bar, el);
         used = min(used + 1, NS);
         if (++s == NS) {
@@ -224,16 +276,19 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
     const int last_steps = (p.kp - (nk - 1) * KE + 63) / 64;
     uint32_t s = 0, phase = 0;       // stage, its parity
     uint32_t sb = 0, sphase = 1;     // scale buffer, parity of its last release
-    uint32_t fphase = 1;             // parity of the last release of the accumulator
+    int b = 0, turn = 0;             // accumulator, how often it has been used
     bool ok = true;
-    for (int t = pair, i = 0; t < ntiles && ok && !*abort_flag; t += npairs, ++i) {
-      if (i > 0 && !mbar_wait(bar_free, fphase)) {
+    for (int t = group, i = 0; t < ntiles && ok && !*abort_flag; t += ngroups, ++i) {
+      // T = 256: the columns shared with the last tile's accumulator have been
+      // read (and all of the one before); else this accumulator's last tile has
+      const bool go = T < 256 ? mbar_wait(bar_free(b), (turn & 1) ^ 1)
+                              : i == 0 || mbar_wait(bar_free(b ^ 1), ((i - 1) >> 1) & 1);
+      if (!go) {
         fail();
         break;
       }
-      fphase ^= 1;
       tc_fence_after();
-      const uint32_t acc = tmem + ((i & 1) ? C::kAcc1 : 0);
+      const uint32_t acc = tmem + b * C::kAccStep;
       for (int kc = 0; kc < nk; ++kc) {
         // a fresh barrier lets a wait for the odd parity through
         if (!mbar_wait(bar_full(s), phase) || !mbar_wait(bar_sf(sb), sphase)) {
@@ -249,10 +304,10 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
 #pragma unroll
         for (int q = 0; q < C::kTiles; ++q) {
           if (q < tiles) {
-            scale_copy<2>(tb + 4 * q, sd + 32 * q, el);
+            scale_copy<CG>(tb + 4 * q, sd + 32 * q, el);
 #pragma unroll
             for (int r = 0; r < C::kRt; ++r)
-              scale_copy<2>(ta + 4 * (q * C::kRt + r), sd + ((1 + r) * C::kSfTile + 512 * q) / 16,
+              scale_copy<CG>(ta + 4 * (q * C::kRt + r), sd + ((1 + r) * C::kSfTile + 512 * q) / 16,
                             el);
           }
         }
@@ -264,12 +319,12 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
           if (j < steps) {
             const int q = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
             const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
-            mma_fp4<FMT, 2>(acc, db + 2 * j, da + 2 * j, fp4_idesc<FMT, T, 2>(id), tb + 4 * q,
+            mma_fp4<FMT, CG>(acc, db + 2 * j, da + 2 * j, fp4_idesc<FMT, T, CG>(id), tb + 4 * q,
                             ta + 4 * C::kRt * q, kc > 0 || j > 0, el);
           }
         }
-        pair_commit(bar_sf(sb), el);
-        pair_commit_both(bar_empty(s), el);
+        commit<CG>(bar_sf(sb), el);
+        commit_all<CG>(bar_empty(s), el);
         if (++s == NS) {
           s = 0;
           phase ^= 1;
@@ -277,10 +332,14 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
         sb ^= 1;
         sphase ^= sb ^ 1;
       }
-      if (ok) pair_commit_both(bar_acc, el);
+      if (ok) commit_all<CG>(bar_acc(b), el);
+      if (++b == C::kAccs) {
+        b = 0;
+        ++turn;
+      }
     }
     // all products issued have finished before TMEM is freed
-    pair_commit(bar_end, el);
+    commit<CG>(bar_end, el);
     mbar_wait(bar_end, 0);
   } else if (warp >= 2) {
     // ---- store: warp w reads TMEM lanes 32 * (w % 4) .. +32 ----
@@ -288,55 +347,66 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
     const float alpha = (p.a_ts ? __ldg(p.a_ts) : 1.f) * (p.b_ts ? __ldg(p.b_ts) : 1.f);
     constexpr int kCrit = T == 256 ? 96 : 0;  // columns the next accumulator shares
     constexpr int C1 = kCrit / 2, C2 = (T - kCrit) / 2;
-    const uint32_t free0 = map_rank(bar_free, 0);
-    int i = 0;
-    for (int t = pair; t < ntiles && !*abort_flag; t += npairs, ++i) {
-      if (!mbar_wait(bar_acc, i & 1)) {
+    auto release = [&](int b) {
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          arrive_remote(map_rank(bar_free(b), 0));
+        else
+          mbar_arrive(bar_free(b));
+      }
+    };
+    const bool pairs = p.n % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+    int b = 0, turn = 0;
+    for (int t = group; t < ntiles && !*abort_flag; t += ngroups) {
+      if (!mbar_wait(bar_acc(b), turn & 1)) {
         fail();
         break;
       }
       tc_fence_after();
-      const uint32_t acc =
-          tmem + (uint32_t(32 * lg) << 16) + uint32_t((i & 1) ? C::kAcc1 : 0);
-      const int64_t col = col0(t) + 32 * lg + lane, m0 = row0(t);
+      const uint32_t acc = tmem + (uint32_t(32 * lg) << 16) + uint32_t(b * C::kAccStep);
+      const int col = col0(t) + 32 * lg + lane, m0 = row0(t);
       const bool live = col < p.n;
       O* out = static_cast<O*>(p.out) + col;
       if constexpr (kCrit > 0) {
-        const int c = ((i & 1) ? 0 : T - kCrit) + half * C1;
+        const int c = (b ? 0 : T - kCrit) + half * C1;
         uint32_t r[C1 / 16][16];
 #pragma unroll
         for (int j = 0; j < C1 / 16; ++j) tmem_ld16(acc + c + 16 * j, r[j]);
         tmem_wait_ld();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_remote(free0);
+        release(b);
 #pragma unroll
         for (int j = 0; j < C1 / 16; ++j)
-          store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, r[j], alpha);
-      } else {
-        // the other accumulator was emptied before this tile's wait
-        __syncwarp();
-        if (lane == 0) arrive_remote(free0);
+          store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, pairs, r[j], alpha);
       }
-      const int c = ((i & 1) ? kCrit : 0) + half * C2;
+      const int c = (kCrit && b ? kCrit : 0) + half * C2;
       uint32_t r[2][16];
       tmem_ld16(acc + c, r[0]);
 #pragma unroll
       for (int j = 0; j < C2 / 16; ++j) {
         tmem_wait_ld();
-        if (j + 1 < C2 / 16) tmem_ld16(acc + c + 16 * (j + 1), r[(j + 1) & 1]);
-        store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, r[j & 1], alpha);
+        if (j + 1 < C2 / 16) {
+          tmem_ld16(acc + c + 16 * (j + 1), r[(j + 1) & 1]);
+        } else if (kCrit == 0) {
+          tc_fence_before();
+          release(b);
+        }
+        store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, pairs, r[j & 1], alpha);
       }
       tc_fence_before();
+      if (++b == C::kAccs) {
+        b = 0;
+        ++turn;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (CG == 2) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
-                 : "memory");
+    tmem_dealloc<CG>(tmem);
   }
 }
 
@@ -358,42 +428,60 @@ int scale_map(CUtensorMap* m, const uint8_t* p, int64_t tiles, int box) {
   return IVFPQ_OK;
 }
 
-template <int FMT, int T, class O>
+template <int FMT, int T, int CG, class O>
 int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
-  using C = WideCfg<FMT, T>;
+  using C = WideCfg<FMT, T, CG>;
   CUtensorMap mb, ma, msb, msa;
   IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, BN));
-  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, T / 2));
+  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, T / CG));
   IVFPQ_TRY(scale_map(&msb, p.b_scales, ceil_div(p.n, 128) * p.ntile, C::kTiles));
   IVFPQ_TRY(scale_map(&msa, p.a_scales, ceil_div(p.m, 128) * p.ntile, C::kTiles));
-  auto kern = fp4_wide_kernel<FMT, T, O>;
+  auto kern = fp4_wide_kernel<FMT, T, CG, O>;
   IVFPQ_TRY(set_dynamic_smem(kern, C::kTotal));
   Tiling tl;
-  tl.tn = int(ceil_div(p.n, 2 * BN));
+  tl.tn = int(ceil_div(p.n, CG * BN));
   tl.tm = int(ceil_div(p.m, T));
   tl.m_fast = p.m <= p.n;  // the smaller operand is the one read again, from L2
-  static int resident = 0;  // pairs that fit the device at once
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(CG);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kTotal;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  static int resident = 0;  // groups that fit the device at once
   if (resident == 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kTotal;
     int nc = 0;
     IVFPQ_CUDA(cudaOccupancyMaxActiveClusters(&nc, kern, &cfg));
     resident = std::max(1, nc);
   }
   const int64_t tiles = int64_t(tl.tn) * tl.tm;
-  const unsigned grid = unsigned(std::min<int64_t>(tiles, resident)) * 2;
-  kern<<<grid, kThreads, C::kTotal, s>>>(mb, ma, msb, msa, p, tl);
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, resident)) * CG);
+  IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, mb, ma, msb, msa, p, tl));
   IVFPQ_LAUNCHED_K(kern, C::kTotal, kThreads);
   return IVFPQ_OK;
 }
 
 template <int FMT, class O>
 int choose(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
-  if (p.m > 128 && ceil_div(p.n, 2 * BN) * ceil_div(p.m, 256) * 2 >= num_sms())
-    return launch<FMT, 256, O>(a, b, p, s);
-  return launch<FMT, 128, O>(a, b, p, s);
+  // Rows per tile: 256, unless 128 take fewer or shorter waves (a 128-row tile
+  // costs 0.65 of a 256-row one: 8192 x 16384 x 4096 takes 255 us in 128-row
+  // tiles and 194 us in 256-row ones; 300 x 100000 x 512, whose second 256 rows
+  // are mostly empty, 33 and 39 us).
+  const int64_t tn = ceil_div(p.n, BN), sms = num_sms();
+  const double w128 = 0.65 * double(ceil_div(tn * ceil_div(p.m, 128), sms));
+  const double w256 = double(ceil_div(tn * ceil_div(p.m, 256), sms));
+  if (w128 < w256) return launch<FMT, 128, 1, O>(a, b, p, s);
+  // Pairs where K is long and there are many tiles (8192 x 16384 x 4096: 183 us,
+  // and 194 us on single CTAs); a pair's hand-over between tiles costs more
+  // (1000 x 100000 x 1024: 102 us, and 86 us).
+  if (p.kp >= 8 * KE && w256 >= 8) return launch<FMT, 256, 2, O>(a, b, p, s);
+  return launch<FMT, 256, 1, O>(a, b, p, s);
 }
 
 }  // namespace
