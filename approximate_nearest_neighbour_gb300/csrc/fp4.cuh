@@ -1,5 +1,5 @@
-// 4-bit block-scaled vectors: element and scale conversions, the packed layout
-// and element-type access shared by the fp4_* kernels.
+// 4-bit block-scaled vectors: element and scale conversions and the packed
+// layout shared by the fp4_* kernels.
 //
 // An element is E2M1 (sign, 2 exponent bits, 1 mantissa bit: 0, .5, 1, 1.5, 2,
 // 3, 4, 6 in magnitude). MXFP4 gives 32 consecutive columns one power-of-two
@@ -15,11 +15,9 @@
 //          lies in TMEM, so that a tile is one copy from shared memory.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "rowvec.cuh"
 
 namespace ivfpq {
 
@@ -32,37 +30,9 @@ inline int fp4_block(int fmt) { return fmt == IVFPQ_MXFP4 ? 32 : 16; }
 inline int64_t fp4_scale_tiles(int64_t cols, int fmt) {
   return ceil_div(fp4_padded_cols(cols), 4 * fp4_block(fmt));
 }
-inline bool known_dtype(int dtype) {
-  return dtype == IVFPQ_F32 || dtype == IVFPQ_F16 || dtype == IVFPQ_BF16;
-}
-inline int dtype_size(int dtype) { return dtype == IVFPQ_F32 ? 4 : 2; }
-
 __host__ __device__ __forceinline__ int64_t fp4_scale_at(int64_t row, int64_t blk, int64_t ntile) {
   return ((row >> 7) * ntile + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
          (blk & 3);
-}
-
-// ---- element access ---------------------------------------------------------------
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <class T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
-}
-
-// Calls f with a null pointer of the element type that `dtype` names.
-template <class F>
-int by_dtype(int dtype, F&& f) {
-  if (dtype == IVFPQ_F32) return f(static_cast<float*>(nullptr));
-  if (dtype == IVFPQ_F16) return f(static_cast<__half*>(nullptr));
-  return f(static_cast<__nv_bfloat16*>(nullptr));
 }
 
 // ---- conversions ------------------------------------------------------------------

@@ -6,21 +6,28 @@
 //   c in the row's bias list:          x += bias
 //   x /= temperature;  not allowed by the mask: x = -inf;  negated if asked
 //
-// Bound by memory: each score is read and written once. A block takes a run
-// of columns of one row, counts the history's tokens that fall into it in
-// shared memory (integer atomics: the result does not depend on their order)
-// and then streams the run once. Bit 31 of a counter marks a token of the
-// prompt, the bits below count occurrences past it.
+// Bound by memory: each score is read and written once (a vector that the mask
+// rules out entirely is not read). A block takes a run of columns of one row:
+//  1. its first scores are loaded, and wait in registers;
+//  2. the history's occurrences in the run are counted in shared memory and the
+//     bias entries noted (integer atomics: the result does not depend on their
+//     order), and a bitmap marks their columns. Bit 31 of a counter marks a
+//     token of the prompt, the bits below count occurrences past it;
+//  3. the run is streamed in 16-byte vectors; only marked columns look at the
+//     tables.
+// Every block of a row reads the whole history, so runs are as long as leaves
+// enough blocks (run_for).
 #include <algorithm>
 
-#include "fp4.cuh"
 #include "internal.h"
+#include "rowvec.cuh"
 
 namespace ivfpq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 4096;  // columns per block
+constexpr int kMaxRun = 8192;  // columns per block: two tables of 32 KB, three blocks per SM
+constexpr int kMinRun = 1024;
 
 struct AdjustArgs {
   const void* scores;
@@ -41,64 +48,181 @@ struct AdjustArgs {
   float sign;
   void* out;
   int64_t ldo;
+  int run;
 };
 
-template <class T, class O>
+// Bits b .. b + 31 of a bit string of words, as far as word `last`.
+template <class W>
+__device__ __forceinline__ uint32_t bits_at(const W* words, int b, int last) {
+  const int w = b >> 5, sh = b & 31;
+  const uint32_t lo = uint32_t(words[w]);
+  return sh == 0 ? lo : __funnelshift_r(lo, w < last ? uint32_t(words[w + 1]) : 0u, sh);
+}
+
+template <class T, class O, bool HIST, bool BIAS, bool MASK>
 __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs a) {
-  __shared__ uint32_t count[kRun];
-  __shared__ uint32_t slot[kRun];  // 1 + the last bias entry for the column
+  extern __shared__ __align__(16) uint32_t adjust_smem[];
+  constexpr bool MARK = HIST || BIAS;
+  uint32_t* mark = adjust_smem;  // a bit per column of the run
+  uint32_t* count = mark + a.run / 32;
+  uint32_t* slot = count + (HIST ? a.run : 0);  // 1 + the last bias entry for the column
   const int64_t row = blockIdx.x;
-  const int64_t c0 = int64_t(blockIdx.y) * kRun;
-  const int len = int(min(int64_t(kRun), a.cols - c0));
-  const bool has_hist = a.history != nullptr, has_bias = a.bias_ids != nullptr;
-  if (has_hist || has_bias) {
-    for (int i = threadIdx.x; i < len; i += kThreads) {
-      count[i] = 0;
-      slot[i] = 0;
+  const int64_t c0 = int64_t(blockIdx.y) * a.run;
+  const int len = int(min(int64_t(a.run), a.cols - c0));
+  const int words = (len + 31) / 32;
+  const T* src = static_cast<const T*>(a.scores) + row * a.lds + c0;
+  O* dst = static_cast<O*>(a.out) + row * a.ldo + c0;
+  const int32_t* mask = MASK ? a.mask + row * a.ldm + (c0 >> 5) : nullptr;
+  // vectors of N scores that start on a 16-byte boundary of the output
+  constexpr int N = Span<T>::N, U = 4;
+  const int head = min(len, int((16 - misalign(dst)) & 15) / int(sizeof(O)));
+  const int nvec = (len - head) / N;
+  const int mis = misalign(src + head);
+  uint4 r[U];
+  uint32_t ok[U];
+  const int first = inner_first(mis), last = inner_last<T>(len - head, mis);
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      ok[u] = ~0u;
+      if (MASK && i < nvec) ok[u] = bits_at(mask, head + i * N, words - 1);
     }
+    if (i0 >= first && i0 + (U - 1) * kThreads <= last) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        r[u] = make_uint4(0, 0, 0, 0);
+        if (!MASK || (ok[u] & ((1u << N) - 1))) r[u] = load_inner(src + head, i0 + u * kThreads, mis);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * kThreads < nvec) r[u] = load_vec(src + head, len - head, i0 + u * kThreads, mis);
+    }
+  };
+  load(threadIdx.x);
+  if constexpr (MARK) {
+    const int32_t* h = HIST ? a.history + row * a.ldh : nullptr;
+    const int32_t* bi = BIAS ? a.bias_ids + row * a.nb : nullptr;
+    int n = 0, np = 0;
+    if (HIST) {
+      n = int(a.hist_cols);
+      if (a.history_len) n = max(0, min(n, a.history_len[row]));
+      if (a.prompt_len) np = a.prompt_len[row];
+    }
+    const int clear = a.run / 32 + a.run * (int(HIST) + int(BIAS));  // a multiple of 4 words
+    for (int i = threadIdx.x; i < clear / 4; i += kThreads)
+      reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (has_hist) {
-      const int64_t n = max(int64_t(0), min(a.history_len ? int64_t(a.history_len[row]) : a.hist_cols,
-                                            a.hist_cols));
-      const int64_t np = a.prompt_len ? int64_t(a.prompt_len[row]) : 0;
-      const int32_t* h = a.history + row * a.ldh;
-      for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t c = int64_t(h[i]) - c0;
-        if (c >= 0 && c < len) {
-          if (i < np)
-            atomicOr(&count[c], 0x80000000u);
-          else
-            atomicAdd(&count[c], 1u);
+    if (HIST) {
+      constexpr int V = 8;
+      for (int i0 = threadIdx.x; i0 < n; i0 += V * kThreads) {
+        int32_t t[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) t[v] = i0 + v * kThreads < n ? __ldg(h + i0 + v * kThreads) : -1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int64_t c = int64_t(t[v]) - c0;
+          if (t[v] >= 0 && c >= 0 && c < len) {
+            atomicOr(&mark[c >> 5], 1u << (c & 31));
+            if (i0 + v * kThreads < np)
+              atomicOr(&count[c], 0x80000000u);
+            else
+              atomicAdd(&count[c], 1u);
+          }
         }
       }
     }
-    if (has_bias) {
-      const int32_t* b = a.bias_ids + row * a.nb;
-      for (int64_t i = threadIdx.x; i < a.nb; i += kThreads) {
-        const int64_t c = int64_t(b[i]) - c0;
-        if (c >= 0 && c < len) atomicMax(&slot[c], uint32_t(i) + 1u);
+    if (BIAS) {
+      for (int i = threadIdx.x; i < int(a.nb); i += kThreads) {
+        const int64_t c = int64_t(__ldg(bi + i)) - c0;
+        if (c >= 0 && c < len) {
+          atomicOr(&mark[c >> 5], 1u << (c & 31));
+          atomicMax(&slot[c], uint32_t(i) + 1u);
+        }
       }
     }
     __syncthreads();
   }
-  const float rep = a.repetition ? a.repetition[row] : 1.f;
-  const float pres = a.presence ? a.presence[row] : 0.f;
-  const float freq = a.frequency ? a.frequency[row] : 0.f;
-  const float temp = a.temperature ? a.temperature[row] : 1.f;
-  const T* src = static_cast<const T*>(a.scores) + row * a.lds + c0;
-  O* dst = static_cast<O*>(a.out) + row * a.ldo + c0;
-  const int32_t* mask = a.mask ? a.mask + row * a.ldm : nullptr;
-  for (int i = threadIdx.x; i < len; i += kThreads) {
-    float x = to_f32(src[i]);
-    if (has_hist && count[i] != 0) {
-      const uint32_t n = count[i] & 0x7fffffffu;
-      x = x > 0.f ? x / rep : x * rep;
+  const float rep = HIST && a.repetition ? a.repetition[row] : 1.f;
+  const float pres = HIST && a.presence ? a.presence[row] : 0.f;
+  const float freq = HIST && a.frequency ? a.frequency[row] : 0.f;
+  // the division by the temperature and the sign, as one factor per row
+  const float f = (a.temperature ? __fdiv_rn(1.f, a.temperature[row]) : 1.f) * a.sign;
+  auto marked = [&](int c, float x) {
+    if (HIST && count[c] != 0) {
+      const uint32_t n = count[c] & 0x7fffffffu;
+      x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
       if (n) x -= float(n) * freq + pres;
     }
-    if (has_bias && slot[i] != 0) x += a.bias_vals[row * a.nb + slot[i] - 1];
-    x /= temp;
-    if (mask && !((uint32_t(mask[(c0 + i) >> 5]) >> ((c0 + i) & 31)) & 1u)) x = -INFINITY;
-    dst[i] = from_f32<O>(x * a.sign);
+    if (BIAS && slot[c] != 0) x += a.bias_vals[row * a.nb + slot[c] - 1];
+    return x;
+  };
+  auto one = [&](int c) {
+    float x = to_f32(src[c]);
+    if (MARK && (mark[c >> 5] >> (c & 31)) & 1u) x = marked(c, x);
+    x *= f;
+    if (MASK && !((uint32_t(mask[c >> 5]) >> (c & 31)) & 1u)) x = -INFINITY * a.sign;
+    dst[c] = from_f32<O>(x);
+  };
+  for (int e = threadIdx.x; e < len - nvec * N; e += kThreads) one(e < head ? e : nvec * N + e);
+  for (int i0 = threadIdx.x; i0 < nvec; i0 += U * kThreads) {
+    if (i0 != int(threadIdx.x)) load(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= nvec) continue;
+      float v[N];
+      unpack_vec<T>(r[u], v);
+      if constexpr (MARK) {
+        const uint32_t m = bits_at(mark, head + i * N, words - 1) & ((1u << N) - 1);
+        if (m) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if ((m >> j) & 1u) v[j] = marked(head + i * N + j, v[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v[j] *= f;
+        if (MASK && !((ok[u] >> j) & 1u)) v[j] = -INFINITY * a.sign;
+      }
+      store_vec<O>(dst + head + i * N, v);
+    }
+  }
+}
+
+// Runs of kMaxRun columns, halved while the blocks do not fill the device
+// three times (three of the longest fit an SM).
+int run_for(int64_t rows, int64_t cols) {
+  int run = kMaxRun;
+  while (run > kMinRun && rows * ceil_div(cols, run) < 3 * num_sms()) run /= 2;
+  return run;
+}
+
+template <class T, class O, bool HIST, bool BIAS, bool MASK>
+int launch(AdjustArgs a, cudaStream_t s) {
+  a.run = run_for(a.rows, a.cols);
+  const size_t smem = size_t(a.run) / 8 + size_t(a.run) * 4 * (int(HIST) + int(BIAS));
+  auto kern = score_adjust_kernel<T, O, HIST, BIAS, MASK>;
+  IVFPQ_TRY(set_dynamic_smem(kern, smem));
+  const dim3 grid(unsigned(a.rows), unsigned(ceil_div(a.cols, a.run)));
+  kern<<<grid, kThreads, smem, s>>>(a);
+  IVFPQ_LAUNCHED_K(kern, smem, kThreads);
+  return IVFPQ_OK;
+}
+template <class T, class O>
+int launch_types(const AdjustArgs& a, cudaStream_t s) {
+  const int which = (a.history ? 4 : 0) | (a.bias_ids ? 2 : 0) | (a.mask ? 1 : 0);
+  switch (which) {
+    case 0: return launch<T, O, false, false, false>(a, s);
+    case 1: return launch<T, O, false, false, true>(a, s);
+    case 2: return launch<T, O, false, true, false>(a, s);
+    case 3: return launch<T, O, false, true, true>(a, s);
+    case 4: return launch<T, O, true, false, false>(a, s);
+    case 5: return launch<T, O, true, false, true>(a, s);
+    case 6: return launch<T, O, true, true, false>(a, s);
+    default: return launch<T, O, true, true, true>(a, s);
   }
 }
 
@@ -136,16 +260,10 @@ extern "C" int score_adjust(const void* scores, int dtype, int64_t rows, int64_t
                 "score_adjust: bias ids and values go together");
   AdjustArgs a{scores, rows, cols, lds, hist_cols ? history : nullptr, hist_cols, ldh, history_len,
                prompt_len, repetition, presence, frequency, nb ? bias_ids : nullptr, bias_vals, nb,
-               temperature, mask, ldm, negate ? -1.f : 1.f, out, ldo};
+               temperature, mask, ldm, negate ? -1.f : 1.f, out, ldo, 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_dtype(dtype, [&](auto* t) -> int {
     using T = std::remove_pointer_t<decltype(t)>;
-    const dim3 grid(unsigned(rows), unsigned(ceil_div(cols, kRun)));
-    if (out_dtype == dtype)
-      score_adjust_kernel<T, T><<<grid, kThreads, 0, s>>>(a);
-    else
-      score_adjust_kernel<T, float><<<grid, kThreads, 0, s>>>(a);
-    IVFPQ_LAUNCHED();
-    return IVFPQ_OK;
+    return out_dtype == dtype ? launch_types<T, T>(a, s) : launch_types<T, float>(a, s);
   });
 }

@@ -12,11 +12,9 @@
 // s_j - m, so scores of any magnitude (a mask of the type's lowest value among
 // them) neither overflow nor cancel. A score of -inf has q = 0.
 #include <algorithm>
-#include <cstring>
-#include <type_traits>
 
-#include "fp4.cuh"
 #include "internal.h"
+#include "rowvec.cuh"
 #include "tc_ptx.cuh"
 
 namespace ivfpq {
@@ -43,105 +41,6 @@ struct DistillArgs {
   int chunk;     // columns of one block
 };
 
-// ---- 16-byte access to a run of a row -----------------------------------------------
-// Elements [0, len) at p by address: a head up to the first 16-byte boundary,
-// whole vectors, a tail.
-template <class T>
-struct Span {
-  static constexpr int N = 16 / int(sizeof(T));
-  int head, nvec, len;
-  __device__ __forceinline__ Span(const T* p, int n) : len(n) {
-    head = min(n, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int(sizeof(T)));
-    nvec = (n - head) / N;
-  }
-  // the e-th element outside the vectors (e < rest())
-  __device__ __forceinline__ int rest() const { return len - nvec * N; }
-  __device__ __forceinline__ int at(int e) const { return e < head ? e : nvec * N + e; }
-};
-__device__ __forceinline__ void unpack(const uint4& r, float (&v)[4]) {
-  v[0] = __uint_as_float(r.x);
-  v[1] = __uint_as_float(r.y);
-  v[2] = __uint_as_float(r.z);
-  v[3] = __uint_as_float(r.w);
-}
-template <class T>
-__device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi);
-template <>
-__device__ __forceinline__ void unpack16<__nv_bfloat16>(uint32_t w, float& lo, float& hi) {
-  lo = __uint_as_float(w << 16);
-  hi = __uint_as_float(w & 0xffff0000u);
-}
-template <>
-__device__ __forceinline__ void unpack16<__half>(uint32_t w, float& lo, float& hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  lo = f.x;
-  hi = f.y;
-}
-template <class T>
-__device__ __forceinline__ void unpack_vec(const uint4& r, float (&v)[Span<T>::N]) {
-  if constexpr (sizeof(T) == 4) {
-    unpack(r, v);
-  } else {
-    unpack16<T>(r.x, v[0], v[1]);
-    unpack16<T>(r.y, v[2], v[3]);
-    unpack16<T>(r.z, v[4], v[5]);
-    unpack16<T>(r.w, v[6], v[7]);
-  }
-}
-template <class T>
-__device__ __forceinline__ T lowest_inf();
-template <>
-__device__ __forceinline__ float lowest_inf<float>() { return -INFINITY; }
-template <>
-__device__ __forceinline__ __half lowest_inf<__half>() { return __ushort_as_half(0xfc00); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 lowest_inf<__nv_bfloat16>() {
-  return __ushort_as_bfloat16(0xff80);
-}
-// Elements i N .. i N + N - 1 of the run at p, whatever its alignment (mis =
-// address mod 16): two neighbouring 16-byte loads shifted together, element by
-// element only in the first and last vectors of a misaligned run, so that
-// nothing outside the run is read. Past the end: -inf. Which elements go into
-// one vector depends on their index alone, and so do the sums over them.
-template <class T>
-__device__ __forceinline__ uint4 load_vec(const T* p, int len, int i, int mis) {
-  constexpr int N = Span<T>::N;
-  if (mis == 0) {
-    if ((i + 1) * N <= len) return reinterpret_cast<const uint4*>(p)[i];
-  } else if (i > 0 && (i + 2) * N <= len) {
-    const uint4* b = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - mis) + i;
-    const uint4 x = b[0], y = b[1];
-    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    if (mis & 8) {
-#pragma unroll
-      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
-    }
-    if (mis & 4) {
-#pragma unroll
-      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
-    }
-    const int bits = (mis & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-  }
-  T t[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) t[j] = i * N + j < len ? p[i * N + j] : lowest_inf<T>();
-  uint4 r;
-  memcpy(&r, t, 16);
-  return r;
-}
-__device__ __forceinline__ int misalign(const void* p) {
-  return int(reinterpret_cast<uintptr_t>(p) & 15);
-}
-template <class T>
-__device__ __forceinline__ uint4 pack_vec(const float (&v)[Span<T>::N]) {
-  T t[Span<T>::N];
-#pragma unroll
-  for (int i = 0; i < Span<T>::N; ++i) t[i] = from_f32<T>(v[i]);
-  return *reinterpret_cast<const uint4*>(t);
-}
-
 // ---- exponentials relative to the row's maximum ------------------------------------
 // exp((s - m) / tau) = 2^((s - m) c), c = log2(e) / tau. The difference first:
 // its rounding error stays relative to the distance from the maximum, and no
@@ -156,33 +55,44 @@ struct Base {
   float m, c;
   __device__ __forceinline__ Base(float m_, float c_) : m(m_ == -INFINITY ? 0.f : m_), c(c_) {}
   __device__ __forceinline__ float operator()(float s) const { return exp2_fast((s - m) * c); }
+  // N values in place
+  template <int N>
+  __device__ __forceinline__ void all(float (&v)[N]) const {
+    const uint64_t nm = pair(-m, -m), cc = pair(c, c);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float x, y;
+      unpair(mul2(add2(pair(v[i], v[i + 1]), nm), cc), x, y);
+      v[i] = exp2_fast(x);
+      v[i + 1] = exp2_fast(y);
+    }
+  }
 };
 
 // A running maximum and sum; the sum is rescaled when the maximum grows.
 struct Online {
   float m = -INFINITY, z = 0.f;
-  template <int N>
-  __device__ __forceinline__ void add(const float (&v)[N], float c) {
-    float t = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) t = fmaxf(t, v[i]);
-    add(v, t, c);
-  }
-  // t: the largest of v
-  template <int N>
-  __device__ __forceinline__ void add(const float (&v)[N], float t, float c) {
+  __device__ __forceinline__ void rise(float t, float c) {
     if (t > m) {
       z *= m == -INFINITY ? 0.f : exp2_fast((m - t) * c);
       m = t;
     }
-    const Base b(m, c);
-    float z0 = 0.f, z1 = 0.f;
+  }
+  __device__ __forceinline__ void add(float v, float c) {
+    rise(v, c);
+    z += Base(m, c)(v);
+  }
+  // N values, t the largest of them
+  template <int N>
+  __device__ __forceinline__ void add(float (&v)[N], float t, float c) {
+    rise(t, c);
+    Base(m, c).all(v);
+    uint64_t a = pair(v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      z0 += b(v[i]);
-      if (i + 1 < N) z1 += b(v[i + 1]);
-    }
-    z += z0 + z1;
+    for (int i = 2; i < N; i += 2) a = add2(a, pair(v[i], v[i + 1]));
+    float x, y;
+    unpair(a, x, y);
+    z += x + y;
   }
   __device__ __forceinline__ void join(float m2, float z2, float c) {
     const float t = fmaxf(m, m2);
@@ -270,8 +180,7 @@ __device__ __forceinline__ void teacher_stats(Teacher& t, float c) {
 #pragma unroll
   for (int q = 0; q < kPerThread; ++q) {
     if (t.id[q] >= 0) {
-      const float v[1] = {t.v[q]};
-      t.all.add(v, c);
+      t.all.add(t.v[q], c);
     }
   }
 }
@@ -371,31 +280,30 @@ __device__ __forceinline__ Online run_stats(const T* s, int len, float c, T* kee
     __syncthreads();
     from = keep;
   }
-  // the next U vectors are on their way while these are summed
   Online o;
-  const int nvec = (len + N - 1) / N;
-  uint4 r[U], next[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (int(threadIdx.x) + u * kThreads < nvec)
-      next[u] = load_vec(from, len, threadIdx.x + u * kThreads, mis);
-  for (int i = threadIdx.x; i < nvec; i += U * kThreads) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r[u] = next[u];
-      if (i + (U + u) * kThreads < nvec)
-        next[u] = load_vec(from, len, i + (U + u) * kThreads, mis);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u * kThreads < nvec) {
-        if (KEEP && mis == 0) reinterpret_cast<uint4*>(keep)[i + u * kThreads] = r[u];
-        float v[N];
-        unpack_vec<T>(r[u], v);
-        o.add(v, vec_max(r[u], static_cast<T*>(nullptr)), c);
-      }
-    }
+  auto sum = [&](const uint4& r, int i) {
+    if (KEEP && mis == 0) reinterpret_cast<uint4*>(keep)[i] = r;
+    float v[N];
+    unpack_vec<T>(r, v);
+    o.add(v, vec_max(r, static_cast<T*>(nullptr)), c);
+  };
+  // a thread's vectors in ascending order: U inner ones at a time, the others
+  // one by one
+  const int nvec = (len + N - 1) / N, last = inner_last<T>(len, mis);
+  int i = threadIdx.x;
+  if (mis != 0 && i < nvec) {
+    sum(load_vec(from, len, i, mis), i);
+    i += kThreads;
   }
+  for (; i + (U - 1) * kThreads <= last; i += U * kThreads) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = load_inner(from, i + u * kThreads, mis);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum(r[u], i + u * kThreads);
+  }
+#pragma unroll 1
+  for (; i < nvec; i += kThreads) sum(load_vec(from, len, i, mis), i);
   return o;
 }
 
@@ -410,14 +318,30 @@ __device__ __forceinline__ void run_grad(const T* s, int len, const Base& b, flo
   const T* src = s + sp.head;
   const int mis = misalign(src);
   uint4* dst = reinterpret_cast<uint4*>(g + sp.head);
-#pragma unroll 2
-  for (int i = threadIdx.x; i < sp.nvec; i += kThreads) {
+  constexpr int U = 4;
+  const int n = len - sp.head, last = min(sp.nvec - 1, inner_last<T>(n, mis));
+  auto put = [&](const uint4& x, int i) {
     float v[N];
-    unpack_vec<T>(load_vec(src, len - sp.head, i, mis), v);
+    unpack_vec<T>(x, v);
+    b.all(v);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = b(v[j]) * r;
+    for (int j = 0; j < N; ++j) v[j] *= r;
     dst[i] = pack_vec<T>(v);
+  };
+  int i = threadIdx.x;
+  if (mis != 0 && i < sp.nvec) {
+    put(load_vec(src, n, i, mis), i);
+    i += kThreads;
   }
+  for (; i + (U - 1) * kThreads <= last; i += U * kThreads) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load_inner(src, i + u * kThreads, mis);
+#pragma unroll
+    for (int u = 0; u < U; ++u) put(x[u], i + u * kThreads);
+  }
+#pragma unroll 1
+  for (; i < sp.nvec; i += kThreads) put(load_vec(src, n, i, mis), i);
 }
 template <class T>
 __device__ __forceinline__ void run_zero(T* g, int len) {
