@@ -182,4 +182,18 @@ __device__ __forceinline__ int misalign(const void* p) {
   return int(reinterpret_cast<uintptr_t>(p) & 15);
 }
 
+// The largest element of a vector; 16-bit types two at a time.
+__device__ __forceinline__ float vec_max(const uint4& r, float*) {
+  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+template <class T>
+__device__ __forceinline__ float vec_max(const uint4& r, T*) {
+  using P = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+  P w[4];
+  memcpy(w, &r, 16);
+  const P t = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+  return fmaxf(to_f32(t.x), to_f32(t.y));
+}
+
 }  // namespace ivfpq

@@ -11,8 +11,7 @@
 //  1. its first scores are loaded, and wait in registers;
 //  2. the history's occurrences in the run are counted in shared memory and the
 //     bias entries noted (integer atomics: the result does not depend on their
-//     order), and a bitmap marks their columns. Bit 31 of a counter marks a
-//     token of the prompt, the bits below count occurrences past it;
+//     order), and a bitmap marks their columns;
 //  3. the run is streamed in 16-byte vectors; only marked columns look at the
 //     tables.
 // Every block of a row reads the whole history, so runs are as long as leaves
@@ -26,8 +25,15 @@ namespace ivfpq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRun = 8192;  // columns per block: two tables of 32 KB, three blocks per SM
+constexpr int kMaxRun = 8192;  // columns per block
 constexpr int kMinRun = 1024;
+
+// A run's table: per column the occurrences past the prompt, whether the prompt
+// has it, and 1 + the last bias entry for it. SHORT packs them into one word
+// (bits 0..14, bit 15, bits 16..31), so that six blocks share an SM instead of
+// three; it holds histories of up to 32,767 tokens and 65,535 bias entries.
+// The long form has the counter with bit 31 for the prompt, and a second word.
+constexpr int kShortHistory = 32767, kShortBias = 65535;
 
 struct AdjustArgs {
   const void* scores;
@@ -59,13 +65,14 @@ __device__ __forceinline__ uint32_t bits_at(const W* words, int b, int last) {
   return sh == 0 ? lo : __funnelshift_r(lo, w < last ? uint32_t(words[w + 1]) : 0u, sh);
 }
 
-template <class T, class O, bool HIST, bool BIAS, bool MASK>
+template <class T, class O, bool HIST, bool BIAS, bool MASK, bool SHORT>
 __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs a) {
   extern __shared__ __align__(16) uint32_t adjust_smem[];
   constexpr bool MARK = HIST || BIAS;
   uint32_t* mark = adjust_smem;  // a bit per column of the run
   uint32_t* count = mark + a.run / 32;
-  uint32_t* slot = count + (HIST ? a.run : 0);  // 1 + the last bias entry for the column
+  uint32_t* slot = count + (SHORT ? 0 : a.run);
+  constexpr uint32_t kPrompt = SHORT ? 0x8000u : 0x80000000u;
   const int64_t row = blockIdx.x;
   const int64_t c0 = int64_t(blockIdx.y) * a.run;
   const int len = int(min(int64_t(a.run), a.cols - c0));
@@ -102,15 +109,15 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
   };
   load(threadIdx.x);
   if constexpr (MARK) {
-    const int32_t* h = HIST ? a.history + row * a.ldh : nullptr;
-    const int32_t* bi = BIAS ? a.bias_ids + row * a.nb : nullptr;
+    const int32_t* h = HIST && a.history ? a.history + row * a.ldh : nullptr;
+    const int32_t* bi = BIAS && a.bias_ids ? a.bias_ids + row * a.nb : nullptr;
     int n = 0, np = 0;
-    if (HIST) {
+    if (HIST && a.history) {
       n = int(a.hist_cols);
       if (a.history_len) n = max(0, min(n, a.history_len[row]));
       if (a.prompt_len) np = a.prompt_len[row];
     }
-    const int clear = a.run / 32 + a.run * (int(HIST) + int(BIAS));  // a multiple of 4 words
+    const int clear = a.run / 32 + a.run * (SHORT ? 1 : 2);  // a multiple of 4 words
     for (int i = threadIdx.x; i < clear / 4; i += kThreads)
       reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -126,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
           if (t[v] >= 0 && c >= 0 && c < len) {
             atomicOr(&mark[c >> 5], 1u << (c & 31));
             if (i0 + v * kThreads < np)
-              atomicOr(&count[c], 0x80000000u);
+              atomicOr(&count[c], kPrompt);
             else
               atomicAdd(&count[c], 1u);
           }
@@ -134,11 +141,22 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
       }
     }
     if (BIAS) {
+      if (HIST && SHORT) __syncthreads();  // the counters are complete
       for (int i = threadIdx.x; i < int(a.nb); i += kThreads) {
         const int64_t c = int64_t(__ldg(bi + i)) - c0;
         if (c >= 0 && c < len) {
           atomicOr(&mark[c >> 5], 1u << (c & 31));
-          atomicMax(&slot[c], uint32_t(i) + 1u);
+          if (SHORT) {
+            uint32_t old = slot[c];
+            while ((old >> 16) < uint32_t(i) + 1u) {
+              const uint32_t seen =
+                  atomicCAS(&slot[c], old, (old & 0xffffu) | ((uint32_t(i) + 1u) << 16));
+              if (seen == old) break;
+              old = seen;
+            }
+          } else {
+            atomicMax(&slot[c], uint32_t(i) + 1u);
+          }
         }
       }
     }
@@ -150,12 +168,17 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
   // the division by the temperature and the sign, as one factor per row
   const float f = (a.temperature ? __fdiv_rn(1.f, a.temperature[row]) : 1.f) * a.sign;
   auto marked = [&](int c, float x) {
-    if (HIST && count[c] != 0) {
-      const uint32_t n = count[c] & 0x7fffffffu;
+    const uint32_t e = count[c];
+    const uint32_t seen = SHORT ? e & 0xffffu : e;
+    if (HIST && seen != 0) {
+      const uint32_t n = seen & (kPrompt - 1u);
       x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
       if (n) x -= float(n) * freq + pres;
     }
-    if (BIAS && slot[c] != 0) x += a.bias_vals[row * a.nb + slot[c] - 1];
+    if (BIAS) {
+      const uint32_t b = SHORT ? e >> 16 : slot[c];
+      if (b != 0) x += a.bias_vals[row * a.nb + b - 1];
+    }
     return x;
   };
   auto one = [&](int c) {
@@ -193,18 +216,19 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
 }
 
 // Runs of kMaxRun columns, halved while the blocks do not fill the device
-// three times (three of the longest fit an SM).
+// three times.
 int run_for(int64_t rows, int64_t cols) {
   int run = kMaxRun;
   while (run > kMinRun && rows * ceil_div(cols, run) < 3 * num_sms()) run /= 2;
   return run;
 }
 
-template <class T, class O, bool HIST, bool BIAS, bool MASK>
+template <class T, class O, bool HIST, bool BIAS, bool MASK, bool SHORT>
 int launch(AdjustArgs a, cudaStream_t s) {
   a.run = run_for(a.rows, a.cols);
-  const size_t smem = size_t(a.run) / 8 + size_t(a.run) * 4 * (int(HIST) + int(BIAS));
-  auto kern = score_adjust_kernel<T, O, HIST, BIAS, MASK>;
+  const size_t smem =
+      HIST || BIAS ? size_t(a.run) / 8 + size_t(a.run) * 4 * (SHORT ? 1 : 2) : 0;
+  auto kern = score_adjust_kernel<T, O, HIST, BIAS, MASK, SHORT>;
   IVFPQ_TRY(set_dynamic_smem(kern, smem));
   const dim3 grid(unsigned(a.rows), unsigned(ceil_div(a.cols, a.run)));
   kern<<<grid, kThreads, smem, s>>>(a);
@@ -214,15 +238,18 @@ int launch(AdjustArgs a, cudaStream_t s) {
 template <class T, class O>
 int launch_types(const AdjustArgs& a, cudaStream_t s) {
   const int which = (a.history ? 4 : 0) | (a.bias_ids ? 2 : 0) | (a.mask ? 1 : 0);
+  if ((a.history && a.hist_cols > kShortHistory) || (a.bias_ids && a.nb > kShortBias))
+    return a.mask ? launch<T, O, true, true, true, false>(a, s)
+                  : launch<T, O, true, true, false, false>(a, s);
   switch (which) {
-    case 0: return launch<T, O, false, false, false>(a, s);
-    case 1: return launch<T, O, false, false, true>(a, s);
-    case 2: return launch<T, O, false, true, false>(a, s);
-    case 3: return launch<T, O, false, true, true>(a, s);
-    case 4: return launch<T, O, true, false, false>(a, s);
-    case 5: return launch<T, O, true, false, true>(a, s);
-    case 6: return launch<T, O, true, true, false>(a, s);
-    default: return launch<T, O, true, true, true>(a, s);
+    case 0: return launch<T, O, false, false, false, true>(a, s);
+    case 1: return launch<T, O, false, false, true, true>(a, s);
+    case 2: return launch<T, O, false, true, false, true>(a, s);
+    case 3: return launch<T, O, false, true, true, true>(a, s);
+    case 4: return launch<T, O, true, false, false, true>(a, s);
+    case 5: return launch<T, O, true, false, true, true>(a, s);
+    case 6: return launch<T, O, true, true, false, true>(a, s);
+    default: return launch<T, O, true, true, true, true>(a, s);
   }
 }
 
@@ -259,7 +286,7 @@ extern "C" int score_adjust(const void* scores, int dtype, int64_t rows, int64_t
   IVFPQ_REQUIRE((bias_ids == nullptr) == (bias_vals == nullptr),
                 "score_adjust: bias ids and values go together");
   AdjustArgs a{scores, rows, cols, lds, hist_cols ? history : nullptr, hist_cols, ldh, history_len,
-               prompt_len, repetition, presence, frequency, nb ? bias_ids : nullptr, bias_vals, nb,
+               prompt_len, repetition, presence, frequency, nb ? bias_ids : nullptr, bias_vals, bias_ids ? nb : 0,
                temperature, mask, ldm, negate ? -1.f : 1.f, out, ldo, 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_dtype(dtype, [&](auto* t) -> int {

@@ -24,7 +24,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kPerThread = IVFPQ_MAX_K / kThreads;  // list entries of one thread
 
 struct DistillArgs {
   const void* scores;
@@ -103,24 +102,7 @@ struct Online {
   }
 };
 
-// Sums over the block and joins of running maxima and sums, in a fixed order.
-__device__ __forceinline__ float2 block_sum2(float2 v, float2* sh) {
-#pragma unroll
-  for (int o = 16; o; o /= 2) {
-    v.x += __shfl_xor_sync(kFullMask, v.x, o);
-    v.y += __shfl_xor_sync(kFullMask, v.y, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float2 r = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    r.x += sh[i].x;
-    r.y += sh[i].y;
-  }
-  return r;
-}
+// Joins of running maxima and sums over the block, in a fixed order.
 // The row's and the list's statistics in one step.
 __device__ __forceinline__ void block_join(Online& o, Online& l, float c, float2* sh) {
 #pragma unroll
@@ -143,167 +125,191 @@ __device__ __forceinline__ void block_join(Online& o, Online& l, float c, float2
 }
 
 // ---- the teacher's list ----------------------------------------------------------------
-// A thread's entries i = threadIdx.x + q kThreads: value and column, -1 where
-// the entry is not valid (its id is no column, or its value -inf: the padding
-// of a short list); and the list's largest value and sum of exp((t - m) / tau),
-// over the thread's entries until block_join. A sum of 0 means no valid entry.
-struct Teacher {
-  float v[kPerThread];
-  int id[kPerThread];
-  Online all;
-  __device__ __forceinline__ bool any() const { return !(all.z == 0.f); }
-  // softmax weight of entry q
-  __device__ __forceinline__ float p(int q, float c, float inv_z) const {
-    return exp2_fast((v[q] - all.m) * c) * inv_z;
+// In shared memory; thread t handles the entries t, t + kThreads, ... in every
+// step, so that they need no barrier between steps. An entry is valid if its
+// id is a column and its value not -inf (the padding of a short list).
+struct List {
+  int* id;         // [k] column, -1 where not valid; then relative to the block's run, -1 outside
+  float* p;        // [k] value; then softmax weight; then the gradient at the column
+  float* fix;      // [k]
+  uint32_t* seen;  // [chunk / 32] columns of the run that are listed
+  __device__ __forceinline__ List(uint8_t* smem, int k) {
+    id = reinterpret_cast<int*>(smem);
+    p = reinterpret_cast<float*>(id + k);
+    fix = p + k;
+    seen = reinterpret_cast<uint32_t*>(fix + k);
   }
 };
-__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t row, Teacher& t) {
-  const float* tv = a.tv + row * a.k;
-  const int64_t* ti = a.ti + row * a.k;
-#pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    const int i = threadIdx.x + q * kThreads;
-    t.id[q] = -1;
-    t.v[q] = 0.f;
-    if (i < a.k) {
-      const float x = __ldg(tv + i) * a.sign;
-      const int64_t id = __ldg(ti + i);
-      if (id >= 0 && id < a.cols && x != -INFINITY) {
-        t.id[q] = int(id);
-        t.v[q] = x;
-      }
-    }
-  }
-}
-__device__ __forceinline__ void teacher_stats(Teacher& t, float c) {
-  t.all = Online{};
-#pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    if (t.id[q] >= 0) {
-      t.all.add(t.v[q], c);
-    }
-  }
+inline size_t list_bytes(int k, int64_t chunk) {
+  return size_t(k) * 12 + size_t(ceil_div(chunk, 32)) * 4;
 }
 
-// The gradient's values at the listed columns of [c0, c0 + len), one per entry,
-// computed before any of them is written (the gradient may overwrite the
-// scores). Entries with one column are found with a bitmap of the columns; only
-// if there are any does a thread look through the list, in list order, for the
-// sum of the weights of its column.
-struct ListSmem {
-  int* id;         // [k], relative to c0, -1 outside
-  float* p;        // [k]
-  uint32_t* seen;  // [chunk / 32]
+// Loads the row's entries; returns the largest value and the sum of
+// exp((t - m) / tau) over the thread's. A sum of 0 means no valid entry.
+__device__ __forceinline__ Online list_load(const DistillArgs& a, int64_t row, const List& l,
+                                            float c) {
+  Online o;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.k; i += kThreads) {
+    const float x = __ldg(a.tv + row * a.k + i) * a.sign;
+    const int64_t id = __ldg(a.ti + row * a.k + i);
+    const bool ok = id >= 0 && id < a.cols && x != -INFINITY;
+    l.id[i] = ok ? int(id) : -1;
+    l.p[i] = x;
+    if (ok) o.add(x, c);
+  }
+  return o;
+}
+
+// What the loss needs of a run of columns, with p and t over the entries in it:
+// sum p log p, sum p, sum p (s - m), m the run's own maximum.
+struct LossPart {
+  float a = 0.f, p = 0.f, y = 0.f;
 };
-__device__ __forceinline__ void list_to_smem(const DistillArgs& a, const Teacher& t, float c,
-                                             int c0, int len, const ListSmem& l, int* repeated) {
-  const float inv_tz = 1.f / t.all.z;
-  for (int i = threadIdx.x; i < (len + 31) / 32; i += kThreads) l.seen[i] = 0;
-  if (threadIdx.x == 0) *repeated = 0;
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    const int i = threadIdx.x + q * kThreads;
-    if (i < a.k) {
-      const int id = t.id[q] - c0;
-      const bool in = t.id[q] >= c0 && id < len;
-      l.id[i] = in ? id : -1;
-      l.p[i] = t.p(q, c, inv_tz);
-      if (in && (atomicOr(&l.seen[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u) *repeated = 1;
+// Entries to run-relative columns and softmax weights. With MARK also a bitmap
+// of the listed columns (cleared before), and *repeated if one comes twice.
+template <bool MARK, class Get>
+__device__ __forceinline__ LossPart list_weights(const DistillArgs& a, const List& l,
+                                                 const Online& t, float c, int c0, int len, float m,
+                                                 int* repeated, Get&& get) {
+  LossPart r;
+  const float inv_tz = 1.f / t.z, logtz = logf(t.z);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.k; i += kThreads) {
+    const int id = l.id[i] - c0;
+    const bool in = l.id[i] >= c0 && id < len;
+    l.id[i] = in ? id : -1;
+    if (in) {
+      const float v = l.p[i], p = exp2_fast((v - t.m) * c) * inv_tz;
+      l.p[i] = p;
+      if (!(p <= 0.f)) {  // also a NaN
+        const float s = get(id);
+        r.a += p * ((v - t.m) * a.inv_tau - logtz);
+        r.p += p;
+        r.y += p * (s == -INFINITY ? s : s - m);
+      }
+      if (MARK && (atomicOr(&l.seen[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u) *repeated = 1;
     }
   }
-  __syncthreads();
+  return r;
 }
+// The gradient at the listed columns, one value per entry, computed before any
+// is written (the gradient may overwrite the scores). Only if a column comes
+// twice does a thread look through the list, in list order, for the sum of its
+// weights.
 template <class Get>
-__device__ __forceinline__ void list_values(const DistillArgs& a, const ListSmem& l, int repeated,
-                                            const Base& b, float inv_z, float w, Get&& get,
-                                            float (&fix)[kPerThread]) {
-#pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    const int i = threadIdx.x + q * kThreads;
-    if (i < a.k && l.id[i] >= 0) {
+__device__ __forceinline__ void list_values(const DistillArgs& a, const List& l, bool repeated,
+                                            const Base& b, float inv_z, float w, Get&& get) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.k; i += kThreads) {
+    const int id = l.id[i];
+    if (id >= 0) {
       float p = l.p[i];
       if (repeated) {
         p = 0.f;
+#pragma unroll 1
         for (int j = 0; j < a.k; ++j)
-          if (l.id[j] == l.id[i]) p += l.p[j];
+          if (l.id[j] == id) p += l.p[j];
       }
-      fix[q] = w * (b(get(l.id[i])) * inv_z - p);
+      l.fix[i] = w * (b(get(id)) * inv_z - p);
     }
   }
 }
 template <class T>
-__device__ __forceinline__ void list_write(const DistillArgs& a, const ListSmem& l, T* g,
-                                           const float (&fix)[kPerThread]) {
-#pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    const int i = threadIdx.x + q * kThreads;
-    if (i < a.k && l.id[i] >= 0) g[l.id[i]] = from_f32<T>(fix[q]);
-  }
+__device__ __forceinline__ void list_write(const DistillArgs& a, const List& l, T* g) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.k; i += kThreads)
+    if (l.id[i] >= 0) g[l.id[i]] = from_f32<T>(l.fix[i]);
 }
 
-// The largest element of a vector; 16-bit types two at a time.
-__device__ __forceinline__ float vec_max(const uint4& r, float*) {
-  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
-               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
-}
+// The sums of a thread's vectors go on in ascending order of their index.
 template <class T>
-__device__ __forceinline__ float vec_max(const uint4& r, T*) {
-  using P = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
-  P w[4];
-  memcpy(w, &r, 16);
-  const P t = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
-  return fmaxf(to_f32(t.x), to_f32(t.y));
+__device__ __forceinline__ void sum_vec(Online& o, const uint4& r, float c) {
+  float v[Span<T>::N];
+  unpack_vec<T>(r, v);
+  o.add(v, vec_max(r, static_cast<T*>(nullptr)), c);
 }
 
-// Maximum and sum over a run of the row. With KEEP the run is also copied to
-// shared memory, with the alignment it has in memory (keep is aligned as s).
-template <class T, bool KEEP>
-__device__ __forceinline__ Online run_stats(const T* s, int len, float c, T* keep) {
+// Maximum and sum over a run of the row.
+template <class T>
+__device__ __forceinline__ Online run_stats(const T* s, int len, float c) {
   constexpr int N = Span<T>::N, U = 4;
   const int mis = misalign(s);
-  const T* from = s;
-  if (KEEP && mis != 0) {
-    const Span<T> sp(s, len);
-    for (int e = threadIdx.x; e < sp.rest(); e += kThreads) keep[sp.at(e)] = s[sp.at(e)];
-    const uint4* src = reinterpret_cast<const uint4*>(s + sp.head);
-    uint4* dst = reinterpret_cast<uint4*>(keep + sp.head);
-    for (int i = threadIdx.x; i < sp.nvec; i += U * kThreads) {
-      uint4 r[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * kThreads < sp.nvec) r[u] = src[i + u * kThreads];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + u * kThreads < sp.nvec) dst[i + u * kThreads] = r[u];
-    }
-    __syncthreads();
-    from = keep;
-  }
   Online o;
-  auto sum = [&](const uint4& r, int i) {
-    if (KEEP && mis == 0) reinterpret_cast<uint4*>(keep)[i] = r;
-    float v[N];
-    unpack_vec<T>(r, v);
-    o.add(v, vec_max(r, static_cast<T*>(nullptr)), c);
-  };
-  // a thread's vectors in ascending order: U inner ones at a time, the others
-  // one by one
+  // U inner vectors at a time, the others one by one
   const int nvec = (len + N - 1) / N, last = inner_last<T>(len, mis);
   int i = threadIdx.x;
   if (mis != 0 && i < nvec) {
-    sum(load_vec(from, len, i, mis), i);
+    sum_vec<T>(o, load_vec(s, len, i, mis), c);
     i += kThreads;
   }
   for (; i + (U - 1) * kThreads <= last; i += U * kThreads) {
     uint4 r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = load_inner(from, i + u * kThreads, mis);
+    for (int u = 0; u < U; ++u) r[u] = load_inner(s, i + u * kThreads, mis);
 #pragma unroll
-    for (int u = 0; u < U; ++u) sum(r[u], i + u * kThreads);
+    for (int u = 0; u < U; ++u) sum_vec<T>(o, r[u], c);
   }
 #pragma unroll 1
-  for (; i < nvec; i += kThreads) sum(load_vec(from, len, i, mis), i);
+  for (; i < nvec; i += kThreads) sum_vec<T>(o, load_vec(s, len, i, mis), c);
+  return o;
+}
+
+// The same, with the run copied to shared memory, where it keeps the alignment
+// it has in memory (keep is aligned as s). All copies are started at once, in
+// four groups, so that a block's whole run is on its way from memory while the
+// blocks beside it compute.
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+template <class T, class F>
+__device__ __forceinline__ Online run_stats_keep(const T* s, int len, float c, T* keep,
+                                                 F&& meanwhile) {
+  constexpr int N = Span<T>::N, G = 4;
+  const int mis = misalign(s);
+  const Span<T> sp(s, len);
+  const uint4* src = reinterpret_cast<const uint4*>(s + sp.head);
+  uint4* dst = reinterpret_cast<uint4*>(keep + sp.head);
+  const int per = (sp.nvec + G * kThreads - 1) / (G * kThreads);  // vectors of a thread and group
+  const uint32_t to = smem_u32(dst);
+#pragma unroll 1
+  for (int g = 0; g < G; ++g) {
+    for (int v = 0; v < per; ++v) {
+      const int i = threadIdx.x + (g * per + v) * kThreads;
+      if (i < sp.nvec)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u * uint32_t(i)),
+                     "l"(src + i)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  for (int e = threadIdx.x; e < sp.rest(); e += kThreads) keep[sp.at(e)] = s[sp.at(e)];
+  meanwhile();
+  Online o;
+  if (mis == 0) {
+    // a thread's own copies, group by group
+    auto group = [&](int g) {
+      for (int v = 0; v < per; ++v) {
+        const int i = threadIdx.x + (g * per + v) * kThreads;
+        if (i < sp.nvec) sum_vec<T>(o, dst[i], c);
+      }
+    };
+    copies_wait<3>();
+    group(0);
+    copies_wait<2>();
+    group(1);
+    copies_wait<1>();
+    group(2);
+    copies_wait<0>();
+    group(3);
+    if (len > sp.nvec * N && sp.nvec % kThreads == int(threadIdx.x))
+      sum_vec<T>(o, load_edge(s, len, sp.nvec), c);
+  } else {
+    copies_wait<0>();
+    __syncthreads();
+    o = run_stats<T>(keep, len, c);
+  }
   return o;
 }
 
@@ -351,38 +357,72 @@ __device__ __forceinline__ void run_zero(T* g, int len) {
     reinterpret_cast<uint4*>(g + sp.head)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// The cluster's blocks each hold (x, y) in *mine; returns all of them joined
-// with f in rank order. A second barrier later keeps *mine alive for readers.
-template <class F>
-__device__ __forceinline__ void cluster_each(float2 v, float2* mine, int nranks, F&& f) {
-  if (threadIdx.x == 0) *mine = v;
-  if (nranks == 1) {
-    f(v);
-    return;
+// A block's part of a row's statistics and loss, and their join over the
+// cluster in rank order. The parts' owners stay until all have read them
+// (cluster_leave); what is in between overlaps with the others' reading.
+struct RowPart {
+  float m, z;
+  LossPart l;
+};
+struct RowSum {
+  Online all;
+  float x = 0.f, y = 0.f;  // sum p (log p + log Z), sum p (s - m)
+};
+__device__ __forceinline__ RowSum row_join(const RowPart& v, RowPart* mine, int nranks, float c) {
+  RowSum s;
+  if (nranks > 1) {
+    if (threadIdx.x == 0) *mine = v;
+    cluster_sync();
   }
-  cluster_sync();
   const uint32_t at = smem_u32(mine);
-  for (int r = 0; r < nranks; ++r) f(make_float2(ld_cluster(at, r), ld_cluster(at + 4, r)));
+  auto part = [&](int r) {
+    if (nranks == 1) return v;
+    RowPart q;
+    q.m = ld_cluster(at, r);
+    q.z = ld_cluster(at + 4, r);
+    q.l.a = ld_cluster(at + 8, r);
+    q.l.p = ld_cluster(at + 12, r);
+    q.l.y = ld_cluster(at + 16, r);
+    return q;
+  };
+#pragma unroll 1
+  for (int r = 0; r < nranks; ++r) {
+    const RowPart q = part(r);
+    s.all.join(q.m, q.z, c);
+  }
+  const float logz = s.all.z == 0.f ? 0.f : logf(s.all.z);
+#pragma unroll 1
+  for (int r = 0; r < nranks; ++r) {
+    const RowPart q = part(r);
+    s.x += q.l.a + logz * q.l.p;
+    s.y += q.l.y;
+    // the part's differences are from its own maximum
+    if (!(q.l.p == 0.f) && q.m != s.all.m) s.y += (q.m - s.all.m) * q.l.p;
+  }
+  if (nranks > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  return s;
 }
-
-// Loss over the entries in [c0, c0 + len): tau^2 sum p (log p + log Z) - tau
-// sum p (s - m). No s - m is divided by tau, so that a listed score of the
-// type's lowest value stays finite.
-template <class Get>
-__device__ __forceinline__ float2 list_loss(const DistillArgs& a, const Teacher& t, float c, int c0,
-                                            int len, float m, float logz, Get&& get) {
-  float2 l = make_float2(0.f, 0.f);
-  const float inv_tz = 1.f / t.all.z, logtz = logf(t.all.z);
+__device__ __forceinline__ void cluster_leave(int nranks) {
+  if (nranks > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// Sums over the block, in a fixed order.
+__device__ __forceinline__ LossPart block_loss(LossPart l, float4* sh) {
 #pragma unroll
-  for (int q = 0; q < kPerThread; ++q) {
-    const int id = t.id[q] - c0;
-    if (t.id[q] >= c0 && id < len) {
-      const float p = t.p(q, c, inv_tz), s = get(id);
-      if (!(p <= 0.f)) {  // also a NaN
-        l.x += p * ((t.v[q] - t.all.m) * a.inv_tau - logtz + logz);
-        l.y += p * (s == -INFINITY ? s : s - m);
-      }
-    }
+  for (int o = 16; o; o /= 2) {
+    l.a += __shfl_xor_sync(kFullMask, l.a, o);
+    l.p += __shfl_xor_sync(kFullMask, l.p, o);
+    l.y += __shfl_xor_sync(kFullMask, l.y, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float4(l.a, l.p, l.y, 0.f);
+  __syncthreads();
+  l = LossPart{};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const float4 v = sh[i];
+    l.a += v.x;
+    l.p += v.y;
+    l.y += v.z;
   }
   return l;
 }
@@ -390,8 +430,9 @@ __device__ __forceinline__ float2 list_loss(const DistillArgs& a, const Teacher&
 // Loss and statistics: a cluster of blocks per row, a run of columns each.
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const DistillArgs a) {
-  __shared__ float2 sh[2 * kWarps];
-  __shared__ float2 part[2];
+  extern __shared__ __align__(16) uint8_t distill_smem[];
+  __shared__ float4 sh[kWarps];
+  __shared__ RowPart part;
   const int nranks = int(gridDim.x), rank = int(blockIdx.x);  // the cluster is a row of the grid
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   if (row >= a.rows) return;  // whole clusters
@@ -399,35 +440,27 @@ __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const Dist
   const int len = int(min(int64_t(a.chunk), a.cols - c0));
   const T* s = static_cast<const T*>(a.scores) + row * a.lds + c0;
   const float c = a.inv_tau * kLog2e;
-  Teacher t;
-  load_teacher(a, row, t);
-  Online o = run_stats<T, false>(s, len, c, nullptr);
-  teacher_stats(t, c);
-  block_join(o, t.all, c, sh);
-  Online all;
-  cluster_each(make_float2(o.m, o.z), &part[0], nranks,
-               [&](float2 v) { all.join(v.x, v.y, c); });
-  const float logz = all.z == 0.f ? 0.f : logf(all.z);
-  float2 l = list_loss(a, t, c, c0, len, all.m, logz, [&](int i) { return to_f32(s[i]); });
-  l = block_sum2(l, sh);
-  float2 sum = make_float2(0.f, 0.f);
-  cluster_each(l, &part[1], nranks, [&](float2 v) {
-    sum.x += v.x;
-    sum.y += v.y;
-  });
+  const List l(distill_smem, a.k);
+  Online t = list_load(a, row, l, c);
+  Online o = run_stats<T>(s, len, c);
+  block_join(o, t, c, reinterpret_cast<float2*>(sh));
+  const LossPart mine = block_loss(
+      list_weights<false>(a, l, t, c, c0, len, o.m, nullptr, [&](int i) { return to_f32(s[i]); }),
+      sh);
+  const RowSum r = row_join(RowPart{o.m, o.z, mine}, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0) {
-    a.loss[row] = t.any() ? a.tau * (a.tau * sum.x - sum.y) : 0.f;
-    a.stats[2 * row] = all.m;
-    a.stats[2 * row + 1] = all.z;
+    a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
+    a.stats[2 * row] = r.all.m;
+    a.stats[2 * row + 1] = r.all.z;
   }
-  if (nranks > 1) cluster_sync();
+  cluster_leave(nranks);
 }
 
 // Gradient from the forward's statistics: a block per run of columns.
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];
-  __shared__ float2 sh[2 * kWarps];
+  __shared__ float4 sh[kWarps];
   __shared__ int repeated;
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   if (row >= a.rows) return;
@@ -438,28 +471,25 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
   const float w = a.row_grad[row] * a.tau;
   if (w == 0.f) return run_zero(g, len);  // a row that does not count, whatever it holds
   const float c = a.inv_tau * kLog2e;
-  Teacher t;
-  load_teacher(a, row, t);
-  teacher_stats(t, c);
-  Online none;
-  block_join(none, t.all, c, sh);
-  ListSmem l;
-  l.id = reinterpret_cast<int*>(distill_smem);
-  l.p = reinterpret_cast<float*>(l.id + a.k);
-  l.seen = reinterpret_cast<uint32_t*>(l.p + a.k);
-  list_to_smem(a, t, c, c0, len, l, &repeated);
+  const List l(distill_smem, a.k);
+  Online t = list_load(a, row, l, c), none;
+  for (int i = threadIdx.x; i < (len + 31) / 32; i += kThreads) l.seen[i] = 0;
+  if (threadIdx.x == 0) repeated = 0;
+  block_join(none, t, c, reinterpret_cast<float2*>(sh));
   const float m = a.stats[2 * row], z = a.stats[2 * row + 1];
+  auto score = [&](int i) { return to_f32(s[i]); };
+  list_weights<true>(a, l, t, c, c0, len, m, &repeated, score);
+  __syncthreads();
   const Base b(m, c);
   const float inv_z = z == 0.f ? 0.f : 1.f / z;  // no score above -inf: q = 0
-  float fix[kPerThread];
-  list_values(a, l, repeated, b, inv_z, w, [&](int i) { return to_f32(s[i]); }, fix);
+  list_values(a, l, repeated != 0, b, inv_z, w, score);
   __syncthreads();
-  if (t.any())
-    run_grad<T>(s, len, b, w * inv_z, g);
-  else
+  if (t.z == 0.f)
     run_zero(g, len);
+  else
+    run_grad<T>(s, len, b, w * inv_z, g);
   __syncthreads();
-  list_write(a, l, g, fix);
+  list_write(a, l, g);
 }
 
 // Loss and gradient with the row held in the shared memory of a cluster: each
@@ -467,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];
-  __shared__ float2 sh[2 * kWarps];
-  __shared__ float2 part[2];
+  __shared__ float4 sh[kWarps];
+  __shared__ RowPart part;
   __shared__ int repeated;
   const int nranks = int(gridDim.x), rank = int(blockIdx.x);
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
@@ -479,44 +509,33 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
   T* g = static_cast<T*>(a.grad) + row * a.ldg + c0;
   const float c = a.inv_tau * kLog2e;
   T* keep = reinterpret_cast<T*>(distill_smem) + misalign(s) / int(sizeof(T));
-  ListSmem l;
-  l.id = reinterpret_cast<int*>(distill_smem + (size_t(a.chunk) + Span<T>::N) * sizeof(T));
-  l.p = reinterpret_cast<float*>(l.id + a.k);
-  l.seen = reinterpret_cast<uint32_t*>(l.p + a.k);
-
-  Teacher t;
-  load_teacher(a, row, t);
-  Online o = run_stats<T, true>(s, len, c, keep);
-  teacher_stats(t, c);
-  block_join(o, t.all, c, sh);  // its barriers also publish the copy
-  Online all;
-  cluster_each(make_float2(o.m, o.z), &part[0], nranks,
-               [&](float2 v) { all.join(v.x, v.y, c); });
-  auto score = [&](int i) { return to_f32(keep[i]); };
-  const float logz = all.z == 0.f ? 0.f : logf(all.z);
-  const float2 mine = block_sum2(list_loss(a, t, c, c0, len, all.m, logz, score), sh);
-  float2 sum = make_float2(0.f, 0.f);
-  cluster_each(mine, &part[1], nranks, [&](float2 v) {
-    sum.x += v.x;
-    sum.y += v.y;
-  });
-  if (rank == 0 && threadIdx.x == 0)
-    a.loss[row] = t.any() ? a.tau * (a.tau * sum.x - sum.y) : 0.f;
-
+  const List l(distill_smem + (size_t(a.chunk) + Span<T>::N) * sizeof(T), a.k);
   const float w = a.row_grad[row] * a.tau;
-  if (w == 0.f || !t.any()) {
+
+  Online t;
+  Online o = run_stats_keep<T>(s, len, c, keep, [&] {
+    t = list_load(a, row, l, c);
+    for (int i = threadIdx.x; i < (len + 31) / 32; i += kThreads) l.seen[i] = 0;
+    if (threadIdx.x == 0) repeated = 0;
+  });
+  block_join(o, t, c, reinterpret_cast<float2*>(sh));  // its barriers also publish the copy
+  auto score = [&](int i) { return to_f32(keep[i]); };
+  const LossPart mine =
+      block_loss(list_weights<true>(a, l, t, c, c0, len, o.m, &repeated, score), sh);
+  const RowSum r = row_join(RowPart{o.m, o.z, mine}, &part, nranks, c);
+  if (rank == 0 && threadIdx.x == 0)
+    a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
+  if (w == 0.f || t.z == 0.f) {
     run_zero(g, len);
   } else {
-    const Base b(all.m, c);
-    const float inv_z = all.z == 0.f ? 0.f : 1.f / all.z;
-    list_to_smem(a, t, c, c0, len, l, &repeated);
-    float fix[kPerThread];
-    list_values(a, l, repeated, b, inv_z, w, score, fix);
+    const Base b(r.all.m, c);
+    const float inv_z = r.all.z == 0.f ? 0.f : 1.f / r.all.z;
+    list_values(a, l, repeated != 0, b, inv_z, w, score);
     run_grad<T>(keep, len, b, w * inv_z, g);
     __syncthreads();
-    list_write(a, l, g, fix);
+    list_write(a, l, g);
   }
-  if (nranks > 1) cluster_sync();
+  cluster_leave(nranks);
 }
 
 int check_distill(const char* fn, int dtype, int64_t rows, int64_t cols, int64_t lds, int k,
@@ -591,7 +610,7 @@ int launch_forward(DistillArgs a, int dtype, cudaStream_t s) {
     using T = std::remove_pointer_t<decltype(t)>;
     const int ranks = ranks_for(a.rows, a.cols, 1);
     a.chunk = chunk_of(a.cols, ranks);
-    return launch_cluster(distill_forward_kernel<T>, a, ranks, 0, s);
+    return launch_cluster(distill_forward_kernel<T>, a, ranks, list_bytes(a.k, 0), s);
   });
 }
 int launch_backward(DistillArgs a, int dtype, cudaStream_t s) {
@@ -603,7 +622,7 @@ int launch_backward(DistillArgs a, int dtype, cudaStream_t s) {
     while (a.rows * per_row < 4 * num_sms() && a.cols > 4096 * per_row) per_row *= 2;
     a.chunk = chunk_of(a.cols, int(per_row));
     per_row = ceil_div(a.cols, a.chunk);
-    const size_t smem = size_t(a.k) * 8 + size_t(ceil_div(a.chunk, 32)) * 4;
+    const size_t smem = list_bytes(a.k, a.chunk);
     distill_backward_kernel<T><<<grid_of(per_row, a.rows), kThreads, smem, s>>>(a);
     IVFPQ_LAUNCHED();
     return IVFPQ_OK;
@@ -614,7 +633,7 @@ bool fits_cluster(const DistillArgs& a, int dtype, int* ranks, size_t* smem) {
   const int size = dtype_size(dtype);
   auto bytes = [&](int r) {
     const int64_t ch = chunk_of(a.cols, r);
-    return size_t(ch + 16 / size) * size + size_t(a.k) * 8 + size_t(ceil_div(ch, 32)) * 4;
+    return size_t(ch + 16 / size) * size + list_bytes(a.k, ch);
   };
   // three blocks share an SM's shared memory, so that one loads while another
   // computes or stores; two or one where a row is too long for that
