@@ -196,4 +196,29 @@ __device__ __forceinline__ float vec_max(const uint4& r, T*) {
   return fmaxf(to_f32(t.x), to_f32(t.y));
 }
 
+// Element j of a vector, j not known at compile time.
+template <class T>
+__device__ __forceinline__ float vec_element(const uint4& r, int j) {
+  const int w = sizeof(T) == 4 ? j : j >> 1;
+  const uint32_t x = w < 2 ? (w == 0 ? r.x : r.y) : (w == 2 ? r.z : r.w);
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(x);
+  } else {
+    float lo, hi;
+    unpack16<T>(x, lo, hi);
+    return j & 1 ? hi : lo;
+  }
+}
+
+// Starts bringing bytes [from, from + bytes) of the run [p, end) into L2; one
+// thread of a block asks for what the block reads a few steps later.
+__device__ __forceinline__ void prefetch_run(const void* p, int64_t from, int64_t bytes,
+                                             const void* end) {
+  const uintptr_t e = reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15);
+  const uintptr_t b = (reinterpret_cast<uintptr_t>(p) + from + 15) & ~uintptr_t(15);
+  if (b >= e) return;
+  const uint32_t n = uint32_t(bytes < int64_t(e - b) ? uintptr_t(bytes) : e - b);
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(b), "r"(n) : "memory");
+}
+
 }  // namespace ivfpq

@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t bits_at(const W* words, int b, int last) {
 }
 
 template <class T, class O, bool HIST, bool BIAS, bool MASK, bool SHORT>
-__global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustArgs a) {
   extern __shared__ __align__(16) uint32_t adjust_smem[];
   constexpr bool MARK = HIST || BIAS;
   uint32_t* mark = adjust_smem;  // a bit per column of the run
@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
         for (int v = 0; v < V; ++v) t[v] = i0 + v * kThreads < n ? __ldg(h + i0 + v * kThreads) : -1;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int64_t c = int64_t(t[v]) - c0;
-          if (t[v] >= 0 && c >= 0 && c < len) {
+          // out of the run (or of the row, or negative): past len
+          const uint32_t c = uint32_t(t[v]) - uint32_t(c0);
+          if (c < uint32_t(len)) {
             atomicOr(&mark[c >> 5], 1u << (c & 31));
             if (i0 + v * kThreads < np)
               atomicOr(&count[c], kPrompt);
@@ -197,20 +198,21 @@ __global__ void __launch_bounds__(kThreads) score_adjust_kernel(const AdjustArgs
       if (i >= nvec) continue;
       float v[N];
       unpack_vec<T>(r[u], v);
-      if constexpr (MARK) {
-        const uint32_t m = bits_at(mark, head + i * N, words - 1) & ((1u << N) - 1);
-        if (m) {
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if ((m >> j) & 1u) v[j] = marked(head + i * N + j, v[j]);
-        }
-      }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[j] *= f;
         if (MASK && !((ok[u] >> j) & 1u)) v[j] = -INFINITY * a.sign;
       }
       store_vec<O>(dst + head + i * N, v);
+      if constexpr (MARK) {
+        // the few marked columns again, one by one, from the loaded scores
+        uint32_t m = bits_at(mark, head + i * N, words - 1) & ok[u] & ((1u << N) - 1);
+        while (m) {
+          const int j = __ffs(m) - 1, c = head + i * N + j;
+          m &= m - 1;
+          dst[c] = from_f32<O>(marked(c, vec_element<T>(r[u], j)) * f);
+        }
+      }
     }
   }
 }

@@ -230,12 +230,15 @@ __device__ __forceinline__ void sum_vec(Online& o, const uint4& r, float c) {
   o.add(v, vec_max(r, static_cast<T*>(nullptr)), c);
 }
 
-// Maximum and sum over a run of the row.
-template <class T>
+// Maximum and sum over a run of the row. AHEAD: the run is in global memory, and
+// is brought into L2 kAhead steps before it is read.
+constexpr int kAhead = 3;
+template <class T, bool AHEAD>
 __device__ __forceinline__ Online run_stats(const T* s, int len, float c) {
   constexpr int N = Span<T>::N, U = 4;
   const int mis = misalign(s);
   Online o;
+  if (AHEAD && threadIdx.x == 0) prefetch_run(s, 0, kAhead * U * kThreads * 16, s + len);
   // U inner vectors at a time, the others one by one
   const int nvec = (len + N - 1) / N, last = inner_last<T>(len, mis);
   int i = threadIdx.x;
@@ -245,6 +248,8 @@ __device__ __forceinline__ Online run_stats(const T* s, int len, float c) {
   }
   for (; i + (U - 1) * kThreads <= last; i += U * kThreads) {
     uint4 r[U];
+    if (AHEAD && threadIdx.x == 0)
+      prefetch_run(s, (i + kAhead * U * kThreads) * 16, U * kThreads * 16, s + len);
 #pragma unroll
     for (int u = 0; u < U; ++u) r[u] = load_inner(s, i + u * kThreads, mis);
 #pragma unroll
@@ -308,14 +313,14 @@ __device__ __forceinline__ Online run_stats_keep(const T* s, int len, float c, T
   } else {
     copies_wait<0>();
     __syncthreads();
-    o = run_stats<T>(keep, len, c);
+    o = run_stats<T, false>(keep, len, c);
   }
   return o;
 }
 
 // g = r exp(...) over a run, from global or shared scores, by the 16-byte
 // vectors of g.
-template <class T>
+template <class T, bool AHEAD>
 __device__ __forceinline__ void run_grad(const T* s, int len, const Base& b, float r, T* g) {
   constexpr int N = Span<T>::N;
   const Span<T> sp(g, len);
@@ -341,6 +346,8 @@ __device__ __forceinline__ void run_grad(const T* s, int len, const Base& b, flo
   }
   for (; i + (U - 1) * kThreads <= last; i += U * kThreads) {
     uint4 x[U];
+    if (AHEAD && threadIdx.x == 0)
+      prefetch_run(src, (i + kAhead * U * kThreads) * 16, U * kThreads * 16, s + len);
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u] = load_inner(src, i + u * kThreads, mis);
 #pragma unroll
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const Dist
   const float c = a.inv_tau * kLog2e;
   const List l(distill_smem, a.k);
   Online t = list_load(a, row, l, c);
-  Online o = run_stats<T>(s, len, c);
+  Online o = run_stats<T, true>(s, len, c);
   block_join(o, t, c, reinterpret_cast<float2*>(sh));
   const LossPart mine = block_loss(
       list_weights<false>(a, l, t, c, c0, len, o.m, nullptr, [&](int i) { return to_f32(s[i]); }),
@@ -470,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
   T* g = static_cast<T*>(a.grad) + row * a.ldg + c0;
   const float w = a.row_grad[row] * a.tau;
   if (w == 0.f) return run_zero(g, len);  // a row that does not count, whatever it holds
+  if (threadIdx.x == 0) prefetch_run(s, 0, kAhead * 4 * kThreads * 16, s + len);
   const float c = a.inv_tau * kLog2e;
   const List l(distill_smem, a.k);
   Online t = list_load(a, row, l, c), none;
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
   if (t.z == 0.f)
     run_zero(g, len);
   else
-    run_grad<T>(s, len, b, w * inv_z, g);
+    run_grad<T, true>(s, len, b, w * inv_z, g);
   __syncthreads();
   list_write(a, l, g);
 }
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     const Base b(r.all.m, c);
     const float inv_z = r.all.z == 0.f ? 0.f : 1.f / r.all.z;
     list_values(a, l, repeated != 0, b, inv_z, w, score);
-    run_grad<T>(keep, len, b, w * inv_z, g);
+    run_grad<T, false>(keep, len, b, w * inv_z, g);
     __syncthreads();
     list_write(a, l, g);
   }
