@@ -21,9 +21,6 @@
 
 namespace ivfpq {
 
-// One 16-column group per thread in the conversion kernels.
-constexpr int kFp4Group = 16;
-
 inline int64_t fp4_padded_cols(int64_t cols) { return ceil_div(cols, 32) * 32; }
 inline int fp4_block(int fmt) { return fmt == IVFPQ_MXFP4 ? 32 : 16; }
 // 4-block scale tiles along the columns

@@ -23,6 +23,7 @@ struct ProdArgs {
   int kp;       // padded K
   int ntile;    // scale tiles along K
   int dtype;
+  int overlap;  // launched to start while the kernel that writes a runs
   int* err;
 };
 

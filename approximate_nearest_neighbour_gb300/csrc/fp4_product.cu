@@ -128,23 +128,35 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   };
 
   if (warp == 0 && lane == 0) {
-    // ---- TMA producer ----
+    // ---- TMA producer. The first stages' rows of b are asked for before the
+    // kernel that writes a has ended (overlapping launch) ----
     const uint8_t* sb = p.b_scales + int64_t(blockIdx.x) * p.ntile * 512;
     const uint8_t* sa = p.a_scales + int64_t(m0 >> 7) * p.ntile * 512;
-    int it = 0;
-    for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc, ++it) {
+    auto sf_bytes = [&](int kc) {
+      return uint32_t(min(C::kTilesPerStage, p.ntile - kc * C::kTilesPerStage)) * 512;
+    };
+    auto load_b = [&](int kc, int s) {
+      mbar_expect_tx(bar_full(s), C::kB + C::kA + 2 * sf_bytes(kc));
+      tma_load_2d(s_b(s), &map_b, kc * KB, n0, bar_full(s));
+      bulk_load(s_sfb(s), sb + int64_t(kc) * C::kTilesPerStage * 512, sf_bytes(kc), bar_full(s));
+    };
+    auto load_a = [&](int kc, int s) {
+      tma_load_2d(s_a(s), &map_a, kc * KB, m0, bar_full(s));
+      bulk_load(s_sfa(s), sa + int64_t(kc) * C::kTilesPerStage * 512, sf_bytes(kc), bar_full(s));
+    };
+    const int early = min(C::kStages, k_hi - k_lo);
+    for (int j = 0; j < early; ++j) load_b(k_lo + j, j);
+    grid_wait();
+    for (int j = 0; j < early; ++j) load_a(k_lo + j, j);
+    int it = early;
+    for (int kc = k_lo + early; kc < k_hi && !*abort_flag; ++kc, ++it) {
       const int s = it % C::kStages;
       if (!mbar_wait(bar_empty(s), ((it / C::kStages) & 1) ^ 1)) {
         fail();
         break;
       }
-      const int t0 = kc * C::kTilesPerStage;
-      const uint32_t sf_bytes = uint32_t(min(C::kTilesPerStage, p.ntile - t0)) * 512;
-      mbar_expect_tx(bar_full(s), C::kB + C::kA + 2 * sf_bytes);
-      tma_load_2d(s_b(s), &map_b, kc * KB, n0, bar_full(s));
-      tma_load_2d(s_a(s), &map_a, kc * KB, m0, bar_full(s));
-      bulk_load(s_sfb(s), sb + int64_t(t0) * 512, sf_bytes, bar_full(s));
-      bulk_load(s_sfa(s), sa + int64_t(t0) * 512, sf_bytes, bar_full(s));
+      load_b(kc, s);
+      load_a(kc, s);
     }
     // copies still in flight land before the CTA ends
     for (int j = max(0, it - C::kStages); j < it; ++j)
@@ -199,6 +211,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   __syncthreads();
   tc_fence_after();
 
+  grid_wait();
   const float alpha = (p.a_ts ? __ldg(p.a_ts) : 1.f) * (p.b_ts ? __ldg(p.b_ts) : 1.f);
   const bool ok = !*abort_flag;
   // ---- epilogue: warp w of 2..5 reads TMEM lanes 32 * (w % 4) .. +32 ----
@@ -220,7 +233,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
     }
   } else {
     // partial sums to this CTA's shared memory ([T][128]; every stage has been
-    // consumed), then each rank joins its share of the rows
+    // consumed), then each rank joins its share, four columns of a row at a
+    // time, in rank order
     float* part = reinterpret_cast<float*>(gbase);
     if (warp >= 2) {
       const int lg = warp & 3;
@@ -235,12 +249,29 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
     }
     cluster_sync();
     const int rank = int(cluster_rank());
-    const int rows = int(min(int64_t(T), p.m - m0));
-    for (int i = rank * kThreads + threadIdx.x; i < rows * BN; i += nslice * kThreads) {
-      float sum = 0.f;
-      for (int r = 0; r < nslice; ++r) sum += ld_cluster(base + 4u * uint32_t(i), uint32_t(r));
-      const int64_t col = n0 + i % BN;
-      if (col < p.n && ok) store_out(p.out, (m0 + i / BN) * p.ldo + col, p.dtype, sum * alpha);
+    const int quads = int(min(int64_t(T), p.m - m0)) * (BN / 4);
+    for (int i = rank * kThreads + threadIdx.x; i < quads; i += nslice * kThreads) {
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < nslice) v[r] = ld_cluster4(map_rank(base + 16u * uint32_t(i), uint32_t(r)));
+      float4 t = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {
+        if (r < nslice) {
+          t.x += v[r].x;
+          t.y += v[r].y;
+          t.z += v[r].z;
+          t.w += v[r].w;
+        }
+      }
+      const int64_t col = n0 + 4 * (i % (BN / 4)), at = (m0 + i / (BN / 4)) * p.ldo + col;
+      if (ok) {
+        if (col < p.n) store_out(p.out, at, p.dtype, t.x * alpha);
+        if (col + 1 < p.n) store_out(p.out, at + 1, p.dtype, t.y * alpha);
+        if (col + 2 < p.n) store_out(p.out, at + 2, p.dtype, t.z * alpha);
+        if (col + 3 < p.n) store_out(p.out, at + 3, p.dtype, t.w * alpha);
+      }
     }
     cluster_sync();
   }
@@ -273,13 +304,15 @@ int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kTotal;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 1;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = unsigned(slices);
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.overlap ? 2 : 1;
   IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, mb, ma, p));
   IVFPQ_LAUNCHED_K(kern, C::kTotal, kThreads);
   return IVFPQ_OK;
@@ -297,8 +330,9 @@ int launch_fmt(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream
 
 int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
                    const uint8_t* b_scales, int64_t n, int64_t cols, int fmt, const float* a_ts,
-                   const float* b_ts, void* out, int dtype, cudaStream_t s) {
+                   const float* b_ts, void* out, int dtype, bool overlap, cudaStream_t s) {
   ProdArgs p{};
+  p.overlap = overlap;
   p.a_scales = a_scales;
   p.b_scales = b_scales;
   p.a_ts = fmt == IVFPQ_NVFP4 ? a_ts : nullptr;
@@ -349,7 +383,7 @@ extern "C" int fp4_product(const uint8_t* a_codes, const uint8_t* a_scales, int6
                     aligned16(b_scales),
                 "fp4_product: codes and scales must be 16-byte aligned");
   return product_device(a_codes, a_scales, m, b_codes, b_scales, n, cols, fmt, a_tensor_scale,
-                        b_tensor_scale, out, dtype, static_cast<cudaStream_t>(stream));
+                        b_tensor_scale, out, dtype, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ldx,
@@ -374,5 +408,5 @@ extern "C" int fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ldx,
   uint8_t* scales = codes + ceil_div(code_bytes, 512) * 512;
   IVFPQ_TRY(fp4_quantize_device(x, x_dtype, m, cols, ldx, fmt, x_tensor_scale, codes, scales, s));
   return product_device(codes, scales, m, w_codes, w_scales, n, cols, fmt, x_tensor_scale,
-                        w_tensor_scale, out, dtype, s);
+                        w_tensor_scale, out, dtype, true, s);
 }

@@ -66,11 +66,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(el)
         : "memory");
 }
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
@@ -233,8 +228,13 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
     // ---- loads: the whole warp runs, one lane issues ----
     const uint32_t el = elect_one();
     uint32_t s = 0, phase = 1;
+    // one row tile and stages that meet the same K step each time: a's rows stay
+    // in the stages after the first turn. Rows are what short K costs (about 6
+    // clocks each, however few bytes).
+    const bool keep_a = tl.tm == 1 && NS % nk == 0;
     int used = 0;
     bool ok = true;
+    grid_wait();
     for (int t = group; t < ntiles && ok && !*abort_flag; t += ngroups) {
       const int n0 = col0(t), m0 = row0(t);
       const int sb = n0 / BN * p.ntile, sa = m0 / 128 * p.ntile;
@@ -244,16 +244,20 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
           ok = false;
           break;
         }
-        if (rank == 0 && el) mbar_expect_tx(bar_full(s), CG * C::kStage);
+        const bool have = keep_a && used == NS;
+        const uint32_t bytes = have ? C::kB + C::kSfTile : C::kStage;
+        if (rank == 0 && el) mbar_expect_tx(bar_full(s), CG * bytes);
         const uint32_t bar = CG == 2 ? map_rank(bar_full(s), 0) : bar_full(s);
-        tma_load<CG>(s_b(s), &map_b, kc * KB, n0, bar, el);
-        tma_load<CG>(s_a(s), &map_a, kc * KB, m0 + rank * (T / CG), bar, el);
         // scale tiles past the row's (or the matrix's) end are read and not used
+        tma_load<CG>(s_b(s), &map_b, kc * KB, n0, bar, el);
         tma_load<CG>(s_sf(s), &map_sb, 0, sb + kc * C::kTiles, bar, el);
+        if (!have) {
+          tma_load<CG>(s_a(s), &map_a, kc * KB, m0 + rank * (T / CG), bar, el);
 #pragma unroll
-        for (int r = 0; r < C::kRt; ++r)
-          tma_load<CG>(s_sf(s) + (1 + r) * C::kSfTile, &map_sa, 0,
-                           sa + r * p.ntile + kc * C::kTiles, bar, el);
+          for (int r = 0; r < C::kRt; ++r)
+            tma_load<CG>(s_sf(s) + (1 + r) * C::kSfTile, &map_sa, 0,
+                         sa + r * p.ntile + kc * C::kTiles, bar, el);
+        }
         used = min(used + 1, NS);
         if (++s == NS) {
           s = 0;
@@ -344,6 +348,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
   } else if (warp >= 2) {
     // ---- store: warp w reads TMEM lanes 32 * (w % 4) .. +32 ----
     const int lg = warp & 3, half = (warp - 2) >> 2;
+    grid_wait();
     const float alpha = (p.a_ts ? __ldg(p.a_ts) : 1.f) * (p.b_ts ? __ldg(p.b_ts) : 1.f);
     constexpr int kCrit = T == 256 ? 96 : 0;  // columns the next accumulator shares
     constexpr int C1 = kCrit / 2, C2 = (T - kCrit) / 2;
@@ -447,11 +452,13 @@ int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kTotal;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = CG;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   static int resident = 0;  // groups that fit the device at once
@@ -462,6 +469,7 @@ int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   }
   const int64_t tiles = int64_t(tl.tn) * tl.tm;
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, resident)) * CG);
+  cfg.numAttrs = p.overlap ? 2 : 1;
   IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, mb, ma, msb, msa, p, tl));
   IVFPQ_LAUNCHED_K(kern, C::kTotal, kThreads);
   return IVFPQ_OK;

@@ -85,12 +85,24 @@ __device__ __forceinline__ void unpack_vec(const uint4& r, float (&v)[Span<T>::N
     unpack16<T>(r.w, v[6], v[7]);
   }
 }
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __nv_bfloat16*) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, __half*) {
+  const __half2 t = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
 template <class T>
 __device__ __forceinline__ uint4 pack_vec(const float (&v)[Span<T>::N]) {
-  T t[Span<T>::N];
-#pragma unroll
-  for (int i = 0; i < Span<T>::N; ++i) t[i] = from_f32<T>(v[i]);
-  return *reinterpret_cast<const uint4*>(t);
+  if constexpr (sizeof(T) == 4) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  } else {
+    T* t = nullptr;
+    return make_uint4(pack16(v[0], v[1], t), pack16(v[2], v[3], t), pack16(v[4], v[5], t),
+                      pack16(v[6], v[7], t));
+  }
 }
 // M values as whole 16-byte vectors of O at p (16-byte aligned).
 template <class O, int M>

@@ -93,34 +93,43 @@ struct Online {
     unpair(a, x, y);
     z += x + y;
   }
-  __device__ __forceinline__ void join(float m2, float z2, float c) {
-    const float t = fmaxf(m, m2);
-    const float f1 = m == t ? 1.f : exp2_fast((m - t) * c);
-    const float f2 = m2 == t ? 1.f : exp2_fast((m2 - t) * c);
-    z = z * f1 + z2 * f2;
-    m = t;
-  }
 };
 
 // Joins of running maxima and sums over the block, in a fixed order.
-// The row's and the list's statistics in one step.
-__device__ __forceinline__ void block_join(Online& o, Online& l, float c, float2* sh) {
+// What a sum relative to the maximum m is, relative to the larger t.
+__device__ __forceinline__ float rescaled(float m, float z, float t, float c) {
+  return m == t ? z : z * exp2_fast((m - t) * c);
+}
+// The row's and the list's statistics in one step: maxima first, so that each
+// sum is rescaled once and the exponentials do not wait for each other.
+__device__ __forceinline__ void block_join(Online& o, Online& l, float c, float4* sh) {
+  float mo = o.m, ml = l.m;
 #pragma unroll
   for (int d = 16; d; d /= 2) {
-    o.join(__shfl_xor_sync(kFullMask, o.m, d), __shfl_xor_sync(kFullMask, o.z, d), c);
-    l.join(__shfl_xor_sync(kFullMask, l.m, d), __shfl_xor_sync(kFullMask, l.z, d), c);
+    mo = fmaxf(mo, __shfl_xor_sync(kFullMask, mo, d));
+    ml = fmaxf(ml, __shfl_xor_sync(kFullMask, ml, d));
+  }
+  float zo = rescaled(o.m, o.z, mo, c), zl = rescaled(l.m, l.z, ml, c);
+#pragma unroll
+  for (int d = 16; d; d /= 2) {
+    zo += __shfl_xor_sync(kFullMask, zo, d);
+    zl += __shfl_xor_sync(kFullMask, zl, d);
   }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    sh[threadIdx.x >> 5] = make_float2(o.m, o.z);
-    sh[kWarps + (threadIdx.x >> 5)] = make_float2(l.m, l.z);
-  }
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float4(mo, zo, ml, zl);
   __syncthreads();
+  float4 v[kWarps];
   o = l = Online{};
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
-    o.join(sh[i].x, sh[i].y, c);
-    l.join(sh[kWarps + i].x, sh[kWarps + i].y, c);
+    v[i] = sh[i];
+    o.m = fmaxf(o.m, v[i].x);
+    l.m = fmaxf(l.m, v[i].z);
+  }
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    o.z += rescaled(v[i].x, v[i].y, o.m, c);
+    l.z += rescaled(v[i].z, v[i].w, l.m, c);
   }
 }
 
@@ -336,7 +345,7 @@ __device__ __forceinline__ void run_grad(const T* s, int len, const Base& b, flo
     unpack_vec<T>(x, v);
     b.all(v);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] *= r;
+    for (int j = 0; j < N; j += 2) unpair(mul2(pair(v[j], v[j + 1]), pair(r, r)), v[j], v[j + 1]);
     dst[i] = pack_vec<T>(v);
   };
   int i = threadIdx.x;
@@ -367,46 +376,57 @@ __device__ __forceinline__ void run_zero(T* g, int len) {
 // A block's part of a row's statistics and loss, and their join over the
 // cluster in rank order. The parts' owners stay until all have read them
 // (cluster_leave); what is in between overlaps with the others' reading.
-struct RowPart {
+struct __align__(16) RowPart {
   float m, z;
   LossPart l;
+  float pad[3];
 };
 struct RowSum {
   Online all;
   float x = 0.f, y = 0.f;  // sum p (log p + log Z), sum p (s - m)
 };
-__device__ __forceinline__ RowSum row_join(const RowPart& v, RowPart* mine, int nranks, float c) {
+__device__ __forceinline__ RowSum row_join(const Online& o, const LossPart& part, RowPart* mine,
+                                           int nranks, float c) {
   RowSum s;
-  if (nranks > 1) {
-    if (threadIdx.x == 0) *mine = v;
-    cluster_sync();
+  if (nranks == 1) {
+    s.all = o;
+    s.x = part.a + (o.z == 0.f ? 0.f : logf(o.z)) * part.p;
+    s.y = part.y;
+    return s;
   }
-  const uint32_t at = smem_u32(mine);
-  auto part = [&](int r) {
-    if (nranks == 1) return v;
-    RowPart q;
-    q.m = ld_cluster(at, r);
-    q.z = ld_cluster(at + 4, r);
-    q.l.a = ld_cluster(at + 8, r);
-    q.l.p = ld_cluster(at + 12, r);
-    q.l.y = ld_cluster(at + 16, r);
-    return q;
-  };
-#pragma unroll 1
-  for (int r = 0; r < nranks; ++r) {
-    const RowPart q = part(r);
-    s.all.join(q.m, q.z, c);
+  if (threadIdx.x == 0) {
+    mine->m = o.m;
+    mine->z = o.z;
+    mine->l = part;
   }
-  const float logz = s.all.z == 0.f ? 0.f : logf(s.all.z);
-#pragma unroll 1
-  for (int r = 0; r < nranks; ++r) {
-    const RowPart q = part(r);
-    s.x += q.l.a + logz * q.l.p;
-    s.y += q.l.y;
-    // the part's differences are from its own maximum
-    if (!(q.l.p == 0.f) && q.m != s.all.m) s.y += (q.m - s.all.m) * q.l.p;
+  cluster_sync();
+  // lane r reads rank r's part
+  const int lane = threadIdx.x & 31;
+  float4 v = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  float y = 0.f;
+  if (lane < nranks) {
+    const uint32_t at = map_rank(smem_u32(mine), uint32_t(lane));
+    v = ld_cluster4(at);
+    y = ld_cluster4(at + 16).x;
   }
-  if (nranks > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  s.all.m = v.x;
+#pragma unroll
+  for (int d = kMaxCluster / 2; d; d /= 2)
+    s.all.m = fmaxf(s.all.m, __shfl_xor_sync(kFullMask, s.all.m, d));
+  s.all.m = __shfl_sync(kFullMask, s.all.m, 0);
+  const float z = rescaled(v.x, v.y, s.all.m, c);
+  // the part's differences are from its own maximum
+  if (!(v.w == 0.f) && v.x != s.all.m) y += (v.x - s.all.m) * v.w;
+  float p = 0.f;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    s.all.z += __shfl_sync(kFullMask, z, r);
+    s.x += __shfl_sync(kFullMask, v.z, r);
+    p += __shfl_sync(kFullMask, v.w, r);
+    s.y += __shfl_sync(kFullMask, y, r);
+  }
+  s.x += (s.all.z == 0.f ? 0.f : logf(s.all.z)) * p;
   return s;
 }
 __device__ __forceinline__ void cluster_leave(int nranks) {
@@ -450,11 +470,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const Dist
   const List l(distill_smem, a.k);
   Online t = list_load(a, row, l, c);
   Online o = run_stats<T, true>(s, len, c);
-  block_join(o, t, c, reinterpret_cast<float2*>(sh));
+  block_join(o, t, c, sh);
   const LossPart mine = block_loss(
       list_weights<false>(a, l, t, c, c0, len, o.m, nullptr, [&](int i) { return to_f32(s[i]); }),
       sh);
-  const RowSum r = row_join(RowPart{o.m, o.z, mine}, &part, nranks, c);
+  const RowSum r = row_join(o, mine, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0) {
     a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
     a.stats[2 * row] = r.all.m;
@@ -483,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
   Online t = list_load(a, row, l, c), none;
   for (int i = threadIdx.x; i < (len + 31) / 32; i += kThreads) l.seen[i] = 0;
   if (threadIdx.x == 0) repeated = 0;
-  block_join(none, t, c, reinterpret_cast<float2*>(sh));
+  block_join(none, t, c, sh);
   const float m = a.stats[2 * row], z = a.stats[2 * row + 1];
   auto score = [&](int i) { return to_f32(s[i]); };
   list_weights<true>(a, l, t, c, c0, len, m, &repeated, score);
@@ -526,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
     for (int i = threadIdx.x; i < (len + 31) / 32; i += kThreads) l.seen[i] = 0;
     if (threadIdx.x == 0) repeated = 0;
   });
-  block_join(o, t, c, reinterpret_cast<float2*>(sh));  // its barriers also publish the copy
+  block_join(o, t, c, sh);  // its barriers also publish the copy
   auto score = [&](int i) { return to_f32(keep[i]); };
   const LossPart mine =
       block_loss(list_weights<true>(a, l, t, c, c0, len, o.m, &repeated, score), sh);
-  const RowSum r = row_join(RowPart{o.m, o.z, mine}, &part, nranks, c);
+  const RowSum r = row_join(o, mine, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0)
     a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
   if (w == 0.f || t.z == 0.f) {
