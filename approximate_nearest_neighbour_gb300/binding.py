@@ -533,16 +533,24 @@ def kselect_noalloc(vals, k, out_vals, out_idx, stream=None):
 # These calls take a few microseconds on the device for small inputs, so their
 # marshalling stays short: one look-up of the stream, no context managers, and
 # the general checks (_need, _out) only where a cheap test does not settle them.
-_dtypes = None
+class _Late(dict):
+    """torch's names these calls use, looked up once (torch is imported late)."""
+
+    def __missing__(self, key):
+        torch = _torch()
+        self.update(Tensor=torch.Tensor, empty=torch.empty, f32=torch.float32, i32=torch.int32,
+                    i64=torch.int64, u8=torch.uint8, device=torch._C._cuda_getDevice,
+                    stream=torch._C._cuda_getCurrentRawStream,
+                    codes={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        return self[key]
+
+
+_late = _Late()
 
 
 def _dtype_code(t, name):
     """ivfpq_dtype of a torch dtype."""
-    global _dtypes
-    if _dtypes is None:
-        torch = _torch()
-        _dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    code = _dtypes.get(t)
+    code = _late["codes"].get(t)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t}")
     return code
@@ -570,29 +578,16 @@ def _rows(t, name):
     return code, rows, cols, ld
 
 
-def _matrix(t, dtype, rows, cols, name, dev):
-    """Address of a contiguous [rows, cols] matrix of dtype on dev."""
-    if not isinstance(t, _torch().Tensor):
+def _array(t, dtype, shape, name, dev):
+    """Address of a contiguous tensor of the given shape and dtype on device
+    dev (an index)."""
+    if not isinstance(t, _late["Tensor"]):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        _need(t, dtype, name)
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _vector(t, dtype, n, name, dev):
-    """Address of an optional contiguous vector of n entries of dtype on dev."""
-    if t is None:
-        return None
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        _need(t, dtype, name)
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.shape != (n,):
-        raise ValueError(f"{name} must have {n} entries, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, name, len(shape))
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     return t.data_ptr()
 
 
@@ -611,12 +606,11 @@ def _out_rows(t, shape, dtype, name, device):
 
 
 def _current(dev):
-    """Handle of the current stream of a tensor's device, which must be the
-    current device (kernels are launched there)."""
-    C_ = _torch()._C
-    if C_._cuda_getDevice() != dev.index:
-        raise ValueError(f"the tensors are on {dev} and the current device is another")
-    return C_._cuda_getCurrentRawStream(dev.index)
+    """Handle of the current stream of device dev (an index), which must be the
+    current device: kernels are launched there."""
+    if _late["device"]() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev} and the current device is another")
+    return _late["stream"](dev)
 
 
 def _on_stream(fn, stream, args, kwargs):
@@ -646,18 +640,16 @@ def fp4_shapes(rows, cols, fmt="mxfp4"):
 
 def _packed(codes, scales, f, name, cols=None):
     """(rows, columns) of packed rows, with the scales' shape checked against the codes'."""
-    torch = _torch()
-    u8 = torch.uint8
+    u8 = _late["u8"]
     try:
         rows, pitch = codes.shape
         shape = scales.shape
+        ok = (codes.dtype is u8 and scales.dtype is u8 and codes.is_cuda
+              and scales.get_device() == codes.get_device() and codes.is_contiguous()
+              and scales.is_contiguous())
     except (AttributeError, ValueError):
-        _need(codes, u8, f"{name} codes", 2)
-        _need(scales, u8, f"{name} scales", 3)
-        raise
-    if (codes.dtype != u8 or scales.dtype != u8 or not codes.is_cuda
-            or not codes.is_contiguous() or not scales.is_contiguous()
-            or scales.device != codes.device):
+        ok = False
+    if not ok:
         _need(codes, u8, f"{name} codes", 2)
         _need(scales, u8, f"{name} scales", 3)
         raise ValueError(f"{name}: codes and scales on several devices")
@@ -681,19 +673,18 @@ def fp4_quantize(x, fmt="mxfp4", tensor_scale=None, codes=None, scales=None, str
     16 columns beside tensor_scale, fp32 [1] on the device, 1 if not given)."""
     if stream is not None:
         return _on_stream(fp4_quantize, stream, (x, fmt, tensor_scale, codes, scales), {})
-    torch = _torch()
     f = _fp4_format(fmt)
     code, rows, cols, ld = _rows(x, "x")
-    dev = x.device
-    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", dev)
+    dev, at = x.device, x.get_device()
+    g = None if tensor_scale is None else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at)
     cs, ss = fp4_shapes(rows, cols, f)
-    u8 = torch.uint8
-    codes = (torch.empty(cs, dtype=u8, device=dev) if codes is None
+    u8 = _late["u8"]
+    codes = (_late["empty"](cs, dtype=u8, device=dev) if codes is None
              else _out(codes, cs, u8, "codes", dev))
-    scales = (torch.empty(ss, dtype=u8, device=dev) if scales is None
+    scales = (_late["empty"](ss, dtype=u8, device=dev) if scales is None
               else _out(scales, ss, u8, "scales", dev))
     rc = (_lib or lib()).fp4_quantize(x.data_ptr(), code, rows, cols, ld, f, g, codes.data_ptr(),
-                                      scales.data_ptr(), _current(dev))
+                                      scales.data_ptr(), _current(at))
     if rc:
         _check("fp4_quantize", rc)
     return codes, scales
@@ -706,18 +697,17 @@ def fp4_dequantize(codes, scales, cols=None, fmt="mxfp4", tensor_scale=None, dty
     if stream is not None:
         return _on_stream(fp4_dequantize, stream,
                           (codes, scales, cols, fmt, tensor_scale, dtype, out), {})
-    torch = _torch()
     f = _fp4_format(fmt)
     rows, cols = _packed(codes, scales, f, "fp4_dequantize:", cols)
-    dev = codes.device
+    dev, at = codes.device, codes.get_device()
     if dtype is None:
-        dtype = torch.float32 if out is None else out.dtype
+        dtype = _late["f32"] if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
-    g = _vector(tensor_scale, torch.float32, 1, "tensor_scale", dev)
-    out = (torch.empty((rows, cols), dtype=dtype, device=dev) if out is None
+    g = None if tensor_scale is None else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at)
+    out = (_late["empty"]((rows, cols), dtype=dtype, device=dev) if out is None
            else _out(out, (rows, cols), dtype, "out", dev))
     rc = (_lib or lib()).fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, f, g,
-                                        out.data_ptr(), code, _current(dev))
+                                        out.data_ptr(), code, _current(at))
     if rc:
         _check("fp4_dequantize", rc)
     return out
@@ -730,25 +720,28 @@ def fp4_product(a_codes, a_scales, b_codes, b_scales, fmt="mxfp4", a_tensor_scal
     if stream is not None:
         return _on_stream(fp4_product, stream, (a_codes, a_scales, b_codes, b_scales, fmt,
                                                 a_tensor_scale, b_tensor_scale, dtype, out), {})
-    torch = _torch()
     f = _fp4_format(fmt)
     m, cols = _packed(a_codes, a_scales, f, "fp4_product: a")
     n, bcols = _packed(b_codes, b_scales, f, "fp4_product: b")
     if cols != bcols:
         raise ValueError(f"fp4_product: a has {cols} packed columns and b {bcols}")
-    dev = a_codes.device
-    if b_codes.device != dev:
+    dev, at = a_codes.device, a_codes.get_device()
+    if b_codes.get_device() != at:
         _same_device("fp4_product", a_codes, b_codes)
+    f32 = _late["f32"]
     if dtype is None:
-        dtype = torch.float32 if out is None else out.dtype
+        dtype = f32 if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
-    ga = _vector(a_tensor_scale, torch.float32, 1, "a_tensor_scale", dev)
-    gb = _vector(b_tensor_scale, torch.float32, 1, "b_tensor_scale", dev)
-    out = (torch.empty((m, n), dtype=dtype, device=dev) if out is None
+    ga = gb = None
+    if a_tensor_scale is not None:
+        ga = _array(a_tensor_scale, f32, (1,), "a_tensor_scale", at)
+    if b_tensor_scale is not None:
+        gb = _array(b_tensor_scale, f32, (1,), "b_tensor_scale", at)
+    out = (_late["empty"]((m, n), dtype=dtype, device=dev) if out is None
            else _out(out, (m, n), dtype, "out", dev))
     rc = (_lib or lib()).fp4_product(
         a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n,
-        cols, f, ga, gb, out.data_ptr(), code, _current(dev))
+        cols, f, ga, gb, out.data_ptr(), code, _current(at))
     if rc:
         _check("fp4_product", rc)
     return out
@@ -761,23 +754,25 @@ def fp4_linear(x, w_codes, w_scales, fmt="mxfp4", x_tensor_scale=None, w_tensor_
     if stream is not None:
         return _on_stream(fp4_linear, stream, (x, w_codes, w_scales, fmt, x_tensor_scale,
                                                w_tensor_scale, dtype, out), {})
-    torch = _torch()
     f = _fp4_format(fmt)
     xcode, m, cols, ld = _rows(x, "x")
     n, _ = _packed(w_codes, w_scales, f, "fp4_linear: w", cols)
-    dev = x.device
-    if w_codes.device != dev:
+    dev, at = x.device, x.get_device()
+    if w_codes.get_device() != at:
         _same_device("fp4_linear", x, w_codes)
     if dtype is None:
         dtype = x.dtype if out is None else out.dtype
-    code = _dtype_code(dtype, "dtype")
-    gx = _vector(x_tensor_scale, torch.float32, 1, "x_tensor_scale", dev)
-    gw = _vector(w_tensor_scale, torch.float32, 1, "w_tensor_scale", dev)
-    out = (torch.empty((m, n), dtype=dtype, device=dev) if out is None
+    code = xcode if dtype is x.dtype else _dtype_code(dtype, "dtype")
+    gx = gw = None
+    if x_tensor_scale is not None:
+        gx = _array(x_tensor_scale, _late["f32"], (1,), "x_tensor_scale", at)
+    if w_tensor_scale is not None:
+        gw = _array(w_tensor_scale, _late["f32"], (1,), "w_tensor_scale", at)
+    out = (_late["empty"]((m, n), dtype=dtype, device=dev) if out is None
            else _out(out, (m, n), dtype, "out", dev))
     rc = (_lib or lib()).fp4_linear(x.data_ptr(), xcode, m, ld, w_codes.data_ptr(),
                                     w_scales.data_ptr(), n, cols, f, gx, gw, out.data_ptr(), code,
-                                    _current(dev))
+                                    _current(at))
     if rc:
         _check("fp4_linear", rc)
     return out
@@ -798,23 +793,25 @@ def score_adjust(scores, history=None, history_len=None, prompt_len=None, repeti
                           (scores, history, history_len, prompt_len, repetition, presence,
                            frequency, bias_ids, bias_vals, temperature, mask, negate, out, dtype),
                           {})
-    torch = _torch()
-    i32, f32 = torch.int32, torch.float32
+    i32, f32, Tensor = _late["i32"], _late["f32"], _late["Tensor"]
     code, rows, cols, lds = _rows(scores, "scores")
-    dev = scores.device
-    hist = hl = pl = bi = bv = mk = None
+    dev, at = scores.device, scores.get_device()
+    hist = hl = pl = bi = bv = mk = rep = pres = freq = temp = None
     hist_cols = ldh = nb = ldm = 0
+    one = (rows,)
     if history is not None:
-        if not isinstance(history, torch.Tensor) or history.dtype != i32:
+        if not isinstance(history, Tensor) or history.dtype is not i32:
             raise TypeError("history must be an int32 tensor")
-        if history.dim() != 2 or history.shape[0] != rows or history.device != dev:
+        if history.dim() != 2 or history.shape[0] != rows or history.get_device() != at:
             raise ValueError(f"history must be [{rows}, length] on {dev}")
         hist_cols = history.shape[1]
         ldh, inner = history.stride()
         if hist_cols > 1 and inner != 1:
             raise ValueError("history must have dense rows (stride 1 along its length)")
-        hl = _vector(history_len, i32, rows, "history_len", dev)
-        pl = _vector(prompt_len, i32, rows, "prompt_len", dev)
+        if history_len is not None:
+            hl = _array(history_len, i32, one, "history_len", at)
+        if prompt_len is not None:
+            pl = _array(prompt_len, i32, one, "prompt_len", at)
         hist = history.data_ptr()
         if hist_cols == 0:
             hist = hl = pl = None
@@ -823,36 +820,40 @@ def score_adjust(scores, history=None, history_len=None, prompt_len=None, repeti
     if (bias_ids is None) != (bias_vals is None):
         raise ValueError("bias_ids and bias_vals go together")
     if bias_ids is not None:
-        if not isinstance(bias_ids, torch.Tensor):
+        if not isinstance(bias_ids, Tensor):
             raise TypeError("bias_ids must be a torch tensor")
         if bias_ids.dim() != 2 or bias_ids.shape[0] != rows:
             raise ValueError(f"bias_ids and bias_vals must both be [{rows}, nb]")
         nb = bias_ids.shape[1]
-        bi = _matrix(bias_ids, i32, rows, nb, "bias_ids", dev)
-        bv = _matrix(bias_vals, f32, rows, nb, "bias_vals", dev)
+        bi = _array(bias_ids, i32, (rows, nb), "bias_ids", at)
+        bv = _array(bias_vals, f32, (rows, nb), "bias_vals", at)
         if nb == 0:
             bi = bv = None
     if mask is not None:
         words = (cols + 31) // 32
-        if not isinstance(mask, torch.Tensor):
+        if not isinstance(mask, Tensor):
             raise TypeError("mask must be a torch tensor")
         mrows = rows if mask.dim() == 2 and mask.shape[0] == rows else 1
-        mk = _matrix(mask, i32, mrows, words, "mask", dev)
+        mk = _array(mask, i32, (mrows, words), "mask", at)
         ldm = words if mrows == rows else 0
-    rep = _vector(repetition, f32, rows, "repetition", dev)
-    pres = _vector(presence, f32, rows, "presence", dev)
-    freq = _vector(frequency, f32, rows, "frequency", dev)
-    temp = _vector(temperature, f32, rows, "temperature", dev)
+    if repetition is not None:
+        rep = _array(repetition, f32, one, "repetition", at)
+    if presence is not None:
+        pres = _array(presence, f32, one, "presence", at)
+    if frequency is not None:
+        freq = _array(frequency, f32, one, "frequency", at)
+    if temperature is not None:
+        temp = _array(temperature, f32, one, "temperature", at)
     if dtype is None:
         dtype = scores.dtype if out is None else out.dtype
     ocode = code if dtype is scores.dtype else _dtype_code(dtype, "dtype")
     if out is None:
-        out, ldo = torch.empty((rows, cols), dtype=dtype, device=dev), cols
+        out, ldo = _late["empty"]((rows, cols), dtype=dtype, device=dev), cols
     else:
         ldo = _out_rows(out, (rows, cols), dtype, "out", dev)
     rc = (_lib or lib()).score_adjust(
         scores.data_ptr(), code, rows, cols, lds, hist, hist_cols, ldh, hl, pl, rep, pres, freq,
-        bi, bv, nb, temp, mk, ldm, 1 if negate else 0, out.data_ptr(), ocode, ldo, _current(dev))
+        bi, bv, nb, temp, mk, ldm, 1 if negate else 0, out.data_ptr(), ocode, ldo, _current(at))
     if rc:
         _check("score_adjust", rc)
     return out
@@ -860,17 +861,16 @@ def score_adjust(scores, history=None, history_len=None, prompt_len=None, repeti
 
 def _teacher(scores, vals, ids):
     """Checks of a distillation call's inputs: (dtype code, rows, cols, row
-    stride, k, addresses of the teacher's values and ids)."""
-    torch = _torch()
+    stride, k, addresses of the teacher's values and ids, device index)."""
     code, rows, cols, ld = _rows(scores, "scores")
     try:
         k = vals.shape[1]
     except (AttributeError, IndexError):
-        _need(vals, torch.float32, "teacher_vals", 2)
+        _need(vals, _late["f32"], "teacher_vals", 2)
         raise
-    dev = scores.device
-    return (code, rows, cols, ld, k, _matrix(vals, torch.float32, rows, k, "teacher_vals", dev),
-            _matrix(ids, torch.int64, rows, k, "teacher_ids", dev))
+    at = scores.get_device()
+    return (code, rows, cols, ld, k, _array(vals, _late["f32"], (rows, k), "teacher_vals", at),
+            _array(ids, _late["i64"], (rows, k), "teacher_ids", at), at)
 
 
 def topk_distill_forward(scores, teacher_vals, teacher_ids, temperature=1.0, negated=False,
@@ -882,14 +882,13 @@ def topk_distill_forward(scores, teacher_vals, teacher_ids, temperature=1.0, neg
     if stream is not None:
         return _on_stream(topk_distill_forward, stream,
                           (scores, teacher_vals, teacher_ids, temperature, negated), {})
-    torch = _torch()
-    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti, at = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
-    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    loss = _late["empty"]((rows,), dtype=_late["f32"], device=dev)
+    stats = _late["empty"]((rows, 2), dtype=_late["f32"], device=dev)
     rc = (_lib or lib()).topk_distill_forward(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
                                               temperature, 1 if negated else 0, loss.data_ptr(),
-                                              stats.data_ptr(), _current(dev))
+                                              stats.data_ptr(), _current(at))
     if rc:
         _check("topk_distill_forward", rc)
     return loss, stats
@@ -903,20 +902,17 @@ def topk_distill_backward(scores, teacher_vals, teacher_ids, stats, row_grad, te
         return _on_stream(topk_distill_backward, stream,
                           (scores, teacher_vals, teacher_ids, stats, row_grad, temperature,
                            negated, grad), {})
-    torch = _torch()
-    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti, at = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    st = _matrix(stats, torch.float32, rows, 2, "stats", dev)
-    if row_grad is None:
-        raise TypeError("row_grad must be a torch tensor")
-    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
+    st = _array(stats, _late["f32"], (rows, 2), "stats", at)
+    w = _array(row_grad, _late["f32"], (rows,), "row_grad", at)
     if grad is None:
-        grad, ldg = torch.empty((rows, cols), dtype=scores.dtype, device=dev), cols
+        grad, ldg = _late["empty"]((rows, cols), dtype=scores.dtype, device=dev), cols
     else:
         ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
     rc = (_lib or lib()).topk_distill_backward(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
                                                temperature, 1 if negated else 0, st, w,
-                                               grad.data_ptr(), ldg, _current(dev))
+                                               grad.data_ptr(), ldg, _current(at))
     if rc:
         _check("topk_distill_backward", rc)
     return grad
@@ -930,20 +926,17 @@ def topk_distill(scores, teacher_vals, teacher_ids, row_grad, temperature=1.0, n
         return _on_stream(topk_distill, stream,
                           (scores, teacher_vals, teacher_ids, row_grad, temperature, negated,
                            grad), {})
-    torch = _torch()
-    code, rows, cols, ld, k, tv, ti = _teacher(scores, teacher_vals, teacher_ids)
+    code, rows, cols, ld, k, tv, ti, at = _teacher(scores, teacher_vals, teacher_ids)
     dev = scores.device
-    if row_grad is None:
-        raise TypeError("row_grad must be a torch tensor")
-    w = _vector(row_grad, torch.float32, rows, "row_grad", dev)
-    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+    w = _array(row_grad, _late["f32"], (rows,), "row_grad", at)
+    loss = _late["empty"]((rows,), dtype=_late["f32"], device=dev)
     if grad is None:
-        grad, ldg = torch.empty((rows, cols), dtype=scores.dtype, device=dev), cols
+        grad, ldg = _late["empty"]((rows, cols), dtype=scores.dtype, device=dev), cols
     else:
         ldg = _out_rows(grad, (rows, cols), scores.dtype, "grad", dev)
     rc = (_lib or lib()).topk_distill(scores.data_ptr(), code, rows, cols, ld, tv, ti, k,
                                       temperature, 1 if negated else 0, w, loss.data_ptr(),
-                                      grad.data_ptr(), ldg, _current(dev))
+                                      grad.data_ptr(), ldg, _current(at))
     if rc:
         _check("topk_distill", rc)
     return loss, grad

@@ -16,6 +16,7 @@
 // release them. Columns 416..511 hold two buffers of scales, each reused when the products two
 // stages back have finished.
 #include <algorithm>
+#include <atomic>
 
 #include "fp4_mma.cuh"
 
@@ -461,14 +462,14 @@ int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  static int resident = 0;  // groups that fit the device at once
+  static std::atomic<int> resident{0};  // groups that fit the device at once
   if (resident == 0) {
     int nc = 0;
     IVFPQ_CUDA(cudaOccupancyMaxActiveClusters(&nc, kern, &cfg));
     resident = std::max(1, nc);
   }
   const int64_t tiles = int64_t(tl.tn) * tl.tm;
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, resident)) * CG);
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, resident.load())) * CG);
   cfg.numAttrs = p.overlap ? 2 : 1;
   IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, mb, ma, msb, msa, p, tl));
   IVFPQ_LAUNCHED_K(kern, C::kTotal, kThreads);

@@ -8,7 +8,7 @@
 //
 // Bound by memory: each score is read and written once (a vector that the mask
 // rules out entirely is not read). A block takes a run of columns of one row:
-//  1. its first scores are loaded, and wait in registers;
+//  1. its first mask words, tokens and scores are loaded, and wait in registers;
 //  2. the history's occurrences in the run are counted in shared memory and the
 //     bias entries noted (integer atomics: the result does not depend on their
 //     order), and a bitmap marks their columns;
@@ -88,13 +88,15 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
   uint4 r[U];
   uint32_t ok[U];
   const int first = inner_first(mis), last = inner_last<T>(len - head, mis);
-  auto load = [&](int i0) {
+  auto load_mask = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads;
       ok[u] = ~0u;
       if (MASK && i < nvec) ok[u] = bits_at(mask, head + i * N, words - 1);
     }
+  };
+  auto load_scores = [&](int i0) {
     if (i0 >= first && i0 + (U - 1) * kThreads <= last) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -107,13 +109,22 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
         if (i0 + u * kThreads < nvec) r[u] = load_vec(src + head, len - head, i0 + u * kThreads, mis);
     }
   };
-  load(threadIdx.x);
+  load_mask(threadIdx.x);
   if constexpr (MARK) {
     const int32_t* h = HIST && a.history ? a.history + row * a.ldh : nullptr;
     const int32_t* bi = BIAS && a.bias_ids ? a.bias_ids + row * a.nb : nullptr;
-    int n = 0, np = 0;
-    if (HIST && a.history) {
-      n = int(a.hist_cols);
+    const int hcols = h ? int(a.hist_cols) : 0;
+    // the first tokens are on their way before their number is known
+    constexpr int V = 8;
+    int32_t t[V];
+    auto load_tokens = [&](int i0, int end) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        t[v] = i0 + v * kThreads < end ? __ldg(h + i0 + v * kThreads) : -1;
+    };
+    if (HIST) load_tokens(threadIdx.x, hcols);
+    int n = hcols, np = 0;
+    if (HIST && h) {
       if (a.history_len) n = max(0, min(n, a.history_len[row]));
       if (a.prompt_len) np = a.prompt_len[row];
     }
@@ -121,19 +132,18 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     for (int i = threadIdx.x; i < clear / 4; i += kThreads)
       reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    load_scores(threadIdx.x);
     if (HIST) {
-      constexpr int V = 8;
       for (int i0 = threadIdx.x; i0 < n; i0 += V * kThreads) {
-        int32_t t[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) t[v] = i0 + v * kThreads < n ? __ldg(h + i0 + v * kThreads) : -1;
+        if (i0 != int(threadIdx.x)) load_tokens(i0, n);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           // out of the run (or of the row, or negative): past len
           const uint32_t c = uint32_t(t[v]) - uint32_t(c0);
-          if (c < uint32_t(len)) {
+          const int i = i0 + v * kThreads;
+          if (c < uint32_t(len) && i < n) {
             atomicOr(&mark[c >> 5], 1u << (c & 31));
-            if (i0 + v * kThreads < np)
+            if (i < np)
               atomicOr(&count[c], kPrompt);
             else
               atomicAdd(&count[c], 1u);
@@ -162,12 +172,15 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       }
     }
     __syncthreads();
+  } else {
+    load_scores(threadIdx.x);
   }
   const float rep = HIST && a.repetition ? a.repetition[row] : 1.f;
   const float pres = HIST && a.presence ? a.presence[row] : 0.f;
   const float freq = HIST && a.frequency ? a.frequency[row] : 0.f;
   // the division by the temperature and the sign, as one factor per row
   const float f = (a.temperature ? __fdiv_rn(1.f, a.temperature[row]) : 1.f) * a.sign;
+  const float masked = -INFINITY * a.sign;
   auto marked = [&](int c, float x) {
     const uint32_t e = count[c];
     const uint32_t seen = SHORT ? e & 0xffffu : e;
@@ -186,12 +199,15 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     float x = to_f32(src[c]);
     if (MARK && (mark[c >> 5] >> (c & 31)) & 1u) x = marked(c, x);
     x *= f;
-    if (MASK && !((uint32_t(mask[c >> 5]) >> (c & 31)) & 1u)) x = -INFINITY * a.sign;
+    if (MASK && !((uint32_t(mask[c >> 5]) >> (c & 31)) & 1u)) x = masked;
     dst[c] = from_f32<O>(x);
   };
   for (int e = threadIdx.x; e < len - nvec * N; e += kThreads) one(e < head ? e : nvec * N + e);
   for (int i0 = threadIdx.x; i0 < nvec; i0 += U * kThreads) {
-    if (i0 != int(threadIdx.x)) load(i0);
+    if (i0 != int(threadIdx.x)) {
+      load_mask(i0);
+      load_scores(i0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads;
@@ -199,9 +215,10 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       float v[N];
       unpack_vec<T>(r[u], v);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        v[j] *= f;
-        if (MASK && !((ok[u] >> j) & 1u)) v[j] = -INFINITY * a.sign;
+      for (int j = 0; j < N; j += 2) unpair(mul2(pair(v[j], v[j + 1]), pair(f, f)), v[j], v[j + 1]);
+      if constexpr (MASK) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = (ok[u] >> j) & 1u ? v[j] : masked;
       }
       store_vec<O>(dst + head + i * N, v);
       if constexpr (MARK) {

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_backward_kernel(const Dis
 // Loss and gradient with the row held in the shared memory of a cluster: each
 // score is read from memory once.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];
   __shared__ float4 sh[kWarps];
   __shared__ RowPart part;
