@@ -5,16 +5,18 @@
 // out, T = 128 or 256, alone (CG = 1) or in pairs (cta_group::2): a pair shares
 // the T rows of a, half in each CTA, so an SM takes in 38 KB per 256 columns
 // of K instead of 54 KB. Filling shared memory is close to a limit: 8192 x
-// 16384 x 4096 nvfp4 takes 157 us for the loads alone, 146 us for the products
-// alone and 194 us together on single CTAs, 183 us in pairs.
+// 16384 x 4096 NVFP4 takes 157 us for the loads alone, 146 us for the products
+// alone and 194 us together on single CTAs, 183 us (6.0 PFLOP/s) in pairs. With
+// short K the result's bytes bound it: 10000 x 65536 x 96 to fp32 437 us, 2.6 GB
+// at 6.0 TB/s.
 //
 // 10 warps: warp 0 loads; warp 1 of the pair's first CTA copies scales to TMEM
-// and issues products for both; warps 2..9 store (two per TMEM lane group, half
-// of the rows each). While a tile is stored the next ones are computed: T = 128
+// and issues products for both; warps 2..9 store (two per TMEM lane group, every
+// other 16 rows each). While a tile is stored the next ones are computed: T = 128
 // has three accumulators; with T = 256 two overlap (TMEM columns 0..255 and
 // 160..415), so the storing warps first empty the 96 shared columns and
-// release them. Columns 416..511 hold two buffers of scales, each reused when the products two
-// stages back have finished.
+// release them. Columns 416..511 hold two buffers of scales, each reused when
+// the products two stages back have finished.
 #include <algorithm>
 #include <atomic>
 
@@ -374,31 +376,40 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
       const int col = col0(t) + 32 * lg + lane, m0 = row0(t);
       const bool live = col < p.n;
       O* out = static_cast<O*>(p.out) + col;
+      // units of 16 rows, every other one this warp's; those past m are not read
+      auto units = [&](int c, int n) {
+        const int64_t left = p.m - m0 - c - 16 * half;
+        return left <= 0 ? 0 : int(min(int64_t(n), (left + 31) / 32));
+      };
       if constexpr (kCrit > 0) {
-        const int c = (b ? 0 : T - kCrit) + half * C1;
+        const int c = (b ? 0 : T - kCrit) + 16 * half, n = units(c - 16 * half, C1 / 16);
         uint32_t r[C1 / 16][16];
 #pragma unroll
-        for (int j = 0; j < C1 / 16; ++j) tmem_ld16(acc + c + 16 * j, r[j]);
+        for (int j = 0; j < C1 / 16; ++j)
+          if (j < n) tmem_ld16(acc + c + 32 * j, r[j]);
         tmem_wait_ld();
         tc_fence_before();
         release(b);
 #pragma unroll
         for (int j = 0; j < C1 / 16; ++j)
-          store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, pairs, r[j], alpha);
+          if (j < n) store16<O>(out, p.ldo, m0 + c + 32 * j, p.m, live, pairs, r[j], alpha);
       }
-      const int c = (kCrit && b ? kCrit : 0) + half * C2;
+      const int c = (kCrit && b ? kCrit : 0) + 16 * half, n = units(c - 16 * half, C2 / 16);
       uint32_t r[2][16];
-      tmem_ld16(acc + c, r[0]);
+      if (n > 0) tmem_ld16(acc + c, r[0]);
+      if (kCrit == 0 && n == 0) release(b);
 #pragma unroll
       for (int j = 0; j < C2 / 16; ++j) {
-        tmem_wait_ld();
-        if (j + 1 < C2 / 16) {
-          tmem_ld16(acc + c + 16 * (j + 1), r[(j + 1) & 1]);
-        } else if (kCrit == 0) {
-          tc_fence_before();
-          release(b);
+        if (j < n) {
+          tmem_wait_ld();
+          if (j + 1 < n) {
+            tmem_ld16(acc + c + 32 * (j + 1), r[(j + 1) & 1]);
+          } else if (kCrit == 0) {
+            tc_fence_before();
+            release(b);
+          }
+          store16<O>(out, p.ldo, m0 + c + 32 * j, p.m, live, pairs, r[j & 1], alpha);
         }
-        store16<O>(out, p.ldo, m0 + c + 16 * j, p.m, live, pairs, r[j & 1], alpha);
       }
       tc_fence_before();
       if (++b == C::kAccs) {

