@@ -14,10 +14,10 @@
 // both in one 121 us (81 us), where the exponentials of both uses and the
 // exchange between them are not hidden behind three blocks per SM.
 //
-// Statistics kept per row: the largest score m
-// and Z = sum_j exp((s_j - m) / tau), both fp32; q_j comes from the difference
-// s_j - m, so scores of any magnitude (a mask of the type's lowest value among
-// them) neither overflow nor cancel. A score of -inf has q = 0.
+// Statistics kept per row: the largest score m and Z = sum_j exp((s_j - m) /
+// tau), both fp32; q_j comes from the difference s_j - m, so scores of any
+// magnitude (a mask of the type's lowest value among them) neither overflow nor
+// cancel. A score of -inf has q = 0.
 #include <algorithm>
 
 #include "internal.h"
@@ -28,7 +28,7 @@ namespace ivfpq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kThreads / 32;  // a power of two
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -125,19 +125,27 @@ __device__ __forceinline__ void block_join(Online& o, Online& l, float c, float4
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float4(mo, zo, ml, zl);
   __syncthreads();
-  float4 v[kWarps];
-  o = l = Online{};
+  // lane i takes warp i's
+  const int lane = threadIdx.x & 31;
+  const float4 v = lane < kWarps ? sh[lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  mo = v.x;
+  ml = v.z;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    v[i] = sh[i];
-    o.m = fmaxf(o.m, v[i].x);
-    l.m = fmaxf(l.m, v[i].z);
+  for (int d = kWarps / 2; d; d /= 2) {
+    mo = fmaxf(mo, __shfl_xor_sync(kFullMask, mo, d));
+    ml = fmaxf(ml, __shfl_xor_sync(kFullMask, ml, d));
   }
+  zo = rescaled(v.x, v.y, mo, c);
+  zl = rescaled(v.z, v.w, ml, c);
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    o.z += rescaled(v[i].x, v[i].y, o.m, c);
-    l.z += rescaled(v[i].z, v[i].w, l.m, c);
+  for (int d = kWarps / 2; d; d /= 2) {
+    zo += __shfl_xor_sync(kFullMask, zo, d);
+    zl += __shfl_xor_sync(kFullMask, zl, d);
   }
+  o.m = __shfl_sync(kFullMask, mo, 0);
+  o.z = __shfl_sync(kFullMask, zo, 0);
+  l.m = __shfl_sync(kFullMask, ml, 0);
+  l.z = __shfl_sync(kFullMask, zl, 0);
 }
 
 // ---- the teacher's list ----------------------------------------------------------------
@@ -389,7 +397,7 @@ __device__ __forceinline__ void run_zero(T* g, int len) {
 }
 
 // A block's part of a row's statistics and loss, and their join over the
-// cluster in rank order. The parts' owners stay until all have read them
+// cluster in a fixed order. The parts' owners stay until all have read them
 // (cluster_leave); what is in between overlaps with the others' reading.
 struct __align__(16) RowPart {
   float m, z;
@@ -425,29 +433,31 @@ __device__ __forceinline__ RowSum row_join(const Online& o, const LossPart& part
     y = ld_cluster4(at + 16).x;
   }
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  s.all.m = v.x;
+  float m = v.x;
 #pragma unroll
-  for (int d = kMaxCluster / 2; d; d /= 2)
-    s.all.m = fmaxf(s.all.m, __shfl_xor_sync(kFullMask, s.all.m, d));
-  s.all.m = __shfl_sync(kFullMask, s.all.m, 0);
-  const float z = rescaled(v.x, v.y, s.all.m, c);
+  for (int d = kMaxCluster / 2; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
+  m = __shfl_sync(kFullMask, m, 0);
+  float z = rescaled(v.x, v.y, m, c), x = v.z, p = v.w;
   // the part's differences are from its own maximum
-  if (!(v.w == 0.f) && v.x != s.all.m) y += (v.x - s.all.m) * v.w;
-  float p = 0.f;
+  if (!(p == 0.f) && v.x != m) y += (v.x - m) * p;
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) {
-    s.all.z += __shfl_sync(kFullMask, z, r);
-    s.x += __shfl_sync(kFullMask, v.z, r);
-    p += __shfl_sync(kFullMask, v.w, r);
-    s.y += __shfl_sync(kFullMask, y, r);
+  for (int d = kMaxCluster / 2; d; d /= 2) {
+    z += __shfl_xor_sync(kFullMask, z, d);
+    x += __shfl_xor_sync(kFullMask, x, d);
+    p += __shfl_xor_sync(kFullMask, p, d);
+    y += __shfl_xor_sync(kFullMask, y, d);
   }
+  s.all.m = m;
+  s.all.z = __shfl_sync(kFullMask, z, 0);
+  s.x = x;  // these two count in thread 0 only
+  s.y = y;
   s.x += (s.all.z == 0.f ? 0.f : logf(s.all.z)) * p;
   return s;
 }
 __device__ __forceinline__ void cluster_leave(int nranks) {
   if (nranks > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// Sums over the block, in a fixed order.
+// Sums over the block, in a fixed order, for thread 0.
 __device__ __forceinline__ LossPart block_loss(LossPart l, float4* sh) {
 #pragma unroll
   for (int o = 16; o; o /= 2) {
@@ -458,13 +468,17 @@ __device__ __forceinline__ LossPart block_loss(LossPart l, float4* sh) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float4(l.a, l.p, l.y, 0.f);
   __syncthreads();
-  l = LossPart{};
+  // of use to thread 0 only
+  const int lane = threadIdx.x & 31;
+  const float4 v = lane < kWarps ? sh[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+  l.a = v.x;
+  l.p = v.y;
+  l.y = v.z;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const float4 v = sh[i];
-    l.a += v.x;
-    l.p += v.y;
-    l.y += v.z;
+  for (int d = kWarps / 2; d; d /= 2) {
+    l.a += __shfl_xor_sync(kFullMask, l.a, d);
+    l.p += __shfl_xor_sync(kFullMask, l.p, d);
+    l.y += __shfl_xor_sync(kFullMask, l.y, d);
   }
   return l;
 }
