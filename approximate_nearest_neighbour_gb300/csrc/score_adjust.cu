@@ -6,8 +6,10 @@
 //   c in the row's bias list:          x += bias
 //   x /= temperature;  not allowed by the mask: x = -inf;  negated if asked
 //
-// Bound by memory: each score is read and written once (a vector that the mask
-// rules out entirely is not read). A block takes a run of columns of one row:
+// Bound by memory: each score is read and written once. (To skip what the mask
+// rules out, the scores would have to wait for the mask: a microsecond more
+// with a quarter of the columns allowed.) A block takes a run of columns of one
+// row:
 //  1. its first mask words, tokens and scores are loaded, and wait in registers;
 //  2. the history's occurrences in the run are counted in shared memory and the
 //     bias entries noted (integer atomics: the result does not depend on their
@@ -16,10 +18,11 @@
 //     tables.
 // Every block of a row reads the whole history, so runs are as long as leaves
 // enough blocks (run_for). Measured at 256 x 131072 bf16: 22 us with the
-// temperature alone (its bytes take 20 us), 29 us with a mask, 35 us with 64
-// biases too, 46 us with histories of up to 4,096 tokens besides; what is above
+// temperature alone (its bytes take 20 us), 29 us with a mask, 33 us with 64
+// biases too, 45 us with histories of up to 4,096 tokens besides; what is above
 // the bytes is instructions (2.4 per clock and SM) and the steps before the
-// stream, not memory.
+// stream, not memory. Runs of 4,096 and 16,384 columns and blocks of 128 and
+// 512 threads measured 46 to 59 us.
 #include <algorithm>
 
 #include "internal.h"
@@ -61,12 +64,14 @@ struct AdjustArgs {
   int run;
 };
 
-// Bits b .. b + 31 of a bit string of words, as far as word `last`.
-template <class W>
+// Bits b .. b + N - 1 of a bit string of words, as far as word `last`, in the
+// low bits. The second word is read only where they reach into it.
+template <int N, class W>
 __device__ __forceinline__ uint32_t bits_at(const W* words, int b, int last) {
   const int w = b >> 5, sh = b & 31;
-  const uint32_t lo = uint32_t(words[w]);
-  return sh == 0 ? lo : __funnelshift_r(lo, w < last ? uint32_t(words[w + 1]) : 0u, sh);
+  uint32_t r = uint32_t(words[w]) >> sh;
+  if (sh > 32 - N && w < last) r |= uint32_t(words[w + 1]) << (32 - sh);
+  return r & ((1u << N) - 1);
 }
 
 template <class T, class O, bool HIST, bool BIAS, bool MASK, bool SHORT>
@@ -96,17 +101,14 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads;
-      ok[u] = ~0u;
-      if (MASK && i < nvec) ok[u] = bits_at(mask, head + i * N, words - 1);
+      ok[u] = (1u << N) - 1;
+      if (MASK && i < nvec) ok[u] = bits_at<N>(mask, head + i * N, words - 1);
     }
   };
   auto load_scores = [&](int i0) {
     if (i0 >= first && i0 + (U - 1) * kThreads <= last) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        r[u] = make_uint4(0, 0, 0, 0);
-        if (!MASK || (ok[u] & ((1u << N) - 1))) r[u] = load_inner(src + head, i0 + u * kThreads, mis);
-      }
+      for (int u = 0; u < U; ++u) r[u] = load_inner(src + head, i0 + u * kThreads, mis);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     }
   };
   load_mask(threadIdx.x);
+  load_scores(threadIdx.x);
   if constexpr (MARK) {
     const int32_t* h = HIST && a.history ? a.history + row * a.ldh : nullptr;
     const int32_t* bi = BIAS && a.bias_ids ? a.bias_ids + row * a.nb : nullptr;
@@ -136,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     for (int i = threadIdx.x; i < clear / 4; i += kThreads)
       reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    load_scores(threadIdx.x);
     if (HIST) {
       for (int i0 = threadIdx.x; i0 < n; i0 += V * kThreads) {
         if (i0 != int(threadIdx.x)) load_tokens(i0, n);
@@ -176,8 +178,6 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       }
     }
     __syncthreads();
-  } else {
-    load_scores(threadIdx.x);
   }
   const float rep = HIST && a.repetition ? a.repetition[row] : 1.f;
   const float pres = HIST && a.presence ? a.presence[row] : 0.f;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       store_vec<O>(dst + head + i * N, v);
       if constexpr (MARK) {
         // the few marked columns again, one by one, from the loaded scores
-        uint32_t m = bits_at(mark, head + i * N, words - 1) & ok[u] & ((1u << N) - 1);
+        uint32_t m = bits_at<N>(mark, head + i * N, words - 1) & ok[u];
         while (m) {
           const int j = __ffs(m) - 1, c = head + i * N + j;
           m &= m - 1;

@@ -159,3 +159,22 @@ def test_rows_past_32_bits(B):
     p = torch.ones((rows,), device="cuda")
     B.score_adjust(x, history=h, presence=p, out=x)
     assert float(x[-1, -1]) == 2.0 and float(x[-2, -1]) == -1.0 and float(x[-1, -2]) == 0.0
+
+
+def test_long_histories_and_bias_lists(B):
+    """Past 32,767 tokens or 65,535 biases: counts of more than 15 bits, slots of more than 16."""
+    import torch
+    r = np.random.default_rng(8)
+    x = torch.from_numpy(r.standard_normal((2, 5000)).astype(np.float32)).cuda()
+    h = r.integers(0, 5000, (2, 70_000)).astype(np.int32)
+    h[:, :50_000] = 3
+    a = {"history": h, "prompt_len": np.array([49_000, 10], np.int32),
+         "repetition": np.array([1.5, 0.7], np.float32),
+         "presence": np.array([0.5, 0.25], np.float32),
+         "frequency": np.array([1e-3, 2e-4], np.float32)}
+    _check(B.score_adjust(x, **_cuda(a)), x, a)
+    b = {"bias_ids": r.integers(-1, 5001, (2, 70_001)).astype(np.int32),
+         "bias_vals": r.standard_normal((2, 70_001)).astype(np.float32)}
+    _check(B.score_adjust(x, **_cuda(b)), x, b)
+    both = {**a, **b, "mask": r.integers(-2**31, 2**31, (1, 157)).astype(np.int32)}
+    _check(B.score_adjust(x, **_cuda(both)), x, both)

@@ -91,7 +91,7 @@ def _check(out, s, tv, ti, g, tau, negated=True):
 @pytest.mark.parametrize("rows,cols,k,tau", [
     (1, 1, 1, 1.0), (5, 7, 7, 2.0), (3, 5, 20, 1.0), (37, 32001, 10, 1.0), (8, 1000, 100, 0.25),
     (6, 4097, 2048, 4.0), (2, 200_003, 1000, 2.0), (300, 129, 3, 1.0), (9, 65536, 33, 1.0),
-    (3, 131072, 64, 1.0)])
+    (3, 131072, 64, 1.0), (2, 400_000, 20, 1.0), (2, 1_000_003, 50, 2.0)])
 def test_against_the_definition(B, dtype, rows, cols, k, tau):
     import torch
     s, tv, ti, g = _case(rows, cols, k, rows + cols)
@@ -229,3 +229,19 @@ def test_a_search_as_the_teacher(B):
     tv, ti = dist.cpu().numpy(), ids.cpu().numpy()
     out = _run(B, s, tv, ti, g.cpu().numpy(), 4.0)
     _check(out, s, tv, ti, g.cpu().numpy(), 4.0)
+
+
+def test_more_rows_than_one_grid_dimension(B):
+    """70,000 rows, the same 7,000 ten times."""
+    import torch
+    s, tv, ti, g = _case(7000, 40, 3, 5)
+    d = [torch.from_numpy(v).cuda() for v in (s, tv, ti, g)]
+    few = B.topk_distill(*d, 2.0, negated=True)
+    d10 = [t.repeat(10, *([1] * (t.dim() - 1))) for t in d]
+    many = B.topk_distill(*d10, 2.0, negated=True)
+    loss, stats = B.topk_distill_forward(*d10[:3], 2.0, negated=True)
+    grad = B.topk_distill_backward(*d10[:3], stats, d10[3], 2.0, negated=True)
+    for t in range(10):
+        at = slice(7000 * t, 7000 * (t + 1))
+        assert torch.equal(many[0][at], few[0]) and torch.equal(many[1][at], few[1])
+        assert torch.equal(loss[at], few[0]) and torch.equal(grad[at], few[1])
