@@ -9,6 +9,10 @@
  * BlockSelect) merged across lists. Exact brute-force k-NN and stand-alone
  * row-wise k-selection are exposed too.
  *
+ * Beside the searches it has what belongs to a score row: products of 4-bit
+ * block-scaled vectors, the adjustments between a product and a selection, and
+ * distillation from a selected list.
+ *
  * Conventions for every entry point:
  *  - Array pointers are DEVICE pointers (for example torch tensors'
  *    data_ptr()) unless stated otherwise; matrices are row-major and densely
@@ -582,8 +586,8 @@ int topk_distill(const void* scores, int dtype, int64_t rows, int64_t cols, int6
 
 /* ivfpq_device_check -- synchronises `stream` and reports whether any kernel
  * of this library on the current device gave up a bounded wait since the
- * last check (the tensor-core distance pipeline waits on its own copies and
- * MMAs with an iteration limit; on expiry it stops, releases its resources
+ * last check (the tensor-core distance and 4-bit product pipelines wait on
+ * their own copies and MMAs with an iteration limit; on expiry it stops, releases its resources
  * and sets a per-device status word instead of hanging). Clears the word.
  * Returns IVFPQ_OK, or IVFPQ_ERR_TIMEOUT (the results of the calls since the
  * previous check are then invalid), or IVFPQ_ERR_CUDA. */
