@@ -28,6 +28,8 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kSfBase = 416;  // first TMEM column of the scales
+constexpr int64_t kL2Bytes = int64_t(129) << 20;
+constexpr int kBounce = 8 * BN * 4;  // 8 rows of a tile on their way out, per half of the warps
 
 template <int FMT, int T, int CG>
 struct WideCfg {
@@ -38,8 +40,9 @@ struct WideCfg {
   static constexpr int kA = T / CG * KB;
   static constexpr int kSf = (1 + kRt) * kSfTile;  // b's scales, then all T rows' of a
   static constexpr int kStage = kB + kA + kSf;
-  static constexpr int kStages = (226 * 1024 - 1536) / kStage < 8 ? (226 * 1024 - 1536) / kStage : 8;
-  static constexpr int kTotal = kStages * kStage + 512 + 1024;
+  static constexpr int kFit = (227 * 1024 - 1536 - 2 * kBounce) / kStage;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kTotal = kStages * kStage + 512 + 1024 + 2 * kBounce;
   static constexpr int kSfCols = 4 * kTiles * (1 + kRt);  // TMEM columns of one scale buffer
   // accumulators and the columns between their starts
   static constexpr int kAccs = T == 256 ? 2 : 3;
@@ -159,6 +162,56 @@ __device__ __forceinline__ void store16(O* out, int64_t ldo, int r0, int64_t m, 
   }
 }
 
+// The same for fp32 rows at odd offsets in a result larger than L2. A warp's 32
+// columns leave two sectors of each row half written, and those reach memory
+// apart: 10000 x 65535 x 96 took 1070 us, and 457 us with 65528 columns (32-byte
+// rows). Here four warps exchange 8 rows of 128 columns through shared memory and
+// each writes whole lines of two of them: 760 us, and 122 us instead of 147 us
+// at 1000 x 100003 x 128. Smaller results (77 x 100003: 17.6 us, and 21.8 us
+// here), rows on 16 bytes (1000 x 100004: 90 and 122 us) and 16-bit results
+// (8192 x 16385 x 4096: 199 and 360 us) are better off without.
+__device__ __forceinline__ void half_sync(int half) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+}
+// Whether all 128 threads of the half say so.
+__device__ __forceinline__ bool half_all(int half, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.and.pred p, %2, 128, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r)
+      : "r"(uint32_t(ok)), "r"(1 + half)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void store16_lines(float* out, int64_t ldo, int r0, int64_t m, int cols,
+                                              float* buf, int lg, int half,
+                                              const uint32_t (&r)[16], float alpha) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      buf[j * BN + 32 * lg + lane] = __uint_as_float(r[8 * h + j]) * alpha;
+    half_sync(half);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int row = r0 + 8 * h + 2 * lg + q;
+      if (row < m) {
+        const float* b = buf + (2 * lg + q) * BN;
+        float* p = out + row * ldo;
+        const int mis = int(reinterpret_cast<uintptr_t>(p) & 127) / 4;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          const int e = i * 32 + lane - mis;
+          if (e >= 0 && e < cols) p[e] = b[e];
+        }
+      }
+    }
+    half_sync(half);
+  }
+}
+
 struct Tiling {
   int tn, tm;   // tiles along n and m
   int m_fast;   // consecutive tiles go along m
@@ -180,7 +233,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
   auto s_a = [&](int s) { return base + s * (C::kB + C::kA) + C::kB; };
   const uint32_t sf0 = base + NS * (C::kB + C::kA);
   auto s_sf = [&](int s) { return sf0 + s * C::kSf; };
-  const uint32_t bars = base + NS * C::kStage;
+  const uint32_t bars = base + NS * C::kStage + 2 * kBounce;
   auto bar_full = [&](int s) { return bars + 8 * s; };          // first CTA's: both CTAs' copies
   auto bar_empty = [&](int s) { return bars + 8 * (NS + s); };  // each CTA's
   auto bar_sf = [&](int b) { return bars + 16 * NS + 8 * b; };
@@ -365,17 +418,36 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
       }
     };
     const bool pairs = p.n % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+    const bool lines =
+        sizeof(O) == 4 &&
+        (p.n % 4 != 0 || (reinterpret_cast<uintptr_t>(p.out) & 15) != 0) &&
+        p.m * p.n * 4 > kL2Bytes;
+    float* bounce = reinterpret_cast<float*>(gbase + NS * C::kStage + half * kBounce);
     int b = 0, turn = 0;
-    for (int t = group; t < ntiles && !*abort_flag; t += ngroups) {
-      if (!mbar_wait(bar_acc(b), turn & 1)) {
+    for (int t = group; t < ntiles; t += ngroups) {
+      bool ok = !*abort_flag;
+      if (ok && !mbar_wait(bar_acc(b), turn & 1)) {
         fail();
-        break;
+        ok = false;
       }
+      // warps that exchange rows go on, or stop, together: none waits at their
+      // barrier for one that has given up
+      if (lines) ok = half_all(half, ok);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t(32 * lg) << 16) + uint32_t(b * C::kAccStep);
       const int col = col0(t) + 32 * lg + lane, m0 = row0(t);
       const bool live = col < p.n;
       O* out = static_cast<O*>(p.out) + col;
+      O* line0 = static_cast<O*>(p.out) + col0(t);
+      const int cols = int(min(int64_t(BN), p.n - col0(t)));
+      auto put = [&](const uint32_t (&r)[16], int r0) {
+        if constexpr (sizeof(O) == 4) {
+          if (lines)
+            return store16_lines(line0, p.ldo, r0, p.m, cols, bounce, lg, half, r, alpha);
+        }
+        store16<O>(out, p.ldo, r0, p.m, live, pairs, r, alpha);
+      };
       // units of 16 rows, every other one this warp's; those past m are not read
       auto units = [&](int c, int n) {
         const int64_t left = p.m - m0 - c - 16 * half;
@@ -392,7 +464,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
         release(b);
 #pragma unroll
         for (int j = 0; j < C1 / 16; ++j)
-          if (j < n) store16<O>(out, p.ldo, m0 + c + 32 * j, p.m, live, pairs, r[j], alpha);
+          if (j < n) put(r[j], m0 + c + 32 * j);
       }
       const int c = (kCrit && b ? kCrit : 0) + 16 * half, n = units(c - 16 * half, C2 / 16);
       uint32_t r[2][16];
@@ -408,7 +480,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
             tc_fence_before();
             release(b);
           }
-          store16<O>(out, p.ldo, m0 + c + 32 * j, p.m, live, pairs, r[j & 1], alpha);
+          put(r[j & 1], m0 + c + 32 * j);
         }
       }
       tc_fence_before();

@@ -275,3 +275,20 @@ def test_output_past_32_bits(B):
     B.device_check()
     assert bool((out[32, -1000:] == 64).all()) and bool((out[31, -1000:] == 32).all())
     assert bool((out[0, :1000] == 32).all())
+
+
+@pytest.mark.parametrize("m,n,cols", [(301, 120_001, 64), (2100, 20_003, 96), (1111, 40_002, 2100)])
+def test_large_results_at_odd_offsets(B, m, n, cols):
+    """fp32 results past L2 whose rows start anywhere: the same values as the same
+    product computed in column blocks, each result small and aligned."""
+    import torch
+    qa, qb = B.fp4_quantize(_x(m, cols, 1, "f32")), B.fp4_quantize(_x(n, cols, 2, "f32"))
+    pad = torch.full((m * n + 3,), 7.0, device="cuda")
+    out = pad[1:1 + m * n].view(m, n)  # 4 bytes past an aligned address
+    B.fp4_product(*qa, *qb, out=out)
+    B.device_check()
+    assert float(pad[0]) == 7 and bool((pad[1 + m * n:] == 7).all())
+    for c in range(0, n, 8192):
+        e = min(n, c + 8192)
+        part = B.fp4_product(*qa, qb[0][c:e], qb[1][c // 128:(e + 127) // 128])
+        assert torch.equal(out[:, c:e], part)
