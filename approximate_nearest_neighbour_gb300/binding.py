@@ -676,7 +676,8 @@ def fp4_quantize(x, fmt="mxfp4", tensor_scale=None, codes=None, scales=None, str
     f = _fp4_format(fmt)
     code, rows, cols, ld = _rows(x, "x")
     dev, at = x.device, x.get_device()
-    g = None if tensor_scale is None else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at)
+    g = (None if tensor_scale is None
+         else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at))
     cs, ss = fp4_shapes(rows, cols, f)
     u8 = _late["u8"]
     codes = (_late["empty"](cs, dtype=u8, device=dev) if codes is None
@@ -703,7 +704,8 @@ def fp4_dequantize(codes, scales, cols=None, fmt="mxfp4", tensor_scale=None, dty
     if dtype is None:
         dtype = _late["f32"] if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
-    g = None if tensor_scale is None else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at)
+    g = (None if tensor_scale is None
+         else _array(tensor_scale, _late["f32"], (1,), "tensor_scale", at))
     out = (_late["empty"]((rows, cols), dtype=dtype, device=dev) if out is None
            else _out(out, (rows, cols), dtype, "out", dev))
     rc = (_lib or lib()).fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, f, g,

@@ -96,7 +96,8 @@ __device__ __forceinline__ void mma_commit_el(uint32_t bar, uint32_t el) {
 template <int FMT, int T, int CG>
 __device__ __forceinline__ uint32_t fp4_idesc(uint32_t sf_id) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(T >> 3) << 17) |
-         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(CG * BN >> 7) << 27) | (sf_id << 29);
+         (uint32_t(FMT == IVFPQ_MXFP4 ? 1 : 0) << 23) | (uint32_t(CG * BN >> 7) << 27) |
+         (sf_id << 29);
 }
 __device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, float v) {
   if (dtype == IVFPQ_F32)

@@ -232,8 +232,8 @@ extern "C" int fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols
                             void* stream) {
   clear_error();
   IVFPQ_TRY(check_rows("fp4_quantize", rows, cols, fmt, dtype));
-  IVFPQ_REQUIRE(ldx >= cols || rows <= 1 || ldx == 0, "fp4_quantize: row stride %lld below cols=%lld",
-                (long long)ldx, (long long)cols);
+  IVFPQ_REQUIRE(ldx >= cols || rows <= 1 || ldx == 0,
+                "fp4_quantize: row stride %lld below cols=%lld", (long long)ldx, (long long)cols);
   if (rows == 0) return IVFPQ_OK;
   IVFPQ_REQUIRE(x && codes && scales, "fp4_quantize: null pointer");
   IVFPQ_REQUIRE(aligned16(codes, 16) && aligned16(scales, 16),

@@ -37,7 +37,7 @@ constexpr int kMinRun = 1024;
 
 // A run's table: per column the occurrences past the prompt, whether the prompt
 // has it, and 1 + the last bias entry for it. SHORT packs them into one word
-// (bits 0..14, bit 15, bits 16..31), so that six blocks share an SM instead of
+// (bits 0..14, bit 15, bits 16..31), so that five blocks share an SM instead of
 // three; it holds histories of up to 32,767 tokens and 65,535 bias entries.
 // The long form has the counter with bit 31 for the prompt, and a second word.
 constexpr int kShortHistory = 32767, kShortBias = 65535;
@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i0 + u * kThreads < nvec) r[u] = load_vec(src + head, len - head, i0 + u * kThreads, mis);
+        if (i0 + u * kThreads < nvec)
+          r[u] = load_vec(src + head, len - head, i0 + u * kThreads, mis);
     }
   };
   load_mask(threadIdx.x);
@@ -291,8 +292,8 @@ extern "C" int score_adjust(const void* scores, int dtype, int64_t rows, int64_t
   clear_error();
   IVFPQ_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), "score_adjust: rows=%lld outside [0, 2^31)",
                 (long long)rows);
-  IVFPQ_REQUIRE(cols >= 0 && cols <= (int64_t(1) << 28), "score_adjust: cols=%lld outside [0, 2^28]",
-                (long long)cols);
+  IVFPQ_REQUIRE(cols >= 0 && cols <= (int64_t(1) << 28),
+                "score_adjust: cols=%lld outside [0, 2^28]", (long long)cols);
   IVFPQ_REQUIRE(known_dtype(dtype) && known_dtype(out_dtype), "score_adjust: unknown element type");
   IVFPQ_REQUIRE(out_dtype == dtype || out_dtype == IVFPQ_F32,
                 "score_adjust: the output is of the scores' type or fp32");
@@ -309,8 +310,8 @@ extern "C" int score_adjust(const void* scores, int dtype, int64_t rows, int64_t
   IVFPQ_REQUIRE((bias_ids == nullptr) == (bias_vals == nullptr),
                 "score_adjust: bias ids and values go together");
   AdjustArgs a{scores, rows, cols, lds, hist_cols ? history : nullptr, hist_cols, ldh, history_len,
-               prompt_len, repetition, presence, frequency, nb ? bias_ids : nullptr, bias_vals, bias_ids ? nb : 0,
-               temperature, mask, ldm, negate ? -1.f : 1.f, out, ldo, 0};
+               prompt_len, repetition, presence, frequency, nb ? bias_ids : nullptr, bias_vals,
+               bias_ids ? nb : 0, temperature, mask, ldm, negate ? -1.f : 1.f, out, ldo, 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return by_dtype(dtype, [&](auto* t) -> int {
     using T = std::remove_pointer_t<decltype(t)>;

@@ -500,9 +500,9 @@ __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const Dist
   Online t = list_load(a, row, l, c);
   Online o = run_stats<T, true>(s, len, c);
   block_join(o, t, c, sh);
-  const LossPart mine = block_loss(
-      list_weights<true, false>(a, l, t, c, c0, len, o.m, nullptr, [&](int i) { return to_f32(s[i]); }),
-      sh);
+  auto score = [&](int i) { return to_f32(s[i]); };
+  const LossPart mine =
+      block_loss(list_weights<true, false>(a, l, t, c, c0, len, o.m, nullptr, score), sh);
   const RowSum r = row_join(o, mine, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0) {
     a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
