@@ -9,8 +9,12 @@
 namespace ivfpq {
 
 constexpr int BN = 128;            // columns of out (rows of b) per CTA
-constexpr int KB = 128;            // bytes of K per stage and row
-constexpr int KE = 2 * KB;         // K columns per stage
+
+// Bytes of K per stage and row: 128, or 64 where all of K fits. A row is one
+// request of the copy engine however much of it lies inside the matrix, and what
+// lies outside costs more than what is read (77 x 100096 took 15.8 us at K = 128
+// in boxes of 128 bytes, half of each outside, and 10.9 us at K = 256).
+constexpr int kShortK = 128;  // columns
 
 struct ProdArgs {
   const uint8_t* a_scales;
@@ -34,6 +38,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           "r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+// Operand tile in shared memory: K-major rows of KB bytes, swizzled over KB bytes,
+// 8-row groups 8 KB bytes apart.
+template <int KB>
+__device__ __forceinline__ uint64_t code_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(8 * KB >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(KB == 128 ? 2 : 4) << 61);
 }
 // Scale tile in shared memory: 32 rows of 16 bytes, no swizzle, 8-row groups
 // 128 bytes apart.
@@ -107,8 +118,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t at, int dtype, floa
   else
     static_cast<__half*>(out)[at] = __float2half_rn(v);
 }
-// Tensor map over packed code rows; a box is 128 bytes of K by box_rows rows.
-int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows);
+// Tensor map over packed code rows; a box is kb bytes of K by box_rows rows.
+int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int kb,
+                 int box_rows);
 
 // The wide kernel (fp4_wide.cu).
 int fp4_product_wide(const uint8_t* a, const uint8_t* b, const ProdArgs& p, int fmt,

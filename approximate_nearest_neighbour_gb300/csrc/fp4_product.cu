@@ -39,15 +39,17 @@ int fp4_quantize_device(const void* x, int dtype, int64_t rows, int64_t cols, in
                         const float* tensor_scale, uint8_t* codes, uint8_t* scales,
                         cudaStream_t s);
 
-int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int box_rows) {
+int fp4_code_map(CUtensorMap* m, const uint8_t* p, int64_t rows, int64_t pitch, int kb,
+                 int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   IVFPQ_TRY(tensor_map_encoder(&enc));
   cuuint64_t dims[2] = {cuuint64_t(pitch), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(pitch)};
-  cuuint32_t box[2] = {KB, cuuint32_t(box_rows)};
+  cuuint32_t box[2] = {cuuint32_t(kb), cuuint32_t(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   kb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld code bytes", int(r),
@@ -61,14 +63,15 @@ namespace {
 
 constexpr int kThreads = 192;
 
-template <int FMT, int T>
+template <int FMT, int T, int KB>
 struct Cfg {
-  static constexpr int kTilesPerStage = FMT == IVFPQ_MXFP4 ? 2 : 4;  // scale tiles of 256 columns
+  static constexpr int KE = 2 * KB;  // K columns per stage
+  static constexpr int kTilesPerStage = KE / (FMT == IVFPQ_MXFP4 ? 128 : 64);  // scale tiles
   static constexpr int kSf = kTilesPerStage * 512;
   static constexpr int kB = BN * KB;
   static constexpr int kA = T * KB;
   static constexpr int kStage = kB + kA + 2 * kSf;
-  static constexpr int kStages = T <= 32 ? 4 : 3;
+  static constexpr int kStages = KB < 128 ? 1 : T <= 32 ? 4 : 3;  // short K is one stage
   static constexpr int kBars = 256;
   static constexpr int kTotal = kStages * kStage + kBars + 1024;
   // TMEM: the accumulator, then each stage's scales of b and of a
@@ -76,15 +79,17 @@ struct Cfg {
   static constexpr int kAccCols = T < 32 ? 32 : T;
   static constexpr int kUsed = kAccCols + kStages * kSfCols;
   static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
-  static_assert(kUsed <= 256 && kTotal > 76 * 1024, "two CTAs per SM, and their TMEM fits");
+  static_assert(kUsed <= 256 && (KB < 128 || kTotal > 76 * 1024),
+                "two CTAs that may wait for others per SM, and their TMEM fits");
 };
 
 // grid (column tiles, row tiles, K slices); the cluster is the K slices.
-template <int FMT, int T>
+template <int FMT, int T, int KB>
 __global__ void __launch_bounds__(kThreads)
 fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_a, const ProdArgs p) {
-  using C = Cfg<FMT, T>;
+  using C = Cfg<FMT, T, KB>;
+  constexpr int KE = C::KE;
   extern __shared__ uint8_t fp4_smem_raw[];
   const uint32_t raw = smem_u32(fp4_smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -172,7 +177,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   } else if (warp == 1) {
     // ---- scale copies and products: the whole warp runs, one lane issues ----
     const uint32_t el = elect_one();
-    const uint64_t d_b = smem_desc(s_b(0)), d_a = smem_desc(s_a(0)), d_sf = scale_desc(s_sfb(0));
+    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0)), d_sf = scale_desc(s_sfb(0));
     uint32_t s = 0, phase = 0;
     for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc) {
       if (!mbar_wait(bar_full(s), phase)) {
@@ -193,9 +198,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
       }
       const uint64_t db = d_b + s * uint32_t((C::kB + C::kA) >> 4);
       const uint64_t da = d_a + s * uint32_t((C::kB + C::kA) >> 4);
-      const int steps = min(4, (p.kp - kc * KE + 63) / 64);
+      const int steps = min(KB / 32, (p.kp - kc * KE + 63) / 64);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < KB / 32; ++j) {
         if (j < steps) {
           const int t = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
           const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
@@ -293,13 +298,14 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   }
 }
 
-template <int FMT, int T>
+template <int FMT, int T, int KB>
 int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
-  using C = Cfg<FMT, T>;
+  using C = Cfg<FMT, T, KB>;
+  constexpr int KE = C::KE;
   CUtensorMap mb, ma;
-  IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, BN));
-  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, T));
-  auto kern = fp4_product_kernel<FMT, T>;
+  IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, KB, BN));
+  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, KB, T));
+  auto kern = fp4_product_kernel<FMT, T, KB>;
   IVFPQ_TRY(set_dynamic_smem(kern, C::kTotal));
   const int64_t tiles_n = ceil_div(p.n, BN), tiles_m = ceil_div(p.m, T);
   const int64_t nk = ceil_div(p.kp, KE);
@@ -326,14 +332,14 @@ int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   return IVFPQ_OK;
 }
 
-template <int FMT>
+template <int FMT, int KB>
 int launch_fmt(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
   // the narrowest instruction that holds all rows; a narrow one starts at row
   // 0 of its scale tile, so it is only taken where one row tile covers m
-  if (p.m <= 16) return launch<FMT, 16>(a, b, p, s);
-  if (p.m <= 32) return launch<FMT, 32>(a, b, p, s);
-  if (p.m <= 64) return launch<FMT, 64>(a, b, p, s);
-  return launch<FMT, 128>(a, b, p, s);
+  if (p.m <= 16) return launch<FMT, 16, KB>(a, b, p, s);
+  if (p.m <= 32) return launch<FMT, 32, KB>(a, b, p, s);
+  if (p.m <= 64) return launch<FMT, 64, KB>(a, b, p, s);
+  return launch<FMT, 128, KB>(a, b, p, s);
 }
 
 int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
@@ -356,8 +362,11 @@ int product_device(const uint8_t* a, const uint8_t* a_scales, int64_t m, const u
   // enough 128 x 128 tiles to keep every SM busy without splitting K
   if (m > 64 && ceil_div(n, BN) * ceil_div(m, 128) >= num_sms())
     return fp4_product_wide(a, b, p, fmt, s);
-  return fmt == IVFPQ_MXFP4 ? launch_fmt<IVFPQ_MXFP4>(a, b, p, s)
-                            : launch_fmt<IVFPQ_NVFP4>(a, b, p, s);
+  if (p.kp <= kShortK)
+    return fmt == IVFPQ_MXFP4 ? launch_fmt<IVFPQ_MXFP4, 64>(a, b, p, s)
+                              : launch_fmt<IVFPQ_NVFP4, 64>(a, b, p, s);
+  return fmt == IVFPQ_MXFP4 ? launch_fmt<IVFPQ_MXFP4, 128>(a, b, p, s)
+                            : launch_fmt<IVFPQ_NVFP4, 128>(a, b, p, s);
 }
 
 int check_product(const char* fn, int64_t m, int64_t n, int64_t cols, int fmt, int dtype) {

@@ -31,9 +31,10 @@ constexpr int kSfBase = 416;  // first TMEM column of the scales
 constexpr int64_t kL2Bytes = int64_t(129) << 20;
 constexpr int kBounce = 8 * BN * 4;  // 8 rows of a tile on their way out, per half of the warps
 
-template <int FMT, int T, int CG>
+template <int FMT, int T, int CG, int KB>
 struct WideCfg {
-  static constexpr int kTiles = FMT == IVFPQ_MXFP4 ? 2 : 4;  // scale tiles per stage and 128 rows
+  static constexpr int KE = 2 * KB;  // K columns per stage
+  static constexpr int kTiles = KE / (FMT == IVFPQ_MXFP4 ? 128 : 64);  // scale tiles per stage
   static constexpr int kRt = T / 128;
   static constexpr int kSfTile = kTiles * 512;
   static constexpr int kB = BN * KB;
@@ -217,13 +218,14 @@ struct Tiling {
   int m_fast;   // consecutive tiles go along m
 };
 
-template <int FMT, int T, int CG, class O>
+template <int FMT, int T, int CG, int KB, class O>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_a,
                 const __grid_constant__ CUtensorMap map_sb,
                 const __grid_constant__ CUtensorMap map_sa, const ProdArgs p, const Tiling tl) {
-  using C = WideCfg<FMT, T, CG>;
+  using C = WideCfg<FMT, T, CG, KB>;
+  constexpr int KE = C::KE;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t fp4_wide_smem[];
   const uint32_t raw = smem_u32(fp4_wide_smem);
@@ -331,7 +333,7 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
   } else if (warp == 1 && rank == 0) {
     // ---- scales and products of both CTAs: the whole warp runs, one lane issues ----
     const uint32_t el = elect_one();
-    const uint64_t d_b = smem_desc(s_b(0)), d_a = smem_desc(s_a(0)), d_sf = scale_desc(s_sf(0));
+    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0)), d_sf = scale_desc(s_sf(0));
     const int last_tiles = p.ntile - (nk - 1) * C::kTiles;
     const int last_steps = (p.kp - (nk - 1) * KE + 63) / 64;
     uint32_t s = 0, phase = 0;       // stage, its parity
@@ -373,9 +375,9 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
         }
         const uint64_t db = d_b + s * uint32_t((C::kB + C::kA) >> 4);
         const uint64_t da = d_a + s * uint32_t((C::kB + C::kA) >> 4);
-        const int steps = last ? last_steps : 4;
+        const int steps = last ? last_steps : KB / 32;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KB / 32; ++j) {
           if (j < steps) {
             const int q = FMT == IVFPQ_MXFP4 ? j >> 1 : j;
             const uint32_t id = FMT == IVFPQ_MXFP4 ? uint32_t(j & 1) * 2 : 0u;
@@ -517,15 +519,15 @@ int scale_map(CUtensorMap* m, const uint8_t* p, int64_t tiles, int box) {
   return IVFPQ_OK;
 }
 
-template <int FMT, int T, int CG, class O>
+template <int FMT, int T, int CG, int KB, class O>
 int launch(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s) {
-  using C = WideCfg<FMT, T, CG>;
+  using C = WideCfg<FMT, T, CG, KB>;
   CUtensorMap mb, ma, msb, msa;
-  IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, BN));
-  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, T / CG));
+  IVFPQ_TRY(fp4_code_map(&mb, b, p.n, p.kp / 2, KB, BN));
+  IVFPQ_TRY(fp4_code_map(&ma, a, p.m, p.kp / 2, KB, T / CG));
   IVFPQ_TRY(scale_map(&msb, p.b_scales, ceil_div(p.n, 128) * p.ntile, C::kTiles));
   IVFPQ_TRY(scale_map(&msa, p.a_scales, ceil_div(p.m, 128) * p.ntile, C::kTiles));
-  auto kern = fp4_wide_kernel<FMT, T, CG, O>;
+  auto kern = fp4_wide_kernel<FMT, T, CG, KB, O>;
   IVFPQ_TRY(set_dynamic_smem(kern, C::kTotal));
   Tiling tl;
   tl.tn = int(ceil_div(p.n, CG * BN));
@@ -568,12 +570,15 @@ int choose(const uint8_t* a, const uint8_t* b, const ProdArgs& p, cudaStream_t s
   const int64_t tn = ceil_div(p.n, BN), sms = num_sms();
   const double w128 = 0.65 * double(ceil_div(tn * ceil_div(p.m, 128), sms));
   const double w256 = double(ceil_div(tn * ceil_div(p.m, 256), sms));
-  if (w128 < w256) return launch<FMT, 128, 1, O>(a, b, p, s);
+  if (p.kp <= kShortK)
+    return w128 < w256 ? launch<FMT, 128, 1, 64, O>(a, b, p, s)
+                       : launch<FMT, 256, 1, 64, O>(a, b, p, s);
+  if (w128 < w256) return launch<FMT, 128, 1, 128, O>(a, b, p, s);
   // Pairs where K is long and there are many tiles (8192 x 16384 x 4096: 183 us,
   // and 194 us on single CTAs); a pair's hand-over between tiles costs more
   // (1000 x 100000 x 1024: 102 us, and 86 us).
-  if (p.kp >= 8 * KE && w256 >= 8) return launch<FMT, 256, 2, O>(a, b, p, s);
-  return launch<FMT, 256, 1, O>(a, b, p, s);
+  if (p.kp >= 2048 && w256 >= 8) return launch<FMT, 256, 2, 128, O>(a, b, p, s);
+  return launch<FMT, 256, 1, 128, O>(a, b, p, s);
 }
 
 }  // namespace
