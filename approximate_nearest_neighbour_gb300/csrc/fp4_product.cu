@@ -9,9 +9,9 @@
 // and a few rows of a cost a narrow instruction instead of a padded one.
 //
 // One CTA per (128 columns of out, T rows of out, slice of K), 6 warps:
-//  * warp 0, one thread: TMA producer. A stage is 256 columns of K: 128 rows
-//    of b and T rows of a (128 bytes each, 128-byte swizzle) and their scale
-//    tiles, which are contiguous;
+//  * warp 0, one thread: TMA producer. A stage is 256 columns of K (128 where
+//    that is all of K): 128 rows of b and T rows of a and their scale tiles,
+//    which are contiguous;
 //  * warp 1: TMEM; one thread copies a stage's scale tiles to TMEM and issues
 //    one product per 64 columns. Each stage has TMEM columns of its own for
 //    its scales: they are rewritten only after the stage's products committed;
@@ -26,9 +26,9 @@
 //
 // A cluster splits K between its CTAs when there are few tiles; the partial
 // sums are joined in rank order through distributed shared memory. Shared
-// memory lets at most two CTAs of any variant share an SM, and two always fit
-// its 512 TMEM columns: no CTA of a cluster waits for TMEM that another
-// cluster holds while it waits itself.
+// memory lets at most two CTAs of a variant that may be split share an SM, and
+// two always fit its 512 TMEM columns: no CTA of a cluster waits for TMEM that
+// another cluster holds while it waits itself. (Short K is never split.)
 #include <algorithm>
 
 #include "fp4_mma.cuh"
