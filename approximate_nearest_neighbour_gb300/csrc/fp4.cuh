@@ -78,13 +78,19 @@ __device__ __forceinline__ float e8m0_value(uint8_t s) {
 //  MXFP4: the scale is 2^(floor(log2(amax)) - 2), so amax / scale lies in
 //         [4, 8); the exponent is read off the bits, the factor is exact.
 //  NVFP4: the scale is amax / (6 g) rounded to E4M3 (saturating at 448); the
-//         factor is 1 / (scale * g), one IEEE division per block.
+//         factor is 1 / (scale * g), one IEEE division per block. With a g for which
+//         scale * g may be subnormal (inexact, and its reciprocal may pass fp32) the
+//         values are multiplied by lift = 2^64 and the factor is that of g * lift;
+//         else lift is 1.
+__device__ __forceinline__ float nvfp4_lift(float g) {
+  return g < 0x1p-117f ? 0x1p64f : 1.f;  // the smallest scale is 2^-9
+}
 struct BlockScale {
   uint8_t byte;
   float factor;
 };
 template <int FMT>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g, float lift) {
   BlockScale r;
   if (amax_bits >= 0x7f800000u) {
     r.byte = FMT == IVFPQ_MXFP4 ? 0xff : 0x7f;
@@ -98,9 +104,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
   } else {
     r.byte = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax_bits), 6.f * g), __NV_SATFINITE,
                                    __NV_E4M3);
-    const float sv = e4m3_value(r.byte) * g;
+    const float sv = e4m3_value(r.byte) * (g * lift);
     r.factor = sv > 0.f ? __fdiv_rn(1.f, sv) : 0.f;
-    if (isinf(r.factor)) r.factor = 0.f;
   }
   return r;
 }

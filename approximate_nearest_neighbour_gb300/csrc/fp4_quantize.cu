@@ -90,7 +90,12 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const QuantArgs a) {
   if (live) amax = load16(static_cast<const T*>(a.x) + row * a.ldx, c0, a.cols, a.vec, v);
 #pragma unroll
   for (int o = 1; o < LB; o *= 2) amax = max(amax, __shfl_xor_sync(kFullMask, amax, o));
-  const BlockScale bs = block_scale<FMT>(amax, g);
+  const float lift = FMT == IVFPQ_NVFP4 ? nvfp4_lift(g) : 1.f;
+  const BlockScale bs = block_scale<FMT>(amax, g, lift);
+  if (FMT == IVFPQ_NVFP4 && lift != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= lift;
+  }
   if (live) {
     uint32_t c[2];
 #pragma unroll
