@@ -102,8 +102,12 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g, f
     r.byte = uint8_t(max(eb - 2, 0));
     r.factor = __int_as_float(uint32_t(254 - int(r.byte)) << 23);
   } else {
-    r.byte = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax_bits), 6.f * g), __NV_SATFINITE,
-                                   __NV_E4M3);
+    // 6 g passes fp32 for the largest g: an eighth of both sides then (exact; a
+    // magnitude it makes subnormal is far below the smallest scale)
+    const float eighth = g > 0x1p125f ? 0.125f : 1.f;
+    r.byte = __nv_cvt_float_to_fp8(
+        __fdiv_rn(__uint_as_float(amax_bits) * eighth, 6.f * eighth * g), __NV_SATFINITE,
+        __NV_E4M3);
     const float sv = e4m3_value(r.byte) * (g * lift);
     r.factor = sv > 0.f ? __fdiv_rn(1.f, sv) : 0.f;
   }

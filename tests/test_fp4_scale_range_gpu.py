@@ -41,3 +41,11 @@ def test_small_scales(B, e, mantissa):
     _round_trip(B, x, g)
     x[5, 3], x[9, 20] = 1.0, -3e38  # far above what the scale can hold: saturates
     _round_trip(B, x, g)
+
+
+@pytest.mark.parametrize("g", [2.0 ** 125, 2.0 ** 126, 1.75 * 2.0 ** 126])
+def test_large_scales(B, g):
+    """Six times the matrix's scale passes fp32."""
+    r = np.random.default_rng(7)
+    x = (r.uniform(-1, 1, (40, 96)) * 2.0 ** r.uniform(118, 127, (40, 1))).astype(np.float32)
+    _round_trip(B, x, g)
