@@ -183,8 +183,12 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
   const float rep = HIST && a.repetition ? a.repetition[row] : 1.f;
   const float pres = HIST && a.presence ? a.presence[row] : 0.f;
   const float freq = HIST && a.frequency ? a.frequency[row] : 0.f;
-  // the division by the temperature and the sign, as one factor per row
-  const float f = (a.temperature ? __fdiv_rn(1.f, a.temperature[row]) : 1.f) * a.sign;
+  // the division by the temperature and the sign, as one factor per row; as two
+  // where the temperature is subnormal, whose reciprocal may pass fp32
+  const float t = a.temperature ? a.temperature[row] : 1.f;
+  const bool twice = t != 0.f && fabsf(t) < 0x1p-126f;
+  const float up = twice ? 0x1p64f : 1.f;
+  const float f = __fdiv_rn(a.sign, t * up);
   const float masked = -INFINITY * a.sign;
   auto marked = [&](int c, float x) {
     const uint32_t e = count[c];
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
   auto one = [&](int c) {
     float x = to_f32(src[c]);
     if (MARK && (mark[c >> 5] >> (c & 31)) & 1u) x = marked(c, x);
-    x *= f;
+    x = x * f * up;
     if (MASK && !((uint32_t(mask[c >> 5]) >> (c & 31)) & 1u)) x = masked;
     dst[c] = from_f32<O>(x);
   };
@@ -221,6 +225,10 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       unpack_vec<T>(r[u], v);
 #pragma unroll
       for (int j = 0; j < N; j += 2) unpair(mul2(pair(v[j], v[j + 1]), pair(f, f)), v[j], v[j + 1]);
+      if (twice) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= up;
+      }
       if constexpr (MASK) {
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = (ok[u] >> j) & 1u ? v[j] : masked;
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
         while (m) {
           const int j = __ffs(m) - 1, c = head + i * N + j;
           m &= m - 1;
-          dst[c] = from_f32<O>(marked(c, vec_element<T>(r[u], j)) * f);
+          dst[c] = from_f32<O>(marked(c, vec_element<T>(r[u], j)) * f * up);
         }
       }
     }
