@@ -183,12 +183,9 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
   const float rep = HIST && a.repetition ? a.repetition[row] : 1.f;
   const float pres = HIST && a.presence ? a.presence[row] : 0.f;
   const float freq = HIST && a.frequency ? a.frequency[row] : 0.f;
-  // the division by the temperature and the sign, as one factor per row; as two
-  // where the temperature is subnormal, whose reciprocal may pass fp32
+  // the division by the temperature and the sign, as one factor per row
   const float t = a.temperature ? a.temperature[row] : 1.f;
-  const bool twice = t != 0.f && fabsf(t) < 0x1p-126f;
-  const float up = twice ? 0x1p64f : 1.f;
-  const float f = __fdiv_rn(a.sign, t * up);
+  const float f = __fdiv_rn(a.sign, t);
   const float masked = -INFINITY * a.sign;
   auto marked = [&](int c, float x) {
     const uint32_t e = count[c];
@@ -204,14 +201,20 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     }
     return x;
   };
-  auto one = [&](int c) {
+  auto one = [&](int c, bool divide) {
     float x = to_f32(src[c]);
     if (MARK && (mark[c >> 5] >> (c & 31)) & 1u) x = marked(c, x);
-    x = x * f * up;
+    x = divide ? __fdiv_rn(x, t) * a.sign : x * f;
     if (MASK && !((uint32_t(mask[c >> 5]) >> (c & 31)) & 1u)) x = masked;
     dst[c] = from_f32<O>(x);
   };
-  for (int e = threadIdx.x; e < len - nvec * N; e += kThreads) one(e < head ? e : nvec * N + e);
+  if (t != 0.f && fabsf(t) < 0x1p-126f) {
+    // a subnormal temperature, whose reciprocal may pass fp32: score by score
+    for (int c = threadIdx.x; c < len; c += kThreads) one(c, true);
+    return;
+  }
+  for (int e = threadIdx.x; e < len - nvec * N; e += kThreads)
+    one(e < head ? e : nvec * N + e, false);
   for (int i0 = threadIdx.x; i0 < nvec; i0 += U * kThreads) {
     if (i0 != int(threadIdx.x)) {
       load_mask(i0);
@@ -225,10 +228,6 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
       unpack_vec<T>(r[u], v);
 #pragma unroll
       for (int j = 0; j < N; j += 2) unpair(mul2(pair(v[j], v[j + 1]), pair(f, f)), v[j], v[j + 1]);
-      if (twice) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] *= up;
-      }
       if constexpr (MASK) {
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = (ok[u] >> j) & 1u ? v[j] : masked;
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
         while (m) {
           const int j = __ffs(m) - 1, c = head + i * N + j;
           m &= m - 1;
-          dst[c] = from_f32<O>(marked(c, vec_element<T>(r[u], j)) * f * up);
+          dst[c] = from_f32<O>(marked(c, vec_element<T>(r[u], j)) * f);
         }
       }
     }
