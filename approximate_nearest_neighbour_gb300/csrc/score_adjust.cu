@@ -121,33 +121,34 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
   if constexpr (MARK) {
     const int32_t* h = HIST && a.history ? a.history + row * a.ldh : nullptr;
     const int32_t* bi = BIAS && a.bias_ids ? a.bias_ids + row * a.nb : nullptr;
-    const int hcols = h ? int(a.hist_cols) : 0;
+    // counters are unsigned: one step past a list of up to 2^31 - 1 does not wrap
+    const uint32_t hcols = h ? uint32_t(a.hist_cols) : 0;
     // the first tokens are on their way before their number is known
     constexpr int V = 8;
     int32_t t[V];
-    auto load_tokens = [&](int i0, int end) {
+    auto load_tokens = [&](uint32_t i0, uint32_t end) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
         t[v] = i0 + v * kThreads < end ? __ldg(h + i0 + v * kThreads) : -1;
     };
     if (HIST) load_tokens(threadIdx.x, hcols);
-    int n = hcols, np = 0;
+    uint32_t n = hcols, np = 0;
     if (HIST && h) {
-      if (a.history_len) n = max(0, min(n, a.history_len[row]));
-      if (a.prompt_len) np = a.prompt_len[row];
+      if (a.history_len) n = min(n, uint32_t(max(0, a.history_len[row])));
+      if (a.prompt_len) np = uint32_t(max(0, a.prompt_len[row]));
     }
     const int clear = a.run / 32 + a.run * (SHORT ? 1 : 2);  // a multiple of 4 words
     for (int i = threadIdx.x; i < clear / 4; i += kThreads)
       reinterpret_cast<uint4*>(mark)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     if (HIST) {
-      for (int i0 = threadIdx.x; i0 < n; i0 += V * kThreads) {
-        if (i0 != int(threadIdx.x)) load_tokens(i0, n);
+      for (uint32_t i0 = threadIdx.x; i0 < n; i0 += V * kThreads) {
+        if (i0 != threadIdx.x) load_tokens(i0, n);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           // out of the run (or of the row, or negative): past len
           const uint32_t c = uint32_t(t[v]) - uint32_t(c0);
-          const int i = i0 + v * kThreads;
+          const uint32_t i = i0 + v * kThreads;
           if (c < uint32_t(len) && i < n) {
             atomicOr(&mark[c >> 5], 1u << (c & 31));
             if (i < np)
@@ -160,20 +161,20 @@ __global__ void __launch_bounds__(kThreads, 5) score_adjust_kernel(const AdjustA
     }
     if (BIAS) {
       if (HIST && SHORT) __syncthreads();  // the counters are complete
-      for (int i = threadIdx.x; i < int(a.nb); i += kThreads) {
+      for (uint32_t i = threadIdx.x; i < uint32_t(a.nb); i += kThreads) {
         const int64_t c = int64_t(__ldg(bi + i)) - c0;
         if (c >= 0 && c < len) {
           atomicOr(&mark[c >> 5], 1u << (c & 31));
           if (SHORT) {
             uint32_t old = slot[c];
-            while ((old >> 16) < uint32_t(i) + 1u) {
+            while ((old >> 16) < i + 1u) {
               const uint32_t seen =
-                  atomicCAS(&slot[c], old, (old & 0xffffu) | ((uint32_t(i) + 1u) << 16));
+                  atomicCAS(&slot[c], old, (old & 0xffffu) | ((i + 1u) << 16));
               if (seen == old) break;
               old = seen;
             }
           } else {
-            atomicMax(&slot[c], uint32_t(i) + 1u);
+            atomicMax(&slot[c], i + 1u);
           }
         }
       }
