@@ -47,6 +47,37 @@ int device_status_word(int** out) {
   return IVFPQ_OK;
 }
 
+// One pool per device, made on first use and kept while the library is loaded.
+// A pool gives what is free back to the device at every synchronisation, down to
+// its release threshold, and the default pool's is 0: a program that waits after
+// each call had its workspace mapped anew each time (fp4_linear of one token,
+// 32000 x 4096, with a wait after each call: 196 us, and 31 us from this pool).
+constexpr uint64_t kKeptWorkspace = uint64_t(256) << 20;
+static std::mutex g_pool_mu;
+static cudaMemPool_t g_pool[64] = {};
+
+int workspace_pool(cudaMemPool_t* out) {
+  int dev = 0;
+  IVFPQ_CUDA(cudaGetDevice(&dev));
+  IVFPQ_REQUIRE(dev >= 0 && dev < 64, "device %d not supported", dev);
+  std::lock_guard<std::mutex> lock(g_pool_mu);
+  if (!g_pool[dev]) {
+    cudaMemPoolProps props{};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t p = nullptr;
+    IVFPQ_CUDA(cudaMemPoolCreate(&p, &props));
+    uint64_t keep = kKeptWorkspace;
+    const cudaError_t e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) cudaMemPoolDestroy(p);
+    IVFPQ_CUDA(e);
+    g_pool[dev] = p;
+  }
+  *out = g_pool[dev];
+  return IVFPQ_OK;
+}
+
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 static std::once_flag g_encode_once;
 

@@ -72,6 +72,9 @@ void count_workspace_alloc();
   } while (0)
 
 // ---- stream-ordered workspace --------------------------------------------------
+// The current device's pool for workspace (abi_util.cu).
+int workspace_pool(cudaMemPool_t* out);
+
 // Frees its allocations on the stream (stream-ordered) when it goes out of
 // scope, so a failing call never leaks workspace.
 class Workspace {
@@ -88,8 +91,10 @@ class Workspace {
       set_error("internal: too many workspace buffers");
       return IVFPQ_ERR_CUDA;
     }
+    cudaMemPool_t pool;
+    IVFPQ_TRY(workspace_pool(&pool));
     void* p = nullptr;
-    cudaError_t e = cudaMallocAsync(&p, count * sizeof(T), s_);
+    cudaError_t e = cudaMallocFromPoolAsync(&p, count * sizeof(T), pool, s_);
     if (e != cudaSuccess) {
       cudaGetLastError();
       set_error("workspace allocation of %zu bytes failed: %s", count * sizeof(T),

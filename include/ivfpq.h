@@ -30,8 +30,9 @@
  *  - Distances are squared L2 distances. Results are ordered by ascending
  *    distance; when fewer than k results exist the tail is (+inf, -1). The
  *    order of equal distances is unspecified.
- *  - Workspace is taken from the device's stream-ordered memory pool
- *    (cudaMallocAsync) on `stream` and returned on the same stream.
+ *  - Workspace is taken from a stream-ordered memory pool that the library makes
+ *    on each device (cudaMallocFromPoolAsync) on `stream` and returned on the same
+ *    stream; the pool keeps up to 256 MiB for the next calls.
  *  - Search calls on one index may run concurrently on different streams;
  *    ivfpq_add must not overlap a search of the same index.
  */
