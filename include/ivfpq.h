@@ -450,13 +450,17 @@ typedef enum {
  * fp4_quantize -- rows to 4-bit block-scaled form.
  * MXFP4: block scale 2^e, e = floor(log2(amax)) - 2 clamped to [-127, 127].
  * NVFP4: block scale s = E4M3(min(448, amax / (6 g))), g = *tensor_scale, and
- * a value stands for element * s * g. Elements are x / scale rounded to
- * nearest (ties to the even code), saturating at 6. A block that holds an
- * infinity or a NaN gets a NaN scale and reads back as NaN.
+ * a value stands for element * s * g. Elements are rounded to nearest (ties to
+ * the even code), saturating at 6: x / 2^e exactly for MXFP4, x * (1 / (s g))
+ * for NVFP4, where 6 g, s g, the reciprocal and the product are each rounded to
+ * fp32, so that a value within 2^-21 of a midpoint may get either neighbour (and
+ * so may a block's scale). A block whose s rounds to 0 has zero codes. A block
+ * that holds an infinity or a NaN gets a NaN scale and reads back as NaN.
  *  x       device [rows, cols] of dtype, row stride ldx elements (>= cols, or
  *          0 to repeat one row); cols need not be a multiple of the block:
  *          the last block is short
- *  tensor_scale  device fp32 [1], > 0 (NVFP4; NULL = 1); ignored for MXFP4
+ *  tensor_scale  device fp32 [1], > 0 and finite (NVFP4; NULL = 1); ignored for
+ *          MXFP4
  *  codes   device uint8 [rows, kp / 2] (out), kp = cols rounded up to 32: two
  *          codes per byte, the even column in the low half, zero past cols
  *  scales  device uint8 (out), tiles of 128 rows x 4 blocks, 512 bytes each,
@@ -464,7 +468,8 @@ typedef enum {
  *          (r % 32) * 16 + (r / 32 % 4) * 4 + c % 4 of its tile; bytes of rows
  *          and blocks beyond the matrix are zero, and must be where a caller
  *          lays scales out
- * codes and scales start on 16-byte boundaries. Errors: INVALID_ARG, CUDA.
+ * codes and scales start on 16-byte boundaries; rows < 2^31, cols <= 2^24 in
+ * every fp4_ call. Errors: INVALID_ARG, CUDA.
  */
 int fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt,
                  const float* tensor_scale, uint8_t* codes, uint8_t* scales, void* stream);
@@ -472,7 +477,7 @@ int fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t l
 /*
  * fp4_dequantize -- the values that packed rows stand for, [rows, cols] of
  * dtype (densely packed): element * block scale in fp32 (exact), times
- * *tensor_scale (NVFP4), rounded once to dtype. Errors: INVALID_ARG, CUDA.
+ * *tensor_scale in fp32 (NVFP4), then rounded to dtype. Errors: INVALID_ARG, CUDA.
  */
 int fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                    int fmt, const float* tensor_scale, void* out, int dtype, void* stream);
@@ -480,14 +485,16 @@ int fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, in
 /*
  * fp4_product -- inner products of packed rows:
  *   out[i, j] = ga gb sum_t a[i, t] b[j, t]
- * on the block-scaled tensor-core product, accumulated in fp32, rounded once
- * to dtype. Both operands have the same format and cols (layout as written by
- * fp4_quantize); ga, gb are the matrices' fp32 scales (device fp32 [1], NULL =
- * 1; NVFP4 only). Many rows or a single one: the narrow case reads b once.
+ * on the block-scaled tensor-core product: the sum is accumulated in fp32, ga gb
+ * is rounded to fp32 (where that underflows or overflows, so does the result), and
+ * their product is rounded to fp32 and then to dtype. Both operands have the same
+ * format and cols (layout as written by fp4_quantize); ga, gb are the matrices'
+ * fp32 scales (device fp32 [1], NULL = 1; NVFP4 only). Many rows or a single one:
+ * the narrow case reads b once.
  * The sum over cols is split in an order fixed by the sizes, so results
  * repeat bit for bit.
  *  out  device [m, n] of dtype, densely packed
- * m <= 8,388,480 rows. Errors: INVALID_ARG, CUDA.
+ * m <= 8,388,480 rows, n < 2^31 - 1024. Errors: INVALID_ARG, CUDA.
  */
 int fp4_product(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                 const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t cols, int fmt,
@@ -515,7 +522,8 @@ int fp4_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const uint8_t
  *   x /= temperature
  *   c not allowed by the mask:  x = -inf (whatever the score was)
  *   negate != 0:                x = -x (kselect selects the smallest)
- * computed in fp32 and rounded once.
+ * computed in fp32 (the division by a normal temperature as a product with its
+ * reciprocal) and rounded once. rows, hist_cols and nb < 2^31, cols <= 2^28.
  *  scores        device [rows, cols] of dtype, row stride lds (0 repeats a row)
  *  history       device int32 [rows, hist_cols], row stride ldh, or NULL;
  *                entries outside [0, cols) are ignored
@@ -557,7 +565,8 @@ int score_adjust(const void* scores, int dtype, int64_t rows, int64_t cols, int6
  *                +inf where a valid entry's score is -inf
  *  stats         device fp32 [rows, 2] (out): the row's largest score m and
  *                sum_j exp((s_j - m) / tau), for topk_distill_backward
- * 1 <= k <= IVFPQ_MAX_K. A score of -inf has q = 0. Errors: INVALID_ARG, CUDA.
+ * 1 <= k <= IVFPQ_MAX_K, rows < 2^31, cols <= 2^28, temperature from 1e-30 to
+ * 1e30. A score of -inf has q = 0. Errors: INVALID_ARG, CUDA.
  */
 int topk_distill_forward(const void* scores, int dtype, int64_t rows, int64_t cols, int64_t lds,
                          const float* teacher_vals, const int64_t* teacher_ids, int k,
