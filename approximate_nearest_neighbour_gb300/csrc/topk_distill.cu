@@ -39,6 +39,7 @@ struct DistillArgs {
   const int64_t* ti;
   int k;
   float tau, inv_tau, sign;
+  float tau_small, tau_large;  // tau kSmall, tau / kSmall
   const float* row_grad;
   float* loss;
   float* stats;  // [rows, 2]
@@ -186,7 +187,10 @@ __device__ __forceinline__ Online list_load(const DistillArgs& a, int64_t row, c
 }
 
 // What the loss needs of a run of columns, with p and t over the entries in it:
-// sum p log p, sum p, sum p (s - m), m the run's own maximum.
+// sum p log p, sum p, sum p (s - m) kSmall, m the run's own maximum. kSmall, a
+// power of two, leaves room above: a list masked throughout by fp32's lowest value
+// has differences of that size, and its weights may sum to a little more than 1.
+constexpr float kSmall = 0x1p-8f;
 struct LossPart {
   float a = 0.f, p = 0.f, y = 0.f;
 };
@@ -211,7 +215,7 @@ __device__ __forceinline__ LossPart list_weights(const DistillArgs& a, const Lis
         const float s = get(id);
         r.a += p * ((v - t.m) * a.inv_tau - logtz);
         r.p += p;
-        r.y += p * (s == -INFINITY ? s : s - m);
+        r.y += p * kSmall * (s == -INFINITY ? s : s - m);
       }
       if (MARK && (atomicOr(&l.seen[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u) *repeated = 1;
     }
@@ -406,7 +410,7 @@ struct __align__(16) RowPart {
 };
 struct RowSum {
   Online all;
-  float x = 0.f, y = 0.f;  // sum p (log p + log Z), sum p (s - m)
+  float x = 0.f, y = 0.f;  // sum p (log p + log Z), sum p (s - m) kSmall
 };
 __device__ __forceinline__ RowSum row_join(const Online& o, const LossPart& part, RowPart* mine,
                                            int nranks, float c) {
@@ -439,7 +443,7 @@ __device__ __forceinline__ RowSum row_join(const Online& o, const LossPart& part
   m = __shfl_sync(kFullMask, m, 0);
   float z = rescaled(v.x, v.y, m, c), x = v.z, p = v.w;
   // the part's differences are from its own maximum
-  if (!(p == 0.f) && v.x != m) y += (v.x - m) * p;
+  if (!(p == 0.f) && v.x != m) y += (v.x - m) * (p * kSmall);
 #pragma unroll
   for (int d = kMaxCluster / 2; d; d /= 2) {
     z += __shfl_xor_sync(kFullMask, z, d);
@@ -453,6 +457,9 @@ __device__ __forceinline__ RowSum row_join(const Online& o, const LossPart& part
   s.y = y;
   s.x += (s.all.z == 0.f ? 0.f : logf(s.all.z)) * p;
   return s;
+}
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Online& t, const RowSum& r) {
+  return t.z == 0.f ? 0.f : a.tau_large * (a.tau_small * r.x - r.y);
 }
 __device__ __forceinline__ void cluster_leave(int nranks) {
   if (nranks > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_forward_kernel(const Dist
       block_loss(list_weights<true, false>(a, l, t, c, c0, len, o.m, nullptr, score), sh);
   const RowSum r = row_join(o, mine, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0) {
-    a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
+    a.loss[row] = row_loss(a, t, r);
     a.stats[2 * row] = r.all.m;
     a.stats[2 * row + 1] = r.all.z;
   }
@@ -581,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillArgs 
       block_loss(list_weights<true, true>(a, l, t, c, c0, len, o.m, &repeated, score), sh);
   const RowSum r = row_join(o, mine, &part, nranks, c);
   if (rank == 0 && threadIdx.x == 0)
-    a.loss[row] = t.z == 0.f ? 0.f : a.tau * (a.tau * r.x - r.y);
+    a.loss[row] = row_loss(a, t, r);
   if (w == 0.f || t.z == 0.f) {
     run_zero(g, len);
   } else {
@@ -623,6 +630,8 @@ DistillArgs distill_args(const void* scores, int64_t rows, int64_t cols, int64_t
   a.k = k;
   a.tau = temperature;
   a.inv_tau = 1.f / temperature;
+  a.tau_small = temperature * kSmall;
+  a.tau_large = temperature / kSmall;
   a.sign = negated ? -1.f : 1.f;
   return a;
 }
