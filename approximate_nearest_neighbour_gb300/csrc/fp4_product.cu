@@ -177,7 +177,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap map_b,
   } else if (warp == 1) {
     // ---- scale copies and products: the whole warp runs, one lane issues ----
     const uint32_t el = elect_one();
-    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0)), d_sf = scale_desc(s_sfb(0));
+    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0));
+    const uint64_t d_sf = scale_desc(s_sfb(0));
     uint32_t s = 0, phase = 0;
     for (int kc = k_lo; kc < k_hi && !*abort_flag; ++kc) {
       if (!mbar_wait(bar_full(s), phase)) {

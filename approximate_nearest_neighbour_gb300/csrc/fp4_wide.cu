@@ -333,7 +333,8 @@ fp4_wide_kernel(const __grid_constant__ CUtensorMap map_b,
   } else if (warp == 1 && rank == 0) {
     // ---- scales and products of both CTAs: the whole warp runs, one lane issues ----
     const uint32_t el = elect_one();
-    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0)), d_sf = scale_desc(s_sf(0));
+    const uint64_t d_b = code_desc<KB>(s_b(0)), d_a = code_desc<KB>(s_a(0));
+    const uint64_t d_sf = scale_desc(s_sf(0));
     const int last_tiles = p.ntile - (nk - 1) * C::kTiles;
     const int last_steps = (p.kp - (nk - 1) * KE + 63) / 64;
     uint32_t s = 0, phase = 0;       // stage, its parity

@@ -50,7 +50,8 @@ def _values(codes, scales, fmt):
     r = torch.arange(rows, device="cuda")[:, None]
     c = torch.arange(2 * pitch // blk, device="cuda")[None, :]
     s = scales[r // 128, c // 4, (r % 32) * 16 + (r // 32 % 4) * 4 + c % 4]
-    table = torch.tensor(R.scale_value(np.arange(256 if fmt == "mxfp4" else 128), fmt), device="cuda")
+    byte = np.arange(256 if fmt == "mxfp4" else 128)
+    table = torch.tensor(R.scale_value(byte, fmt), device="cuda")
     return (v * table[s.long()][..., None]).view(rows, -1)
 
 
@@ -100,7 +101,8 @@ def test_wide_product(B, fmt, m, n, cols):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("m,n,cols", [(300, 20_000, 2100), (700, 20_000, 100), (2500, 20_001, 2100)])
+@pytest.mark.parametrize("m,n,cols",
+                         [(300, 20_000, 2100), (700, 20_000, 100), (2500, 20_001, 2100)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_wide_linear(B, fmt, m, n, cols, dtype):
     """128-row tiles, short K, and pairs, started while the rows are still quantized."""

@@ -20,8 +20,9 @@ def test_the_longest_history():
     h[0, n - 2000] = 63
     x = torch.full((1, 64), 10.0, device="cuda")
     f = torch.ones((1,), device="cuda")
-    got = B.score_adjust(x, history=h, prompt_len=torch.tensor([n - 1000], dtype=torch.int32, device="cuda"),
-                         repetition=2 * f, frequency=f, presence=0.5 * f)
+    prompt = torch.tensor([n - 1000], dtype=torch.int32, device="cuda")
+    got = B.score_adjust(x, history=h, prompt_len=prompt, repetition=2 * f, frequency=f,
+                         presence=0.5 * f)
     want = torch.full((1, 64), 10.0)
     # 10 / 2, less one count and the presence penalty past the prompt
     want[0, 3], want[0, 5], want[0, 63] = 3.5, 3.5, 5.0

@@ -19,7 +19,7 @@ def test_temperatures_at_the_ends_of_fp32(B, dtype, listed, negate):
     """Scores over temperatures from 2^-149 to 2^127, zero and tiny scores among them.
     Three fp32 roundings (the factor, the product, the scaling back) and a bias that is 0."""
     import torch
-    t = np.array([2.0 ** -149, 1e-40, 2.0 ** -128, 2.0 ** -127, 2.0 ** -126, 1e-30, 1.0, 2.0 ** 127],
+    t = np.array([2.0 ** -149, 1e-40, 2.0 ** -128, 2.0 ** -127, 2.0 ** -126, 1e-30, 1, 2.0 ** 127],
                  np.float32)
     r = np.random.default_rng(2)
     x = (r.standard_normal((8, 77)) * 2.0 ** r.uniform(-140, 2, (8, 77))).astype(np.float32)

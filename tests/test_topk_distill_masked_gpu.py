@@ -26,7 +26,8 @@ def test_every_listed_column_at_the_lowest_value(dtype, cols, k, tau):
     s = torch.from_numpy((r.standard_normal((rows, cols)) * 3).astype(np.float32)).to(dt)
     s.scatter_(1, torch.from_numpy(ti), low)
     s = s.cuda()
-    tvd, tid, g = torch.from_numpy(tv).cuda(), torch.from_numpy(ti).cuda(), torch.ones(rows, device="cuda")
+    tvd, tid = torch.from_numpy(tv).cuda(), torch.from_numpy(ti).cuda()
+    g = torch.ones(rows, device="cuda")
     forward, stats = B.topk_distill_forward(s, tvd, tid, tau, negated=True)
     both, grad = B.topk_distill(s, tvd, tid, g, tau, negated=True)
     assert torch.equal(grad, B.topk_distill_backward(s, tvd, tid, stats, g, tau, negated=True))
