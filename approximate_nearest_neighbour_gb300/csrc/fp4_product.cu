@@ -21,8 +21,10 @@
 // CTAs per SM keep 160 KB per SM in flight. After fp4_linear's quantisation it
 // starts while that kernel runs (griddepcontrol) and has its first stages of b
 // on their way before a is complete. Measured with the quantisation, on the
-// device: one token, 32000 x 4096 MXFP4, 14.6 us (70 MB: 10.4 us at the measured
-// copy rate); 37 tokens, 16384 x 4096 NVFP4, 13.6 us (39 MB, 5.9 us).
+// device: one token, 32000 x 4096 MXFP4, 14.8 us (70 MB: 10.4 us at the measured
+// copy rate); 37 tokens, 16384 x 4096 NVFP4, 13.7 us (39 MB, 5.9 us). A CTA of
+// short K sets up barriers and TMEM for one stage: 16 x 100003 x 128 to fp32 7.2 us
+// (2.0 us for the bytes), 16 x 10,000,000 x 128 397 us (197 us).
 //
 // A cluster splits K between its CTAs when there are few tiles; the partial
 // sums are joined in rank order through distributed shared memory. Shared

@@ -6,7 +6,8 @@
 // the T rows of a, half in each CTA, so an SM takes in 38 KB per 256 columns
 // of K instead of 54 KB. Filling shared memory is close to a limit: 8192 x
 // 16384 x 4096 NVFP4 takes 157 us for the loads alone, 146 us for the products
-// alone and 194 us together on single CTAs, 183 us (6.0 PFLOP/s) in pairs. With
+// alone (64 columns of K an instruction) and 194 us together on single CTAs, 183 us
+// (6.0 PFLOP/s) in pairs; up to 218 us where the device lowers its clock. With
 // short K the result's bytes bound it: 10000 x 65536 x 96 to fp32 437 us, 2.6 GB
 // at 6.0 TB/s.
 //
@@ -167,7 +168,7 @@ __device__ __forceinline__ void store16(O* out, int64_t ldo, int r0, int64_t m, 
 // columns leave two sectors of each row half written, and those reach memory
 // apart: 10000 x 65535 x 96 took 1070 us, and 457 us with 65528 columns (32-byte
 // rows). Here four warps exchange 8 rows of 128 columns through shared memory and
-// each writes whole lines of two of them: 760 us, and 122 us instead of 147 us
+// each writes whole lines of two of them: 760 to 795 us, and 122 us instead of 147 us
 // at 1000 x 100003 x 128. Smaller results (77 x 100003: 17.6 us, and 21.8 us
 // here), rows on 16 bytes (1000 x 100004: 90 and 122 us) and 16-bit results
 // (8192 x 16385 x 4096: 199 and 360 us) are better off without.

@@ -9,10 +9,14 @@
 // Bound by memory: the forward pass reads each score once, the backward pass
 // reads and writes each once, and so does topk_distill, which holds a row in the
 // shared memory of a cluster of up to eight blocks between its two uses (rows
-// too long for that take the two passes). Measured at 2048 x 65536 bf16, k =
-// 100: forward 51 us (40 us at the measured copy rate), backward 82 us (81 us),
-// both in one 121 us (81 us), where the exponentials of both uses and the
-// exchange between them are not hidden behind three blocks per SM.
+// too long for that take the two passes). Measured on the device at 2048 x 65536
+// bf16, k = 100: forward 51 us (40 us at the measured copy rate), backward 92 us
+// (81 us; 82 us at 65537 columns, which two blocks share), both in one 119 us (81
+// us), where the exponentials of both uses and the exchange between them are not
+// hidden behind three blocks per SM. Rows of odd length cost the forward pass its
+// shifted loads (2048 x 65537: 72 us), and short rows are bound by the joins and
+// list work of a whole block per row (4000 x 5001 binary16, k = 300: both in one 52
+// us, 14 us for the bytes).
 //
 // Statistics kept per row: the largest score m and Z = sum_j exp((s_j - m) /
 // tau), both fp32; q_j comes from the difference s_j - m, so scores of any
