@@ -30,6 +30,8 @@ LUT_TYPES = {"fp32": LUT_FP32, "fp16": LUT_FP16, "fp8": LUT_FP8}
 MAX_K = 2048
 MXFP4, NVFP4 = 0, 1
 FP4_FORMATS = {"mxfp4": MXFP4, "nvfp4": NVFP4}
+MAX_BEAMS, MAX_BEAM_K = 64, 128
+MAX_RANK, MAX_ADAPTERS = 128, 8191
 
 # name -> (restype, argtypes); mirrors include/ivfpq.h
 _VP, _I, _I64, _F = C.c_void_p, C.c_int, C.c_int64, C.c_float
@@ -73,6 +75,14 @@ SIGNATURES = {
                                    _VP, _I64, _VP]),
     "topk_distill": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _F, _I, _VP, _VP, _VP, _I64,
                           _VP]),
+    "beam_select": (_I, [_VP, _I, _I64, _I, _I64, _I64, _VP, _VP, C.c_int32, _I, _VP, _VP, _VP,
+                         _VP]),
+    "beam_reorder": (_I, [_VP, _I, _VP, _I64, _I, _I, _VP, _VP]),
+    "embedding_lookup": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I64, _F, _VP, _I, _I64, _VP]),
+    "embedding_gradient": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _I, _I64, _F, _I64, _I, _VP, _I,
+                                _I64, _VP]),
+    "adapter_linear": (_I, [_VP, _I, _I64, _I64, _I64, _VP, _VP, _I, _I, _I64, _VP, _VP, _VP,
+                            _I64, _VP, _I, _I64, _VP]),
     "ivfpq_device_check": (_I, [_VP]),
     "ivfpq_selftest_wait_timeout": (_I, [_I, _VP]),
     "ivfpq_last_error": (C.c_char_p, []),
@@ -539,7 +549,8 @@ class _Late(dict):
     def __missing__(self, key):
         torch = _torch()
         self.update(Tensor=torch.Tensor, empty=torch.empty, f32=torch.float32, i32=torch.int32,
-                    i64=torch.int64, u8=torch.uint8, device=torch._C._cuda_getDevice,
+                    i64=torch.int64, u8=torch.uint8, bool=torch.bool,
+                    device=torch._C._cuda_getDevice,
                     stream=torch._C._cuda_getCurrentRawStream,
                     codes={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
         return self[key]
@@ -942,3 +953,284 @@ def topk_distill(scores, teacher_vals, teacher_ids, row_grad, temperature=1.0, n
     if rc:
         _check("topk_distill", rc)
     return loss, grad
+
+
+# ---- beams, embeddings and adapters ------------------------------------------
+def beam_select(scores, totals, k, finished=None, end_id=0, stream=None):
+    """(totals fp32, beams int32, ids int32), all [groups, k]: the k best
+    continuations of each group's beams, best first (include/ivfpq.h states the
+    order). scores: [groups * beams, cols], rows may be strided; totals: fp32
+    [groups, beams], -inf for a beam that is not alive; finished: bool or uint8
+    [groups, beams], beams whose only continuation is end_id at their own total.
+    Fewer than k continuations: (-inf, -1, -1) at the tail."""
+    if stream is not None:
+        return _on_stream(beam_select, stream, (scores, totals, k, finished, end_id), {})
+    code, rows, cols, lds = _rows(scores, "scores")
+    at, dev, empty, f32 = scores.get_device(), scores.device, _late["empty"], _late["f32"]
+    try:
+        groups, beams = totals.shape
+    except (AttributeError, ValueError):
+        _need(totals, f32, "totals", 2)
+        raise
+    if groups * beams != rows:
+        raise ValueError(f"totals are {groups} x {beams} and scores have {rows} rows")
+    t = _array(totals, f32, (groups, beams), "totals", at)
+    fin = None
+    if finished is not None:
+        if not isinstance(finished, _late["Tensor"]):
+            raise TypeError("finished must be a torch tensor")
+        if finished.dtype is not _late["u8"] and finished.dtype is not _late["bool"]:
+            raise TypeError(f"finished must be bool or uint8, got {finished.dtype}")
+        fin = _array(finished, finished.dtype, (groups, beams), "finished", at)
+    shape = (groups, k)
+    out = empty(shape, dtype=f32, device=dev)
+    which = empty(shape, dtype=_late["i32"], device=dev)
+    ids = empty(shape, dtype=_late["i32"], device=dev)
+    rc = (_lib or lib()).beam_select(scores.data_ptr(), code, groups, beams, cols, lds, t, fin,
+                                     end_id, k, out.data_ptr(), which.data_ptr(), ids.data_ptr(),
+                                     _current(at))
+    if rc:
+        _check("beam_select", rc)
+    return out, which, ids
+
+
+class _State(C.Structure):
+    """ivfpq_state of include/ivfpq.h."""
+    _fields_ = [("src", _VP), ("dst", _VP), ("src_row", _I64), ("dst_row", _I64),
+                ("outer", _I64), ("src_outer", _I64), ("dst_outer", _I64), ("inner", _I64),
+                ("unit", _I64)]
+
+
+def _dense_tail(shape, stride):
+    """Leading dimensions left when the dense trailing ones are one run."""
+    run, i = 1, len(shape)
+    while i > 1 and (shape[i - 1] == 1 or stride[i - 1] == run):
+        run *= shape[i - 1]
+        i -= 1
+    return i
+
+
+def _segments(shape, stride, end, name):
+    """(number, stride) of the segments that dimensions 1 .. end - 1 count."""
+    n, step = 1, 0
+    for size, st in zip(shape[end - 1:0:-1], stride[end - 1:0:-1]):
+        if size == 1:
+            continue
+        if n == 1:
+            n, step = size, st
+        elif st == step * n:
+            n *= size
+        else:
+            raise ValueError(f"{name}: dimensions before the positions must have one stride")
+    return n, step
+
+
+def _state(t, o, axis, groups, width, n, lengths, at, name):
+    """The ivfpq_state of tensor t written to o, positions along dimension axis."""
+    Tensor = _late["Tensor"]
+    if not isinstance(t, Tensor) or not isinstance(o, Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != at or o.get_device() != at or not t.is_cuda:
+        raise ValueError(f"{name} and its output must be on cuda:{at}")
+    shape, so, size = t.shape, o.shape, t.element_size()
+    dims = len(shape)
+    if dims < 1 or shape[0] != groups * width:
+        raise ValueError(f"{name} must have {groups * width} rows, got shape {tuple(shape)}")
+    if o.dtype != t.dtype or so[0] != groups * n or so[1:] != shape[1:]:
+        raise ValueError(f"the output of {name} must be {t.dtype} with {groups * n} rows of its "
+                         f"shape, got {o.dtype} {tuple(so)}")
+    st, sto = t.stride(), o.stride()
+    first = max(_dense_tail(shape, st), _dense_tail(shape, sto))
+    unit = 0
+    if lengths:
+        if not 1 <= axis < dims:
+            raise ValueError(f"{name}: positions must be one of its dimensions 1 to {dims - 1}")
+        if first > axis:
+            raise ValueError(f"{name}: positions and what follows them must be dense")
+        first, unit = axis, size
+        for v in shape[axis + 1:]:
+            unit *= v
+    inner = size
+    for v in shape[first:]:
+        inner *= v
+    outer, src_outer = _segments(shape, st, first, name)
+    _, dst_outer = _segments(shape, sto, first, name)
+    src_row = st[0] if shape[0] > 1 else 0
+    dst_row = sto[0] if so[0] > 1 else 0
+    return _State(t.data_ptr(), o.data_ptr(), src_row * size, dst_row * size, outer,
+                  src_outer * size, dst_outer * size, inner, unit)
+
+
+def beam_reorder(states, beams, lengths=None, axis=1, out=None, stream=None):
+    """The states of the beams (a tensor or a sequence of tensors, each with
+    groups * width rows of any dtype) in the order of the selected continuations:
+    row g * n + j becomes row g * width + beams[g, j]. beams: int32 [groups, n], as
+    beam_select returns them; a beam outside the group leaves its row as it was.
+    lengths: int32 [groups], the positions in use along dimension `axis` (one
+    number, or one per state); what lies past them stays as it was. In place (n =
+    width) unless out, tensors of groups * n rows, is given; returns what was
+    written. States must not overlap each other, nor a state an output other than
+    its own. A state that repeats memory within its rows is refused in place."""
+    if stream is not None:
+        flat = [states] if not isinstance(states, (list, tuple)) else list(states)
+        flat += ([] if out is None else [out] if not isinstance(out, (list, tuple)) else list(out))
+        for t in flat:
+            if isinstance(t, _late["Tensor"]) and t.is_cuda:
+                t.record_stream(stream)
+        return _on_stream(beam_reorder, stream, (states, beams, lengths, axis, out), {})
+    one = not isinstance(states, (list, tuple))
+    src = [states] if one else states
+    dst = src if out is None else [out] if one else out
+    if len(dst) != len(src):
+        raise ValueError(f"{len(src)} states and {len(dst)} outputs")
+    i32 = _late["i32"]
+    try:
+        groups, n = beams.shape
+    except (AttributeError, ValueError):
+        _need(beams, i32, "beams", 2)
+        raise
+    at = beams.get_device()
+    b = _array(beams, i32, (groups, n), "beams", at)
+    if not beams.is_cuda:
+        raise ValueError("beams must be a CUDA tensor")
+    length = None if lengths is None else _array(lengths, i32, (groups,), "lengths", at)
+    if not src or groups == 0 or n == 0:
+        return out if out is not None else states
+    axes = axis if isinstance(axis, (list, tuple)) else [axis] * len(src)
+    if len(axes) != len(src):
+        raise ValueError(f"{len(src)} states and {len(axes)} position dimensions")
+    rows = src[0].shape[0] if isinstance(src[0], _late["Tensor"]) and src[0].dim() else -1
+    if rows < 0 or rows % groups:
+        raise ValueError(f"states[0] must have a multiple of {groups} rows")
+    width = rows // groups
+    if out is None and width != n:
+        raise ValueError(f"in place, {n} continuations need as many rows, not {width}")
+    array = (_State * len(src))()
+    seen = set()
+    for i, (t, o, d) in enumerate(zip(src, dst, axes)):
+        s = _state(t, o, d, groups, width, n, length is not None, at, f"states[{i}]")
+        if s.dst in seen and s.inner:
+            raise ValueError(f"states[{i}] is written twice")
+        seen.add(s.dst)
+        array[i] = s
+    rc = (_lib or lib()).beam_reorder(array, len(src), b, groups, width, n, length, _current(at))
+    if rc:
+        _check("beam_reorder", rc)
+    return out if out is not None else states
+
+
+def _ids(ids, name, dev):
+    """(address, bytes per id, count) of a contiguous int32 or int64 tensor."""
+    if not isinstance(ids, _late["Tensor"]):
+        raise TypeError(f"{name} must be a torch tensor")
+    dtype = ids.dtype
+    if dtype is not _late["i32"] and dtype is not _late["i64"]:
+        raise TypeError(f"{name} must be int32 or int64, got {dtype}")
+    return _array(ids, dtype, ids.shape, name, dev), 4 if dtype is _late["i32"] else 8, ids.numel()
+
+
+def embedding_lookup(table, ids, scale=1.0, dtype=None, out=None, stream=None):
+    """scale * table[ids], [*ids.shape, cols] in dtype (the table's if not given,
+    or float32); zeros where an id is outside the table. table: [rows, cols],
+    rows may be strided; ids: int32 or int64, any shape; out: 2-d with strided
+    rows for 1-d ids, contiguous otherwise."""
+    if stream is not None:
+        return _on_stream(embedding_lookup, stream, (table, ids, scale, dtype, out), {})
+    code, rows, cols, ldt = _rows(table, "table")
+    at = table.get_device()
+    p, size, tokens = _ids(ids, "ids", at)
+    if dtype is None:
+        dtype = table.dtype if out is None else out.dtype
+    ocode = code if dtype is table.dtype else _dtype_code(dtype, "dtype")
+    ldo = cols
+    if out is None:
+        out = _late["empty"]((*ids.shape, cols), dtype=dtype, device=table.device)
+    elif ids.dim() == 1:
+        ldo = _out_rows(out, (tokens, cols), dtype, "out", table.device)
+    else:
+        out = _out(out, (*ids.shape, cols), dtype, "out", table.device)
+    rc = (_lib or lib()).embedding_lookup(table.data_ptr(), code, rows, cols, ldt, p, size, tokens,
+                                          scale, out.data_ptr(), ocode, ldo, _current(at))
+    if rc:
+        _check("embedding_lookup", rc)
+    return out
+
+
+def embedding_gradient(grad, ids, rows, scale=1.0, padding=None, accumulate=False, dtype=None,
+                       out=None, stream=None):
+    """The gradient [rows, cols] of embedding_lookup's table from grad [tokens,
+    cols] (rows may be strided or one repeated) and ids, int32 or int64 of as many
+    elements: scale times the sums by token, in dtype (grad's if not given, or
+    float32). Ids outside the table and the id `padding` have none. accumulate:
+    the sums are added to out, which must be given; rows without a token stay."""
+    if stream is not None:
+        return _on_stream(embedding_gradient, stream,
+                          (grad, ids, rows, scale, padding, accumulate, dtype, out), {})
+    code, tokens, cols, ldg = _rows(grad, "grad")
+    at = grad.get_device()
+    p, size, count = _ids(ids, "ids", at)
+    if count != tokens:
+        raise ValueError(f"{count} ids and {tokens} rows of grad")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if dtype is None:
+        dtype = grad.dtype if out is None else out.dtype
+    ocode = code if dtype is grad.dtype else _dtype_code(dtype, "dtype")
+    if out is None:
+        out, ldo = _late["empty"]((rows, cols), dtype=dtype, device=grad.device), cols
+    else:
+        ldo = _out_rows(out, (rows, cols), dtype, "out", grad.device)
+    rc = (_lib or lib()).embedding_gradient(
+        grad.data_ptr(), code, tokens, cols, ldg, p, size, rows, scale,
+        -1 if padding is None else padding, 1 if accumulate else 0, out.data_ptr(), ocode, ldo,
+        _current(at))
+    if rc:
+        _check("embedding_gradient", rc)
+    return out
+
+
+def adapter_linear(x, a, b, ids, scales=None, base=None, dtype=None, out=None, stream=None):
+    """base[t] + scales[i] * (x[t] @ a[i].T) @ b[i].T with i = ids[t], [tokens, n]:
+    low-rank adapters beside a projection that all requests share (base: its
+    result; zeros if not given). x: fp16 or bf16 [tokens, cols], rows may be
+    strided; a: [adapters, rank, cols], b: [adapters, n, rank] of x's dtype; ids:
+    int32 [tokens], outside [0, adapters) for a token without one; scales: fp32
+    [adapters]. In base's dtype, or dtype (x's if not given, or float32). out may be
+    base itself."""
+    if stream is not None:
+        return _on_stream(adapter_linear, stream, (x, a, b, ids, scales, base, dtype, out), {})
+    code, tokens, cols, ldx = _rows(x, "x")
+    at, dev, i32 = x.get_device(), x.device, _late["i32"]
+    try:
+        adapters, rank, _ = a.shape
+        _, n, _ = b.shape
+    except (AttributeError, ValueError):
+        _need(a, x.dtype, "a", 3)
+        _need(b, x.dtype, "b", 3)
+        raise
+    pa = _array(a, x.dtype, (adapters, rank, cols), "a", at)
+    pb = _array(b, x.dtype, (adapters, n, rank), "b", at)
+    pi = _array(ids, i32, (tokens,), "ids", at)
+    ps = None if scales is None else _array(scales, _late["f32"], (adapters,), "scales", at)
+    pbase, ldb = None, 0
+    if base is not None:
+        if dtype is None:
+            dtype = base.dtype if out is None else out.dtype
+        _, brows, bcols, ldb = _rows(base, "base")
+        if base.dtype != dtype or (brows, bcols) != (tokens, n) or base.get_device() != at:
+            raise ValueError(f"base must be {dtype} [{tokens}, {n}] on {dev}, got {base.dtype} "
+                             f"{tuple(base.shape)} on {base.device}")
+        pbase = base.data_ptr()
+    if dtype is None:
+        dtype = x.dtype if out is None else out.dtype
+    ocode = code if dtype is x.dtype else _dtype_code(dtype, "dtype")
+    if out is None:
+        out, ldo = _late["empty"]((tokens, n), dtype=dtype, device=dev), n
+    else:
+        ldo = _out_rows(out, (tokens, n), dtype, "out", dev)
+    rc = (_lib or lib()).adapter_linear(x.data_ptr(), code, tokens, cols, ldx, pa, pb, adapters,
+                                        rank, n, pi, ps, pbase, ldb, out.data_ptr(), ocode, ldo,
+                                        _current(at))
+    if rc:
+        _check("adapter_linear", rc)
+    return out

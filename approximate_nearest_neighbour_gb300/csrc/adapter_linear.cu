@@ -1,0 +1,621 @@
+// adapter_linear: low-rank adapters of many requests, added to the result of a
+// projection that they share,
+//   out[t] = base[t] + scale_i (x[t] A_i^T) B_i^T,   i = ids[t]
+// with A_i [rank, cols] and B_i [n, rank]; a token without an adapter (an id
+// outside the list) gets its base row.
+//
+// Bound by memory: of 2 tokens rank (cols + n) operations per tokens (cols + 2 n)
+// elements moved, even rank 64 is 40 operations per byte, a fifth of what the
+// tensor cores need to be the limit. So both products run on warp-level matrix
+// instructions whose operands come straight from memory into registers: the sum
+// over K may run in any order if both operands take the same one, so that each
+// lane loads 16 consecutive bytes of a row and uses them as its part of two
+// instructions, and the columns of a result tile may be any 8, so that a lane's
+// results of four tiles are 8 neighbouring columns.
+//  1. Tokens are grouped by adapter into tiles (one block; left out where there
+//     are so few tokens that each is a tile). Order within a tile does not matter:
+//     a token's sums do not depend on its neighbours.
+//  2. h = x A^T: a block takes 16 or 32 tokens of a tile and a part of K, its warps
+//     parts of that; parts are added in shared memory, then by the readers, in
+//     fixed order.
+//  3. out = base + scale h B^T: a block keeps the tile's h in shared memory and runs
+//     over columns. h is fp32: it is cut into two terms of the operands' type
+//     (three, if bf16 operands make an fp32 output), each exact to the next, so
+//     that nothing of it is rounded away beyond 2^-17 (2^-22 for fp16, 2^-25 for three).
+#include <algorithm>
+
+#include "internal.h"
+#include "rowvec.cuh"
+#include "tc_ptx.cuh"
+
+namespace ivfpq {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxTile = 128;
+
+struct AdapterArgs {
+  const void* x;
+  int64_t tokens, cols, ldx;
+  const void* a;
+  const void* b;
+  int adapters, rank;
+  int64_t n;
+  const int32_t* ids;
+  const float* scales;
+  const void* base;
+  int64_t ldb;
+  void* out;
+  int64_t ldo;
+  // the plan (null: every token is a tile)
+  int32_t* order;  // [tokens] tokens by adapter
+  int4* tiles;     // (adapter or -1, first slot, tokens, 0)
+  int32_t* ntiles;
+  int tile;     // tokens of a tile
+  float* h;     // [splits, tokens, pitch]
+  int splits;   // parts of K
+  int kpart;    // columns of a part, a multiple of 32
+  int pitch;    // rank rounded up to whole instructions
+  int run;      // output columns of a block
+};
+
+struct Tile {
+  int adapter, first, count;
+};
+__device__ __forceinline__ Tile tile_at(const AdapterArgs& a, int64_t i) {
+  if (a.tiles) {
+    if (i >= *a.ntiles) return {-1, 0, 0};
+    const int4 t = a.tiles[i];
+    return {t.x, t.y, t.z};
+  }
+  if (i >= a.tokens) return {-1, 0, 0};
+  const int id = a.ids[i];
+  return {id >= 0 && id < a.adapters ? id : -1, int(i), 1};
+}
+__device__ __forceinline__ int64_t token_of(const AdapterArgs& a, int slot) {
+  return a.order ? a.order[slot] : slot;
+}
+
+// ---- tokens by adapter ------------------------------------------------------------------
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const AdapterArgs a) {
+  extern __shared__ int plan_smem[];
+  int* slot = plan_smem;            // [adapters + 1]: counts, then the next slot
+  __shared__ int sh[2][32];
+  const int bins = a.adapters + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < bins; i += kPlanThreads) slot[i] = 0;
+  __syncthreads();
+  // one addition per adapter and warp: prompts bring thousands of tokens of one
+  auto take = [&](int64_t t) {
+    int id = t < a.tokens ? a.ids[t] : -2;
+    if (id != -2 && (id < 0 || id >= a.adapters)) id = a.adapters;
+    if (t >= a.tokens) id = -2;
+    const unsigned same = __match_any_sync(kFullMask, id);
+    int at = 0;
+    if (id >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&slot[id], __popc(same));
+    at = __shfl_sync(kFullMask, at, __ffs(same) - 1);
+    return make_int2(id, at + __popc(same & ((1u << lane) - 1u)));
+  };
+  const int64_t steps = (a.tokens + kPlanThreads - 1) / kPlanThreads;
+  for (int64_t s = 0; s < steps; ++s) take(s * kPlanThreads + threadIdx.x);
+  __syncthreads();
+  // running sums of the counts and of the tiles
+  int slots = 0, tiles = 0;
+  for (int i0 = 0; i0 < bins; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    const int c = i < bins ? slot[i] : 0, t = (c + a.tile - 1) / a.tile;
+    int ic = c, it = t;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int u = __shfl_up_sync(kFullMask, ic, d), v = __shfl_up_sync(kFullMask, it, d);
+      if (lane >= d) {
+        ic += u;
+        it += v;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      sh[0][warp] = ic;
+      sh[1][warp] = it;
+    }
+    __syncthreads();
+    const int wc = sh[0][lane], wt = sh[1][lane];
+    const int bc = int(__reduce_add_sync(kFullMask, unsigned(lane < warp ? wc : 0)));
+    const int bt = int(__reduce_add_sync(kFullMask, unsigned(lane < warp ? wt : 0)));
+    const int first = slots + bc + ic - c, ftile = tiles + bt + it - t;
+    if (i < bins) {
+      slot[i] = first;
+      for (int k = 0; k < t; ++k)
+        a.tiles[ftile + k] = make_int4(i < a.adapters ? i : -1, first + k * a.tile,
+                                       min(a.tile, c - k * a.tile), 0);
+    }
+    slots += int(__reduce_add_sync(kFullMask, unsigned(wc)));
+    tiles += int(__reduce_add_sync(kFullMask, unsigned(wt)));
+  }
+  if (threadIdx.x == 0) *a.ntiles = tiles;
+  __syncthreads();
+  for (int64_t s = 0; s < steps; ++s) {
+    const int64_t t = s * kPlanThreads + threadIdx.x;
+    const int2 p = take(t);
+    if (p.x >= 0) a.order[p.y] = int32_t(t);
+  }
+}
+
+// ---- matrix instructions ----------------------------------------------------------------
+// D += A B for 16 x 16 and 16 x 8 operands of 16-bit type.
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1, __nv_bfloat16*) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1, __half*) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Elements 8 i .. 8 i + 7 of a row of `len`, zero past its end, whatever its alignment.
+template <class T>
+__device__ __noinline__ uint4 edge8(const T* p, int64_t len, int64_t at) {
+  T t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = at + j < len ? p[at + j] : from_f32<T>(0.f);
+  uint4 r;
+  memcpy(&r, t, 16);
+  return r;
+}
+template <class T>
+__device__ __forceinline__ uint4 row8(const T* p, int64_t len, int64_t at) {
+  if (p == nullptr || at >= len) return make_uint4(0, 0, 0, 0);
+  const int mis = misalign(p);
+  if (mis == 0 && at + 8 <= len) return *reinterpret_cast<const uint4*>(p + at);
+  // two neighbouring vectors inside the row
+  if (mis != 0 && at >= 8 && at + 16 <= len) return load_inner(p + at, 0, mis);
+  return edge8(p, len, at);
+}
+
+// ---- h = x A^T ----------------------------------------------------------------------------
+template <class T, int NT, int MT>
+__global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(16) float shrink_smem[];  // [kWarps, 16 MT, 8 NT]
+  T* const type = nullptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
+  const int subs = (a.tile + 16 * MT - 1) / (16 * MT);
+  const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  grid_wait();
+  grid_go();
+  const Tile t = tile_at(a, item / subs);
+  const int m0 = int(item % subs) * 16 * MT, rows = min(16 * MT, t.count - m0);
+  if (rows <= 0 || t.adapter < 0) return;
+  const T* x[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = m * 16 + e * 8 + r;
+      x[m][e] = i < rows ? static_cast<const T*>(a.x) + token_of(a, t.first + m0 + i) * a.ldx
+                         : nullptr;
+    }
+  const T* w[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    w[j] = j * 8 + r < a.rank ? static_cast<const T*>(a.a) +
+                                    (int64_t(t.adapter) * a.rank + j * 8 + r) * a.cols
+                              : nullptr;
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+  const int64_t k0 = int64_t(blockIdx.x) * a.kpart, k1 = min(a.cols, k0 + a.kpart);
+  constexpr int U = NT * MT <= 4 ? 4 : NT * MT <= 8 ? 2 : 1;
+  for (int64_t k = k0 + warp * 32; k < k1; k += kWarps * 32 * U) {
+    uint4 xv[U][MT][2], wv[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = k + u * kWarps * 32 + 8 * q;
+      const int64_t len = k + u * kWarps * 32 < k1 ? a.cols : 0;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) wv[u][j] = row8(w[j], len, at);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) xv[u][m][e] = row8(x[m][e], len, at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 &p = xv[u][m][0], &s = xv[u][m][1], &v = wv[u][j];
+          mma16(acc[m][j], p.x, s.x, p.y, s.y, v.x, v.y, type);
+          mma16(acc[m][j], p.z, s.z, p.w, s.w, v.z, v.w, type);
+        }
+  }
+  constexpr int R = NT * 8;
+  float* red = shrink_smem + warp * 16 * MT * R;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2*>(red + (m * 16 + e * 8 + r) * R + j * 8 + 2 * q) =
+            make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
+  __syncthreads();
+  float* h = a.h + (int64_t(blockIdx.x) * a.tokens + t.first + m0) * a.pitch;
+  for (int i = threadIdx.x; i < rows * R; i += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) s += shrink_smem[v * 16 * MT * R + i];
+    h[(i / R) * a.pitch + i % R] = s;
+  }
+}
+
+// ---- out = base + scale h B^T ----------------------------------------------------------------
+// The next term of v as an element of T; what is left of it stays in v.
+template <class T>
+__device__ __forceinline__ float term(float& v) {
+  const float t = to_f32(from_f32<T>(v));
+  v = fabsf(t) < INFINITY ? v - t : 0.f;
+  return t;
+}
+
+// A lane's part of a row of B: 4 KS consecutive elements from 4 KS q on, as two
+// registers per instruction.
+template <class T, int KS>
+__device__ __forceinline__ void load_b(const T* p, int rank, int q, bool whole,
+                                       uint32_t (&b)[KS][2]) {
+#pragma unroll
+  for (int s = 0; s < KS; ++s) b[s][0] = b[s][1] = 0;
+  if (p == nullptr) return;
+  const int k = 4 * KS * q;
+  if (whole) {
+    if constexpr (KS == 1) {
+      if (k < rank) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p + k);
+        b[0][0] = v.x;
+        b[0][1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; s += 2) {
+        if (k + 4 * s < rank) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p + k + 4 * s);
+          b[s][0] = v.x;
+          b[s][1] = v.y;
+          b[s + 1][0] = v.z;
+          b[s + 1][1] = v.w;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        T t[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int i = k + 4 * s + 2 * e + f;
+          t[f] = i < rank ? p[i] : from_f32<T>(0.f);
+        }
+        memcpy(&b[s][e], t, 4);
+      }
+  }
+}
+
+// 8 neighbouring elements of a row, `have` of them in it.
+template <class O>
+__device__ __forceinline__ void load8(const O* p, int have, float (&v)[8]) {
+  if (have == 8 && misalign(p) == 0) {
+    constexpr int M = Span<O>::N;
+#pragma unroll
+    for (int g = 0; g < 8 / M; ++g) {
+      float w[M];
+      unpack_vec<O>(reinterpret_cast<const uint4*>(p)[g], w);
+#pragma unroll
+      for (int j = 0; j < M; ++j) v[g * M + j] = w[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < have ? to_f32(p[j]) : 0.f;
+  }
+}
+template <class O>
+__device__ __forceinline__ void store8(O* p, int have, const float (&v)[8]) {
+  if (have == 8 && misalign(p) == 0) {
+    store_vec<O>(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < have) p[j] = from_f32<O>(v[j]);
+  }
+}
+
+template <class T, class O, int KS, int TERMS>
+__global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(16) uint4 expand_smem[];  // [m tiles, KS, TERMS, 32]
+  __shared__ float up[kMaxTile];                        // a row's power of two
+  __shared__ int64_t token[kMaxTile];
+  T* const type = nullptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
+  grid_wait();
+  const Tile t = tile_at(a, blockIdx.y + int64_t(blockIdx.z) * gridDim.y);
+  if (t.count == 0) return;
+  const bool some = t.adapter >= 0;
+  const O* base = static_cast<const O*>(a.base);
+  O* out = static_cast<O*>(a.out);
+  if (!some && base == out) return;  // in place: nothing changes
+  for (int i = threadIdx.x; i < t.count; i += kThreads) token[i] = token_of(a, t.first + i);
+  const int mtiles = (t.count + 15) / 16;
+  if (some) {
+    const float scale = a.scales ? a.scales[t.adapter] : 1.f;
+    for (int m = warp; m < mtiles; m += kWarps) {
+      float v[2][4 * KS];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = m * 16 + e * 8 + r;
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * KS; ++k) v[e][k] = 0.f;
+        if (i < t.count) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const int k = 4 * KS * q + 4 * s;
+            if (k >= a.pitch) continue;
+            for (int p = 0; p < a.splits; ++p) {
+              const float4 f = *reinterpret_cast<const float4*>(
+                  a.h + (int64_t(p) * a.tokens + t.first + i) * a.pitch + k);
+              v[e][4 * s] += f.x;
+              v[e][4 * s + 1] += f.y;
+              v[e][4 * s + 2] += f.z;
+              v[e][4 * s + 3] += f.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4 * KS; ++k) {
+          v[e][k] *= scale;
+          top = fmaxf(top, fabsf(v[e][k]));
+        }
+        if constexpr (std::is_same<T, __half>::value) {
+          // fp16's range: the row's largest value to [2^14, 2^15)
+          top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+          const int ex = int(__float_as_uint(top) >> 23);  // 127 + its exponent
+          const bool ok = top > 0.f && top < INFINITY;
+          const int down = ok ? min(141 - ex, 126) : 0;
+          const float f = __uint_as_float(uint32_t(127 + max(down, -126)) << 23);
+#pragma unroll
+          for (int k = 0; k < 4 * KS; ++k) v[e][k] *= f;
+          if (q == 0 && i < t.count) up[i] = __uint_as_float(uint32_t(127 - max(down, -126)) << 23);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int n = 0; n < TERMS; ++n) {
+          float f[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[e][k] = term<T>(v[e][4 * s + k]);
+          expand_smem[((m * KS + s) * TERMS + n) * 32 + lane] =
+              make_uint4(pack16(f[0][0], f[0][1], type), pack16(f[1][0], f[1][1], type),
+                         pack16(f[0][2], f[0][3], type), pack16(f[1][2], f[1][3], type));
+        }
+    }
+  }
+  __syncthreads();
+  const bool whole = a.rank % (KS == 1 ? 4 : 8) == 0 && misalign(a.b) == 0;
+  const T* b0 = some ? static_cast<const T*>(a.b) + int64_t(t.adapter) * a.n * a.rank : nullptr;
+  const int64_t cend = min(a.n, (int64_t(blockIdx.x) + 1) * a.run);
+  for (int64_t c0 = int64_t(blockIdx.x) * a.run + warp * 32; c0 < cend; c0 += kWarps * 32) {
+    uint32_t b[4][KS][2];
+    if (some) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t c = c0 + 8 * (r / 2) + 2 * j + (r & 1);
+        load_b<T, KS>(c < a.n ? b0 + c * a.rank : nullptr, a.rank, q, whole, b[j]);
+      }
+    }
+    const int64_t col = c0 + 8 * q;
+    const int have = int(min(int64_t(8), a.n - col));
+    for (int m = 0; m < mtiles; ++m) {
+      float y[2][8];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = m * 16 + e * 8 + r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[e][j] = 0.f;
+        if (base && i < t.count && have > 0) load8(base + token[i] * a.ldb + col, have, y[e]);
+      }
+      if (some) {
+        float acc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+        for (int n = TERMS - 1; n >= 0; --n)  // the small terms first
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const uint4 f = expand_smem[((m * KS + s) * TERMS + n) * 32 + lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma16(acc[j], f.x, f.y, f.z, f.w, b[j][s][0], b[j][s][1], type);
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = m * 16 + e * 8 + r;
+          float f = 1.f;
+          if constexpr (std::is_same<T, __half>::value) f = i < t.count ? up[i] : 1.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            y[e][2 * j] += acc[j][2 * e] * f;
+            y[e][2 * j + 1] += acc[j][2 * e + 1] * f;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = m * 16 + e * 8 + r;
+        if (i < t.count && have > 0) store8(out + token[i] * a.ldo + col, have, y[e]);
+      }
+    }
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------------------
+dim3 grid_of(int64_t per_row, int64_t rows) {
+  const int64_t y = std::min<int64_t>(rows, 65535);
+  return dim3(unsigned(per_row), unsigned(y), unsigned(ceil_div(rows, y)));
+}
+template <class K>
+int launch_after(K kern, dim3 grid, int threads, size_t smem, const AdapterArgs& a, bool overlap,
+                 cudaStream_t s) {
+  IVFPQ_TRY(set_dynamic_smem(kern, smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlap ? 1 : 0;
+  IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+  IVFPQ_LAUNCHED_K(kern, smem, threads);
+  return IVFPQ_OK;
+}
+
+template <class T, int NT, int MT>
+int launch_shrink(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+  const int64_t subs = ceil_div(a.tile, 16 * MT);
+  const size_t smem = size_t(kWarps) * 16 * MT * 8 * NT * 4;
+  return launch_after(adapter_shrink_kernel<T, NT, MT>, grid_of(a.splits, tiles * subs), kThreads,
+                      smem, a, a.tiles != nullptr, s);
+}
+template <class T>
+int launch_shrink_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+  const bool two = a.tile >= 32;
+  switch (a.pitch / 8) {
+    case 1: return two ? launch_shrink<T, 1, 2>(a, tiles, s) : launch_shrink<T, 1, 1>(a, tiles, s);
+    case 2: return two ? launch_shrink<T, 2, 2>(a, tiles, s) : launch_shrink<T, 2, 1>(a, tiles, s);
+    case 4: return two ? launch_shrink<T, 4, 2>(a, tiles, s) : launch_shrink<T, 4, 1>(a, tiles, s);
+    case 8: return two ? launch_shrink<T, 8, 2>(a, tiles, s) : launch_shrink<T, 8, 1>(a, tiles, s);
+    default:
+      return two ? launch_shrink<T, 16, 2>(a, tiles, s) : launch_shrink<T, 16, 1>(a, tiles, s);
+  }
+}
+template <class T, class O, int KS>
+int launch_expand(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+  constexpr int TERMS =
+      std::is_same<T, __nv_bfloat16>::value && std::is_same<O, float>::value ? 3 : 2;
+  const size_t smem = size_t((a.tile + 15) / 16) * KS * TERMS * 512;
+  return launch_after(adapter_expand_kernel<T, O, KS, TERMS>,
+                      grid_of(ceil_div(a.n, a.run), tiles), kThreads, smem, a, true, s);
+}
+template <class T, class O>
+int launch_expand_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+  switch (a.pitch / 8) {
+    case 1:
+    case 2: return launch_expand<T, O, 1>(a, tiles, s);
+    case 4: return launch_expand<T, O, 2>(a, tiles, s);
+    case 8: return launch_expand<T, O, 4>(a, tiles, s);
+    default: return launch_expand<T, O, 8>(a, tiles, s);
+  }
+}
+template <class T>
+int launch_types(const AdapterArgs& a, int out_dtype, int64_t tiles, cudaStream_t s) {
+  IVFPQ_TRY(launch_shrink_rank<T>(a, tiles, s));
+  return out_dtype == IVFPQ_F32 ? launch_expand_rank<T, float>(a, tiles, s)
+                                : launch_expand_rank<T, T>(a, tiles, s);
+}
+
+}  // namespace
+}  // namespace ivfpq
+
+using namespace ivfpq;
+
+extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t cols, int64_t ldx,
+                              const void* a, const void* b, int adapters, int rank, int64_t n,
+                              const int32_t* ids, const float* scales, const void* base,
+                              int64_t ldb, void* out, int out_dtype, int64_t ldo, void* stream) {
+  clear_error();
+  IVFPQ_REQUIRE(dtype == IVFPQ_F16 || dtype == IVFPQ_BF16,
+                "adapter_linear: x and the adapters are fp16 or bf16");
+  IVFPQ_REQUIRE(out_dtype == dtype || out_dtype == IVFPQ_F32,
+                "adapter_linear: the output is of x's type or fp32");
+  IVFPQ_REQUIRE(tokens >= 0 && tokens < (int64_t(1) << 24),
+                "adapter_linear: tokens=%lld outside [0, 2^24)", (long long)tokens);
+  IVFPQ_REQUIRE(cols >= 1 && cols <= (int64_t(1) << 20) && n >= 0 && n <= (int64_t(1) << 24),
+                "adapter_linear: cols=%lld outside [1, 2^20] or n=%lld outside [0, 2^24]",
+                (long long)cols, (long long)n);
+  IVFPQ_REQUIRE(rank >= 1 && rank <= IVFPQ_MAX_RANK, "adapter_linear: rank=%d outside [1, %d]",
+                rank, IVFPQ_MAX_RANK);
+  IVFPQ_REQUIRE(adapters >= 0 && adapters <= IVFPQ_MAX_ADAPTERS,
+                "adapter_linear: adapters=%d outside [0, %d]", adapters, IVFPQ_MAX_ADAPTERS);
+  IVFPQ_REQUIRE(tokens <= 1 || ((ldx >= cols || ldx == 0) && ldo >= n &&
+                                (!base || ldb >= n || ldb == 0)),
+                "adapter_linear: a row stride below its row");
+  if (tokens == 0 || n == 0) return IVFPQ_OK;
+  IVFPQ_REQUIRE(x && ids && out && ((a && b) || adapters == 0), "adapter_linear: null pointer");
+  IVFPQ_REQUIRE(base != out || tokens <= 1 || ldb == ldo,
+                "adapter_linear: in place, base and out have one row stride");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AdapterArgs p{};
+  p.x = x;
+  p.tokens = tokens;
+  p.cols = cols;
+  p.ldx = ldx;
+  p.a = a;
+  p.b = b;
+  p.adapters = adapters;
+  p.rank = rank;
+  p.n = n;
+  p.ids = ids;
+  p.scales = scales;
+  p.base = base;
+  p.ldb = ldb;
+  p.out = out;
+  p.ldo = ldo;
+  p.pitch = 8;
+  while (p.pitch < rank) p.pitch *= 2;
+  const bool planned = tokens > 16;
+  p.tile = !planned ? 1 : tokens <= 256 ? 32 : kMaxTile;
+  const int64_t tiles =
+      planned ? tokens / p.tile + std::min<int64_t>(tokens, int64_t(adapters) + 1) : tokens;
+  // parts of K until there are blocks for every SM, of at least one step each
+  const int64_t items = planned ? ceil_div(tokens, 32) : tokens;
+  p.splits = 1;
+  while (p.splits < 16 && items * p.splits < 2 * num_sms() && cols > 128 * int64_t(p.splits))
+    p.splits *= 2;
+  p.kpart = int(ceil_div(ceil_div(cols, p.splits), 32) * 32);
+  // runs of columns, long where there are many tiles
+  p.run = 128;
+  while (p.run < 512 && ceil_div(n, p.run) * tiles > 8 * num_sms()) p.run *= 2;
+  Workspace ws(s);
+  IVFPQ_TRY(ws.alloc(&p.h, size_t(p.splits) * size_t(tokens) * size_t(p.pitch)));
+  if (planned) {
+    IVFPQ_TRY(ws.alloc(&p.tiles, size_t(tiles) + size_t(ceil_div(tokens + 1, 4))));
+    p.order = reinterpret_cast<int32_t*>(p.tiles + tiles);
+    p.ntiles = p.order + tokens;
+    const size_t smem = size_t(adapters + 1) * 4;
+    IVFPQ_TRY(launch_after(adapter_plan_kernel, dim3(1), kPlanThreads, smem, p, false, s));
+  }
+  return dtype == IVFPQ_F16 ? launch_types<__half>(p, out_dtype, tiles, s)
+                            : launch_types<__nv_bfloat16>(p, out_dtype, tiles, s);
+}

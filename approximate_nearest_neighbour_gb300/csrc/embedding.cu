@@ -1,0 +1,553 @@
+// embedding_lookup: rows of a table by token, scaled; and embedding_gradient, the
+// table's gradient, row v = scale times the sum of the gradient rows of token v.
+//
+// Both are bound by memory. The lookup reads and writes each row once, in vectors
+// that start on a 16-byte boundary of the output.
+//
+// The gradient's sums are taken in the order of the positions, so that they repeat
+// bit for bit:
+//  1. The positions are sorted by token (stably). Block c owns the tokens that are
+//     c modulo the number of blocks, so that neighbouring frequent tokens fall to
+//     different blocks; it reads all ids, which are few bytes beside the gradient's
+//     rows, counts its own and those of the lower classes, and so knows where its
+//     tokens go without hearing from the other blocks. One warp places them, 32 in
+//     order at a time.
+//  2. The sorted positions are cut into slabs of equal length, whatever the tokens:
+//     a frequent token is many slabs' work, not one block's. A block adds a slab's
+//     rows over a run of columns in registers (fp32) and writes a row where the
+//     token changes; a token that goes on beyond the slab leaves a partial sum.
+//     Further blocks zero the rows without a token.
+//  3. The partial sums of a token are added in slab order.
+#include <algorithm>
+
+#include "internal.h"
+#include "rowvec.cuh"
+#include "tc_ptx.cuh"
+
+namespace ivfpq {
+namespace {
+
+dim3 grid_of(int64_t per_row, int64_t rows) {
+  const int64_t y = std::min<int64_t>(rows, 65535);
+  return dim3(unsigned(per_row), unsigned(y), unsigned(ceil_div(rows, y)));
+}
+__device__ __forceinline__ int64_t grid_row() {
+  return blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+}
+
+// ---- lookup ---------------------------------------------------------------------------
+constexpr int kLookupThreads = 256;
+
+struct LookupArgs {
+  const void* table;
+  int64_t rows, cols, ldt;
+  const void* ids;
+  int wide;  // ids are int64
+  int64_t tokens;
+  float scale;
+  void* out;
+  int64_t ldo;
+  int tx;  // threads along a row, a power of two
+};
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
+  return wide ? static_cast<const int64_t*>(ids)[t] : int64_t(static_cast<const int32_t*>(ids)[t]);
+}
+
+template <class T, class O, int U>
+__global__ void __launch_bounds__(kLookupThreads) embedding_lookup_kernel(const LookupArgs a) {
+  constexpr int N = Span<T>::N;
+  const int ty = kLookupThreads / a.tx, x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx;
+  const int64_t t0 = grid_row() * (ty * U) + y;
+  const int cols = int(a.cols);
+  int64_t id[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * ty;
+    id[u] = t < a.tokens ? id_at(a.ids, a.wide, t) : -1;
+    if (id[u] < 0 || id[u] >= a.rows) id[u] = -1;
+  }
+  const T* table = static_cast<const T*>(a.table);
+  O* out = static_cast<O*>(a.out);
+  const int step = int(gridDim.x) * a.tx;
+  // a row has up to N - 1 elements before its first vector and as many after the last
+  for (int i = int(blockIdx.x) * a.tx + x; i * N < cols + 2 * N; i += step) {
+    uint4 r[U];
+    int head[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * ty;
+      head[u] = -1;
+      if (t >= a.tokens) continue;
+      const O* dst = out + t * a.ldo;
+      head[u] = min(cols, int((16 - misalign(dst)) & 15) / int(sizeof(O)));
+      const int nvec = (cols - head[u]) / N;
+      r[u] = make_uint4(0, 0, 0, 0);
+      if (i < nvec && id[u] >= 0) {
+        const T* src = table + id[u] * a.ldt + head[u];
+        r[u] = load_vec(src, cols - head[u], i, misalign(src));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (head[u] < 0) continue;
+      const int64_t t = t0 + u * ty;
+      O* dst = out + t * a.ldo;
+      const int nvec = (cols - head[u]) / N;
+      if (i < nvec) {
+        float v[N];
+        unpack_vec<T>(r[u], v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= a.scale;
+        store_vec<O>(dst + head[u] + i * N, v);
+      } else {
+        // the elements outside the vectors, up to N of them to each of the last two
+        const int rest = cols - nvec * N, from = (i - nvec) * N;
+        for (int e = from; e < min(rest, from + N); ++e) {
+          const int c = e < head[u] ? e : nvec * N + e;
+          const float v = id[u] >= 0 ? to_f32(table[id[u] * a.ldt + c]) : 0.f;
+          dst[c] = from_f32<O>(v * a.scale);
+        }
+      }
+    }
+  }
+}
+
+template <class T, class O>
+int launch_lookup(LookupArgs a, cudaStream_t s) {
+  const int64_t nvec = a.cols / Span<T>::N + 2;
+  a.tx = 32;
+  while (a.tx < kLookupThreads && a.tx < nvec) a.tx *= 2;
+  const int ty = kLookupThreads / a.tx;
+  const int64_t runs = std::min<int64_t>(ceil_div(nvec, a.tx), 64);
+  // four tokens per thread hide their latency behind each other; one while there
+  // are few, for more blocks
+  const bool many = a.tokens * runs >= int64_t(16) * num_sms() * ty;
+  if (many) {
+    embedding_lookup_kernel<T, O, 4>
+        <<<grid_of(runs, ceil_div(a.tokens, 4 * ty)), kLookupThreads, 0, s>>>(a);
+  } else {
+    embedding_lookup_kernel<T, O, 1>
+        <<<grid_of(runs, ceil_div(a.tokens, ty)), kLookupThreads, 0, s>>>(a);
+  }
+  IVFPQ_LAUNCHED();
+  return IVFPQ_OK;
+}
+
+// ---- gradient: positions by token ----------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kMaxLocal = 16384;  // a block's tokens: 64 KB of counters
+constexpr int kPerThread = 4;     // consecutive ids per thread and step
+
+struct SortArgs {
+  const void* ids;
+  int wide;
+  int64_t tokens, rows, padding;
+  int shift;  // 2^shift classes, one per block
+  int local;  // tokens of a class
+  int32_t* list;   // [tokens] scratch: the class's positions in order
+  int32_t* pos;    // [tokens] positions sorted by (class, token, position)
+  int32_t* token;  // [tokens] their tokens
+  int32_t* count;  // [rows] positions of each token
+  int32_t* valid;  // [1] positions that hold a token
+};
+
+__device__ __forceinline__ int block_sum(int v, int* sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = int(__reduce_add_sync(kFullMask, unsigned(v)));
+  __syncthreads();
+  if (lane == 0) sh[warp] = v;
+  __syncthreads();
+  return int(__reduce_add_sync(kFullMask, unsigned(lane < int(blockDim.x) / 32 ? sh[lane] : 0)));
+}
+// The sum of v over the threads before this one; all: over the block.
+__device__ __forceinline__ int block_before(int v, int* sh, int* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = int(blockDim.x) / 32;
+  int in = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int t = __shfl_up_sync(kFullMask, in, d);
+    if (lane >= d) in += t;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = in;
+  __syncthreads();
+  const int w = lane < warps ? sh[lane] : 0;
+  *all = int(__reduce_add_sync(kFullMask, unsigned(w)));
+  return int(__reduce_add_sync(kFullMask, unsigned(lane < warp ? w : 0))) + in - v;
+}
+
+// The tokens of kPerThread consecutive positions, -1 where there is none to count.
+__device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t, int (&v)[kPerThread]) {
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    int64_t id = -1;
+    if (t + j < a.tokens) id = id_at(a.ids, a.wide, t + j);
+    v[j] = id >= 0 && id < a.rows && id != a.padding ? int(id) : -1;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const SortArgs a) {
+  extern __shared__ int sort_smem[];
+  int* next = sort_smem;  // [local]: counts, then where a token's next position goes
+  __shared__ int sh[32];
+  const int c = blockIdx.x, mask = (1 << a.shift) - 1;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < a.local; i += kSortThreads) next[i] = 0;
+  __syncthreads();
+  int before = 0, v[kPerThread];
+  for (int64_t t = int64_t(threadIdx.x) * kPerThread; t < a.tokens;
+       t += kSortThreads * kPerThread) {
+    read_tokens(a, t, v);
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      if (v[j] < 0) continue;
+      const int cls = v[j] & mask;
+      before += cls < c;
+      if (cls == c) atomicAdd(&next[v[j] >> a.shift], 1);
+    }
+  }
+  const int base = block_sum(before, sh);
+  // counts out; their running sums stay
+  int n = 0;
+  for (int i0 = 0; i0 < a.local; i0 += kSortThreads) {
+    const int i = i0 + threadIdx.x;
+    const int64_t token = (int64_t(i) << a.shift) + c;
+    const int k = i < a.local ? next[i] : 0;
+    if (i < a.local && token < a.rows) a.count[token] = k;
+    int all;
+    const int at = block_before(k, sh, &all);
+    if (i < a.local) next[i] = n + at;
+    n += all;
+  }
+  if (c == mask && threadIdx.x == 0) *a.valid = base + n;
+  if (n == 0) return;
+  // the class's positions in order
+  int found = 0;
+  for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += kSortThreads * kPerThread) {
+    const int64_t t = t0 + int64_t(threadIdx.x) * kPerThread;
+    read_tokens(a, t, v);
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) mine += v[j] >= 0 && (v[j] & mask) == c;
+    int all, at = found + block_before(mine, sh, &all);
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      if (v[j] >= 0 && (v[j] & mask) == c) {
+        a.list[base + at] = int32_t(t + j);
+        ++at;
+      }
+    }
+    found += all;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const bool live = i0 + lane < n;
+    const int p = live ? a.list[base + i0 + lane] : -1;
+    const int id = live ? int(id_at(a.ids, a.wide, p)) : -1;
+    const unsigned same = __match_any_sync(kFullMask, id);
+    const unsigned below = same & ((1u << lane) - 1u);
+    int at = 0;
+    if (live) at = next[id >> a.shift] + __popc(below);
+    __syncwarp();
+    if (live) {
+      a.pos[base + at] = p;
+      a.token[base + at] = id;
+      if (below == 0) next[id >> a.shift] = at + __popc(same);
+    }
+    __syncwarp();
+  }
+}
+
+// ---- gradient: sums ---------------------------------------------------------------------
+constexpr int kMaxSlab = 256;
+constexpr int kZeroRows = 8;  // rows that one block looks at to zero them
+
+struct SumArgs {
+  const void* grad;
+  int64_t cols, ldg, rows, tokens;
+  const int32_t* pos;
+  const int32_t* token;
+  const int32_t* count;
+  const int32_t* valid;
+  int slab;
+  int64_t slabs;
+  float scale;
+  int accumulate;
+  float* part;  // [slabs, 2, pitch]: of the token that goes on from the slab before, and
+                // of the one that starts here and goes on into the next
+  int64_t pitch;
+  void* out;
+  int64_t ldo;
+};
+
+// Row values of columns N cv .. N cv + N - 1 of token v.
+template <class T, class O>
+__device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int cv,
+                                          const float (&s)[Span<T>::N]) {
+  constexpr int N = Span<T>::N;
+  O* dst = static_cast<O*>(a.out) + v * a.ldo + int64_t(cv) * N;
+  const int have = int(min(int64_t(N), a.cols - int64_t(cv) * N));
+  if (have == N && misalign(dst) == 0) {
+    float w[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] = s[j] * a.scale;
+    if (a.accumulate) {
+      constexpr int M = Span<O>::N;
+#pragma unroll
+      for (int q = 0; q < N / M; ++q) {
+        float old[M];
+        unpack_vec<O>(reinterpret_cast<const uint4*>(dst)[q], old);
+#pragma unroll
+        for (int j = 0; j < M; ++j) w[q * M + j] += old[j];
+      }
+    }
+    store_vec<O>(dst, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j < have) {
+        float w = s[j] * a.scale;
+        if (a.accumulate) w += to_f32(dst[j]);
+        dst[j] = from_f32<O>(w);
+      }
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ float* part_at(const SumArgs& a, int64_t slab, int which, int cv) {
+  return a.part + (slab * 2 + which) * a.pitch + int64_t(cv) * N;
+}
+
+template <class T, class O>
+__device__ void zero_row(O* p, int len, int x, int step) {
+  const Span<O> sp(p, len);
+  for (int e = x; e < sp.rest(); e += step) p[sp.at(e)] = from_f32<O>(0.f);
+  for (int i = x; i < sp.nvec; i += step)
+    reinterpret_cast<uint4*>(p + sp.head)[i] = make_uint4(0, 0, 0, 0);
+}
+
+template <class T, class O>
+__global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
+  constexpr int N = Span<T>::N, U = 8;
+  __shared__ int32_t pos[kMaxSlab], token[kMaxSlab + 2];
+  const int64_t slab = grid_row();
+  grid_wait();
+  if (slab >= a.slabs) {
+    // rows without a token
+    const int step = int(gridDim.x * blockDim.x), x = int(blockIdx.x * blockDim.x + threadIdx.x);
+    const int64_t v0 = (slab - a.slabs) * kZeroRows;
+    for (int64_t v = v0; v < min(v0 + kZeroRows, a.rows); ++v)
+      if (a.count[v] == 0)
+        zero_row<T, O>(static_cast<O*>(a.out) + v * a.ldo, int(a.cols), x, step);
+    return;
+  }
+  const int valid = *a.valid;
+  const int64_t i0 = slab * a.slab;
+  if (i0 >= valid) return;
+  const int n = int(min(int64_t(a.slab), valid - i0));
+  // token[0] and token[n + 1]: the neighbours
+  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+    const int64_t j = i0 + i - 1;
+    token[i] = j >= 0 && j < valid ? a.token[j] : -1;
+    if (i >= 1 && i <= n) pos[i - 1] = a.pos[j];
+  }
+  __syncthreads();
+  const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
+  if (int64_t(cv) * N >= a.cols) return;
+  const T* grad = static_cast<const T*>(a.grad);
+  const int cols = int(a.cols);
+  float s[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = 0.f;
+  bool first = token[0] == token[1];  // the running token began in an earlier slab
+  for (int b = 0; b < n; b += U) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u < n) {
+        const T* p = grad + pos[b + u] * a.ldg;
+        r[u] = load_vec(p, cols, cv, misalign(p));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = b + u;
+      if (i >= n) break;
+      float v[N];
+      unpack_vec<T>(r[u], v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[j] += v[j];
+      const bool ends = token[i + 2] != token[i + 1];
+      if (ends || i == n - 1) {
+        if (!ends || first) {
+          float* q = part_at<N>(a, slab, first ? 0 : 1, cv);
+#pragma unroll
+          for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<float4*>(q + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+        } else {
+          write_row<T, O>(a, token[i + 1], cv, s);
+        }
+        first = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j] = 0.f;
+      }
+    }
+  }
+}
+
+// The tokens that go on into the next slab, at the slab in which they start.
+template <class T, class O>
+__global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs a) {
+  constexpr int N = Span<T>::N;
+  grid_wait();
+  const int64_t slab = grid_row();
+  const int valid = *a.valid;
+  const int64_t i0 = slab * a.slab, i1 = i0 + a.slab;
+  if (slab >= a.slabs || i1 >= valid) return;
+  const int32_t id = a.token[i1 - 1];
+  if (a.token[i1] != id) return;
+  if (i0 > 0 && a.token[i0 - 1] == id) return;  // it started before this slab
+  const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
+  if (int64_t(cv) * N >= a.cols) return;
+  float s[N];
+  const float* q = part_at<N>(a, slab, 1, cv);
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = q[j];
+  for (int64_t k = slab + 1; k < a.slabs && k * a.slab < valid && a.token[k * a.slab] == id; ++k) {
+    q = part_at<N>(a, k, 0, cv);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] += q[j];
+  }
+  write_row<T, O>(a, id, cv, s);
+}
+
+template <class K, class A>
+int launch_after(K kern, dim3 grid, int threads, const A& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+  IVFPQ_LAUNCHED_K(kern, 0, threads);
+  return IVFPQ_OK;
+}
+
+template <class T, class O>
+int launch_sums(const SumArgs& a, cudaStream_t s) {
+  const int64_t nvec = ceil_div(a.cols, Span<T>::N);
+  int threads = 32;
+  while (threads < 128 && threads < nvec) threads *= 2;
+  const int64_t runs = ceil_div(nvec, threads);
+  const int64_t zero = a.accumulate ? 0 : ceil_div(a.rows, kZeroRows);
+  IVFPQ_TRY(launch_after(embedding_sum_kernel<T, O>, grid_of(runs, a.slabs + zero), threads, a, s));
+  if (a.slabs <= 1) return IVFPQ_OK;
+  return launch_after(embedding_join_kernel<T, O>, grid_of(runs, a.slabs), threads, a, s);
+}
+
+int check_common(const char* fn, int dtype, int out_dtype, int64_t rows, int64_t cols,
+                 int64_t tokens, int ids_bytes) {
+  IVFPQ_REQUIRE(known_dtype(dtype) && known_dtype(out_dtype), "%s: unknown element type", fn);
+  IVFPQ_REQUIRE(out_dtype == dtype || out_dtype == IVFPQ_F32,
+                "%s: the output is of the input's type or fp32", fn);
+  IVFPQ_REQUIRE(rows >= 0 && rows <= (int64_t(1) << 24), "%s: rows=%lld outside [0, 2^24]", fn,
+                (long long)rows);
+  IVFPQ_REQUIRE(cols >= 0 && cols <= (int64_t(1) << 20), "%s: cols=%lld outside [0, 2^20]", fn,
+                (long long)cols);
+  IVFPQ_REQUIRE(tokens >= 0 && tokens < (int64_t(1) << 30), "%s: tokens=%lld outside [0, 2^30)",
+                fn, (long long)tokens);
+  IVFPQ_REQUIRE(ids_bytes == 4 || ids_bytes == 8, "%s: ids of %d bytes", fn, ids_bytes);
+  return IVFPQ_OK;
+}
+
+}  // namespace
+}  // namespace ivfpq
+
+using namespace ivfpq;
+
+extern "C" int embedding_lookup(const void* table, int dtype, int64_t rows, int64_t cols,
+                                int64_t ldt, const void* ids, int ids_bytes, int64_t tokens,
+                                float scale, void* out, int out_dtype, int64_t ldo, void* stream) {
+  clear_error();
+  IVFPQ_TRY(check_common("embedding_lookup", dtype, out_dtype, rows, cols, tokens, ids_bytes));
+  IVFPQ_REQUIRE(rows <= 1 || ldt >= cols || ldt == 0,
+                "embedding_lookup: row stride %lld below cols=%lld", (long long)ldt,
+                (long long)cols);
+  IVFPQ_REQUIRE(tokens <= 1 || ldo >= cols, "embedding_lookup: row stride %lld below cols=%lld",
+                (long long)ldo, (long long)cols);
+  if (tokens == 0 || cols == 0) return IVFPQ_OK;
+  IVFPQ_REQUIRE(ids && out && (table || rows == 0), "embedding_lookup: null pointer");
+  const LookupArgs a{table, rows, cols, ldt, ids, ids_bytes == 8, tokens, scale, out, ldo, 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return by_dtype(dtype, [&](auto* t) -> int {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return out_dtype == dtype ? launch_lookup<T, T>(a, s) : launch_lookup<T, float>(a, s);
+  });
+}
+
+extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols,
+                                  int64_t ldg, const void* ids, int ids_bytes, int64_t rows,
+                                  float scale, int64_t padding, int accumulate, void* out,
+                                  int out_dtype, int64_t ldo, void* stream) {
+  clear_error();
+  IVFPQ_TRY(check_common("embedding_gradient", dtype, out_dtype, rows, cols, tokens, ids_bytes));
+  IVFPQ_REQUIRE(tokens <= 1 || ldg >= cols || ldg == 0,
+                "embedding_gradient: row stride %lld below cols=%lld", (long long)ldg,
+                (long long)cols);
+  IVFPQ_REQUIRE(rows <= 1 || ldo >= cols, "embedding_gradient: row stride %lld below cols=%lld",
+                (long long)ldo, (long long)cols);
+  if (rows == 0 || cols == 0 || (tokens == 0 && accumulate)) return IVFPQ_OK;
+  IVFPQ_REQUIRE(out && ((ids && grad) || tokens == 0), "embedding_gradient: null pointer");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  SortArgs o{};
+  o.ids = ids;
+  o.wide = ids_bytes == 8;
+  o.tokens = tokens;
+  o.rows = rows;
+  o.padding = padding;
+  // a block per SM or nearly, and more where a class would have too many tokens
+  o.shift = 7;
+  while (ceil_div(rows, int64_t(1) << o.shift) > kMaxLocal) ++o.shift;
+  o.local = int(ceil_div(rows, int64_t(1) << o.shift));
+  SumArgs a{};
+  a.grad = grad;
+  a.cols = cols;
+  a.ldg = ldg;
+  a.rows = rows;
+  a.tokens = tokens;
+  a.scale = scale;
+  a.accumulate = accumulate != 0;
+  a.out = out;
+  a.ldo = ldo;
+  a.slab = 32;
+  while (a.slab < kMaxSlab && tokens > int64_t(a.slab) * 1024) a.slab *= 2;
+  a.slabs = ceil_div(tokens, a.slab);
+  a.pitch = ceil_div(cols, 8) * 8;
+  Workspace ws(s);
+  int32_t* w = nullptr;
+  IVFPQ_TRY(ws.alloc(&w, size_t(tokens) * 3 + size_t(rows) + 1));
+  o.list = w;
+  o.pos = w + tokens;
+  o.token = w + 2 * tokens;
+  o.count = w + 3 * tokens;
+  o.valid = o.count + rows;
+  if (a.slabs > 1) IVFPQ_TRY(ws.alloc(&a.part, size_t(a.slabs) * 2 * size_t(a.pitch)));
+  a.pos = o.pos;
+  a.token = o.token;
+  a.count = o.count;
+  a.valid = o.valid;
+  const size_t smem = size_t(o.local) * 4;
+  IVFPQ_TRY(set_dynamic_smem(embedding_sort_kernel, smem));
+  embedding_sort_kernel<<<1u << o.shift, kSortThreads, smem, s>>>(o);
+  IVFPQ_LAUNCHED_K(embedding_sort_kernel, smem, kSortThreads);
+  return by_dtype(dtype, [&](auto* t) -> int {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return out_dtype == dtype ? launch_sums<T, T>(a, s) : launch_sums<T, float>(a, s);
+  });
+}

@@ -10,8 +10,10 @@
  * row-wise k-selection are exposed too.
  *
  * Beside the searches it has what belongs to a score row: products of 4-bit
- * block-scaled vectors, the adjustments between a product and a selection, and
- * distillation from a selected list.
+ * block-scaled vectors with the adapters of many requests, the adjustments between
+ * a product and a selection, the selection over beams with the reordering of
+ * their states, the embeddings of what was selected, and distillation from a
+ * selected list.
  *
  * Conventions for every entry point:
  *  - Array pointers are DEVICE pointers (for example torch tensors'
@@ -593,6 +595,119 @@ int topk_distill(const void* scores, int dtype, int64_t rows, int64_t cols, int6
                  const float* teacher_vals, const int64_t* teacher_ids, int k, float temperature,
                  int negated, const float* row_grad, float* loss, void* grad, int64_t ldg,
                  void* stream);
+
+/* Limits of the beam and adapter calls. */
+#define IVFPQ_MAX_BEAMS 64     /* beams of a group */
+#define IVFPQ_MAX_BEAM_K 128   /* continuations taken per group */
+#define IVFPQ_MAX_RANK 128     /* an adapter's rank */
+#define IVFPQ_MAX_ADAPTERS 8191
+
+/*
+ * beam_select -- the best continuations of every group's beams. For beam b of
+ * group g, whose score row is row g * beams + b,
+ *   total(b, c) = totals[g, b] + s_c - log sum_j exp(s_j)
+ * and the k largest over all (b, c) are taken, best first, equal ones by (b, c).
+ * Totals are compared in fp64 (the sum of exponentials is held in fp32) and
+ * rounded once; entries of one beam are compared by their scores.
+ *  scores     device [groups * beams, cols] of dtype, row stride lds (0 repeats
+ *             a row). A score of -inf is no continuation; a row that has nothing
+ *             else, or that holds a NaN or +inf, has none
+ *  totals     device fp32 [groups, beams]: a beam whose total is not finite has
+ *             none (-inf: a beam that is not alive yet)
+ *  finished   device uint8 [groups, beams] or NULL: a beam that is nonzero has
+ *             one continuation, (b, end_id), with its own total; its scores are
+ *             not read
+ *  end_id     in [0, cols) where finished is given
+ *  out_totals device fp32 [groups, k], out_beams, out_ids device int32
+ *             [groups, k]; where there are fewer than k, (-inf, -1, -1). A total
+ *             past fp32's range is -inf beside its beam and id
+ * beams <= IVFPQ_MAX_BEAMS, k <= IVFPQ_MAX_BEAM_K, groups * beams < 2^31,
+ * cols <= 2^28. Errors: INVALID_ARG, OOM, CUDA.
+ */
+int beam_select(const void* scores, int dtype, int64_t groups, int beams, int64_t cols,
+                int64_t lds, const float* totals, const uint8_t* finished, int32_t end_id, int k,
+                float* out_totals, int32_t* out_beams, int32_t* out_ids, void* stream);
+
+/* A state of the beams (a cache, a history): rows of `outer` segments of `inner`
+ * bytes. Strides are in bytes, none negative; the rows and segments of dst do not
+ * overlap, and dst is src (in place, with the same strides) or does not overlap it. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_row, dst_row;     /* between rows (src_row 0 repeats one) */
+  int64_t outer;                /* segments of a row, < 2^31 */
+  int64_t src_outer, dst_outer; /* between segments */
+  int64_t inner;                /* < 2^40 */
+  int64_t unit;                 /* bytes of one position of a segment (lengths); 0: the
+                                   whole segment whatever the lengths */
+} ivfpq_state;
+
+/*
+ * beam_reorder -- states into the order of the selected continuations: row
+ * g * n + j of dst is row g * width + beams[g, j] of src.
+ *  states   HOST array of `count` states of different memory
+ *  beams    device int32 [groups, n], as beam_select returns them; a row whose
+ *           beam is outside [0, width) stays as it was
+ *  width    rows of a group in src; n: rows of a group in dst (width where a state
+ *           is reordered in place)
+ *  lengths  device int32 [groups] or NULL: positions of each group that are in
+ *           use; what lies past them stays as it was
+ * width, n <= IVFPQ_MAX_BEAMS. Errors: INVALID_ARG, CUDA.
+ */
+int beam_reorder(const ivfpq_state* states, int count, const int32_t* beams, int64_t groups,
+                 int width, int n, const int32_t* lengths, void* stream);
+
+/*
+ * embedding_lookup -- out[t] = scale * table[ids[t]], the product rounded to fp32
+ * and then to out_dtype; zeros where the id is outside [0, rows).
+ *  table  device [rows, cols] of dtype, row stride ldt (0 repeats a row)
+ *  ids    device int32 or int64 (ids_bytes 4 or 8) [tokens]
+ *  out    device [tokens, cols] of out_dtype (dtype or IVFPQ_F32), row stride ldo
+ * rows <= 2^24, cols <= 2^20, tokens < 2^30. Errors: INVALID_ARG, CUDA.
+ */
+int embedding_lookup(const void* table, int dtype, int64_t rows, int64_t cols, int64_t ldt,
+                     const void* ids, int ids_bytes, int64_t tokens, float scale, void* out,
+                     int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * embedding_gradient -- the gradient of embedding_lookup's table:
+ *   out[v] = scale * sum of grad[t] over the t with ids[t] = v
+ * (added to what out holds, if accumulate is nonzero). Sums are taken in fp32, in
+ * an order fixed by the ids and sizes, so results repeat bit for bit.
+ *  grad     device [tokens, cols] of dtype, row stride ldg (0: one row for all)
+ *  ids      as above; ids outside [0, rows), and the id `padding`, have no gradient
+ *  out      device [rows, cols] of out_dtype (dtype or IVFPQ_F32), row stride ldo:
+ *           every row is written; with accumulate only those of tokens that occur
+ * Errors: INVALID_ARG, OOM, CUDA.
+ */
+int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols, int64_t ldg,
+                       const void* ids, int ids_bytes, int64_t rows, float scale, int64_t padding,
+                       int accumulate, void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * adapter_linear -- low-rank adapters of many requests beside a projection that
+ * they share (fp4_linear's, for instance):
+ *   out[t] = base[t] + scales[i] (x[t] a[i]^T) b[i]^T,  i = ids[t]
+ * x[t] a[i]^T is held in fp32 and enters the second product with a relative error
+ * of at most 2^-16 per element (2^-22 where the output is fp32); sums are fp32, the
+ * result is rounded once.
+ *  x       device [tokens, cols] of dtype (IVFPQ_F16 or IVFPQ_BF16), row stride ldx
+ *          (0 repeats a row)
+ *  a       device [adapters, rank, cols], b device [adapters, n, rank] of dtype,
+ *          densely packed
+ *  ids     device int32 [tokens]: a token whose id is outside [0, adapters) has
+ *          no adapter and gets its base row
+ *  scales  device fp32 [adapters] or NULL (1)
+ *  base    device [tokens, n] of out_dtype, row stride ldb (0 repeats a row), or
+ *          NULL (zeros); may be out (same stride)
+ *  out     device [tokens, n] of out_dtype (dtype or IVFPQ_F32), row stride ldo
+ * rank <= IVFPQ_MAX_RANK, adapters <= IVFPQ_MAX_ADAPTERS, tokens < 2^24, cols <=
+ * 2^20, n <= 2^24. Errors: INVALID_ARG, OOM, CUDA.
+ */
+int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t cols, int64_t ldx,
+                   const void* a, const void* b, int adapters, int rank, int64_t n,
+                   const int32_t* ids, const float* scales, const void* base, int64_t ldb,
+                   void* out, int out_dtype, int64_t ldo, void* stream);
 
 /* ivfpq_device_check -- synchronises `stream` and reports whether any kernel
  * of this library on the current device gave up a bounded wait since the
