@@ -1036,23 +1036,35 @@ def _state(t, o, axis, groups, width, n, lengths, at, name):
     dims = len(shape)
     if dims < 1 or shape[0] != groups * width:
         raise ValueError(f"{name} must have {groups * width} rows, got shape {tuple(shape)}")
-    if o.dtype != t.dtype or so[0] != groups * n or so[1:] != shape[1:]:
+    if o is not t and (o.dtype != t.dtype or so[0] != groups * n or so[1:] != shape[1:]):
         raise ValueError(f"the output of {name} must be {t.dtype} with {groups * n} rows of its "
                          f"shape, got {o.dtype} {tuple(so)}")
-    st, sto = t.stride(), o.stride()
-    first = max(_dense_tail(shape, st), _dense_tail(shape, sto))
-    unit = 0
+    if lengths and not 1 <= axis < dims:
+        raise ValueError(f"{name}: positions must be one of its dimensions 1 to {dims - 1}")
+    st = t.stride()
+    sto = st if o is t else o.stride()
     if lengths:
-        if not 1 <= axis < dims:
-            raise ValueError(f"{name}: positions must be one of its dimensions 1 to {dims - 1}")
-        if first > axis:
-            raise ValueError(f"{name}: positions and what follows them must be dense")
-        first, unit = axis, size
+        unit = size
         for v in shape[axis + 1:]:
             unit *= v
-    inner = size
-    for v in shape[first:]:
-        inner *= v
+        inner = unit * shape[axis]
+    if t.is_contiguous() and (o is t or o.is_contiguous()):
+        row = size
+        for v in shape[1:]:
+            row *= v
+        if not lengths:
+            return _State(t.data_ptr(), o.data_ptr(), row, row, 1, 0, 0, row, 0)
+        return _State(t.data_ptr(), o.data_ptr(), row, row, row // inner if inner else 0, inner,
+                      inner, inner, unit)
+    first = max(_dense_tail(shape, st), _dense_tail(shape, sto))
+    if lengths:
+        if first > axis:
+            raise ValueError(f"{name}: positions and what follows them must be dense")
+        first = axis
+    else:
+        unit, inner = 0, size
+        for v in shape[first:]:
+            inner *= v
     outer, src_outer = _segments(shape, st, first, name)
     _, dst_outer = _segments(shape, sto, first, name)
     src_row = st[0] if shape[0] > 1 else 0

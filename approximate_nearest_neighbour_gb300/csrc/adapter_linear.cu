@@ -54,8 +54,8 @@ struct AdapterArgs {
   int4* tiles;     // (adapter or -1, first slot, tokens, 0)
   int32_t* ntiles;
   int tile;     // tokens of a tile
-  float* h;     // [splits, tokens, pitch]
-  int splits;   // parts of K
+  float* h;     // [tokens, pitch], by slot
+  int splits;   // parts of K, one per block of a cluster
   int kpart;    // columns of a part, a multiple of 32
   int pitch;    // rank rounded up to whole instructions
   int run;      // output columns of a block
@@ -84,21 +84,34 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const Adapte
   int* slot = plan_smem;            // [adapters + 1]: counts, then the next slot
   __shared__ int sh[2][32];
   const int bins = a.adapters + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_go();
   for (int i = threadIdx.x; i < bins; i += kPlanThreads) slot[i] = 0;
   __syncthreads();
   // one addition per adapter and warp: prompts bring thousands of tokens of one
-  auto take = [&](int64_t t) {
-    int id = t < a.tokens ? a.ids[t] : -2;
-    if (id != -2 && (id < 0 || id >= a.adapters)) id = a.adapters;
-    if (t >= a.tokens) id = -2;
+  auto take = [&](int id) {
     const unsigned same = __match_any_sync(kFullMask, id);
     int at = 0;
     if (id >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&slot[id], __popc(same));
     at = __shfl_sync(kFullMask, at, __ffs(same) - 1);
-    return make_int2(id, at + __popc(same & ((1u << lane) - 1u)));
+    return at + __popc(same & ((1u << lane) - 1u));
   };
-  const int64_t steps = (a.tokens + kPlanThreads - 1) / kPlanThreads;
-  for (int64_t s = 0; s < steps; ++s) take(s * kPlanThreads + threadIdx.x);
+  constexpr int kIds = 8;  // per thread and step
+  constexpr int64_t step = int64_t(kPlanThreads) * kIds;
+  int v[kIds];
+  auto read = [&](int64_t t0) {
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      const int64_t t = t0 + j * kPlanThreads + threadIdx.x;
+      v[j] = t < a.tokens ? a.ids[t] : -1;
+      if (t < a.tokens && (v[j] < 0 || v[j] >= a.adapters)) v[j] = a.adapters;
+    }
+  };
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
+    read(t0);
+#pragma unroll
+    for (int j = 0; j < kIds; ++j)
+      if (t0 + j * kPlanThreads < a.tokens) take(v[j]);
+  }
   __syncthreads();
   // running sums of the counts and of the tiles
   int slots = 0, tiles = 0;
@@ -135,10 +148,14 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const Adapte
   }
   if (threadIdx.x == 0) *a.ntiles = tiles;
   __syncthreads();
-  for (int64_t s = 0; s < steps; ++s) {
-    const int64_t t = s * kPlanThreads + threadIdx.x;
-    const int2 p = take(t);
-    if (p.x >= 0) a.order[p.y] = int32_t(t);
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
+    if (a.tokens > step) read(t0);
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      if (t0 + j * kPlanThreads >= a.tokens) break;
+      const int at = take(v[j]);
+      if (v[j] >= 0) a.order[at] = int32_t(t0 + j * kPlanThreads + threadIdx.x);
+    }
   }
 }
 
@@ -182,84 +199,250 @@ __device__ __forceinline__ uint4 row8(const T* p, int64_t len, int64_t at) {
 }
 
 // ---- h = x A^T ----------------------------------------------------------------------------
-template <class T, int NT, int MT>
+// The parts of K, each in its block's shared memory ([rows, R]), added in the order
+// of the blocks and written to the slots from `first` on; a share per block.
+template <int R>
+__device__ __forceinline__ void join_parts(const AdapterArgs& a, const float* part, int rows,
+                                           int first) {
+  static_assert(R % 4 == 0, "whole vectors");
+  if (a.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const uint32_t base = smem_u32(part);
+  float* h = a.h + int64_t(first) * R;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < rows * R / 4; i += a.splits * kThreads) {
+    float4 s = ld_cluster4(map_rank(base + 16u * uint32_t(i), 0));
+    for (int v = 1; v < a.splits; ++v) {
+      const float4 f = ld_cluster4(map_rank(base + 16u * uint32_t(i), uint32_t(v)));
+      s.x += f.x;
+      s.y += f.y;
+      s.z += f.z;
+      s.w += f.w;
+    }
+    reinterpret_cast<float4*>(h)[i] = s;
+  }
+  if (a.splits > 1) cluster_sync();  // no block leaves while others read its part
+}
+
+template <class T, int NT>
 __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const AdapterArgs a) {
-  extern __shared__ __align__(16) float shrink_smem[];  // [kWarps, 16 MT, 8 NT]
+  constexpr int R = NT * 8;
+  __shared__ __align__(16) float part[kWarps][16 * R];
   T* const type = nullptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
-  const int subs = (a.tile + 16 * MT - 1) / (16 * MT);
-  const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   grid_wait();
   grid_go();
-  const Tile t = tile_at(a, item / subs);
-  const int m0 = int(item % subs) * 16 * MT, rows = min(16 * MT, t.count - m0);
-  if (rows <= 0 || t.adapter < 0) return;
-  const T* x[MT][2];
+  const Tile t = tile_at(a, blockIdx.y + int64_t(blockIdx.z) * gridDim.y);
+  if (t.count == 0 || t.adapter < 0) return;
+  const T* x[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = m * 16 + e * 8 + r;
-      x[m][e] = i < rows ? static_cast<const T*>(a.x) + token_of(a, t.first + m0 + i) * a.ldx
-                         : nullptr;
-    }
-  const T* w[NT];
+  for (int e = 0; e < 2; ++e)
+    x[e] = e * 8 + r < t.count
+               ? static_cast<const T*>(a.x) + token_of(a, t.first + e * 8 + r) * a.ldx
+               : nullptr;
+  const T* w = static_cast<const T*>(a.a) + (int64_t(t.adapter) * a.rank + r) * a.cols;
+  float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
-    w[j] = j * 8 + r < a.rank ? static_cast<const T*>(a.a) +
-                                    (int64_t(t.adapter) * a.rank + j * 8 + r) * a.cols
-                              : nullptr;
-  float acc[MT][NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
   const int64_t k0 = int64_t(blockIdx.x) * a.kpart, k1 = min(a.cols, k0 + a.kpart);
-  constexpr int U = NT * MT <= 4 ? 4 : NT * MT <= 8 ? 2 : 1;
+  constexpr int U = NT <= 4 ? 4 : NT <= 8 ? 2 : 1;
   for (int64_t k = k0 + warp * 32; k < k1; k += kWarps * 32 * U) {
-    uint4 xv[U][MT][2], wv[U][NT];
+    uint4 xv[U][2], wv[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t at = k + u * kWarps * 32 + 8 * q;
       const int64_t len = k + u * kWarps * 32 < k1 ? a.cols : 0;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) wv[u][j] = row8(w[j], len, at);
+      for (int j = 0; j < NT; ++j)
+        wv[u][j] = row8(j * 8 + r < a.rank ? w + int64_t(j * 8) * a.cols : nullptr, len, at);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) xv[u][m][e] = row8(x[m][e], len, at);
+      for (int e = 0; e < 2; ++e) xv[u][e] = row8(x[e], len, at);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4 &p = xv[u][m][0], &s = xv[u][m][1], &v = wv[u][j];
-          mma16(acc[m][j], p.x, s.x, p.y, s.y, v.x, v.y, type);
-          mma16(acc[m][j], p.z, s.z, p.w, s.w, v.z, v.w, type);
-        }
+      for (int j = 0; j < NT; ++j) {
+        const uint4 &p = xv[u][0], &s = xv[u][1], &v = wv[u][j];
+        mma16(acc[j], p.x, s.x, p.y, s.y, v.x, v.y, type);
+        mma16(acc[j], p.z, s.z, p.w, s.w, v.z, v.w, type);
+      }
   }
-  constexpr int R = NT * 8;
-  float* red = shrink_smem + warp * 16 * MT * R;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float2*>(red + (m * 16 + e * 8 + r) * R + j * 8 + 2 * q) =
-            make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float2*>(&part[warp][(e * 8 + r) * R + j * 8 + 2 * q]) =
+          make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
   __syncthreads();
-  float* h = a.h + (int64_t(blockIdx.x) * a.tokens + t.first + m0) * a.pitch;
-  for (int i = threadIdx.x; i < rows * R; i += kThreads) {
-    float s = 0.f;
+  // the warps' parts into the first warp's place
+  for (int i = threadIdx.x; i < t.count * R; i += kThreads) {
+    float s = part[0][i];
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) s += shrink_smem[v * 16 * MT * R + i];
-    h[(i / R) * a.pitch + i % R] = s;
+    for (int v = 1; v < kWarps; ++v) s += part[v][i];
+    part[0][i] = s;
   }
+  join_parts<R>(a, part[0], t.count, t.first);
+}
+
+// The same for many tokens: a block takes 64 tokens of a tile, 16 per warp, and
+// brings both operands through shared memory, 64 columns (128 bytes) of every row
+// at a time, kStages of them on their way. The 16-byte chunks of a row are swapped
+// around by its number modulo 8, so that the 8 rows that a matrix load takes lie in
+// different banks. Rows that do not lie on 16-byte boundaries (ALIGNED false) go
+// through registers instead of asynchronous copies; the sums are the same.
+constexpr int kStages = 4;
+constexpr int kTokens = 64;
+template <int NT>
+constexpr size_t wide_smem() {
+  return size_t(kStages) * (kTokens + NT * 8) * 128;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void matrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void matrix2(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
+}
+
+template <class T, int NT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) adapter_shrink_wide_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(128) char wide_bytes[];
+  constexpr int R = NT * 8, kStage = (kTokens + R) * 128;
+  T* const type = nullptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
+  const int subs = (a.tile + kTokens - 1) / kTokens;
+  const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  grid_wait();
+  grid_go();
+  const Tile t = tile_at(a, item / subs);
+  const int m0 = int(item % subs) * kTokens, rows = min(kTokens, t.count - m0);
+  if (rows <= 0 || t.adapter < 0) return;
+  // this thread's chunks: column chunk ch of rows r0, r0 + 16, ...
+  const int ch = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  constexpr int XR = kTokens / 16, WR = (R + 15) / 16;
+  const T* x[XR];
+#pragma unroll
+  for (int i = 0; i < XR; ++i) {
+    const int row = r0 + 16 * i;
+    x[i] = row < rows ? static_cast<const T*>(a.x) + token_of(a, t.first + m0 + row) * a.ldx
+                      : nullptr;
+  }
+  const T* w = static_cast<const T*>(a.a) + int64_t(t.adapter) * a.rank * a.cols;
+  auto w_row = [&](int row) { return row < a.rank ? w + int64_t(row) * a.cols : nullptr; };
+  const int64_t k0 = int64_t(blockIdx.x) * a.kpart, k1 = min(a.cols, k0 + a.kpart);
+  const int steps = k1 > k0 ? int((k1 - k0 + 63) / 64) : 0;
+  const uint32_t smem = smem_u32(wide_bytes);
+  auto place = [&](int step) {
+    return uint32_t((step % kStages) * kStage + r0 * 128 + ((ch ^ (r0 & 7)) * 16));
+  };
+  // aligned rows: asynchronous copies
+  auto fetch = [&](int step) {
+    if (step < steps) {
+      const uint32_t base = smem + place(step);
+      const int64_t k = k0 + int64_t(step) * 64 + ch * 8;
+#pragma unroll
+      for (int i = 0; i < XR; ++i) {
+        const bool live = k < k1 && x[i];
+        copy16(base + 16 * i * 128, live ? x[i] + k : a.x, live);
+      }
+#pragma unroll
+      for (int i = 0; i < WR; ++i) {
+        if (R % 16 == 0 || r0 + 16 * i < R) {
+          const T* p = w_row(r0 + 16 * i);
+          const bool live = k < k1 && p;
+          copy16(base + (kTokens + 16 * i) * 128, live ? p + k : a.a, live);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // other rows: into registers, and from there to their place a step later
+  uint4 kept[ALIGNED ? 1 : XR + WR];
+  auto load = [&](int step) {
+    const int64_t k = k0 + int64_t(step) * 64 + ch * 8, len = step < steps && k < k1 ? a.cols : 0;
+#pragma unroll
+    for (int i = 0; i < XR; ++i) kept[ALIGNED ? 0 : i] = row8(x[i], len, k);
+#pragma unroll
+    for (int i = 0; i < WR; ++i)
+      kept[ALIGNED ? 0 : XR + i] = row8(R % 16 == 0 || r0 + 16 * i < R ? w_row(r0 + 16 * i) : nullptr,
+                                        len, k);
+  };
+  auto put = [&](int step) {
+    char* base = wide_bytes + place(step);
+#pragma unroll
+    for (int i = 0; i < XR; ++i)
+      *reinterpret_cast<uint4*>(base + 16 * i * 128) = kept[ALIGNED ? 0 : i];
+#pragma unroll
+    for (int i = 0; i < WR; ++i)
+      if (R % 16 == 0 || r0 + 16 * i < R)
+        *reinterpret_cast<uint4*>(base + (kTokens + 16 * i) * 128) = kept[ALIGNED ? 0 : XR + i];
+  };
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if constexpr (ALIGNED) {
+      fetch(i);
+    } else {
+      load(i);
+      put(i);
+    }
+  }
+  for (int step = 0; step < steps; ++step) {
+    if constexpr (ALIGNED) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();
+    // into the stage that the last step has read
+    if constexpr (ALIGNED)
+      fetch(step + kStages - 1);
+    else
+      load(step + kStages - 1);
+    const uint32_t base = smem + (step % kStages) * kStage;
+    const uint32_t xa = base + (warp * 16 + (lane & 15)) * 128;
+    const uint32_t wa = base + (kTokens + (lane >> 4) * 8 + (lane & 7)) * 128;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t f[4];
+      matrix4(xa + (((2 * kk + (lane >> 4)) ^ (lane & 7)) * 16), f);
+      const uint32_t wc = ((2 * kk + ((lane >> 3) & 1)) ^ (lane & 7)) * 16;
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {
+        uint32_t g[4];
+        if constexpr (NT == 1)
+          matrix2(base + (kTokens + (lane & 7)) * 128 + wc, g);
+        else
+          matrix4(wa + j * 1024 + wc, g);
+        mma16(acc[j], f[0], f[1], f[2], f[3], g[0], g[1], type);
+        if (NT > 1) mma16(acc[j + (NT > 1)], f[0], f[1], f[2], f[3], g[2], g[3], type);
+      }
+    }
+    if constexpr (!ALIGNED) put(step + kStages - 1);
+  }
+  if constexpr (ALIGNED) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(wide_bytes);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float2*>(red + (warp * 16 + e * 8 + r) * R + j * 8 + 2 * q) =
+          make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+  join_parts<R>(a, red, rows, t.first + m0);
 }
 
 // ---- out = base + scale h B^T ----------------------------------------------------------------
@@ -315,39 +498,13 @@ __device__ __forceinline__ void load_b(const T* p, int rank, int q, bool whole,
   }
 }
 
-// 8 neighbouring elements of a row, `have` of them in it.
-template <class O>
-__device__ __forceinline__ void load8(const O* p, int have, float (&v)[8]) {
-  if (have == 8 && misalign(p) == 0) {
-    constexpr int M = Span<O>::N;
-#pragma unroll
-    for (int g = 0; g < 8 / M; ++g) {
-      float w[M];
-      unpack_vec<O>(reinterpret_cast<const uint4*>(p)[g], w);
-#pragma unroll
-      for (int j = 0; j < M; ++j) v[g * M + j] = w[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < have ? to_f32(p[j]) : 0.f;
-  }
-}
-template <class O>
-__device__ __forceinline__ void store8(O* p, int have, const float (&v)[8]) {
-  if (have == 8 && misalign(p) == 0) {
-    store_vec<O>(p, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < have) p[j] = from_f32<O>(v[j]);
-  }
-}
-
-template <class T, class O, int KS, int TERMS>
+// VEC: base and output rows lie on 16-byte boundaries and are whole vectors.
+template <class T, class O, int KS, int TERMS, bool VEC>
 __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterArgs a) {
   extern __shared__ __align__(16) uint4 expand_smem[];  // [m tiles, KS, TERMS, 32]
   __shared__ float up[kMaxTile];                        // a row's power of two
   __shared__ int64_t token[kMaxTile];
+  __shared__ float turned[VEC ? 1 : kWarps][VEC ? 1 : 16 * 33];
   T* const type = nullptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
   grid_wait();
@@ -374,14 +531,12 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
           for (int s = 0; s < KS; ++s) {
             const int k = 4 * KS * q + 4 * s;
             if (k >= a.pitch) continue;
-            for (int p = 0; p < a.splits; ++p) {
-              const float4 f = *reinterpret_cast<const float4*>(
-                  a.h + (int64_t(p) * a.tokens + t.first + i) * a.pitch + k);
-              v[e][4 * s] += f.x;
-              v[e][4 * s + 1] += f.y;
-              v[e][4 * s + 2] += f.z;
-              v[e][4 * s + 3] += f.w;
-            }
+            const float4 f =
+                *reinterpret_cast<const float4*>(a.h + int64_t(t.first + i) * a.pitch + k);
+            v[e][4 * s] = f.x;
+            v[e][4 * s + 1] = f.y;
+            v[e][4 * s + 2] = f.z;
+            v[e][4 * s + 3] = f.w;
           }
         }
 #pragma unroll
@@ -421,32 +576,60 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
   const bool whole = a.rank % (KS == 1 ? 4 : 8) == 0 && misalign(a.b) == 0;
   const T* b0 = some ? static_cast<const T*>(a.b) + int64_t(t.adapter) * a.n * a.rank : nullptr;
   const int64_t cend = min(a.n, (int64_t(blockIdx.x) + 1) * a.run);
-  for (int64_t c0 = int64_t(blockIdx.x) * a.run + warp * 32; c0 < cend; c0 += kWarps * 32) {
-    uint32_t b[4][KS][2];
-    if (some) {
+  const int64_t c0 = int64_t(blockIdx.x) * a.run + warp * 32;
+  if (c0 >= cend) return;
+  const int items = int((cend - c0 + kWarps * 32 - 1) / (kWarps * 32)) * mtiles;
+  auto fetch_b = [&](int64_t at, uint32_t (&b)[4][KS][2]) {
+    if (!some) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t c = c0 + 8 * (r / 2) + 2 * j + (r & 1);
-        load_b<T, KS>(c < a.n ? b0 + c * a.rank : nullptr, a.rank, q, whole, b[j]);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = at + 8 * (r / 2) + 2 * j + (r & 1);
+      load_b<T, KS>(c < cend ? b0 + c * a.rank : nullptr, a.rank, q, whole, b[j]);
+    }
+  };
+  // the base rows of the coming items, on their way
+  constexpr int W = int(sizeof(O)) / 2;
+  constexpr int D = VEC ? (W == 1 ? 4 : 2) : 1;
+  uint4 raw[D][2][W];
+  int fm = 0;
+  int64_t fc = c0;  // the next item to fetch
+  auto fetch = [&](uint4 (&v)[2][W]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = fm * 16 + e * 8 + r;
+#pragma unroll
+      for (int g = 0; g < W; ++g) {
+        v[e][g] = make_uint4(0, 0, 0, 0);
+        if (VEC && base && i < t.count && fc + 8 * q < cend)
+          v[e][g] = reinterpret_cast<const uint4*>(base + token[i] * a.ldb + fc + 8 * q)[g];
       }
     }
-    const int64_t col = c0 + 8 * q;
-    const int have = int(min(int64_t(8), a.n - col));
-    for (int m = 0; m < mtiles; ++m) {
-      float y[2][8];
+    if (++fm == mtiles) {
+      fm = 0;
+      fc += kWarps * 32;
+    }
+  };
+  uint32_t bq[4][KS][2];
+  constexpr bool AHEAD = KS <= 2;  // the next columns' B as well, where it takes few registers
+  uint32_t bn[4][AHEAD ? KS : 1][2];
+  fetch_b(c0, bq);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = m * 16 + e * 8 + r;
+  for (int d = 0; d < D; ++d) fetch(raw[d]);
+  int m = 0;
+  int64_t c = c0;
+  for (int it0 = 0; it0 < items; it0 += D) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[e][j] = 0.f;
-        if (base && i < t.count && have > 0) load8(base + token[i] * a.ldb + col, have, y[e]);
+    for (int d = 0; d < D; ++d) {
+      if (it0 + d >= items) break;
+      if constexpr (AHEAD) {
+        if (m == 0 && c + kWarps * 32 < cend) fetch_b(c + kWarps * 32, bn);
       }
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
       if (some) {
-        float acc[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 #pragma unroll
         for (int n = TERMS - 1; n >= 0; --n)  // the small terms first
 #pragma unroll
@@ -454,24 +637,80 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
             const uint4 f = expand_smem[((m * KS + s) * TERMS + n) * 32 + lane];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma16(acc[j], f.x, f.y, f.z, f.w, b[j][s][0], b[j][s][1], type);
+              mma16(acc[j], f.x, f.y, f.z, f.w, bq[j][s][0], bq[j][s][1], type);
           }
+        if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = m * 16 + e * 8 + r;
-          float f = 1.f;
-          if constexpr (std::is_same<T, __half>::value) f = i < t.count ? up[i] : 1.f;
+          for (int e = 0; e < 2; ++e) {
+            const int i = m * 16 + e * 8 + r;
+            const float f = i < t.count ? up[i] : 1.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[e][2 * j] += acc[j][2 * e] * f;
-            y[e][2 * j + 1] += acc[j][2 * e + 1] * f;
+            for (int j = 0; j < 4; ++j) {
+              acc[j][2 * e] *= f;
+              acc[j][2 * e + 1] *= f;
+            }
           }
         }
       }
+      if constexpr (VEC) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = m * 16 + e * 8 + r;
-        if (i < t.count && have > 0) store8(out + token[i] * a.ldo + col, have, y[e]);
+        for (int e = 0; e < 2; ++e) {
+          const int i = m * 16 + e * 8 + r;
+          float y[8];
+          constexpr int M = Span<O>::N;
+#pragma unroll
+          for (int g = 0; g < W; ++g) {
+            float w[M];
+            unpack_vec<O>(raw[d][e][g], w);
+#pragma unroll
+            for (int j = 0; j < M; ++j) y[g * M + j] = w[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            y[2 * j] += acc[j][2 * e];
+            y[2 * j + 1] += acc[j][2 * e + 1];
+          }
+          if (i < t.count && c + 8 * q < cend) store_vec<O>(out + token[i] * a.ldo + c + 8 * q, y);
+        }
+        fetch(raw[d]);
+      } else {
+        // rows at any offset: through shared memory, a column per lane
+        float* mine = turned[warp];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mine[(e * 8 + r) * 33 + 8 * q + 2 * j] = acc[j][2 * e];
+            mine[(e * 8 + r) * 33 + 8 * q + 2 * j + 1] = acc[j][2 * e + 1];
+          }
+        __syncwarp();
+        const bool in = c + lane < cend;
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          y[i] = base && in && m * 16 + i < t.count
+                     ? to_f32(base[token[m * 16 + i] * a.ldb + c + lane])
+                     : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (in && m * 16 + i < t.count)
+            out[token[m * 16 + i] * a.ldo + c + lane] = from_f32<O>(y[i] + mine[i * 33 + lane]);
+      }
+      if (++m == mtiles) {
+        m = 0;
+        c += kWarps * 32;
+        if constexpr (AHEAD) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              bq[j][s][0] = bn[j][s][0];
+              bq[j][s][1] = bn[j][s][1];
+            }
+        } else if (c < cend) {
+          fetch_b(c, bq);
+        }
       }
     }
   }
@@ -483,59 +722,82 @@ dim3 grid_of(int64_t per_row, int64_t rows) {
   return dim3(unsigned(per_row), unsigned(y), unsigned(ceil_div(rows, y)));
 }
 template <class K>
-int launch_after(K kern, dim3 grid, int threads, size_t smem, const AdapterArgs& a, bool overlap,
-                 cudaStream_t s) {
-  IVFPQ_TRY(set_dynamic_smem(kern, smem));
+int launch(K kern, dim3 grid, int threads, size_t smem, const AdapterArgs& a, bool overlap,
+           int cluster, cudaStream_t s) {
+  // 48 KB with the static part need no leave
+  if (smem > 32 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = unsigned(cluster);
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  if (overlap) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = unsigned(n);
   IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   IVFPQ_LAUNCHED_K(kern, smem, threads);
   return IVFPQ_OK;
 }
 
-template <class T, int NT, int MT>
+template <class T, int NT>
 int launch_shrink(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  const int64_t subs = ceil_div(a.tile, 16 * MT);
-  const size_t smem = size_t(kWarps) * 16 * MT * 8 * NT * 4;
-  return launch_after(adapter_shrink_kernel<T, NT, MT>, grid_of(a.splits, tiles * subs), kThreads,
-                      smem, a, a.tiles != nullptr, s);
+  const bool planned = a.tiles != nullptr;
+  if (a.tile < kMaxTile)
+    return launch(adapter_shrink_kernel<T, NT>, grid_of(a.splits, tiles), kThreads, 0, a, planned,
+                  a.splits, s);
+  const dim3 grid = grid_of(a.splits, tiles * (kMaxTile / kTokens));
+  const bool aligned = a.cols % 8 == 0 && a.ldx % 8 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.a) % 16 == 0;
+  return aligned ? launch(adapter_shrink_wide_kernel<T, NT, true>, grid, kThreads, wide_smem<NT>(),
+                          a, planned, a.splits, s)
+                 : launch(adapter_shrink_wide_kernel<T, NT, false>, grid, kThreads,
+                          wide_smem<NT>(), a, planned, a.splits, s);
 }
 template <class T>
 int launch_shrink_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  const bool two = a.tile >= 32;
   switch (a.pitch / 8) {
-    case 1: return two ? launch_shrink<T, 1, 2>(a, tiles, s) : launch_shrink<T, 1, 1>(a, tiles, s);
-    case 2: return two ? launch_shrink<T, 2, 2>(a, tiles, s) : launch_shrink<T, 2, 1>(a, tiles, s);
-    case 4: return two ? launch_shrink<T, 4, 2>(a, tiles, s) : launch_shrink<T, 4, 1>(a, tiles, s);
-    case 8: return two ? launch_shrink<T, 8, 2>(a, tiles, s) : launch_shrink<T, 8, 1>(a, tiles, s);
-    default:
-      return two ? launch_shrink<T, 16, 2>(a, tiles, s) : launch_shrink<T, 16, 1>(a, tiles, s);
+    case 1: return launch_shrink<T, 1>(a, tiles, s);
+    case 2: return launch_shrink<T, 2>(a, tiles, s);
+    case 4: return launch_shrink<T, 4>(a, tiles, s);
+    case 8: return launch_shrink<T, 8>(a, tiles, s);
+    default: return launch_shrink<T, 16>(a, tiles, s);
   }
 }
 template <class T, class O, int KS>
-int launch_expand(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+int launch_expand(const AdapterArgs& a, int64_t tiles, bool vec, cudaStream_t s) {
   constexpr int TERMS =
       std::is_same<T, __nv_bfloat16>::value && std::is_same<O, float>::value ? 3 : 2;
   const size_t smem = size_t((a.tile + 15) / 16) * KS * TERMS * 512;
-  return launch_after(adapter_expand_kernel<T, O, KS, TERMS>,
-                      grid_of(ceil_div(a.n, a.run), tiles), kThreads, smem, a, true, s);
+  const dim3 grid = grid_of(ceil_div(a.n, a.run), tiles);
+  return vec ? launch(adapter_expand_kernel<T, O, KS, TERMS, true>, grid, kThreads, smem, a, true,
+                      1, s)
+             : launch(adapter_expand_kernel<T, O, KS, TERMS, false>, grid, kThreads, smem, a, true,
+                      1, s);
 }
 template <class T, class O>
 int launch_expand_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
+  const int64_t per = 16 / int64_t(sizeof(O));
+  const bool vec = a.n % 8 == 0 && a.ldo % per == 0 && a.ldb % per == 0 &&
+                   reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(a.base) % 16 == 0;
   switch (a.pitch / 8) {
     case 1:
-    case 2: return launch_expand<T, O, 1>(a, tiles, s);
-    case 4: return launch_expand<T, O, 2>(a, tiles, s);
-    case 8: return launch_expand<T, O, 4>(a, tiles, s);
-    default: return launch_expand<T, O, 8>(a, tiles, s);
+    case 2: return launch_expand<T, O, 1>(a, tiles, vec, s);
+    case 4: return launch_expand<T, O, 2>(a, tiles, vec, s);
+    case 8: return launch_expand<T, O, 4>(a, tiles, vec, s);
+    default: return launch_expand<T, O, 8>(a, tiles, vec, s);
   }
 }
 template <class T>
@@ -595,26 +857,31 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   p.pitch = 8;
   while (p.pitch < rank) p.pitch *= 2;
   const bool planned = tokens > 16;
-  p.tile = !planned ? 1 : tokens <= 256 ? 32 : kMaxTile;
-  const int64_t tiles =
-      planned ? tokens / p.tile + std::min<int64_t>(tokens, int64_t(adapters) + 1) : tokens;
-  // parts of K until there are blocks for every SM, of at least one step each
-  const int64_t items = planned ? ceil_div(tokens, 32) : tokens;
+  p.tile = !planned ? 1 : tokens <= 256 ? 16 : kMaxTile;
+  const int64_t some = std::min<int64_t>(tokens, int64_t(adapters) + 1);
+  const int64_t tiles = planned ? tokens / p.tile + some : tokens;
+  const bool wide = p.tile == kMaxTile;
+  // parts of K until there are blocks for every SM, of some steps each
+  const int64_t items = wide ? ceil_div(tokens, kTokens) : tiles;
+  const int64_t least = wide ? 256 : 128;
   p.splits = 1;
-  while (p.splits < 16 && items * p.splits < 2 * num_sms() && cols > 128 * int64_t(p.splits))
-    p.splits *= 2;
-  p.kpart = int(ceil_div(ceil_div(cols, p.splits), 32) * 32);
+  while (p.splits < 8 && items * p.splits < 2 * num_sms() && cols > least * p.splits) p.splits *= 2;
+  p.kpart = int(ceil_div(ceil_div(cols, p.splits), 64) * 64);
   // runs of columns, long where there are many tiles
   p.run = 128;
-  while (p.run < 512 && ceil_div(n, p.run) * tiles > 8 * num_sms()) p.run *= 2;
+  while (p.run < 1024 && ceil_div(n, p.run) * tiles > 8 * num_sms()) p.run *= 2;
   Workspace ws(s);
-  IVFPQ_TRY(ws.alloc(&p.h, size_t(p.splits) * size_t(tokens) * size_t(p.pitch)));
+  // the sums, and behind them the plan
+  const size_t h = size_t(tokens) * size_t(p.pitch) / 4;
+  float4* w = nullptr;
+  IVFPQ_TRY(ws.alloc(&w, h + (planned ? size_t(tiles) + size_t(ceil_div(tokens + 1, 4)) : 0)));
+  p.h = reinterpret_cast<float*>(w);
   if (planned) {
-    IVFPQ_TRY(ws.alloc(&p.tiles, size_t(tiles) + size_t(ceil_div(tokens + 1, 4))));
+    p.tiles = reinterpret_cast<int4*>(w + h);
     p.order = reinterpret_cast<int32_t*>(p.tiles + tiles);
     p.ntiles = p.order + tokens;
-    const size_t smem = size_t(adapters + 1) * 4;
-    IVFPQ_TRY(launch_after(adapter_plan_kernel, dim3(1), kPlanThreads, smem, p, false, s));
+    IVFPQ_TRY(launch(adapter_plan_kernel, dim3(1), kPlanThreads, size_t(adapters + 1) * 4, p, false,
+                     1, s));
   }
   return dtype == IVFPQ_F16 ? launch_types<__half>(p, out_dtype, tiles, s)
                             : launch_types<__nv_bfloat16>(p, out_dtype, tiles, s);

@@ -97,7 +97,7 @@ __device__ __forceinline__ void move(const char* src, char* dst, int64_t src_row
 }
 
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(IN_PLACE ? kInPlaceThreads : kThreads)
+__global__ void __launch_bounds__(IN_PLACE ? kInPlaceThreads : kThreads, 4)
     beam_reorder_kernel(const __grid_constant__ ReorderArgs a) {
   extern __shared__ __align__(16) char reorder_smem[];
   __shared__ uint8_t to[IVFPQ_MAX_BEAMS], from[IVFPQ_MAX_BEAMS];
@@ -141,7 +141,7 @@ int launch(ReorderArgs& a, cudaStream_t s) {
   if (a.count == 0 || a.blocks == 0) return IVFPQ_OK;
   const int threads = IN_PLACE ? kInPlaceThreads : kThreads;
   const size_t smem = IN_PLACE ? size_t(a.n) * threads * 16 : 0;
-  IVFPQ_TRY(set_dynamic_smem(beam_reorder_kernel<IN_PLACE>, smem));
+  if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(beam_reorder_kernel<IN_PLACE>, smem));
   const unsigned grid = unsigned(std::min<int64_t>(a.blocks, int64_t(1) << 30));
   beam_reorder_kernel<IN_PLACE><<<grid, threads, smem, s>>>(a);
   IVFPQ_LAUNCHED_K(beam_reorder_kernel<IN_PLACE>, smem, threads);

@@ -243,7 +243,7 @@ struct alignas(16) Part {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) beam_rows_kernel(const SelectArgs a) {
   constexpr int N = Span<T>::N;
   extern __shared__ __align__(16) uint64_t select_smem[];
   uint64_t* kept = select_smem;                 // [kCap]
@@ -392,7 +392,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
     const bool ok = j.z > 0.f && j.z < INFINITY;
     a.o.len[row] = ok ? min(total, a.k) : 0;
     a.o.m[row] = j.m;
-    a.o.base[row] = double(t) - log2(double(j.z)) / double(kLog2e);
+    // log Z from its exponent, exactly, and its mantissa in [3/4, 3/2), whose
+    // logarithm in fp32 is off by 2^-25 at most
+    const uint32_t u = __float_as_uint(j.z) - 0x3f400000u;
+    const int ex = int(u) >> 23;
+    const float f = __uint_as_float((u & 0x007fffffu) + 0x3f400000u);
+    a.o.base[row] = double(t) - (double(ex) * 0.69314718055994530942 + double(logf(f)));
   }
 }
 
@@ -479,7 +484,7 @@ int launch_rows(SelectArgs a, cudaStream_t s) {
   while ((loads >> a.shift) + 1 > kMaxBatches) ++a.shift;
   const size_t smem = (size_t(kCap) + size_t(a.k) * (ranks == 1 ? 1 : 1 + ranks)) * 8;
   auto kern = beam_rows_kernel<T>;
-  IVFPQ_TRY(set_dynamic_smem(kern, smem));
+  if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid_of(ranks, a.rows);
   cfg.blockDim = dim3(kThreads);
@@ -499,7 +504,7 @@ int launch_rows(SelectArgs a, cudaStream_t s) {
 
 int launch_merge(const MergeArgs& a, cudaStream_t s) {
   const size_t smem = size_t(a.beams + (a.beams + 1) / 2) * a.k * 16;
-  IVFPQ_TRY(set_dynamic_smem(beam_merge_kernel, smem));
+  if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(beam_merge_kernel, smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(std::min<int64_t>(a.groups, int64_t(1) << 20)));
   cfg.blockDim = dim3(kThreads);

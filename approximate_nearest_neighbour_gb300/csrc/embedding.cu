@@ -54,80 +54,106 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
   return wide ? static_cast<const int64_t*>(ids)[t] : int64_t(static_cast<const int32_t*>(ids)[t]);
 }
 
+// Rows whose vectors all lie on 16-byte boundaries, in the table and the output.
 template <class T, class O, int U>
-__global__ void __launch_bounds__(kLookupThreads) embedding_lookup_kernel(const LookupArgs a) {
+__global__ void __launch_bounds__(kLookupThreads) lookup_aligned_kernel(const LookupArgs a) {
   constexpr int N = Span<T>::N;
   const int ty = kLookupThreads / a.tx, x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx;
   const int64_t t0 = grid_row() * (ty * U) + y;
-  const int cols = int(a.cols);
+  const int nvec = int(a.cols) / N, step = int(gridDim.x) * a.tx;
   int64_t id[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = t0 + u * ty;
     id[u] = t < a.tokens ? id_at(a.ids, a.wide, t) : -1;
-    if (id[u] < 0 || id[u] >= a.rows) id[u] = -1;
   }
-  const T* table = static_cast<const T*>(a.table);
-  O* out = static_cast<O*>(a.out);
-  const int step = int(gridDim.x) * a.tx;
-  // a row has up to N - 1 elements before its first vector and as many after the last
-  for (int i = int(blockIdx.x) * a.tx + x; i * N < cols + 2 * N; i += step) {
+  for (int i = int(blockIdx.x) * a.tx + x; i < nvec; i += step) {
     uint4 r[U];
-    int head[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t t = t0 + u * ty;
-      head[u] = -1;
-      if (t >= a.tokens) continue;
-      const O* dst = out + t * a.ldo;
-      head[u] = min(cols, int((16 - misalign(dst)) & 15) / int(sizeof(O)));
-      const int nvec = (cols - head[u]) / N;
       r[u] = make_uint4(0, 0, 0, 0);
-      if (i < nvec && id[u] >= 0) {
-        const T* src = table + id[u] * a.ldt + head[u];
-        r[u] = load_vec(src, cols - head[u], i, misalign(src));
-      }
+      if (id[u] >= 0 && id[u] < a.rows)
+        r[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.table) +
+                                                    id[u] * a.ldt) + i);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (head[u] < 0) continue;
       const int64_t t = t0 + u * ty;
-      O* dst = out + t * a.ldo;
-      const int nvec = (cols - head[u]) / N;
-      if (i < nvec) {
-        float v[N];
-        unpack_vec<T>(r[u], v);
+      if (t >= a.tokens) continue;
+      float v[N];
+      unpack_vec<T>(r[u], v);
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] *= a.scale;
-        store_vec<O>(dst + head[u] + i * N, v);
-      } else {
-        // the elements outside the vectors, up to N of them to each of the last two
-        const int rest = cols - nvec * N, from = (i - nvec) * N;
-        for (int e = from; e < min(rest, from + N); ++e) {
-          const int c = e < head[u] ? e : nvec * N + e;
-          const float v = id[u] >= 0 ? to_f32(table[id[u] * a.ldt + c]) : 0.f;
-          dst[c] = from_f32<O>(v * a.scale);
-        }
-      }
+      for (int j = 0; j < N; ++j) v[j] *= a.scale;
+      store_vec<O>(static_cast<O*>(a.out) + t * a.ldo + int64_t(i) * N, v);
+    }
+  }
+}
+
+// Rows at any offset: vectors that start on a 16-byte boundary of the output, each
+// from two of the table's, and single elements before and after them.
+template <class T, class O>
+__global__ void __launch_bounds__(kLookupThreads) lookup_any_kernel(const LookupArgs a) {
+  constexpr int N = Span<T>::N, U = 2;
+  const int ty = kLookupThreads / a.tx, x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx;
+  const int64_t t = grid_row() * ty + y;
+  if (t >= a.tokens) return;
+  const int cols = int(a.cols), step = int(gridDim.x) * a.tx;
+  int64_t id = id_at(a.ids, a.wide, t);
+  if (id < 0 || id >= a.rows) id = -1;
+  O* dst = static_cast<O*>(a.out) + t * a.ldo;
+  const T* src = static_cast<const T*>(a.table) + (id < 0 ? 0 : id * a.ldt);
+  const int head = min(cols, int((16 - misalign(dst)) & 15) / int(sizeof(O)));
+  const int nvec = (cols - head) / N, rest = cols - nvec * N;
+  const int mis = misalign(src + head);
+  const int first = inner_first(mis), last = inner_last<T>(cols - head, mis);
+  const int x0 = int(blockIdx.x) * a.tx + x;
+  for (int e = x0; e < rest; e += step) {
+    const int c = e < head ? e : nvec * N + e;
+    dst[c] = from_f32<O>((id >= 0 ? to_f32(src[c]) : 0.f) * a.scale);
+  }
+  for (int i0 = x0; i0 < nvec; i0 += U * step) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * step;
+      r[u] = make_uint4(0, 0, 0, 0);
+      if (id >= 0 && i < nvec)
+        r[u] = i >= first && i <= last ? load_inner(src + head, i, mis)
+                                       : load_edge(src + head, cols - head, i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * step;
+      if (i >= nvec) continue;
+      float v[N];
+      unpack_vec<T>(r[u], v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] *= a.scale;
+      store_vec<O>(dst + head + i * N, v);
     }
   }
 }
 
 template <class T, class O>
 int launch_lookup(LookupArgs a, cudaStream_t s) {
-  const int64_t nvec = a.cols / Span<T>::N + 2;
-  a.tx = 32;
+  constexpr int N = Span<T>::N;
+  const int64_t nvec = std::max<int64_t>(1, a.cols / N);
+  a.tx = 8;
   while (a.tx < kLookupThreads && a.tx < nvec) a.tx *= 2;
   const int ty = kLookupThreads / a.tx;
-  const int64_t runs = std::min<int64_t>(ceil_div(nvec, a.tx), 64);
-  // four tokens per thread hide their latency behind each other; one while there
-  // are few, for more blocks
-  const bool many = a.tokens * runs >= int64_t(16) * num_sms() * ty;
-  if (many) {
-    embedding_lookup_kernel<T, O, 4>
+  const bool aligned = a.cols % N == 0 && a.ldt % N == 0 && a.ldo % N == 0 &&
+                       reinterpret_cast<uintptr_t>(a.table) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  int64_t runs = std::min<int64_t>(ceil_div(nvec, a.tx), 64);
+  if (!aligned) {
+    lookup_any_kernel<T, O><<<grid_of(runs, ceil_div(a.tokens, ty)), kLookupThreads, 0, s>>>(a);
+  } else if (a.tokens * runs >= int64_t(16) * num_sms() * ty) {
+    // four tokens per thread hide their latency behind each other; one while there
+    // are few, for more blocks
+    lookup_aligned_kernel<T, O, 4>
         <<<grid_of(runs, ceil_div(a.tokens, 4 * ty)), kLookupThreads, 0, s>>>(a);
   } else {
-    embedding_lookup_kernel<T, O, 1>
+    lookup_aligned_kernel<T, O, 1>
         <<<grid_of(runs, ceil_div(a.tokens, ty)), kLookupThreads, 0, s>>>(a);
   }
   IVFPQ_LAUNCHED();
@@ -137,7 +163,8 @@ int launch_lookup(LookupArgs a, cudaStream_t s) {
 // ---- gradient: positions by token ----------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kMaxLocal = 16384;  // a block's tokens: 64 KB of counters
-constexpr int kPerThread = 4;     // consecutive ids per thread and step
+constexpr int kPerThread = 16;    // consecutive ids per thread and step
+constexpr int kListed = 4096;     // a class's positions kept in shared memory
 
 struct SortArgs {
   const void* ids;
@@ -179,32 +206,61 @@ __device__ __forceinline__ int block_before(int v, int* sh, int* all) {
 
 // The tokens of kPerThread consecutive positions, -1 where there is none to count.
 __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t, int (&v)[kPerThread]) {
+  auto token = [&](int64_t id) {
+    return id >= 0 && id < a.rows && id != a.padding ? int(id) : -1;
+  };
+  if (t + kPerThread <= a.tokens && misalign(a.ids) == 0) {
+    if (a.wide) {
+      longlong2 w[kPerThread / 2];
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    int64_t id = -1;
-    if (t + j < a.tokens) id = id_at(a.ids, a.wide, t + j);
-    v[j] = id >= 0 && id < a.rows && id != a.padding ? int(id) : -1;
+      for (int j = 0; j < kPerThread / 2; ++j)
+        w[j] = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.ids) + t)[j];
+#pragma unroll
+      for (int j = 0; j < kPerThread / 2; ++j) {
+        v[2 * j] = token(w[j].x);
+        v[2 * j + 1] = token(w[j].y);
+      }
+    } else {
+      int4 w[kPerThread / 4];
+#pragma unroll
+      for (int j = 0; j < kPerThread / 4; ++j)
+        w[j] = reinterpret_cast<const int4*>(static_cast<const int32_t*>(a.ids) + t)[j];
+#pragma unroll
+      for (int j = 0; j < kPerThread / 4; ++j) {
+        v[4 * j] = token(w[j].x);
+        v[4 * j + 1] = token(w[j].y);
+        v[4 * j + 2] = token(w[j].z);
+        v[4 * j + 3] = token(w[j].w);
+      }
+    }
+    return;
   }
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j)
+    v[j] = t + j < a.tokens ? token(id_at(a.ids, a.wide, t + j)) : -1;
 }
 
-__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const SortArgs a) {
   extern __shared__ int sort_smem[];
   int* next = sort_smem;  // [local]: counts, then where a token's next position goes
+  __shared__ int2 listed[kListed];  // (position, token) in order
   __shared__ int sh[32];
   const int c = blockIdx.x, mask = (1 << a.shift) - 1;
   const int lane = threadIdx.x & 31;
+  constexpr int64_t step = int64_t(kSortThreads) * kPerThread;
+  const int64_t t = int64_t(threadIdx.x) * kPerThread;
+  grid_go();
+  int before = 0, v[kPerThread];
+  if (t < a.tokens) read_tokens(a, t, v);
   for (int i = threadIdx.x; i < a.local; i += kSortThreads) next[i] = 0;
   __syncthreads();
-  int before = 0, v[kPerThread];
-  for (int64_t t = int64_t(threadIdx.x) * kPerThread; t < a.tokens;
-       t += kSortThreads * kPerThread) {
-    read_tokens(a, t, v);
+  for (int64_t t0 = t; t0 < a.tokens; t0 += step) {
+    if (t0 != t) read_tokens(a, t0, v);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
-      if (v[j] < 0) continue;
       const int cls = v[j] & mask;
-      before += cls < c;
-      if (cls == c) atomicAdd(&next[v[j] >> a.shift], 1);
+      before += v[j] >= 0 && cls < c;
+      if (v[j] >= 0 && cls == c) atomicAdd(&next[v[j] >> a.shift], 1);
     }
   }
   const int base = block_sum(before, sh);
@@ -222,41 +278,61 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const Sort
   }
   if (c == mask && threadIdx.x == 0) *a.valid = base + n;
   if (n == 0) return;
-  // the class's positions in order
+  // the class's positions in order, in shared memory while they fit
   int found = 0;
-  for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += kSortThreads * kPerThread) {
-    const int64_t t = t0 + int64_t(threadIdx.x) * kPerThread;
-    read_tokens(a, t, v);
+  const bool fits = n <= kListed;
+  for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += step) {
+    if (a.tokens > step) {
+      if (t0 + t < a.tokens) {
+        read_tokens(a, t0 + t, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j) v[j] = -1;
+      }
+    }
     int mine = 0;
+    if (t0 + t < a.tokens) {
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) mine += v[j] >= 0 && (v[j] & mask) == c;
+      for (int j = 0; j < kPerThread; ++j) mine += v[j] >= 0 && (v[j] & mask) == c;
+    }
     int all, at = found + block_before(mine, sh, &all);
+    if (mine > 0) {
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      if (v[j] >= 0 && (v[j] & mask) == c) {
-        a.list[base + at] = int32_t(t + j);
-        ++at;
+      for (int j = 0; j < kPerThread; ++j) {
+        if (v[j] >= 0 && (v[j] & mask) == c) {
+          if (fits)
+            listed[at] = make_int2(int(t0 + t) + j, v[j]);
+          else
+            a.list[base + at] = int32_t(t0 + t) + j;
+          ++at;
+        }
       }
     }
     found += all;
   }
   __syncthreads();
   if (threadIdx.x >= 32) return;
+  auto entry = [&](int i) {
+    if (i >= n) return make_int2(-1, -1);
+    if (fits) return listed[i];
+    const int p = a.list[base + i];
+    return make_int2(p, int(id_at(a.ids, a.wide, p)));
+  };
+  int2 e = entry(lane);
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const bool live = i0 + lane < n;
-    const int p = live ? a.list[base + i0 + lane] : -1;
-    const int id = live ? int(id_at(a.ids, a.wide, p)) : -1;
-    const unsigned same = __match_any_sync(kFullMask, id);
+    const int2 ahead = entry(i0 + 32 + lane);
+    const unsigned same = __match_any_sync(kFullMask, e.y);
     const unsigned below = same & ((1u << lane) - 1u);
     int at = 0;
-    if (live) at = next[id >> a.shift] + __popc(below);
+    if (e.y >= 0) at = next[e.y >> a.shift] + __popc(below);
     __syncwarp();
-    if (live) {
-      a.pos[base + at] = p;
-      a.token[base + at] = id;
-      if (below == 0) next[id >> a.shift] = at + __popc(same);
+    if (e.y >= 0) {
+      a.pos[base + at] = e.x;
+      a.token[base + at] = e.y;
+      if (below == 0) next[e.y >> a.shift] = at + __popc(same);
     }
     __syncwarp();
+    e = ahead;
   }
 }
 
@@ -334,6 +410,7 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   __shared__ int32_t pos[kMaxSlab], token[kMaxSlab + 2];
   const int64_t slab = grid_row();
   grid_wait();
+  grid_go();
   if (slab >= a.slabs) {
     // rows without a token
     const int step = int(gridDim.x * blockDim.x), x = int(blockIdx.x * blockDim.x + threadIdx.x);
@@ -409,16 +486,42 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs a) {
   const int32_t id = a.token[i1 - 1];
   if (a.token[i1] != id) return;
   if (i0 > 0 && a.token[i0 - 1] == id) return;  // it started before this slab
+  // how many slabs it goes on for
+  int more = 0;
+  for (int64_t k0 = slab + 1;; k0 += blockDim.x) {
+    const int64_t k = k0 + threadIdx.x;
+    const bool on = k < a.slabs && k * a.slab < valid && a.token[k * a.slab] == id;
+    const int c = __syncthreads_count(on);
+    more += c;
+    if (c < int(blockDim.x)) break;
+  }
   const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
   if (int64_t(cv) * N >= a.cols) return;
   float s[N];
-  const float* q = part_at<N>(a, slab, 1, cv);
+  auto part = [&](int64_t k, int which, float (&w)[N]) {
+    const float4* q = reinterpret_cast<const float4*>(part_at<N>(a, k, which, cv));
 #pragma unroll
-  for (int j = 0; j < N; ++j) s[j] = q[j];
-  for (int64_t k = slab + 1; k < a.slabs && k * a.slab < valid && a.token[k * a.slab] == id; ++k) {
-    q = part_at<N>(a, k, 0, cv);
+    for (int j = 0; j < N; j += 4) {
+      const float4 f = q[j / 4];
+      w[j] = f.x;
+      w[j + 1] = f.y;
+      w[j + 2] = f.z;
+      w[j + 3] = f.w;
+    }
+  };
+  part(slab, 1, s);
+  constexpr int U = 32 / N;
+  for (int k = 1; k <= more; k += U) {
+    float w[U][N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) s[j] += q[j];
+    for (int u = 0; u < U; ++u)
+      if (k + u <= more) part(slab + k + u, 0, w[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u <= more) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j] += w[u][j];
+      }
   }
   write_row<T, O>(a, id, cv, s);
 }
@@ -543,7 +646,8 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.count = o.count;
   a.valid = o.valid;
   const size_t smem = size_t(o.local) * 4;
-  IVFPQ_TRY(set_dynamic_smem(embedding_sort_kernel, smem));
+  // 48 KB with the static part need no leave
+  if (smem > 12 * 1024) IVFPQ_TRY(set_dynamic_smem(embedding_sort_kernel, smem));
   embedding_sort_kernel<<<1u << o.shift, kSortThreads, smem, s>>>(o);
   IVFPQ_LAUNCHED_K(embedding_sort_kernel, smem, kSortThreads);
   return by_dtype(dtype, [&](auto* t) -> int {
