@@ -24,8 +24,8 @@
 //     that nothing of it is rounded away beyond 2^-17 (2^-22 for fp16, 2^-25 for three).
 #include <algorithm>
 
+#include "adapter.cuh"
 #include "internal.h"
-#include "rowvec.cuh"
 #include "tc_ptx.cuh"
 
 namespace ivfpq {
@@ -34,49 +34,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPlanThreads = 1024;
-constexpr int kMaxTile = 128;
-
-struct AdapterArgs {
-  const void* x;
-  int64_t tokens, cols, ldx;
-  const void* a;
-  const void* b;
-  int adapters, rank;
-  int64_t n;
-  const int32_t* ids;
-  const float* scales;
-  const void* base;
-  int64_t ldb;
-  void* out;
-  int64_t ldo;
-  // the plan (null: every token is a tile)
-  int32_t* order;  // [tokens] tokens by adapter
-  int4* tiles;     // (adapter or -1, first slot, tokens, 0)
-  int32_t* ntiles;
-  int tile;     // tokens of a tile
-  float* h;     // [tokens, pitch], by slot
-  int splits;   // parts of K, one per block of a cluster
-  int kpart;    // columns of a part, a multiple of 32
-  int pitch;    // rank rounded up to whole instructions
-  int run;      // output columns of a block
-};
-
-struct Tile {
-  int adapter, first, count;
-};
-__device__ __forceinline__ Tile tile_at(const AdapterArgs& a, int64_t i) {
-  if (a.tiles) {
-    if (i >= *a.ntiles) return {-1, 0, 0};
-    const int4 t = a.tiles[i];
-    return {t.x, t.y, t.z};
-  }
-  if (i >= a.tokens) return {-1, 0, 0};
-  const int id = a.ids[i];
-  return {id >= 0 && id < a.adapters ? id : -1, int(i), 1};
-}
-__device__ __forceinline__ int64_t token_of(const AdapterArgs& a, int slot) {
-  return a.order ? a.order[slot] : slot;
-}
 
 // ---- tokens by adapter ------------------------------------------------------------------
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const AdapterArgs a) {
@@ -178,53 +135,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Elements 8 i .. 8 i + 7 of a row of `len`, zero past its end, whatever its alignment.
-template <class T>
-__device__ __noinline__ uint4 edge8(const T* p, int64_t len, int64_t at) {
-  T t[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) t[j] = at + j < len ? p[at + j] : from_f32<T>(0.f);
-  uint4 r;
-  memcpy(&r, t, 16);
-  return r;
-}
-template <class T>
-__device__ __forceinline__ uint4 row8(const T* p, int64_t len, int64_t at) {
-  if (p == nullptr || at >= len) return make_uint4(0, 0, 0, 0);
-  const int mis = misalign(p);
-  if (mis == 0 && at + 8 <= len) return *reinterpret_cast<const uint4*>(p + at);
-  // two neighbouring vectors inside the row
-  if (mis != 0 && at >= 8 && at + 16 <= len) return load_inner(p + at, 0, mis);
-  return edge8(p, len, at);
-}
-
 // ---- h = x A^T ----------------------------------------------------------------------------
-// The parts of K, each in its block's shared memory ([rows, R]), added in the order
-// of the blocks and written to the slots from `first` on; a share per block.
-template <int R>
-__device__ __forceinline__ void join_parts(const AdapterArgs& a, const float* part, int rows,
-                                           int first) {
-  static_assert(R % 4 == 0, "whole vectors");
-  if (a.splits > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  const uint32_t base = smem_u32(part);
-  float* h = a.h + int64_t(first) * R;
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < rows * R / 4; i += a.splits * kThreads) {
-    float4 s = ld_cluster4(map_rank(base + 16u * uint32_t(i), 0));
-    for (int v = 1; v < a.splits; ++v) {
-      const float4 f = ld_cluster4(map_rank(base + 16u * uint32_t(i), uint32_t(v)));
-      s.x += f.x;
-      s.y += f.y;
-      s.z += f.z;
-      s.w += f.w;
-    }
-    reinterpret_cast<float4*>(h)[i] = s;
-  }
-  if (a.splits > 1) cluster_sync();  // no block leaves while others read its part
-}
-
 template <class T, int NT>
 __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const AdapterArgs a) {
   constexpr int R = NT * 8;
@@ -284,176 +195,10 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const AdapterA
     for (int v = 1; v < kWarps; ++v) s += part[v][i];
     part[0][i] = s;
   }
-  join_parts<R>(a, part[0], t.count, t.first);
-}
-
-// The same for many tokens: a block takes 64 tokens of a tile, 16 per warp, and
-// brings both operands through shared memory, 64 columns (128 bytes) of every row
-// at a time, kStages of them on their way. The 16-byte chunks of a row are swapped
-// around by its number modulo 8, so that the 8 rows that a matrix load takes lie in
-// different banks. Rows that do not lie on 16-byte boundaries (ALIGNED false) go
-// through registers instead of asynchronous copies; the sums are the same.
-constexpr int kStages = 4;
-constexpr int kTokens = 64;
-template <int NT>
-constexpr size_t wide_smem() {
-  return size_t(kStages) * (kTokens + NT * 8) * 128;
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void matrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void matrix2(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-               : "=r"(r[0]), "=r"(r[1])
-               : "r"(addr)
-               : "memory");
-}
-
-template <class T, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) adapter_shrink_wide_kernel(const AdapterArgs a) {
-  extern __shared__ __align__(128) char wide_bytes[];
-  constexpr int R = NT * 8, kStage = (kTokens + R) * 128;
-  T* const type = nullptr;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
-  const int subs = (a.tile + kTokens - 1) / kTokens;
-  const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
-  grid_wait();
-  grid_go();
-  const Tile t = tile_at(a, item / subs);
-  const int m0 = int(item % subs) * kTokens, rows = min(kTokens, t.count - m0);
-  if (rows <= 0 || t.adapter < 0) return;
-  // this thread's chunks: column chunk ch of rows r0, r0 + 16, ...
-  const int ch = threadIdx.x & 7, r0 = threadIdx.x >> 3;
-  constexpr int XR = kTokens / 16, WR = (R + 15) / 16;
-  const T* x[XR];
-#pragma unroll
-  for (int i = 0; i < XR; ++i) {
-    const int row = r0 + 16 * i;
-    x[i] = row < rows ? static_cast<const T*>(a.x) + token_of(a, t.first + m0 + row) * a.ldx
-                      : nullptr;
-  }
-  const T* w = static_cast<const T*>(a.a) + int64_t(t.adapter) * a.rank * a.cols;
-  auto w_row = [&](int row) { return row < a.rank ? w + int64_t(row) * a.cols : nullptr; };
-  const int64_t k0 = int64_t(blockIdx.x) * a.kpart, k1 = min(a.cols, k0 + a.kpart);
-  const int steps = k1 > k0 ? int((k1 - k0 + 63) / 64) : 0;
-  const uint32_t smem = smem_u32(wide_bytes);
-  auto place = [&](int step) {
-    return uint32_t((step % kStages) * kStage + r0 * 128 + ((ch ^ (r0 & 7)) * 16));
-  };
-  // aligned rows: asynchronous copies
-  auto fetch = [&](int step) {
-    if (step < steps) {
-      const uint32_t base = smem + place(step);
-      const int64_t k = k0 + int64_t(step) * 64 + ch * 8;
-#pragma unroll
-      for (int i = 0; i < XR; ++i) {
-        const bool live = k < k1 && x[i];
-        copy16(base + 16 * i * 128, live ? x[i] + k : a.x, live);
-      }
-#pragma unroll
-      for (int i = 0; i < WR; ++i) {
-        if (R % 16 == 0 || r0 + 16 * i < R) {
-          const T* p = w_row(r0 + 16 * i);
-          const bool live = k < k1 && p;
-          copy16(base + (kTokens + 16 * i) * 128, live ? p + k : a.a, live);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // other rows: into registers, and from there to their place a step later
-  uint4 kept[ALIGNED ? 1 : XR + WR];
-  auto load = [&](int step) {
-    const int64_t k = k0 + int64_t(step) * 64 + ch * 8, len = step < steps && k < k1 ? a.cols : 0;
-#pragma unroll
-    for (int i = 0; i < XR; ++i) kept[ALIGNED ? 0 : i] = row8(x[i], len, k);
-#pragma unroll
-    for (int i = 0; i < WR; ++i)
-      kept[ALIGNED ? 0 : XR + i] = row8(R % 16 == 0 || r0 + 16 * i < R ? w_row(r0 + 16 * i) : nullptr,
-                                        len, k);
-  };
-  auto put = [&](int step) {
-    char* base = wide_bytes + place(step);
-#pragma unroll
-    for (int i = 0; i < XR; ++i)
-      *reinterpret_cast<uint4*>(base + 16 * i * 128) = kept[ALIGNED ? 0 : i];
-#pragma unroll
-    for (int i = 0; i < WR; ++i)
-      if (R % 16 == 0 || r0 + 16 * i < R)
-        *reinterpret_cast<uint4*>(base + (kTokens + 16 * i) * 128) = kept[ALIGNED ? 0 : XR + i];
-  };
-  float acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if constexpr (ALIGNED) {
-      fetch(i);
-    } else {
-      load(i);
-      put(i);
-    }
-  }
-  for (int step = 0; step < steps; ++step) {
-    if constexpr (ALIGNED) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncthreads();
-    // into the stage that the last step has read
-    if constexpr (ALIGNED)
-      fetch(step + kStages - 1);
-    else
-      load(step + kStages - 1);
-    const uint32_t base = smem + (step % kStages) * kStage;
-    const uint32_t xa = base + (warp * 16 + (lane & 15)) * 128;
-    const uint32_t wa = base + (kTokens + (lane >> 4) * 8 + (lane & 7)) * 128;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t f[4];
-      matrix4(xa + (((2 * kk + (lane >> 4)) ^ (lane & 7)) * 16), f);
-      const uint32_t wc = ((2 * kk + ((lane >> 3) & 1)) ^ (lane & 7)) * 16;
-#pragma unroll
-      for (int j = 0; j < NT; j += 2) {
-        uint32_t g[4];
-        if constexpr (NT == 1)
-          matrix2(base + (kTokens + (lane & 7)) * 128 + wc, g);
-        else
-          matrix4(wa + j * 1024 + wc, g);
-        mma16(acc[j], f[0], f[1], f[2], f[3], g[0], g[1], type);
-        if (NT > 1) mma16(acc[j + (NT > 1)], f[0], f[1], f[2], f[3], g[2], g[3], type);
-      }
-    }
-    if constexpr (!ALIGNED) put(step + kStages - 1);
-  }
-  if constexpr (ALIGNED) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(wide_bytes);
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      *reinterpret_cast<float2*>(red + (warp * 16 + e * 8 + r) * R + j * 8 + 2 * q) =
-          make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
-  join_parts<R>(a, red, rows, t.first + m0);
+  join_parts<R, kThreads>(a, part[0], t.count, t.first);
 }
 
 // ---- out = base + scale h B^T ----------------------------------------------------------------
-// The next term of v as an element of T; what is left of it stays in v.
-template <class T>
-__device__ __forceinline__ float term(float& v) {
-  const float t = to_f32(from_f32<T>(v));
-  v = fabsf(t) < INFINITY ? v - t : 0.f;
-  return t;
-}
-
 // A lane's part of a row of B: 4 KS consecutive elements from 4 KS q on, as two
 // registers per instruction.
 template <class T, int KS>
@@ -548,13 +293,10 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
           // fp16's range: the row's largest value to [2^14, 2^15)
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-          const int ex = int(__float_as_uint(top) >> 23);  // 127 + its exponent
-          const bool ok = top > 0.f && top < INFINITY;
-          const int down = ok ? min(141 - ex, 126) : 0;
-          const float f = __uint_as_float(uint32_t(127 + max(down, -126)) << 23);
+          const float2 f = fp16_range(top);
 #pragma unroll
-          for (int k = 0; k < 4 * KS; ++k) v[e][k] *= f;
-          if (q == 0 && i < t.count) up[i] = __uint_as_float(uint32_t(127 - max(down, -126)) << 23);
+          for (int k = 0; k < 4 * KS; ++k) v[e][k] *= f.x;
+          if (q == 0 && i < t.count) up[i] = f.y;
         }
       }
 #pragma unroll
@@ -752,18 +494,8 @@ int launch(K kern, dim3 grid, int threads, size_t smem, const AdapterArgs& a, bo
 
 template <class T, int NT>
 int launch_shrink(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  const bool planned = a.tiles != nullptr;
-  if (a.tile < kMaxTile)
-    return launch(adapter_shrink_kernel<T, NT>, grid_of(a.splits, tiles), kThreads, 0, a, planned,
-                  a.splits, s);
-  const dim3 grid = grid_of(a.splits, tiles * (kMaxTile / kTokens));
-  const bool aligned = a.cols % 8 == 0 && a.ldx % 8 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.a) % 16 == 0;
-  return aligned ? launch(adapter_shrink_wide_kernel<T, NT, true>, grid, kThreads, wide_smem<NT>(),
-                          a, planned, a.splits, s)
-                 : launch(adapter_shrink_wide_kernel<T, NT, false>, grid, kThreads,
-                          wide_smem<NT>(), a, planned, a.splits, s);
+  return launch(adapter_shrink_kernel<T, NT>, grid_of(a.splits, tiles), kThreads, 0, a,
+                a.tiles != nullptr, a.splits, s);
 }
 template <class T>
 int launch_shrink_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
@@ -788,10 +520,7 @@ int launch_expand(const AdapterArgs& a, int64_t tiles, bool vec, cudaStream_t s)
 }
 template <class T, class O>
 int launch_expand_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  const int64_t per = 16 / int64_t(sizeof(O));
-  const bool vec = a.n % 8 == 0 && a.ldo % per == 0 && a.ldb % per == 0 &&
-                   reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(a.base) % 16 == 0;
+  const bool vec = whole_rows<O>(a);
   switch (a.pitch / 8) {
     case 1:
     case 2: return launch_expand<T, O, 1>(a, tiles, vec, s);
@@ -802,7 +531,14 @@ int launch_expand_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
 }
 template <class T>
 int launch_types(const AdapterArgs& a, int out_dtype, int64_t tiles, cudaStream_t s) {
-  IVFPQ_TRY(launch_shrink_rank<T>(a, tiles, s));
+  const int dtype = std::is_same<T, __half>::value ? IVFPQ_F16 : IVFPQ_BF16;
+  if (a.tile == kMaxTile)
+    IVFPQ_TRY(adapter_shrink_wide(a, dtype, tiles, s));
+  else
+    IVFPQ_TRY(launch_shrink_rank<T>(a, tiles, s));
+  if (a.tile == kMaxTile && a.adapters > 0 && a.rank % 8 == 0 &&
+      reinterpret_cast<uintptr_t>(a.b) % 16 == 0)
+    return adapter_expand_wide(a, dtype, out_dtype, s);
   return out_dtype == IVFPQ_F32 ? launch_expand_rank<T, float>(a, tiles, s)
                                 : launch_expand_rank<T, T>(a, tiles, s);
 }
@@ -862,10 +598,12 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   const int64_t tiles = planned ? tokens / p.tile + some : tokens;
   const bool wide = p.tile == kMaxTile;
   // parts of K until there are blocks for every SM, of some steps each
-  const int64_t items = wide ? ceil_div(tokens, kTokens) : tiles;
+  const int64_t items = wide ? ceil_div(tokens, kMaxTile) : tiles;
   const int64_t least = wide ? 256 : 128;
   p.splits = 1;
-  while (p.splits < 8 && items * p.splits < 2 * num_sms() && cols > least * p.splits) p.splits *= 2;
+  while (p.splits < 8 && items * p.splits * (wide ? 2 : 1) < (wide ? 1 : 2) * num_sms() &&
+         cols > least * p.splits)
+    p.splits *= 2;
   p.kpart = int(ceil_div(ceil_div(cols, p.splits), 64) * 64);
   // runs of columns, long where there are many tiles
   p.run = 128;

@@ -6,13 +6,13 @@
 //
 // Bound by memory: each score is read once. Within a row totals are ordered as
 // scores, so a row's own k best are enough and need no normalisation:
-//  1. A warp's load of 32 vectors is a batch. One pass keeps per thread the
-//     largest score and the sum of exponentials relative to it (rescaled when it
-//     grows), and per batch the largest score, in shared memory.
+//  1. One pass keeps per thread the largest score and the sum of exponentials
+//     relative to it (rescaled when it grows), and of every four vectors that a
+//     thread takes (a batch) the largest score, in shared memory.
 //  2. The k-th largest of the batches' maxima is a lower bound of the k-th
-//     largest score, found by bisection over its bits by one warp. Only batches
-//     that reach it are read again (about k of them, from L2), and their scores
-//     at or above it kept: about k, more only where scores are equal.
+//     largest score; bisection over its bits finds it, or something a little
+//     lower. Only batches that reach the bound are read again (about k of them, a
+//     thread each, from L2), and their scores at or above it kept.
 //  3. The kept ones are ranked among themselves; a cluster of blocks that shares
 //     a row ranks its lists against each other by binary search.
 //  4. A second kernel, already waiting, merges the beams' lists of a group, two
@@ -32,9 +32,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxBatches = 1024;  // a block's maxima: 32 per lane of the bisecting warp
+constexpr int kUnroll = 4;         // vectors of a batch
+constexpr int kMaxSteps = 4;       // batches per thread whose maxima are kept apart
+constexpr int kSlack = 32;         // how many batches more than k the bound may let pass
 constexpr int kCap = 4096;         // kept scores before the worse ones are dropped
-constexpr int kRound = kWarps * 32 * 8;  // most scores that one round can keep
+constexpr int kRound = kThreads * 8;  // most scores that one round can keep
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What the row kernel leaves for the merge. Z is relative to m, so that totals
@@ -121,57 +123,91 @@ struct Run {
   }
 };
 
+// The batch of step i: vectors (i * kUnroll + u) * kThreads + thread.
 template <class T>
-__device__ __forceinline__ void run_stats(const Run<T>& run, int shift, uint32_t* bmax,
-                                          Online& o) {
-  constexpr int N = Span<T>::N, U = 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nload = (run.nvec + 31) / 32;
-  for (int l0 = warp * U; l0 < nload; l0 += kWarps * U) {
-    uint4 r[U];
-    const int i0 = l0 * 32 + lane;
-    if (i0 >= run.first && i0 + (U - 1) * 32 <= run.last) {
+__device__ __forceinline__ void load_batch(const Run<T>& run, int step, uint4 (&r)[kUnroll]) {
+  const int i0 = step * kUnroll * kThreads + threadIdx.x;
+  if (i0 >= run.first && i0 + (kUnroll - 1) * kThreads <= run.last) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = load_inner(run.p, i0 + u * 32, run.mis);
-    } else {
+    for (int u = 0; u < kUnroll; ++u) r[u] = load_inner(run.p, i0 + u * kThreads, run.mis);
+  } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = run.at(i0 + u * 32);
-    }
-    float vm[U], m = -INFINITY;
+    for (int u = 0; u < kUnroll; ++u) r[u] = run.at(i0 + u * kThreads);
+  }
+}
+
+// Adds a batch's exponentials to o, whose m is at least its largest score.
+template <class T>
+__device__ __forceinline__ void add_batch(const uint4 (&r)[kUnroll], Online& o) {
+  constexpr int N = Span<T>::N;
+  const uint64_t scale = pair(kLog2e, kLog2e);
+  uint64_t z = pair(0.f, 0.f);
+  float z0, z1;
+  if (fabsf(o.m) < 1e38f) {
+    // exp2(s c - b) with b = m c rounded, one operation per score; what the
+    // rounding of b does to all of them alike is taken back below
+    const float b = o.m * kLog2e;
+    const uint64_t minus = pair(-b, -b);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      vm[u] = vec_max(r[u], static_cast<T*>(nullptr));
-      m = fmaxf(m, vm[u]);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t k = __reduce_max_sync(kFullMask, score_key(vm[u]));
-      if (lane == u && l0 + u < nload) {
-        if (shift == 0)
-          bmax[l0 + u] = k;
-        else
-          atomicMax(&bmax[(l0 + u) >> shift], k);
-      }
-    }
-    o.raise(m);
-    const float ref = o.m == -INFINITY ? 0.f : o.m;
-    const uint64_t minus = pair(-ref, -ref), scale = pair(kLog2e, kLog2e);
-    float z[2] = {0.f, 0.f};
-    uint64_t zz = pair(0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       float v[N];
       unpack_vec<T>(r[u], v);
 #pragma unroll
       for (int j = 0; j < N; j += 2) {
-        float a, b;
-        unpair(mul2(add2(pair(v[j], v[j + 1]), minus), scale), a, b);
-        zz = add2(zz, pair(exp2_fast(a), exp2_fast(b)));
+        float x, y;
+        unpair(fma2(pair(v[j], v[j + 1]), scale, minus), x, y);
+        z = add2(z, pair(exp2_fast(x), exp2_fast(y)));
       }
     }
-    unpair(zz, z[0], z[1]);
-    o.z += z[0] + z[1];
+    unpair(z, z0, z1);
+    o.z += (z0 + z1) * exp2_fast(-fmaf(o.m, kLog2e, -b));
+  } else {
+    // nothing yet, or scores whose products pass fp32
+    const float ref = o.m == -INFINITY ? 0.f : o.m;
+    const uint64_t minus = pair(-ref, -ref);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float v[N];
+      unpack_vec<T>(r[u], v);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        float x, y;
+        unpair(mul2(add2(pair(v[j], v[j + 1]), minus), scale), x, y);
+        z = add2(z, pair(exp2_fast(x), exp2_fast(y)));
+      }
+    }
+    unpair(z, z0, z1);
+    o.z += z0 + z1;
+  }
+}
+
+// One pass over the run. peak[g * kThreads + thread]: the largest score of the
+// thread's steps g << shift and following, as a key; r: its first batch.
+template <class T>
+__device__ __forceinline__ void run_stats(const Run<T>& run, int steps, int shift,
+                                          uint4 (&r)[kUnroll], uint32_t* peak, Online& o) {
+  float top = -INFINITY;
+  auto take = [&](int i, const uint4 (&v)[kUnroll]) {
+    float m = vec_max(v[0], static_cast<T*>(nullptr));
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) m = fmaxf(m, vec_max(v[u], static_cast<T*>(nullptr)));
+    top = fmaxf(top, m);
+    if (((i + 1) & ((1 << shift) - 1)) == 0 || i + 1 == steps) {
+      peak[(i >> shift) * kThreads + threadIdx.x] = score_key(top);
+      top = -INFINITY;
+    }
+    o.raise(m);
+    add_batch<T>(v, o);
+  };
+  // one batch on its way while the other is taken
+  uint4 q[kUnroll];
+  for (int i = 0; i < steps; i += 2) {
+    if (i + 1 < steps) load_batch(run, i + 1, q);
+    take(i, r);
+    if (i + 1 < steps) {
+      if (i + 2 < steps) load_batch(run, i + 2, r);
+      take(i + 1, q);
+    }
   }
 }
 
@@ -197,35 +233,47 @@ __device__ void sort_entries(uint64_t* e, int n) {
   __syncthreads();
 }
 
-// The largest 2^16-aligned key that at least k of the n keys reach (0 if there
-// are fewer): one warp, its keys in registers, a bit per step from the highest
-// one in which they differ.
-__device__ __forceinline__ uint32_t kth_bound(const uint32_t* keys, int n, int k) {
+// A key that at least k of the block's peaks reach (`groups` per thread), and no more
+// than k + kSlack of them unless peaks are equal in their upper 16 bits; 0 if there
+// are fewer than k. A bit per step, from the highest one in which peaks differ.
+// votes: [34] zeros.
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t* peak, int groups, int k,
+                                              unsigned* votes) {
   const int lane = threadIdx.x & 31;
-  if (n < k) return 0;
-  uint32_t v[kMaxBatches / 32], lo = 0xffffffffu, hi = 0;
+  uint32_t v[kMaxSteps], lo = 0xffffffffu, hi = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxBatches / 32; ++i) {
-    v[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0u;
-    if (i * 32 + lane < n) lo = min(lo, v[i]);
+  for (int i = 0; i < kMaxSteps; ++i) {
+    v[i] = i < groups ? peak[i * kThreads + threadIdx.x] : 0u;
+    if (i < groups) lo = min(lo, v[i]);
     hi = max(hi, v[i]);
   }
-  lo = __reduce_min_sync(kFullMask, lo);
+  // votes[32], votes[33]: the largest key, and of the inverted ones
   hi = __reduce_max_sync(kFullMask, hi);
+  lo = __reduce_min_sync(kFullMask, lo);
+  if (lane == 0) {
+    atomicMax(&votes[32], hi);
+    atomicMax(&votes[33], ~lo);
+  }
+  __syncthreads();
+  if (groups * kThreads < k) return 0;
+  hi = votes[32];
+  lo = ~votes[33];
   if ((lo ^ hi) >> 16 == 0) return lo & 0xffff0000u;
   const int top = 31 - __clz(lo ^ hi);
   uint32_t bound = hi & ~((2u << top) - 1u);
   for (int bit = top; bit >= 16; --bit) {
     const uint32_t t = bound | (1u << bit);
     int c = 0;
-    if (n <= kMaxBatches / 4) {
 #pragma unroll
-      for (int i = 0; i < kMaxBatches / 128; ++i) c += v[i] >= t;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kMaxBatches / 32; ++i) c += v[i] >= t;
+    for (int i = 0; i < kMaxSteps; ++i) c += v[i] >= t;
+    const unsigned w = __reduce_add_sync(kFullMask, unsigned(c));
+    if (lane == 0 && w) atomicAdd(&votes[bit], w);
+    __syncthreads();
+    const int all = int(votes[bit]);
+    if (all >= k) {
+      bound = t;
+      if (all <= k + kSlack) break;
     }
-    if (int(__reduce_add_sync(kFullMask, unsigned(c))) >= k) bound = t;
   }
   return bound;
 }
@@ -243,26 +291,35 @@ struct alignas(16) Part {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 5) beam_rows_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs a) {
   constexpr int N = Span<T>::N;
   extern __shared__ __align__(16) uint64_t select_smem[];
-  uint64_t* kept = select_smem;                 // [kCap]
-  uint64_t* top = kept + kCap;                  // [k]
-  uint64_t* others = top + a.k;                 // [ranks, k] where a row has several blocks
-  __shared__ uint32_t bmax[kMaxBatches];
-  __shared__ uint16_t chosen[kMaxBatches];
+  uint64_t* kept = select_smem;  // [kCap]
+  uint64_t* top = kept + kCap;   // [k]
+  uint64_t* others = top + a.k;  // [ranks, k] where a row has several blocks
+  // the peaks (one array with `kept`, which is filled when they have been read)
+  uint32_t* peak = reinterpret_cast<uint32_t*>(select_smem);
+  __shared__ uint16_t chosen[kMaxSteps * kThreads];
   __shared__ float2 sh[kWarps];
   __shared__ Part part;
   __shared__ Part all[kMaxCluster];
   __shared__ int nkept, nchosen;
-  __shared__ uint32_t bound;
+  __shared__ unsigned votes[34];
   const int ranks = int(gridDim.x), rank = int(blockIdx.x);
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   if (row >= a.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float t = a.totals[row];
+  const bool done = a.finished && a.finished[row];
+  const int64_t c0 = min(int64_t(rank) * a.chunk, a.cols);
+  const Run<T> run(static_cast<const T*>(a.scores) + row * a.lds + c0,
+                   int(min(int64_t(a.chunk), a.cols - c0)));
+  uint4 r[kUnroll];
+  load_batch(run, 0, r);  // on its way while the total is
+  if (threadIdx.x < 34) votes[threadIdx.x] = 0;
+  if (threadIdx.x == 0) nkept = nchosen = 0;
   const bool alive = fabsf(t) < INFINITY;  // neither infinite nor NaN
-  if (!alive || (a.finished && a.finished[row])) {
+  if (!alive || done) {
     if (rank == 0 && threadIdx.x == 0) {
       a.o.len[row] = alive ? 1 : 0;
       a.o.val[row * a.k] = 0.f;
@@ -272,60 +329,50 @@ __global__ void __launch_bounds__(kThreads, 5) beam_rows_kernel(const SelectArgs
     }
     return;
   }
-  const int64_t c0 = min(int64_t(rank) * a.chunk, a.cols);
-  const Run<T> run(static_cast<const T*>(a.scores) + row * a.lds + c0,
-                   int(min(int64_t(a.chunk), a.cols - c0)));
-  const int nload = (run.nvec + 31) / 32;
-  const int nbatch = (nload + (1 << a.shift) - 1) >> a.shift;
-  if (threadIdx.x == 0) nkept = nchosen = 0;
-  if (a.shift > 0) {
-    for (int i = threadIdx.x; i < nbatch; i += kThreads) bmax[i] = 0;
-    __syncthreads();
-  }
+  const int steps = (run.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+  const int groups = (steps + (1 << a.shift) - 1) >> a.shift;
   Online o;
-  run_stats<T>(run, a.shift, bmax, o);
+  run_stats<T>(run, steps, a.shift, r, peak, o);
   grid_go();
   // the block's statistics
+  {
+    const float m = key_to_float(__reduce_max_sync(kFullMask, score_key(o.m)));
+    float z = o.z * exp2_fast(m == -INFINITY ? 0.f : (o.m - m) * kLog2e);
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
-    const float m2 = __shfl_xor_sync(kFullMask, o.m, d), z2 = __shfl_xor_sync(kFullMask, o.z, d);
-    const float m1 = o.m, z1 = o.z;
-    // the same operations in both lanes of a pair
-    Online j;
-    j.join(lane & d ? m2 : m1, lane & d ? z2 : z1);
-    j.join(lane & d ? m1 : m2, lane & d ? z1 : z2);
-    o = j;
+    for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(kFullMask, z, d);
+    if (lane == 0) sh[warp] = make_float2(m, z);
   }
-  if (lane == 0) sh[warp] = make_float2(o.m, o.z);
   __syncthreads();
-  if (warp == 0) {
-    const uint32_t b = kth_bound(bmax, nbatch, a.k);
-    if (lane == 0) bound = b;
-  } else if (warp == 1 && lane == 0) {
+  if (threadIdx.x == 0) {
     Online j;
     for (int w = 0; w < kWarps; ++w) j.join(sh[w].x, sh[w].y);
     part.m = j.m;
     part.z = j.z;
   }
-  __syncthreads();
+  const uint32_t bound = kth_bound(peak, groups, a.k, votes);
   // the batches that reach the bound
-  for (int i = threadIdx.x; i < nbatch; i += kThreads)
-    if (bmax[i] >= bound) chosen[atomicAdd(&nchosen, 1)] = uint16_t(i);
-  __syncthreads();
-  const int nread = nchosen << a.shift;
+  for (int g = 0; g < groups; ++g)
+    if (peak[g * kThreads + threadIdx.x] >= bound)
+      chosen[atomicAdd(&nchosen, 1)] = uint16_t(g * kThreads + threadIdx.x);
+  __syncthreads();  // also: the peaks are read
+  const int per = kUnroll << a.shift, nread = nchosen * per;  // vectors
   uint64_t bar = uint64_t(bound) << 32;
-  for (int r0 = 0; r0 < nread; r0 += kWarps) {
-    const int r = r0 + warp;
-    if (r < nread) {
-      const int i = ((int(chosen[r >> a.shift]) << a.shift) + (r & ((1 << a.shift) - 1))) * 32 + lane;
-      const uint4 q = run.at(i);
+  // the same as a score; -inf (and what lies past the end) is no continuation
+  const float least = fmaxf(key_to_float(bound), -3.402823466e38f);
+  for (int v0 = 0; v0 < nread; v0 += kThreads) {
+    const int q = v0 + threadIdx.x;
+    if (q < nread) {
+      const int b = chosen[q / per], e = q % per;
+      const int i = ((b / kThreads) * per + e) * kThreads + b % kThreads;
+      const uint4 w = run.at(i);
       float v[N];
-      unpack_vec<T>(q, v);
+      unpack_vec<T>(w, v);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const uint64_t e = entry(score_key(v[j]), uint32_t(c0) + uint32_t(i * N + j));
-        // a score of -inf (and what lies past the end) is no continuation
-        if (v[j] > -INFINITY && e >= bar) kept[atomicAdd(&nkept, 1)] = e;
+        if (v[j] >= least) {
+          const uint64_t x = entry(score_key(v[j]), uint32_t(c0) + uint32_t(i * N + j));
+          if (x >= bar) kept[atomicAdd(&nkept, 1)] = x;
+        }
       }
     }
     __syncthreads();
@@ -335,16 +382,19 @@ __global__ void __launch_bounds__(kThreads, 5) beam_rows_kernel(const SelectArgs
       bar = kept[a.k - 1];
       if (threadIdx.x == 0) nkept = a.k;
       __syncthreads();
-    } else if (r0 + kWarps < nread) {
+    } else if (v0 + kThreads < nread) {
       __syncthreads();  // n is read before the next round adds to it
     }
   }
   int n = nkept;
   if (n <= kThreads) {
-    const uint64_t e = threadIdx.x < n ? kept[threadIdx.x] : 0;
-    int above = 0;
-    for (int i = 0; i < n; ++i) above += kept[i] > e;
-    if (threadIdx.x < n && above < a.k) top[above] = e;
+    if (threadIdx.x < n) {
+      const uint64_t e = kept[threadIdx.x];
+      int above = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) above += kept[i] > e;
+      if (above < a.k) top[above] = e;
+    }
   } else {
     sort_entries(kept, n);
     for (int i = threadIdx.x; i < min(n, a.k); i += kThreads) top[i] = kept[i];
@@ -367,15 +417,15 @@ __global__ void __launch_bounds__(kThreads, 5) beam_rows_kernel(const SelectArgs
     }
     cluster_sync();
     total = 0;
-    for (int r = 0; r < ranks; ++r) {
-      j.join(all[r].m, all[r].z);
-      const int len = all[r].len;
+    for (int p = 0; p < ranks; ++p) {
+      j.join(all[p].m, all[p].z);
+      const int len = all[p].len;
       total += len;
-      if (r == rank || threadIdx.x >= n) continue;
+      if (p == rank || threadIdx.x >= n) continue;
       int lo = 0, hi = len;  // entries of that list above mine
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (others[r * a.k + mid] > mine)
+        if (others[p * a.k + mid] > mine)
           lo = mid + 1;
         else
           hi = mid;
@@ -479,9 +529,9 @@ int launch_rows(SelectArgs a, cudaStream_t s) {
   while (ranks < kMaxCluster && a.rows * ranks < 2 * num_sms() && a.cols > 4096 * int64_t(ranks))
     ranks *= 2;
   a.chunk = int(ceil_div(ceil_div(a.cols, ranks), 8) * 8);
-  const int64_t loads = ceil_div(a.chunk, 32 * Span<T>::N);
+  const int64_t steps = ceil_div(a.chunk, int64_t(kThreads) * kUnroll * Span<T>::N);
   a.shift = 0;
-  while ((loads >> a.shift) + 1 > kMaxBatches) ++a.shift;
+  while (ceil_div(steps, int64_t(1) << a.shift) > kMaxSteps) ++a.shift;
   const size_t smem = (size_t(kCap) + size_t(a.k) * (ranks == 1 ? 1 : 1 + ranks)) * 8;
   auto kern = beam_rows_kernel<T>;
   if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));

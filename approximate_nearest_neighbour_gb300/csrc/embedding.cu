@@ -12,12 +12,13 @@
 //     rows, counts its own and those of the lower classes, and so knows where its
 //     tokens go without hearing from the other blocks. One warp places them, 32 in
 //     order at a time.
-//  2. The sorted positions are cut into slabs of equal length, whatever the tokens:
-//     a frequent token is many slabs' work, not one block's. A block adds a slab's
+//  2. The sorted positions are cut into slabs of equal length. A block adds a slab's
 //     rows over a run of columns in registers (fp32) and writes a row where the
-//     token changes; a token that goes on beyond the slab leaves a partial sum.
+//     token changes. A token that goes on beyond its slab is finished by the block in
+//     whose slab it starts; one with more positions than a slab has (a frequent token
+//     is many slabs' work, not one block's) leaves a partial sum in every slab.
 //     Further blocks zero the rows without a token.
-//  3. The partial sums of a token are added in slab order.
+//  3. The partial sums of a frequent token are added in slab order.
 #include <algorithm>
 
 #include "internal.h"
@@ -161,9 +162,9 @@ int launch_lookup(LookupArgs a, cudaStream_t s) {
 }
 
 // ---- gradient: positions by token ----------------------------------------------------
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kMaxLocal = 16384;  // a block's tokens: 64 KB of counters
-constexpr int kPerThread = 16;    // consecutive ids per thread and step
+constexpr int kPerThread = 16;    // ids per thread and step
 constexpr int kListed = 4096;     // a class's positions kept in shared memory
 
 struct SortArgs {
@@ -177,44 +178,61 @@ struct SortArgs {
   int32_t* token;  // [tokens] their tokens
   int32_t* count;  // [rows] positions of each token
   int32_t* valid;  // [1] positions that hold a token
+  int slab;
+  int4* frequent;  // (token, first sorted position, positions, 0), by class
+  int2* classes;   // [classes] each class's first entry there and how many it has
 };
 
-__device__ __forceinline__ int block_sum(int v, int* sh) {
+__device__ __forceinline__ int block_sum(int v, uint64_t* sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   v = int(__reduce_add_sync(kFullMask, unsigned(v)));
   __syncthreads();
-  if (lane == 0) sh[warp] = v;
+  if (lane == 0) sh[warp] = uint64_t(v);
   __syncthreads();
-  return int(__reduce_add_sync(kFullMask, unsigned(lane < int(blockDim.x) / 32 ? sh[lane] : 0)));
+  return int(__reduce_add_sync(kFullMask, lane < kSortThreads / 32 ? unsigned(sh[lane]) : 0u));
 }
-// The sum of v over the threads before this one; all: over the block.
-__device__ __forceinline__ int block_before(int v, int* sh, int* all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = int(blockDim.x) / 32;
-  int in = v;
+// The sum of v over the threads before this one; all: over the block. v may hold
+// several counters side by side.
+__device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t* sh, uint64_t* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int W = kSortThreads / 32;
+  uint64_t in = v;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const int t = __shfl_up_sync(kFullMask, in, d);
+    const uint64_t t = __shfl_up_sync(kFullMask, in, d);
     if (lane >= d) in += t;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = in;
   __syncthreads();
-  const int w = lane < warps ? sh[lane] : 0;
-  *all = int(__reduce_add_sync(kFullMask, unsigned(w)));
-  return int(__reduce_add_sync(kFullMask, unsigned(lane < warp ? w : 0))) + in - v;
+  uint64_t below = 0;
+  *all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const uint64_t t = sh[w];
+    if (w < warp) below += t;
+    *all += t;
+  }
+  return below + in - v;
 }
 
-// The tokens of kPerThread consecutive positions, -1 where there is none to count.
-__device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t, int (&v)[kPerThread]) {
+// The positions of a step that thread x takes: four groups of four, (j kSortThreads + x)
+// 4 + e, so that a warp's loads are whole lines.
+__device__ __forceinline__ int64_t position(int64_t t0, int j) {
+  return t0 + (int64_t(j) * kSortThreads + threadIdx.x) * 4;
+}
+// Their tokens, -1 where there is none to count.
+__device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0, int (&v)[kPerThread]) {
   auto token = [&](int64_t id) {
     return id >= 0 && id < a.rows && id != a.padding ? int(id) : -1;
   };
-  if (t + kPerThread <= a.tokens && misalign(a.ids) == 0) {
+  if (t0 + kSortThreads * kPerThread <= a.tokens && misalign(a.ids) == 0) {
     if (a.wide) {
       longlong2 w[kPerThread / 2];
 #pragma unroll
       for (int j = 0; j < kPerThread / 2; ++j)
-        w[j] = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.ids) + t)[j];
+        w[j] = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.ids) +
+                                                  position(t0, j / 2))[j % 2];
 #pragma unroll
       for (int j = 0; j < kPerThread / 2; ++j) {
         v[2 * j] = token(w[j].x);
@@ -224,7 +242,7 @@ __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t, int (&
       int4 w[kPerThread / 4];
 #pragma unroll
       for (int j = 0; j < kPerThread / 4; ++j)
-        w[j] = reinterpret_cast<const int4*>(static_cast<const int32_t*>(a.ids) + t)[j];
+        w[j] = *reinterpret_cast<const int4*>(static_cast<const int32_t*>(a.ids) + position(t0, j));
 #pragma unroll
       for (int j = 0; j < kPerThread / 4; ++j) {
         v[4 * j] = token(w[j].x);
@@ -236,26 +254,30 @@ __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t, int (&
     return;
   }
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j)
-    v[j] = t + j < a.tokens ? token(id_at(a.ids, a.wide, t + j)) : -1;
+  for (int j = 0; j < kPerThread; ++j) {
+    const int64_t t = position(t0, j / 4) + j % 4;
+    v[j] = t < a.tokens ? token(id_at(a.ids, a.wide, t)) : -1;
+  }
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const SortArgs a) {
   extern __shared__ int sort_smem[];
   int* next = sort_smem;  // [local]: counts, then where a token's next position goes
   __shared__ int2 listed[kListed];  // (position, token) in order
-  __shared__ int sh[32];
+  __shared__ uint64_t sh[kSortThreads / 32];
+  __shared__ int nfrequent;
   const int c = blockIdx.x, mask = (1 << a.shift) - 1;
   const int lane = threadIdx.x & 31;
   constexpr int64_t step = int64_t(kSortThreads) * kPerThread;
-  const int64_t t = int64_t(threadIdx.x) * kPerThread;
+  constexpr int G = kPerThread / 4;
   grid_go();
   int before = 0, v[kPerThread];
-  if (t < a.tokens) read_tokens(a, t, v);
+  read_tokens(a, 0, v);
+  if (threadIdx.x == 0) nfrequent = 0;
   for (int i = threadIdx.x; i < a.local; i += kSortThreads) next[i] = 0;
   __syncthreads();
-  for (int64_t t0 = t; t0 < a.tokens; t0 += step) {
-    if (t0 != t) read_tokens(a, t0, v);
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
+    if (t0 > 0) read_tokens(a, t0, v);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const int cls = v[j] & mask;
@@ -271,44 +293,51 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const S
     const int64_t token = (int64_t(i) << a.shift) + c;
     const int k = i < a.local ? next[i] : 0;
     if (i < a.local && token < a.rows) a.count[token] = k;
-    int all;
-    const int at = block_before(k, sh, &all);
+    uint64_t all;
+    const int at = int(block_before(uint64_t(k), sh, &all));
     if (i < a.local) next[i] = n + at;
-    n += all;
+    // a class of n positions has at most n / (slab + 1) frequent tokens, so that no
+    // two classes' entries meet
+    if (k > a.slab)
+      a.frequent[base / (a.slab + 1) + atomicAdd(&nfrequent, 1)] =
+          make_int4(int(token), base + n + at, k, 0);
+    n += int(all);
   }
   if (c == mask && threadIdx.x == 0) *a.valid = base + n;
+  __syncthreads();
+  if (threadIdx.x == 0) a.classes[c] = make_int2(base / (a.slab + 1), nfrequent);
   if (n == 0) return;
   // the class's positions in order, in shared memory while they fit
   int found = 0;
   const bool fits = n <= kListed;
   for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += step) {
-    if (a.tokens > step) {
-      if (t0 + t < a.tokens) {
-        read_tokens(a, t0 + t, v);
-      } else {
+    if (a.tokens > step) read_tokens(a, t0, v);
+    // a 16-bit counter per group of four: a group has 4 kSortThreads at most
+    uint64_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < kPerThread; ++j) v[j] = -1;
-      }
-    }
-    int mine = 0;
-    if (t0 + t < a.tokens) {
+    for (int j = 0; j < kPerThread; ++j)
+      mine += uint64_t(v[j] >= 0 && (v[j] & mask) == c) << (16 * (j / 4));
+    uint64_t all;
+    const uint64_t at = block_before(mine, sh, &all);
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j) mine += v[j] >= 0 && (v[j] & mask) == c;
-    }
-    int all, at = found + block_before(mine, sh, &all);
-    if (mine > 0) {
+    for (int g = 0; g < G; ++g) {
+      int place = found + int(at >> (16 * g) & 0xffff);
+      if (mine >> (16 * g) & 0xffff) {
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        if (v[j] >= 0 && (v[j] & mask) == c) {
-          if (fits)
-            listed[at] = make_int2(int(t0 + t) + j, v[j]);
-          else
-            a.list[base + at] = int32_t(t0 + t) + j;
-          ++at;
+        for (int e = 0; e < 4; ++e) {
+          const int id = v[4 * g + e];
+          if (id >= 0 && (id & mask) == c) {
+            const int p = int(position(t0, g)) + e;
+            if (fits)
+              listed[place] = make_int2(p, id);
+            else
+              a.list[base + place] = p;
+            ++place;
+          }
         }
       }
+      found += int(all >> (16 * g) & 0xffff);
     }
-    found += all;
   }
   __syncthreads();
   if (threadIdx.x >= 32) return;
@@ -318,21 +347,28 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const S
     const int p = a.list[base + i];
     return make_int2(p, int(id_at(a.ids, a.wide, p)));
   };
-  int2 e = entry(lane);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int2 ahead = entry(i0 + 32 + lane);
-    const unsigned same = __match_any_sync(kFullMask, e.y);
-    const unsigned below = same & ((1u << lane) - 1u);
-    int at = 0;
-    if (e.y >= 0) at = next[e.y >> a.shift] + __popc(below);
-    __syncwarp();
-    if (e.y >= 0) {
-      a.pos[base + at] = e.x;
-      a.token[base + at] = e.y;
-      if (below == 0) next[e.y >> a.shift] = at + __popc(same);
+  // what does not depend on the rows before is there ahead, four rows at a time
+  constexpr int U = 4;
+  for (int i0 = 0; i0 < n; i0 += 32 * U) {
+    int2 e[U];
+    unsigned same[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) e[u] = entry(i0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) same[u] = __match_any_sync(kFullMask, e[u].y);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned below = same[u] & ((1u << lane) - 1u);
+      int at = 0;
+      if (e[u].y >= 0) at = next[e[u].y >> a.shift] + __popc(below);
+      __syncwarp();
+      if (e[u].y >= 0) {
+        if (below == 0) next[e[u].y >> a.shift] = at + __popc(same[u]);
+        a.pos[base + at] = e[u].x;
+        a.token[base + at] = e[u].y;
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    e = ahead;
   }
 }
 
@@ -347,12 +383,14 @@ struct SumArgs {
   const int32_t* token;
   const int32_t* count;
   const int32_t* valid;
+  const int4* frequent;
+  const int2* classes;
   int slab;
   int64_t slabs;
   float scale;
   int accumulate;
-  float* part;  // [slabs, 2, pitch]: of the token that goes on from the slab before, and
-                // of the one that starts here and goes on into the next
+  float* part;  // [slabs, 2, pitch]: of the frequent token that goes on from the slab
+                // before, and of the one that starts here and goes on into the next
   int64_t pitch;
   void* out;
   int64_t ldo;
@@ -407,7 +445,7 @@ __device__ void zero_row(O* p, int len, int x, int step) {
 template <class T, class O>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   constexpr int N = Span<T>::N, U = 8;
-  __shared__ int32_t pos[kMaxSlab], token[kMaxSlab + 2];
+  __shared__ int32_t pos[2 * kMaxSlab], token[2 * kMaxSlab + 1];
   const int64_t slab = grid_row();
   grid_wait();
   grid_go();
@@ -424,13 +462,41 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   const int64_t i0 = slab * a.slab;
   if (i0 >= valid) return;
   const int n = int(min(int64_t(a.slab), valid - i0));
-  // token[0] and token[n + 1]: the neighbours
-  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+  // this slab's and the next one's; token[0]: the last of the one before
+  for (int i = threadIdx.x; i <= 2 * a.slab; i += blockDim.x) {
     const int64_t j = i0 + i - 1;
     token[i] = j >= 0 && j < valid ? a.token[j] : -1;
-    if (i >= 1 && i <= n) pos[i - 1] = a.pos[j];
+    if (i >= 1) pos[i - 1] = j < valid ? a.pos[j] : 0;
   }
   __syncthreads();
+  // where a run of equal tokens that starts at i ends
+  auto run_end = [&](int i, int hi) {
+    const int32_t id = token[i];
+    int lo = i;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (token[mid] == id)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return hi;
+  };
+  // entries begin .. end - 1 (token[1 + i], pos[i]) are this block's
+  int begin = 0, end = n;
+  bool first = false, last = false;  // the first and the last token's sums are partial
+  if (token[0] >= 0 && token[0] == token[1]) {
+    if (a.count[token[1]] > a.slab)
+      first = true;
+    else
+      begin = run_end(1, n + 1) - 1;
+  }
+  if (n == a.slab && token[n + 1] >= 0 && token[n] == token[n + 1]) {
+    if (a.count[token[n]] > a.slab)
+      last = true;
+    else if (begin < n)
+      end = run_end(n, 2 * a.slab + 1) - 1;
+  }
   const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
   if (int64_t(cv) * N >= a.cols) return;
   const T* grad = static_cast<const T*>(a.grad);
@@ -438,12 +504,11 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   float s[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) s[j] = 0.f;
-  bool first = token[0] == token[1];  // the running token began in an earlier slab
-  for (int b = 0; b < n; b += U) {
+  for (int b = begin; b < end; b += U) {
     uint4 r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (b + u < n) {
+      if (b + u < end) {
         const T* p = grad + pos[b + u] * a.ldg;
         r[u] = load_vec(p, cols, cv, misalign(p));
       }
@@ -451,14 +516,13 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = b + u;
-      if (i >= n) break;
+      if (i >= end) break;
       float v[N];
       unpack_vec<T>(r[u], v);
 #pragma unroll
       for (int j = 0; j < N; ++j) s[j] += v[j];
-      const bool ends = token[i + 2] != token[i + 1];
-      if (ends || i == n - 1) {
-        if (!ends || first) {
+      if (i == end - 1 || token[i + 2] != token[i + 1]) {
+        if (first || (last && i == end - 1)) {
           float* q = part_at<N>(a, slab, first ? 0 : 1, cv);
 #pragma unroll
           for (int j = 0; j < N; j += 4)
@@ -474,63 +538,71 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   }
 }
 
-// The tokens that go on into the next slab, at the slab in which they start.
-template <class T, class O>
-__global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs a) {
-  constexpr int N = Span<T>::N;
+// The frequent tokens, a class per row of blocks.
+constexpr int kJoinThreads = 64, kJoinParts = 4;
+template <class O>
+__global__ void __launch_bounds__(kJoinThreads* kJoinParts) embedding_join_kernel(const SumArgs a) {
+  __shared__ float4 sums[kJoinParts][kJoinThreads];
   grid_wait();
-  const int64_t slab = grid_row();
-  const int valid = *a.valid;
-  const int64_t i0 = slab * a.slab, i1 = i0 + a.slab;
-  if (slab >= a.slabs || i1 >= valid) return;
-  const int32_t id = a.token[i1 - 1];
-  if (a.token[i1] != id) return;
-  if (i0 > 0 && a.token[i0 - 1] == id) return;  // it started before this slab
-  // how many slabs it goes on for
-  int more = 0;
-  for (int64_t k0 = slab + 1;; k0 += blockDim.x) {
-    const int64_t k = k0 + threadIdx.x;
-    const bool on = k < a.slabs && k * a.slab < valid && a.token[k * a.slab] == id;
-    const int c = __syncthreads_count(on);
-    more += c;
-    if (c < int(blockDim.x)) break;
-  }
-  const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
-  if (int64_t(cv) * N >= a.cols) return;
-  float s[N];
-  auto part = [&](int64_t k, int which, float (&w)[N]) {
-    const float4* q = reinterpret_cast<const float4*>(part_at<N>(a, k, which, cv));
+  const int2 mine = a.classes[blockIdx.y];
+  const int c = int(blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+  for (int i = 0; i < mine.y; ++i) {
+    const int4 token = a.frequent[mine.x + i];
+    const int64_t slab = token.y / a.slab;
+    const int more = int((int64_t(token.y) + token.z - 1) / a.slab - slab);
+    // the first partial sum and those of the slabs it goes on for, in kJoinParts runs
+    // of equal length, each summed in order, and the runs' sums in order
+    const int run = (more + kJoinParts) / kJoinParts;
+    const int k0 = threadIdx.y * run, k1 = min(k0 + run, more + 1);
+    const float* from = a.part + slab * 2 * a.pitch + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;
+    for (int k = k0; k < k1 && c < a.cols; k += U) {
+      float4 w[U];
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      const float4 f = q[j / 4];
-      w[j] = f.x;
-      w[j + 1] = f.y;
-      w[j + 2] = f.z;
-      w[j + 3] = f.w;
+      for (int u = 0; u < U; ++u)
+        if (k + u < k1)
+          w[u] = *reinterpret_cast<const float4*>(from + ((k + u) * 2 + (k + u == 0)) * a.pitch);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k + u < k1) {
+          s.x += w[u].x;
+          s.y += w[u].y;
+          s.z += w[u].z;
+          s.w += w[u].w;
+        }
     }
-  };
-  part(slab, 1, s);
-  constexpr int U = 32 / N;
-  for (int k = 1; k <= more; k += U) {
-    float w[U][N];
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < a.cols) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u <= more) part(slab + k + u, 0, w[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u <= more) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) s[j] += w[u][j];
+      for (int y = 1; y < kJoinParts; ++y) {
+        const float4 t = sums[y][threadIdx.x];
+        s.x += t.x;
+        s.y += t.y;
+        s.z += t.z;
+        s.w += t.w;
       }
+      const float v[4] = {s.x, s.y, s.z, s.w};
+      O* dst = static_cast<O*>(a.out) + token.x * a.ldo + c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + j < a.cols) {
+          float w = v[j] * a.scale;
+          if (a.accumulate) w += to_f32(dst[j]);
+          dst[j] = from_f32<O>(w);
+        }
+      }
+    }
+    __syncthreads();
   }
-  write_row<T, O>(a, id, cv, s);
 }
 
 template <class K, class A>
-int launch_after(K kern, dim3 grid, int threads, const A& a, cudaStream_t s) {
+int launch_after(K kern, dim3 grid, dim3 threads, const A& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
+  cfg.blockDim = threads;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -538,20 +610,23 @@ int launch_after(K kern, dim3 grid, int threads, const A& a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   IVFPQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
-  IVFPQ_LAUNCHED_K(kern, 0, threads);
+  IVFPQ_LAUNCHED_K(kern, 0, int(threads.x * threads.y));
   return IVFPQ_OK;
 }
 
 template <class T, class O>
-int launch_sums(const SumArgs& a, cudaStream_t s) {
+int launch_sums(const SumArgs& a, int classes, cudaStream_t s) {
   const int64_t nvec = ceil_div(a.cols, Span<T>::N);
   int threads = 32;
   while (threads < 128 && threads < nvec) threads *= 2;
   const int64_t runs = ceil_div(nvec, threads);
   const int64_t zero = a.accumulate ? 0 : ceil_div(a.rows, kZeroRows);
-  IVFPQ_TRY(launch_after(embedding_sum_kernel<T, O>, grid_of(runs, a.slabs + zero), threads, a, s));
+  IVFPQ_TRY(launch_after(embedding_sum_kernel<T, O>, grid_of(runs, a.slabs + zero),
+                         dim3(unsigned(threads)), a, s));
   if (a.slabs <= 1) return IVFPQ_OK;
-  return launch_after(embedding_join_kernel<T, O>, grid_of(runs, a.slabs), threads, a, s);
+  return launch_after(embedding_join_kernel<O>,
+                      dim3(unsigned(ceil_div(a.cols, 4 * kJoinThreads)), unsigned(classes)),
+                      dim3(kJoinThreads, kJoinParts), a, s);
 }
 
 int check_common(const char* fn, int dtype, int out_dtype, int64_t rows, int64_t cols,
@@ -633,14 +708,23 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.slabs = ceil_div(tokens, a.slab);
   a.pitch = ceil_div(cols, 8) * 8;
   Workspace ws(s);
-  int32_t* w = nullptr;
-  IVFPQ_TRY(ws.alloc(&w, size_t(tokens) * 3 + size_t(rows) + 1));
-  o.list = w;
-  o.pos = w + tokens;
-  o.token = w + 2 * tokens;
-  o.count = w + 3 * tokens;
+  // the slabs' partial sums, the frequent tokens and the sorted positions
+  const size_t parts = a.slabs > 1 ? size_t(a.slabs) * 2 * size_t(a.pitch) : 0;
+  const size_t frequent = size_t(tokens / (a.slab + 1) + 1), classes = size_t(1) << o.shift;
+  int4* w = nullptr;
+  IVFPQ_TRY(ws.alloc(&w, parts / 4 + frequent + (classes + 1) / 2 +
+                             (size_t(tokens) * 3 + size_t(rows) + 4) / 4));
+  a.part = reinterpret_cast<float*>(w);
+  o.frequent = w + parts / 4;
+  o.classes = reinterpret_cast<int2*>(o.frequent + frequent);
+  o.list = reinterpret_cast<int32_t*>(o.frequent + frequent + (classes + 1) / 2);
+  o.pos = o.list + tokens;
+  o.token = o.pos + tokens;
+  o.count = o.token + tokens;
   o.valid = o.count + rows;
-  if (a.slabs > 1) IVFPQ_TRY(ws.alloc(&a.part, size_t(a.slabs) * 2 * size_t(a.pitch)));
+  o.slab = a.slab;
+  a.frequent = o.frequent;
+  a.classes = o.classes;
   a.pos = o.pos;
   a.token = o.token;
   a.count = o.count;
@@ -652,6 +736,7 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   IVFPQ_LAUNCHED_K(embedding_sort_kernel, smem, kSortThreads);
   return by_dtype(dtype, [&](auto* t) -> int {
     using T = std::remove_pointer_t<decltype(t)>;
-    return out_dtype == dtype ? launch_sums<T, T>(a, s) : launch_sums<T, float>(a, s);
+    return out_dtype == dtype ? launch_sums<T, T>(a, 1 << o.shift, s)
+                              : launch_sums<T, float>(a, 1 << o.shift, s);
   });
 }
