@@ -163,19 +163,21 @@ int launch_lookup(LookupArgs a, cudaStream_t s) {
 
 // ---- gradient: positions by token ----------------------------------------------------
 constexpr int kSortThreads = 512;
-constexpr int kMaxLocal = 16384;  // a block's tokens: 64 KB of counters
+constexpr int kMaxLocal = 16384;  // a block's tokens: 128 KB of counters
 constexpr int kPerThread = 16;    // ids per thread and step
-constexpr int kListed = 4096;     // a class's positions kept in shared memory
+constexpr int kHot = 64;
+constexpr int kListed = 3584;     // a class's positions kept in shared memory
 
 struct SortArgs {
   const void* ids;
-  int wide;
-  int64_t tokens, rows, padding;
+  int64_t tokens;
+  uint32_t rows, padding;  // padding: no row where there is none
   int shift;  // 2^shift classes, one per block
   int local;  // tokens of a class
-  int32_t* list;   // [tokens] scratch: the class's positions in order
+  int2* list;      // [tokens] scratch: a class's (position, token) in order of position
+  int32_t* bucket; // [tokens] scratch: its positions by token, in any order
   int32_t* pos;    // [tokens] positions sorted by (class, token, position)
-  int32_t* token;  // [tokens] their tokens
+  int32_t* token;  // [tokens] their tokens; kFrequent marks those with more than `slab`
   int32_t* count;  // [rows] positions of each token
   int32_t* valid;  // [1] positions that hold a token
   int slab;
@@ -221,68 +223,67 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t* sh, uint6
 __device__ __forceinline__ int64_t position(int64_t t0, int j) {
   return t0 + (int64_t(j) * kSortThreads + threadIdx.x) * 4;
 }
-// Their tokens, -1 where there is none to count.
-__device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0, int (&v)[kPerThread]) {
-  auto token = [&](int64_t id) {
-    return id >= 0 && id < a.rows && id != a.padding ? int(id) : -1;
+// Their tokens, kNone where there is none to count.
+constexpr uint32_t kNone = 0xffffffffu;
+constexpr int32_t kFrequent = 1 << 30;  // above any token
+template <bool WIDE>
+__device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0,
+                                            uint32_t (&v)[kPerThread]) {
+  using Id = std::conditional_t<WIDE, int64_t, int32_t>;
+  const Id* ids = static_cast<const Id*>(a.ids);
+  auto token = [&](Id id) {
+    const uint32_t u = uint32_t(id);
+    const bool ok = u < a.rows && u != a.padding && (!WIDE || Id(u) == id);
+    return ok ? u : kNone;
   };
   if (t0 + kSortThreads * kPerThread <= a.tokens && misalign(a.ids) == 0) {
-    if (a.wide) {
-      longlong2 w[kPerThread / 2];
+    Id w[kPerThread];
+    constexpr int V = 16 / int(sizeof(Id));  // ids of a load
 #pragma unroll
-      for (int j = 0; j < kPerThread / 2; ++j)
-        w[j] = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.ids) +
-                                                  position(t0, j / 2))[j % 2];
+    for (int j = 0; j < kPerThread / V; ++j)
+      *reinterpret_cast<uint4*>(w + j * V) =
+          reinterpret_cast<const uint4*>(ids + position(t0, j * V / 4))[j % (4 / V)];
 #pragma unroll
-      for (int j = 0; j < kPerThread / 2; ++j) {
-        v[2 * j] = token(w[j].x);
-        v[2 * j + 1] = token(w[j].y);
-      }
-    } else {
-      int4 w[kPerThread / 4];
-#pragma unroll
-      for (int j = 0; j < kPerThread / 4; ++j)
-        w[j] = *reinterpret_cast<const int4*>(static_cast<const int32_t*>(a.ids) + position(t0, j));
-#pragma unroll
-      for (int j = 0; j < kPerThread / 4; ++j) {
-        v[4 * j] = token(w[j].x);
-        v[4 * j + 1] = token(w[j].y);
-        v[4 * j + 2] = token(w[j].z);
-        v[4 * j + 3] = token(w[j].w);
-      }
-    }
+    for (int j = 0; j < kPerThread; ++j) v[j] = token(w[j]);
     return;
   }
-#pragma unroll
+#pragma unroll 4
   for (int j = 0; j < kPerThread; ++j) {
     const int64_t t = position(t0, j / 4) + j % 4;
-    v[j] = t < a.tokens ? token(id_at(a.ids, a.wide, t)) : -1;
+    v[j] = t < a.tokens ? token(ids[t]) : kNone;
   }
 }
 
+template <bool WIDE>
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const SortArgs a) {
   extern __shared__ int sort_smem[];
-  int* next = sort_smem;  // [local]: counts, then where a token's next position goes
-  __shared__ int2 listed[kListed];  // (position, token) in order
+  int* start = sort_smem;         // [local + 1]: counts, then where a token's positions start
+  int* fill = start + a.local + 1;  // [local]: how many of them have a place
+  __shared__ int2 list_smem[kListed];
+  __shared__ int bucket_smem[kListed];
+  __shared__ int hot[kHot];  // frequent tokens
   __shared__ uint64_t sh[kSortThreads / 32];
   __shared__ int nfrequent;
-  const int c = blockIdx.x, mask = (1 << a.shift) - 1;
-  const int lane = threadIdx.x & 31;
+  const uint32_t c = blockIdx.x, mask = (1u << a.shift) - 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int64_t step = int64_t(kSortThreads) * kPerThread;
   constexpr int G = kPerThread / 4;
   grid_go();
-  int before = 0, v[kPerThread];
-  read_tokens(a, 0, v);
+  int before = 0;
+  uint32_t v[kPerThread];
+  read_tokens<WIDE>(a, 0, v);
   if (threadIdx.x == 0) nfrequent = 0;
-  for (int i = threadIdx.x; i < a.local; i += kSortThreads) next[i] = 0;
+  for (int i = threadIdx.x; i < 2 * a.local + 1; i += kSortThreads) start[i] = 0;
   __syncthreads();
   for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
-    if (t0 > 0) read_tokens(a, t0, v);
+    if (t0 > 0) read_tokens<WIDE>(a, t0, v);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
-      const int cls = v[j] & mask;
-      before += v[j] >= 0 && cls < c;
-      if (v[j] >= 0 && cls == c) atomicAdd(&next[v[j] >> a.shift], 1);
+      const uint32_t cls = v[j] & mask;
+      if (v[j] != kNone) {
+        before += cls < c;
+        if (cls == c) atomicAdd(&start[v[j] >> a.shift], 1);
+      }
     }
   }
   const int base = block_sum(before, sh);
@@ -291,83 +292,96 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const S
   for (int i0 = 0; i0 < a.local; i0 += kSortThreads) {
     const int i = i0 + threadIdx.x;
     const int64_t token = (int64_t(i) << a.shift) + c;
-    const int k = i < a.local ? next[i] : 0;
+    const int k = i < a.local ? start[i] : 0;
     if (i < a.local && token < a.rows) a.count[token] = k;
     uint64_t all;
-    const int at = int(block_before(uint64_t(k), sh, &all));
-    if (i < a.local) next[i] = n + at;
-    // a class of n positions has at most n / (slab + 1) frequent tokens, so that no
-    // two classes' entries meet
-    if (k > a.slab)
-      a.frequent[base / (a.slab + 1) + atomicAdd(&nfrequent, 1)] =
-          make_int4(int(token), base + n + at, k, 0);
+    const int at = n + int(block_before(uint64_t(k), sh, &all));
+    if (i < a.local) start[i] = at;
+    if (k > a.slab) {
+      // a class of n positions has at most n / (slab + 1) frequent tokens, so that no
+      // two classes' entries meet
+      const int j = atomicAdd(&nfrequent, 1);
+      a.frequent[base / (a.slab + 1) + j] = make_int4(int(token), base + at, k, 0);
+      if (j < kHot) hot[j] = int(token);
+    }
     n += int(all);
   }
+  if (threadIdx.x == 0) start[a.local] = n;
   if (c == mask && threadIdx.x == 0) *a.valid = base + n;
   __syncthreads();
   if (threadIdx.x == 0) a.classes[c] = make_int2(base / (a.slab + 1), nfrequent);
   if (n == 0) return;
-  // the class's positions in order, in shared memory while they fit
-  int found = 0;
+  // the class's positions in order
   const bool fits = n <= kListed;
+  int2* list = fits ? list_smem : a.list + base;
+  int* bucket = fits ? bucket_smem : a.bucket + base;
+  int found = 0;
   for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += step) {
-    if (a.tokens > step) read_tokens(a, t0, v);
+    if (a.tokens > step) read_tokens<WIDE>(a, t0, v);
     // a 16-bit counter per group of four: a group has 4 kSortThreads at most
     uint64_t mine = 0;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j)
-      mine += uint64_t(v[j] >= 0 && (v[j] & mask) == c) << (16 * (j / 4));
+      mine += uint64_t(v[j] != kNone && (v[j] & mask) == c) << (16 * (j / 4));
     uint64_t all;
     const uint64_t at = block_before(mine, sh, &all);
+    if (mine) {
+      int before_group = found;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      int place = found + int(at >> (16 * g) & 0xffff);
-      if (mine >> (16 * g) & 0xffff) {
+      for (int g = 0; g < G; ++g) {
+        int place = before_group + int(at >> (16 * g) & 0xffff);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int id = v[4 * g + e];
-          if (id >= 0 && (id & mask) == c) {
-            const int p = int(position(t0, g)) + e;
-            if (fits)
-              listed[place] = make_int2(p, id);
-            else
-              a.list[base + place] = p;
-            ++place;
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          if (v[4 * g + e] != kNone && (v[4 * g + e] & mask) == c)
+            list[place++] = make_int2(int(position(t0, g)) + e, int(v[4 * g + e]));
+        before_group += int(all >> (16 * g) & 0xffff);
       }
-      found += int(all >> (16 * g) & 0xffff);
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g) found += int(all >> (16 * g) & 0xffff);
   }
   __syncthreads();
-  if (threadIdx.x >= 32) return;
-  auto entry = [&](int i) {
-    if (i >= n) return make_int2(-1, -1);
-    if (fits) return listed[i];
-    const int p = a.list[base + i];
-    return make_int2(p, int(id_at(a.ids, a.wide, p)));
-  };
-  // what does not depend on the rows before is there ahead, four rows at a time
-  constexpr int U = 4;
-  for (int i0 = 0; i0 < n; i0 += 32 * U) {
-    int2 e[U];
-    unsigned same[U];
+  // tokens that are not frequent: their positions into a bucket, in any order, ...
+  auto size_of = [&](int l) { return start[l + 1] - start[l]; };
+  for (int i = threadIdx.x; i < n; i += kSortThreads) {
+    const int2 e = list[i];
+    const int l = e.y >> a.shift;
+    if (size_of(l) <= a.slab) bucket[start[l] + atomicAdd(&fill[l], 1)] = e.x;
+  }
+  __syncthreads();
+  // ... and each to its rank among them
+  for (int i = threadIdx.x; i < n; i += kSortThreads) {
+    const int2 e = list[i];
+    const int l = e.y >> a.shift, k = size_of(l);
+    if (k > a.slab) continue;
+    const int* of = bucket + start[l];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) rank += of[j] < e.x;
+    a.pos[base + start[l] + rank] = e.x;
+    a.token[base + start[l] + rank] = e.y;
+  }
+  // a frequent token's in order, by a warp that goes through the list
+  const int4* frequent = a.frequent + base / (a.slab + 1);
+  for (int f = warp; f < nfrequent; f += kSortThreads / 32) {
+    const int id = f < kHot ? hot[f] : frequent[f].x;
+    int at = base + start[id >> a.shift];
+    constexpr int U = 4;
+    for (int i0 = 0; i0 < n; i0 += 32 * U) {
+      int2 e[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) e[u] = entry(i0 + 32 * u + lane);
+      for (int u = 0; u < U; ++u)
+        e[u] = i0 + 32 * u + lane < n ? list[i0 + 32 * u + lane] : make_int2(-1, -1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) same[u] = __match_any_sync(kFullMask, e[u].y);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned below = same[u] & ((1u << lane) - 1u);
-      int at = 0;
-      if (e[u].y >= 0) at = next[e[u].y >> a.shift] + __popc(below);
-      __syncwarp();
-      if (e[u].y >= 0) {
-        if (below == 0) next[e[u].y >> a.shift] = at + __popc(same[u]);
-        a.pos[base + at] = e[u].x;
-        a.token[base + at] = e[u].y;
+      for (int u = 0; u < U; ++u) {
+        const unsigned same = __ballot_sync(kFullMask, e[u].y == id);
+        if (e[u].y == id) {
+          const int to = at + __popc(same & ((1u << lane) - 1u));
+          a.pos[to] = e[u].x;
+          a.token[to] = id | kFrequent;
+        }
+        at += __popc(same);
       }
-      __syncwarp();
     }
   }
 }
@@ -396,29 +410,29 @@ struct SumArgs {
   int64_t ldo;
 };
 
+// VEC: rows of grad and out are whole vectors on 16-byte boundaries.
 // Row values of columns N cv .. N cv + N - 1 of token v.
-template <class T, class O>
+template <class T, class O, bool VEC>
 __device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int cv,
                                           const float (&s)[Span<T>::N]) {
-  constexpr int N = Span<T>::N;
+  constexpr int N = Span<T>::N, M = Span<O>::N;
   O* dst = static_cast<O*>(a.out) + v * a.ldo + int64_t(cv) * N;
-  const int have = int(min(int64_t(N), a.cols - int64_t(cv) * N));
-  if (have == N && misalign(dst) == 0) {
-    float w[N];
+  if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) w[j] = s[j] * a.scale;
-    if (a.accumulate) {
-      constexpr int M = Span<O>::N;
+    for (int q = 0; q < N / M; ++q) {
+      float w[M];
 #pragma unroll
-      for (int q = 0; q < N / M; ++q) {
+      for (int j = 0; j < M; ++j) w[j] = s[q * M + j] * a.scale;
+      if (a.accumulate) {
         float old[M];
         unpack_vec<O>(reinterpret_cast<const uint4*>(dst)[q], old);
 #pragma unroll
-        for (int j = 0; j < M; ++j) w[q * M + j] += old[j];
+        for (int j = 0; j < M; ++j) w[j] += old[j];
       }
+      reinterpret_cast<uint4*>(dst)[q] = pack_vec<O>(w);
     }
-    store_vec<O>(dst, w);
   } else {
+    const int have = int(min(int64_t(N), a.cols - int64_t(cv) * N));
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (j < have) {
@@ -434,15 +448,15 @@ __device__ __forceinline__ float* part_at(const SumArgs& a, int64_t slab, int wh
   return a.part + (slab * 2 + which) * a.pitch + int64_t(cv) * N;
 }
 
-template <class T, class O>
-__device__ void zero_row(O* p, int len, int x, int step) {
+template <class O>
+__device__ __forceinline__ void zero_row(O* p, int len, int x, int step) {
   const Span<O> sp(p, len);
   for (int e = x; e < sp.rest(); e += step) p[sp.at(e)] = from_f32<O>(0.f);
   for (int i = x; i < sp.nvec; i += step)
     reinterpret_cast<uint4*>(p + sp.head)[i] = make_uint4(0, 0, 0, 0);
 }
 
-template <class T, class O>
+template <class T, class O, bool VEC>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   constexpr int N = Span<T>::N, U = 8;
   __shared__ int32_t pos[2 * kMaxSlab], token[2 * kMaxSlab + 1];
@@ -453,21 +467,31 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
     // rows without a token
     const int step = int(gridDim.x * blockDim.x), x = int(blockIdx.x * blockDim.x + threadIdx.x);
     const int64_t v0 = (slab - a.slabs) * kZeroRows;
-    for (int64_t v = v0; v < min(v0 + kZeroRows, a.rows); ++v)
-      if (a.count[v] == 0)
-        zero_row<T, O>(static_cast<O*>(a.out) + v * a.ldo, int(a.cols), x, step);
+    int32_t count[kZeroRows];
+#pragma unroll
+    for (int i = 0; i < kZeroRows; ++i) count[i] = v0 + i < a.rows ? a.count[v0 + i] : 1;
+#pragma unroll 1
+    for (int i = 0; i < kZeroRows; ++i) {
+      if (count[0] == 0)
+        zero_row(static_cast<O*>(a.out) + (v0 + i) * a.ldo, int(a.cols), x, step);
+#pragma unroll
+      for (int j = 0; j + 1 < kZeroRows; ++j) count[j] = count[j + 1];
+    }
     return;
   }
-  const int valid = *a.valid;
   const int64_t i0 = slab * a.slab;
-  if (i0 >= valid) return;
-  const int n = int(min(int64_t(a.slab), valid - i0));
-  // this slab's and the next one's; token[0]: the last of the one before
+  const int valid = *a.valid;
+  // this slab's and the next one's; token[0]: the last of the one before. (What lies
+  // past the valid positions is read along with them and not looked at.)
   for (int i = threadIdx.x; i <= 2 * a.slab; i += blockDim.x) {
     const int64_t j = i0 + i - 1;
-    token[i] = j >= 0 && j < valid ? a.token[j] : -1;
-    if (i >= 1) pos[i - 1] = j < valid ? a.pos[j] : 0;
+    const bool there = j >= 0 && j < a.tokens;
+    const int32_t id = there ? a.token[j] : -1, p = there ? a.pos[j] : 0;
+    token[i] = j < valid ? id : -1;
+    if (i >= 1) pos[i - 1] = p;
   }
+  if (i0 >= valid) return;
+  const int n = int(min(int64_t(a.slab), valid - i0));
   __syncthreads();
   // where a run of equal tokens that starts at i ends
   auto run_end = [&](int i, int hi) {
@@ -486,13 +510,13 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   int begin = 0, end = n;
   bool first = false, last = false;  // the first and the last token's sums are partial
   if (token[0] >= 0 && token[0] == token[1]) {
-    if (a.count[token[1]] > a.slab)
+    if (token[1] & kFrequent)
       first = true;
     else
       begin = run_end(1, n + 1) - 1;
   }
   if (n == a.slab && token[n + 1] >= 0 && token[n] == token[n + 1]) {
-    if (a.count[token[n]] > a.slab)
+    if (token[n] & kFrequent)
       last = true;
     else if (begin < n)
       end = run_end(n, 2 * a.slab + 1) - 1;
@@ -500,7 +524,7 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
   const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
   if (int64_t(cv) * N >= a.cols) return;
   const T* grad = static_cast<const T*>(a.grad);
-  const int cols = int(a.cols);
+  [[maybe_unused]] const int cols = int(a.cols);
   float s[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) s[j] = 0.f;
@@ -510,7 +534,10 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
     for (int u = 0; u < U; ++u) {
       if (b + u < end) {
         const T* p = grad + pos[b + u] * a.ldg;
-        r[u] = load_vec(p, cols, cv, misalign(p));
+        if constexpr (VEC)
+          r[u] = reinterpret_cast<const uint4*>(p)[cv];
+        else
+          r[u] = load_vec(p, cols, cv, misalign(p));
       }
     }
 #pragma unroll
@@ -528,7 +555,7 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
           for (int j = 0; j < N; j += 4)
             *reinterpret_cast<float4*>(q + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
         } else {
-          write_row<T, O>(a, token[i + 1], cv, s);
+          write_row<T, O, VEC>(a, token[i + 1] & ~kFrequent, cv, s);
         }
         first = false;
 #pragma unroll
@@ -621,8 +648,11 @@ int launch_sums(const SumArgs& a, int classes, cudaStream_t s) {
   while (threads < 128 && threads < nvec) threads *= 2;
   const int64_t runs = ceil_div(nvec, threads);
   const int64_t zero = a.accumulate ? 0 : ceil_div(a.rows, kZeroRows);
-  IVFPQ_TRY(launch_after(embedding_sum_kernel<T, O>, grid_of(runs, a.slabs + zero),
-                         dim3(unsigned(threads)), a, s));
+  const bool vec = a.cols % Span<T>::N == 0 && a.ldg % Span<T>::N == 0 &&
+                   a.ldo % Span<O>::N == 0 && reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  IVFPQ_TRY(launch_after(vec ? embedding_sum_kernel<T, O, true> : embedding_sum_kernel<T, O, false>,
+                         grid_of(runs, a.slabs + zero), dim3(unsigned(threads)), a, s));
   if (a.slabs <= 1) return IVFPQ_OK;
   return launch_after(embedding_join_kernel<O>,
                       dim3(unsigned(ceil_div(a.cols, 4 * kJoinThreads)), unsigned(classes)),
@@ -683,12 +713,12 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   if (rows == 0 || cols == 0 || (tokens == 0 && accumulate)) return IVFPQ_OK;
   IVFPQ_REQUIRE(out && ((ids && grad) || tokens == 0), "embedding_gradient: null pointer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool wide = ids_bytes == 8;
   SortArgs o{};
   o.ids = ids;
-  o.wide = ids_bytes == 8;
   o.tokens = tokens;
-  o.rows = rows;
-  o.padding = padding;
+  o.rows = uint32_t(rows);
+  o.padding = padding >= 0 && padding < rows ? uint32_t(padding) : kNone;
   // a block per SM or nearly, and more where a class would have too many tokens
   o.shift = 7;
   while (ceil_div(rows, int64_t(1) << o.shift) > kMaxLocal) ++o.shift;
@@ -703,22 +733,24 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.accumulate = accumulate != 0;
   a.out = out;
   a.ldo = ldo;
-  a.slab = 32;
-  while (a.slab < kMaxSlab && tokens > int64_t(a.slab) * 1024) a.slab *= 2;
+  // short slabs while they are few: a block takes its positions one after the other
+  a.slab = 8;
+  while (a.slab < kMaxSlab && tokens > int64_t(a.slab) * 512) a.slab *= 2;
   a.slabs = ceil_div(tokens, a.slab);
   a.pitch = ceil_div(cols, 8) * 8;
   Workspace ws(s);
   // the slabs' partial sums, the frequent tokens and the sorted positions
   const size_t parts = a.slabs > 1 ? size_t(a.slabs) * 2 * size_t(a.pitch) : 0;
   const size_t frequent = size_t(tokens / (a.slab + 1) + 1), classes = size_t(1) << o.shift;
+  const size_t words = size_t(tokens) * 5 + size_t(rows) + 1;
   int4* w = nullptr;
-  IVFPQ_TRY(ws.alloc(&w, parts / 4 + frequent + (classes + 1) / 2 +
-                             (size_t(tokens) * 3 + size_t(rows) + 4) / 4));
+  IVFPQ_TRY(ws.alloc(&w, parts / 4 + frequent + (classes + 1) / 2 + (words + 3) / 4));
   a.part = reinterpret_cast<float*>(w);
   o.frequent = w + parts / 4;
   o.classes = reinterpret_cast<int2*>(o.frequent + frequent);
-  o.list = reinterpret_cast<int32_t*>(o.frequent + frequent + (classes + 1) / 2);
-  o.pos = o.list + tokens;
+  o.list = o.classes + 2 * ((classes + 1) / 2);
+  o.bucket = reinterpret_cast<int32_t*>(o.list + tokens);
+  o.pos = o.bucket + tokens;
   o.token = o.pos + tokens;
   o.count = o.token + tokens;
   o.valid = o.count + rows;
@@ -729,11 +761,11 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.token = o.token;
   a.count = o.count;
   a.valid = o.valid;
-  const size_t smem = size_t(o.local) * 4;
-  // 48 KB with the static part need no leave
-  if (smem > 12 * 1024) IVFPQ_TRY(set_dynamic_smem(embedding_sort_kernel, smem));
-  embedding_sort_kernel<<<1u << o.shift, kSortThreads, smem, s>>>(o);
-  IVFPQ_LAUNCHED_K(embedding_sort_kernel, smem, kSortThreads);
+  const size_t smem = (size_t(o.local) * 2 + 1) * 4;
+  auto sort = wide ? embedding_sort_kernel<true> : embedding_sort_kernel<false>;
+  IVFPQ_TRY(set_dynamic_smem(sort, smem));
+  sort<<<1u << o.shift, kSortThreads, smem, s>>>(o);
+  IVFPQ_LAUNCHED_K(sort, smem, kSortThreads);
   return by_dtype(dtype, [&](auto* t) -> int {
     using T = std::remove_pointer_t<decltype(t)>;
     return out_dtype == dtype ? launch_sums<T, T>(a, 1 << o.shift, s)
