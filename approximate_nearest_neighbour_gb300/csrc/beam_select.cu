@@ -9,12 +9,12 @@
 //  1. One pass keeps per thread the largest score and the sum of exponentials
 //     relative to it (rescaled when it grows), and of every four vectors that a
 //     thread takes (a batch) the largest score, in shared memory.
-//  2. The k-th largest of the batches' maxima is a lower bound of the k-th
-//     largest score; bisection over its bits finds it, or something a little
-//     lower. Only batches that reach the bound are read again (about k of them, a
-//     thread each, from L2), and their scores at or above it kept.
-//  3. The kept ones are ranked among themselves; a cluster of blocks that shares
-//     a row ranks its lists against each other by binary search.
+//  2. The k-th largest of the threads' maxima is a lower bound of the k-th largest
+//     score; every warp finds it, or something a little lower, by halving the range
+//     between them. Only batches that reach the bound are read again, a vector per
+//     thread, from L2, and their scores at or above it kept.
+//  3. The kept ones are ranked among themselves. Where a cluster of blocks shares a
+//     row, its first block gets the lists of the others and ranks all of them.
 //  4. A second kernel, already waiting, merges the beams' lists of a group, two
 //     at a time. Totals are compared in fp64: they differ by the rounding of
 //     their sums of exponentials, not of the comparison.
@@ -33,8 +33,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;         // vectors of a batch
-constexpr int kMaxSteps = 4;       // batches per thread whose maxima are kept apart
-constexpr int kSlack = 32;         // how many batches more than k the bound may let pass
+constexpr int kMaxSteps = 16;      // batches per thread whose maxima are kept apart
+constexpr int kSlack = 8;          // how many threads more than k the bound may let pass
 constexpr int kCap = 4096;         // kept scores before the worse ones are dropped
 constexpr int kRound = kThreads * 8;  // most scores that one round can keep
 constexpr float kLog2e = 1.4426950408889634f;
@@ -106,34 +106,53 @@ __device__ __forceinline__ uint4 empty_vec() {
   return make_uint4(w, w, w, w);
 }
 
-// A run's vectors; past its end -inf.
-template <class T>
+// A run's vectors; past its end -inf. VEC: rows are whole vectors on 16-byte boundaries.
+template <class T, bool VEC>
 struct Run {
   const T* p;
   int len, nvec, mis, first, last;
   __device__ __forceinline__ Run(const T* q, int n) : p(q), len(n) {
     nvec = (n + Span<T>::N - 1) / Span<T>::N;
-    mis = misalign(q);
+    mis = VEC ? 0 : misalign(q);
     first = inner_first(mis);
-    last = inner_last<T>(n, mis);
+    last = VEC ? nvec - 1 : inner_last<T>(n, mis);
+  }
+  __device__ __forceinline__ uint4 inner(int i) const {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p) + i);
+    return load_inner(p, i, mis);
   }
   __device__ __forceinline__ uint4 at(int i) const {
-    if (i >= first && i <= last) return load_inner(p, i, mis);
-    return i < nvec ? load_edge(p, len, i) : empty_vec<T>();
+    if (i >= first && i <= last) return inner(i);
+    if constexpr (!VEC) {
+      if (i < nvec) return load_edge(p, len, i);
+    }
+    return empty_vec<T>();
   }
 };
 
 // The batch of step i: vectors (i * kUnroll + u) * kThreads + thread.
-template <class T>
-__device__ __forceinline__ void load_batch(const Run<T>& run, int step, uint4 (&r)[kUnroll]) {
+template <class T, bool VEC>
+__device__ __forceinline__ void load_batch(const Run<T, VEC>& run, int step, uint4 (&r)[kUnroll]) {
   const int i0 = step * kUnroll * kThreads + threadIdx.x;
   if (i0 >= run.first && i0 + (kUnroll - 1) * kThreads <= run.last) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) r[u] = load_inner(run.p, i0 + u * kThreads, run.mis);
+    for (int u = 0; u < kUnroll; ++u) r[u] = run.inner(i0 + u * kThreads);
   } else {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) r[u] = run.at(i0 + u * kThreads);
   }
+}
+
+// The sum of a vector's exponentials relative to m where there is nothing yet (m = 0), or
+// where the products of scores pass fp32.
+template <class T>
+__device__ __noinline__ float far_vec(uint4 r, float m) {
+  constexpr int N = Span<T>::N;
+  float v[N], z = 0.f;
+  unpack_vec<T>(r, v);
+#pragma unroll
+  for (int j = 0; j < N; ++j) z += exp2_fast((v[j] - m) * kLog2e);
+  return z;
 }
 
 // Adds a batch's exponentials to o, whose m is at least its largest score.
@@ -162,29 +181,16 @@ __device__ __forceinline__ void add_batch(const uint4 (&r)[kUnroll], Online& o) 
     unpair(z, z0, z1);
     o.z += (z0 + z1) * exp2_fast(-fmaf(o.m, kLog2e, -b));
   } else {
-    // nothing yet, or scores whose products pass fp32
-    const float ref = o.m == -INFINITY ? 0.f : o.m;
-    const uint64_t minus = pair(-ref, -ref);
+    const float m = o.m == -INFINITY ? 0.f : o.m;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float v[N];
-      unpack_vec<T>(r[u], v);
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        float x, y;
-        unpair(mul2(add2(pair(v[j], v[j + 1]), minus), scale), x, y);
-        z = add2(z, pair(exp2_fast(x), exp2_fast(y)));
-      }
-    }
-    unpair(z, z0, z1);
-    o.z += z0 + z1;
+    for (int u = 0; u < kUnroll; ++u) o.z += far_vec<T>(r[u], m);
   }
 }
 
 // One pass over the run. peak[g * kThreads + thread]: the largest score of the
 // thread's steps g << shift and following, as a key; r: its first batch.
-template <class T>
-__device__ __forceinline__ void run_stats(const Run<T>& run, int steps, int shift,
+template <class T, bool VEC>
+__device__ __forceinline__ void run_stats(const Run<T, VEC>& run, int steps, int shift,
                                           uint4 (&r)[kUnroll], uint32_t* peak, Online& o) {
   float top = -INFINITY;
   auto take = [&](int i, const uint4 (&v)[kUnroll]) {
@@ -233,64 +239,68 @@ __device__ void sort_entries(uint64_t* e, int n) {
   __syncthreads();
 }
 
-// A key that at least k of the block's peaks reach (`groups` per thread), and no more
-// than k + kSlack of them unless peaks are equal in their upper 16 bits; 0 if there
-// are fewer than k. A bit per step, from the highest one in which peaks differ.
-// votes: [34] zeros.
-__device__ __forceinline__ uint32_t kth_bound(const uint32_t* peak, int groups, int k,
-                                              unsigned* votes) {
+// A key that at least k of the block's keys (one per thread) reach, and no more than
+// k + kSlack of them unless keys are equal; 0 if fewer than k are above that of -inf.
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t* keys, int k) {
+  constexpr uint32_t kNothing = 0x007fffffu;  // -inf
   const int lane = threadIdx.x & 31;
-  uint32_t v[kMaxSteps], lo = 0xffffffffu, hi = 0;
+  uint32_t v[kThreads / 32], lo = 0xffffffffu, hi = 0;
+  unsigned n = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxSteps; ++i) {
-    v[i] = i < groups ? peak[i * kThreads + threadIdx.x] : 0u;
-    if (i < groups) lo = min(lo, v[i]);
+  for (int i = 0; i < kThreads / 32; ++i) {
+    v[i] = keys[i * 32 + lane];
+    if (v[i] > kNothing) {
+      lo = min(lo, v[i]);
+      ++n;
+    }
     hi = max(hi, v[i]);
   }
-  // votes[32], votes[33]: the largest key, and of the inverted ones
   hi = __reduce_max_sync(kFullMask, hi);
   lo = __reduce_min_sync(kFullMask, lo);
-  if (lane == 0) {
-    atomicMax(&votes[32], hi);
-    atomicMax(&votes[33], ~lo);
-  }
-  __syncthreads();
-  if (groups * kThreads < k) return 0;
-  hi = votes[32];
-  lo = ~votes[33];
-  if ((lo ^ hi) >> 16 == 0) return lo & 0xffff0000u;
-  const int top = 31 - __clz(lo ^ hi);
-  uint32_t bound = hi & ~((2u << top) - 1u);
-  for (int bit = top; bit >= 16; --bit) {
-    const uint32_t t = bound | (1u << bit);
-    int c = 0;
+  if (int(__reduce_add_sync(kFullMask, n)) < k) return 0;
+  while (lo < hi) {  // at least k keys reach lo, fewer than k pass hi
+    const uint32_t mid = hi - (hi - lo) / 2;
+    unsigned c = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxSteps; ++i) c += v[i] >= t;
-    const unsigned w = __reduce_add_sync(kFullMask, unsigned(c));
-    if (lane == 0 && w) atomicAdd(&votes[bit], w);
-    __syncthreads();
-    const int all = int(votes[bit]);
-    if (all >= k) {
-      bound = t;
+    for (int i = 0; i < kThreads / 32; ++i) c += v[i] >= mid;
+    const int all = int(__reduce_add_sync(kFullMask, c));
+    if (all < k) {
+      hi = mid - 1;
+    } else {
+      lo = mid;
       if (all <= k + kSlack) break;
     }
   }
-  return bound;
+  return lo;
 }
 
-__device__ __forceinline__ uint64_t ld_cluster64(uint32_t addr) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// What a block tells the others of its row.
+// A block's statistics and the length of its list.
 struct alignas(16) Part {
   float m, z;
   int len, pad;
 };
+// The statistics of `parts` parts (at most 8), in every lane of a warp.
+__device__ __forceinline__ Online join_stats(float m, float z) {
+  Online o;
+  o.m = m;
+  o.z = z;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2) {
+    const float m2 = __shfl_xor_sync(kFullMask, o.m, d), z2 = __shfl_xor_sync(kFullMask, o.z, d);
+    const bool upper = (threadIdx.x & d) != 0;  // the same operations in both lanes
+    Online j;
+    j.join(upper ? m2 : o.m, upper ? z2 : o.z);
+    j.join(upper ? o.m : m2, upper ? o.z : z2);
+    o = j;
+  }
+  return o;
+}
 
-template <class T>
+template <class T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs a) {
   constexpr int N = Span<T>::N;
   extern __shared__ __align__(16) uint64_t select_smem[];
@@ -301,10 +311,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
   uint32_t* peak = reinterpret_cast<uint32_t*>(select_smem);
   __shared__ uint16_t chosen[kMaxSteps * kThreads];
   __shared__ float2 sh[kWarps];
-  __shared__ Part part;
-  __shared__ Part all[kMaxCluster];
+  __shared__ Part all[kMaxCluster];  // in the first block of a cluster: of all its blocks
   __shared__ int nkept, nchosen;
-  __shared__ unsigned votes[34];
+  __shared__ uint32_t keys[kThreads];
   const int ranks = int(gridDim.x), rank = int(blockIdx.x);
   const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   if (row >= a.rows) return;
@@ -312,12 +321,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
   const float t = a.totals[row];
   const bool done = a.finished && a.finished[row];
   const int64_t c0 = min(int64_t(rank) * a.chunk, a.cols);
-  const Run<T> run(static_cast<const T*>(a.scores) + row * a.lds + c0,
+  const Run<T, VEC> run(static_cast<const T*>(a.scores) + row * a.lds + c0,
                    int(min(int64_t(a.chunk), a.cols - c0)));
   uint4 r[kUnroll];
   load_batch(run, 0, r);  // on its way while the total is
-  if (threadIdx.x < 34) votes[threadIdx.x] = 0;
   if (threadIdx.x == 0) nkept = nchosen = 0;
+  // the blocks of a cluster must have started before one writes to another
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const bool alive = fabsf(t) < INFINITY;  // neither infinite nor NaN
   if (!alive || done) {
     if (rank == 0 && threadIdx.x == 0) {
@@ -327,13 +337,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
       a.o.m[row] = 0.f;
       a.o.base[row] = double(t);
     }
+    if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
   const int steps = (run.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
   const int groups = (steps + (1 << a.shift) - 1) >> a.shift;
   Online o;
-  run_stats<T>(run, steps, a.shift, r, peak, o);
+  run_stats(run, steps, a.shift, r, peak, o);
   grid_go();
+  keys[threadIdx.x] = score_key(o.m);
   // the block's statistics
   {
     const float m = key_to_float(__reduce_max_sync(kFullMask, score_key(o.m)));
@@ -343,17 +355,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
     if (lane == 0) sh[warp] = make_float2(m, z);
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    Online j;
-    for (int w = 0; w < kWarps; ++w) j.join(sh[w].x, sh[w].y);
-    part.m = j.m;
-    part.z = j.z;
-  }
-  const uint32_t bound = kth_bound(peak, groups, a.k, votes);
+  const uint32_t bound = kth_bound(keys, a.k);
   // the batches that reach the bound
-  for (int g = 0; g < groups; ++g)
-    if (peak[g * kThreads + threadIdx.x] >= bound)
-      chosen[atomicAdd(&nchosen, 1)] = uint16_t(g * kThreads + threadIdx.x);
+  if (score_key(o.m) >= bound) {
+    for (int g = 0; g < groups; ++g)
+      if (peak[g * kThreads + threadIdx.x] >= bound)
+        chosen[atomicAdd(&nchosen, 1)] = uint16_t(g * kThreads + threadIdx.x);
+  }
   __syncthreads();  // also: the peaks are read
   const int per = kUnroll << a.shift, nread = nchosen * per;  // vectors
   uint64_t bar = uint64_t(bound) << 32;
@@ -400,47 +408,66 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
     for (int i = threadIdx.x; i < min(n, a.k); i += kThreads) top[i] = kept[i];
   }
   n = min(n, a.k);
-  if (threadIdx.x == 0) part.len = n;
+  Online o_block;
+  if (warp == kWarps - 1) o_block = join_stats(sh[lane % kWarps].x, sh[lane % kWarps].y);
   __syncthreads();
-  Online j;
-  int total = n, place = threadIdx.x;
-  const uint64_t mine = threadIdx.x < n ? top[threadIdx.x] : 0;
-  if (ranks == 1) {
-    j.join(part.m, part.z);
-  } else {
-    cluster_sync();
-    for (int i = threadIdx.x; i < ranks * a.k; i += kThreads)
-      others[i] = ld_cluster64(map_rank(smem_u32(top + i % a.k), uint32_t(i / a.k)));
-    if (threadIdx.x < ranks) {
-      const float4 p = ld_cluster4(map_rank(smem_u32(&part), threadIdx.x));
-      all[threadIdx.x] = {p.x, p.y, __float_as_int(p.z), 0};
+  int count = n;
+  uint64_t* lists = top;
+  if (ranks > 1) {
+    // to the first block: its `others` and `all`
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    for (int i = threadIdx.x; i < a.k; i += kThreads)
+      st_cluster64(map_rank(smem_u32(others + rank * a.k + i), 0), i < n ? top[i] : 0);
+    if (threadIdx.x == kThreads - 1) {
+      const uint32_t at = map_rank(smem_u32(&all[rank]), 0);
+      st_cluster64(at, pair(o_block.m, o_block.z));
+      st_cluster64(at + 8, uint64_t(n));
     }
-    cluster_sync();
-    total = 0;
-    for (int p = 0; p < ranks; ++p) {
-      j.join(all[p].m, all[p].z);
-      const int len = all[p].len;
-      total += len;
-      if (p == rank || threadIdx.x >= n) continue;
-      int lo = 0, hi = len;  // entries of that list above mine
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank > 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    lists = others;
+    count = 0;
+    for (int p = 0; p < ranks; ++p) count += all[p].len;
+    if (warp == kWarps - 1) {
+      const Part& p = all[lane % ranks];
+      o_block = join_stats(lane % kMaxCluster < ranks ? p.m : -INFINITY,
+                           lane % kMaxCluster < ranks ? p.z : 0.f);
+    }
+  }
+  for (int i = threadIdx.x; i < ranks * a.k; i += kThreads) {
+    const int mine = i / a.k, at = i - mine * a.k;
+    if (at >= (ranks > 1 ? all[mine].len : n)) continue;
+    const uint64_t e = lists[i];
+    int place = at;
+    if (ranks > 1 && ranks * a.k <= kThreads) {
+      // few: those above this one, counted (nothing is below every entry)
+      place = 0;
+#pragma unroll 4
+      for (int j = 0; j < ranks * a.k; ++j) place += lists[j] > e;
+    }
+    for (int p = 0; p < ranks && ranks * a.k > kThreads; ++p) {
+      if (p == mine) continue;
+      int lo = 0, hi = all[p].len;  // entries of that list above mine
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (others[p * a.k + mid] > mine)
+        if (lists[p * a.k + mid] > e)
           lo = mid + 1;
         else
           hi = mid;
       }
       place += lo;
     }
+    if (place < a.k) {
+      a.o.val[row * a.k + place] = key_to_float(uint32_t(e >> 32));
+      a.o.id[row * a.k + place] = int32_t(~uint32_t(e));
+    }
   }
-  if (threadIdx.x < n && place < a.k) {
-    a.o.val[row * a.k + place] = key_to_float(uint32_t(mine >> 32));
-    a.o.id[row * a.k + place] = int32_t(~uint32_t(mine));
-  }
-  if (rank == 0 && threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 1) {
+    const Online& j = o_block;
     // no softmax: only -inf, or a NaN or +inf among the scores
     const bool ok = j.z > 0.f && j.z < INFINITY;
-    a.o.len[row] = ok ? min(total, a.k) : 0;
+    a.o.len[row] = ok ? min(count, a.k) : 0;
     a.o.m[row] = j.m;
     // log Z from its exponent, exactly, and its mantissa in [3/4, 3/2), whose
     // logarithm in fp32 is off by 2^-25 at most
@@ -533,8 +560,12 @@ int launch_rows(SelectArgs a, cudaStream_t s) {
   a.shift = 0;
   while (ceil_div(steps, int64_t(1) << a.shift) > kMaxSteps) ++a.shift;
   const size_t smem = (size_t(kCap) + size_t(a.k) * (ranks == 1 ? 1 : 1 + ranks)) * 8;
-  auto kern = beam_rows_kernel<T>;
-  if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));
+  constexpr int N = Span<T>::N;
+  const bool vec = a.cols % N == 0 && a.lds % N == 0 &&
+                   reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
+  auto kern = vec ? beam_rows_kernel<T, true> : beam_rows_kernel<T, false>;
+  // 48 KB with the static part need no leave
+  if (smem > 36 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid_of(ranks, a.rows);
   cfg.blockDim = dim3(kThreads);
