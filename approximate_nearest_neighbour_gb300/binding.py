@@ -982,10 +982,9 @@ def beam_select(scores, totals, k, finished=None, end_id=0, stream=None):
         if finished.dtype is not _late["u8"] and finished.dtype is not _late["bool"]:
             raise TypeError(f"finished must be bool or uint8, got {finished.dtype}")
         fin = _array(finished, finished.dtype, (groups, beams), "finished", at)
-    shape = (groups, k)
-    out = empty(shape, dtype=f32, device=dev)
-    which = empty(shape, dtype=_late["i32"], device=dev)
-    ids = empty(shape, dtype=_late["i32"], device=dev)
+    # one allocation for the three
+    out, which, ids = empty((3, groups, k), dtype=_late["i32"], device=dev).unbind(0)
+    out = out.view(f32)
     rc = (_lib or lib()).beam_select(scores.data_ptr(), code, groups, beams, cols, lds, t, fin,
                                      end_id, k, out.data_ptr(), which.data_ptr(), ids.data_ptr(),
                                      _current(at))
@@ -994,11 +993,9 @@ def beam_select(scores, totals, k, finished=None, end_id=0, stream=None):
     return out, which, ids
 
 
-class _State(C.Structure):
-    """ivfpq_state of include/ivfpq.h."""
-    _fields_ = [("src", _VP), ("dst", _VP), ("src_row", _I64), ("dst_row", _I64),
-                ("outer", _I64), ("src_outer", _I64), ("dst_outer", _I64), ("inner", _I64),
-                ("unit", _I64)]
+# ivfpq_state of include/ivfpq.h as nine int64: src, dst, src_row, dst_row, outer,
+# src_outer, dst_outer, inner, unit
+_STATE = 9
 
 
 def _dense_tail(shape, stride):
@@ -1025,22 +1022,23 @@ def _segments(shape, stride, end, name):
     return n, step
 
 
-def _state(t, o, axis, groups, width, n, lengths, at, name):
-    """The ivfpq_state of tensor t written to o, positions along dimension axis."""
+def _state(t, o, axis, groups, width, n, lengths, at, index):
+    """The ivfpq_state (nine numbers) of tensor t written to o, positions along
+    dimension axis."""
     Tensor = _late["Tensor"]
     if not isinstance(t, Tensor) or not isinstance(o, Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+        raise TypeError(f"states[{index}] must be a torch tensor")
     if t.get_device() != at or o.get_device() != at or not t.is_cuda:
-        raise ValueError(f"{name} and its output must be on cuda:{at}")
+        raise ValueError(f"states[{index}] and its output must be on cuda:{at}")
     shape, so, size = t.shape, o.shape, t.element_size()
     dims = len(shape)
     if dims < 1 or shape[0] != groups * width:
-        raise ValueError(f"{name} must have {groups * width} rows, got shape {tuple(shape)}")
+        raise ValueError(f"states[{index}] must have {groups * width} rows, got shape {tuple(shape)}")
     if o is not t and (o.dtype != t.dtype or so[0] != groups * n or so[1:] != shape[1:]):
-        raise ValueError(f"the output of {name} must be {t.dtype} with {groups * n} rows of its "
+        raise ValueError(f"the output of states[{index}] must be {t.dtype} with {groups * n} rows of its "
                          f"shape, got {o.dtype} {tuple(so)}")
     if lengths and not 1 <= axis < dims:
-        raise ValueError(f"{name}: positions must be one of its dimensions 1 to {dims - 1}")
+        raise ValueError(f"states[{index}]: positions must be one of its dimensions 1 to {dims - 1}")
     st = t.stride()
     sto = st if o is t else o.stride()
     if lengths:
@@ -1053,23 +1051,23 @@ def _state(t, o, axis, groups, width, n, lengths, at, name):
         for v in shape[1:]:
             row *= v
         if not lengths:
-            return _State(t.data_ptr(), o.data_ptr(), row, row, 1, 0, 0, row, 0)
-        return _State(t.data_ptr(), o.data_ptr(), row, row, row // inner if inner else 0, inner,
+            return (t.data_ptr(), o.data_ptr(), row, row, 1, 0, 0, row, 0)
+        return (t.data_ptr(), o.data_ptr(), row, row, row // inner if inner else 0, inner,
                       inner, inner, unit)
     first = max(_dense_tail(shape, st), _dense_tail(shape, sto))
     if lengths:
         if first > axis:
-            raise ValueError(f"{name}: positions and what follows them must be dense")
+            raise ValueError(f"states[{index}]: positions and what follows them must be dense")
         first = axis
     else:
         unit, inner = 0, size
         for v in shape[first:]:
             inner *= v
-    outer, src_outer = _segments(shape, st, first, name)
-    _, dst_outer = _segments(shape, sto, first, name)
+    outer, src_outer = _segments(shape, st, first, f"states[{index}]")
+    _, dst_outer = _segments(shape, sto, first, f"states[{index}]")
     src_row = st[0] if shape[0] > 1 else 0
     dst_row = sto[0] if so[0] > 1 else 0
-    return _State(t.data_ptr(), o.data_ptr(), src_row * size, dst_row * size, outer,
+    return (t.data_ptr(), o.data_ptr(), src_row * size, dst_row * size, outer,
                   src_outer * size, dst_outer * size, inner, unit)
 
 
@@ -1117,14 +1115,15 @@ def beam_reorder(states, beams, lengths=None, axis=1, out=None, stream=None):
     width = rows // groups
     if out is None and width != n:
         raise ValueError(f"in place, {n} continuations need as many rows, not {width}")
-    array = (_State * len(src))()
+    numbers = []
     seen = set()
     for i, (t, o, d) in enumerate(zip(src, dst, axes)):
-        s = _state(t, o, d, groups, width, n, length is not None, at, f"states[{i}]")
-        if s.dst in seen and s.inner:
+        st = _state(t, o, d, groups, width, n, length is not None, at, i)
+        if st[1] in seen and st[7]:
             raise ValueError(f"states[{i}] is written twice")
-        seen.add(s.dst)
-        array[i] = s
+        seen.add(st[1])
+        numbers += st
+    array = (C.c_int64 * len(numbers))(*numbers)
     rc = (_lib or lib()).beam_reorder(array, len(src), b, groups, width, n, length, _current(at))
     if rc:
         _check("beam_reorder", rc)

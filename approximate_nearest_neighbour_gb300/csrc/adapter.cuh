@@ -22,12 +22,13 @@ struct AdapterArgs {
   int64_t ldb;
   void* out;
   int64_t ldo;
-  // the plan (null: every token is a tile)
-  int32_t* order;  // [tokens] tokens by adapter
-  int4* tiles;     // (adapter or -1, first slot, tokens, 0)
-  int32_t* ntiles;
-  int tile;     // tokens of a tile
-  float* h;     // [tokens, pitch], by slot
+  // tiles of tokens that share an adapter; h and order go by slot, a tile's one after
+  // the other
+  int32_t* order;   // a slot's token
+  int4* tiles;      // (adapter or -1, first slot, tokens, 0)
+  int32_t* ntiles;  // null: as many as there are blocks for, some of 0 tokens
+  int tile;     // most tokens of a tile
+  float* h;     // [slots, pitch]
   int splits;   // parts of K, one per block of a cluster
   int kpart;    // columns of a part, a multiple of 32
   int pitch;    // rank rounded up to whole instructions
@@ -38,17 +39,12 @@ struct Tile {
   int adapter, first, count;
 };
 __device__ __forceinline__ Tile tile_at(const AdapterArgs& a, int64_t i) {
-  if (a.tiles) {
-    if (i >= *a.ntiles) return {-1, 0, 0};
-    const int4 t = a.tiles[i];
-    return {t.x, t.y, t.z};
-  }
-  if (i >= a.tokens) return {-1, 0, 0};
-  const int id = a.ids[i];
-  return {id >= 0 && id < a.adapters ? id : -1, int(i), 1};
+  if (a.ntiles && i >= *a.ntiles) return {-1, 0, 0};
+  const int4 t = a.tiles[i];
+  return {t.x, t.y, t.z};
 }
 __device__ __forceinline__ int64_t token_of(const AdapterArgs& a, int slot) {
-  return a.order ? a.order[slot] : slot;
+  return a.order[slot];
 }
 
 // The next term of v as an element of T; what is left of it stays in v.

@@ -12,12 +12,12 @@
 // lane loads 16 consecutive bytes of a row and uses them as its part of two
 // instructions, and the columns of a result tile may be any 8, so that a lane's
 // results of four tiles are 8 neighbouring columns.
-//  1. Tokens are grouped by adapter into tiles (one block; left out where there
-//     are so few tokens that each is a tile). Order within a tile does not matter:
-//     a token's sums do not depend on its neighbours.
-//  2. h = x A^T: a block takes 16 or 32 tokens of a tile and a part of K, its warps
-//     parts of that; parts are added in shared memory, then by the readers, in
-//     fixed order.
+//  1. Tokens are grouped by adapter into tiles: by every block for itself up to 256
+//     tokens (tiles of 16), by a kernel of one block above (tiles of 128). Order
+//     within a tile does not matter: a token's sums do not depend on its neighbours.
+//  2. h = x A^T: a block takes a tile and a part of K, its warps parts of that; the
+//     warps' parts are added in shared memory, then the blocks', which are a
+//     cluster, in fixed order.
 //  3. out = base + scale h B^T: a block keeps the tile's h in shared memory and runs
 //     over columns. h is fp32: it is cut into two terms of the operands' type
 //     (three, if bf16 operands make an fp32 output), each exact to the next, so
@@ -136,21 +136,97 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 }
 
 // ---- h = x A^T ----------------------------------------------------------------------------
+constexpr int kFew = 256;  // tokens up to which every block finds its tile itself
+constexpr int kFewTile = 16;
+struct FewPlan {
+  int4 bin[kFew / 4];         // tokens' adapters, `adapters` for none
+  unsigned heads[kFew / 32];  // tokens that begin a tile
+  int token[kFewTile];
+  int first, rank, count;
+};
+// Tile `index` of the tokens: tiles are numbered by their first tokens, a token begins
+// one if the number of earlier tokens of its adapter is a multiple of kFewTile.
+__device__ __forceinline__ Tile few_tile(const AdapterArgs& a, int index, FewPlan& p) {
+  const int tokens = int(a.tokens), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int* bin = reinterpret_cast<int*>(p.bin);
+  constexpr int J = kFew / kThreads;
+  int mine[J], before[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int t = j * kThreads + threadIdx.x;
+    mine[j] = t < tokens ? a.ids[t] : -2;
+    if (t < tokens && (mine[j] < 0 || mine[j] >= a.adapters)) mine[j] = a.adapters;
+    if (t >= tokens) mine[j] = -2;
+    bin[t] = mine[j];
+    before[j] = 0;
+  }
+  if (threadIdx.x == 0) {
+    p.first = -1;
+    p.count = 0;
+  }
+  __syncthreads();
+  for (int i = 0; i < (tokens + 3) / 4; ++i) {
+    const int4 v = p.bin[i];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int t = j * kThreads + threadIdx.x - 4 * i;
+      before[j] += (v.x == mine[j] && t > 0) + (v.y == mine[j] && t > 1) +
+                   (v.z == mine[j] && t > 2) + (v.w == mine[j] && t > 3);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const unsigned h =
+        __ballot_sync(kFullMask, mine[j] != -2 && before[j] % kFewTile == 0);
+    if (lane == 0) p.heads[j * kWarps + warp] = h;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int w = j * kWarps + warp;
+    if (p.heads[w] >> lane & 1) {
+      int at = __popc(p.heads[w] & ((1u << lane) - 1u));
+      for (int i = 0; i < w; ++i) at += __popc(p.heads[i]);
+      if (at == index) {
+        p.first = mine[j];
+        p.rank = before[j];
+      }
+    }
+  }
+  __syncthreads();
+  const int of = p.first;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int at = before[j] - p.rank;
+    if (of >= 0 && mine[j] == of && at >= 0 && at < kFewTile) {
+      p.token[at] = j * kThreads + threadIdx.x;
+      atomicAdd(&p.count, 1);
+    }
+  }
+  __syncthreads();
+  return {of >= 0 && of < a.adapters ? of : -1, index * kFewTile, p.count};
+}
+
 template <class T, int NT>
 __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const AdapterArgs a) {
   constexpr int R = NT * 8;
   __shared__ __align__(16) float part[kWarps][16 * R];
+  __shared__ FewPlan plan;
   T* const type = nullptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
-  grid_wait();
   grid_go();
-  const Tile t = tile_at(a, blockIdx.y + int64_t(blockIdx.z) * gridDim.y);
-  if (t.count == 0 || t.adapter < 0) return;
+  const int index = int(blockIdx.y + int64_t(blockIdx.z) * gridDim.y);
+  const Tile t = few_tile(a, index, plan);
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) a.tiles[index] = make_int4(t.adapter, t.first, t.count, 0);
+    if (threadIdx.x < t.count) a.order[t.first + threadIdx.x] = plan.token[threadIdx.x];
+  }
+  if (t.count == 0 || t.adapter < 0) return;  // a cluster's blocks alike
   const T* x[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     x[e] = e * 8 + r < t.count
-               ? static_cast<const T*>(a.x) + token_of(a, t.first + e * 8 + r) * a.ldx
+               ? static_cast<const T*>(a.x) + int64_t(plan.token[e * 8 + r]) * a.ldx
                : nullptr;
   const T* w = static_cast<const T*>(a.a) + (int64_t(t.adapter) * a.rank + r) * a.cols;
   float acc[NT][4];
@@ -244,7 +320,8 @@ __device__ __forceinline__ void load_b(const T* p, int rank, int q, bool whole,
 }
 
 // VEC: base and output rows lie on 16-byte boundaries and are whole vectors.
-template <class T, class O, int KS, int TERMS, bool VEC>
+// ONE: tiles have at most 16 tokens.
+template <class T, class O, int KS, int TERMS, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterArgs a) {
   extern __shared__ __align__(16) uint4 expand_smem[];  // [m tiles, KS, TERMS, 32]
   __shared__ float up[kMaxTile];                        // a row's power of two
@@ -259,8 +336,25 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
   const O* base = static_cast<const O*>(a.base);
   O* out = static_cast<O*>(a.out);
   if (!some && base == out) return;  // in place: nothing changes
+  // B's first columns are asked for before h is looked at
+  const bool whole = a.rank % (KS == 1 ? 4 : 8) == 0 && misalign(a.b) == 0;
+  const T* b0 = some ? static_cast<const T*>(a.b) + int64_t(t.adapter) * a.n * a.rank : nullptr;
+  const int64_t cend = min(a.n, (int64_t(blockIdx.x) + 1) * a.run);
+  const int64_t c0 = int64_t(blockIdx.x) * a.run + warp * 32;
+  auto fetch_b = [&](int64_t at, uint32_t (&b)[4][KS][2]) {
+    if (!some) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = at + 8 * (r / 2) + 2 * j + (r & 1);
+      load_b<T, KS>(c < cend ? b0 + c * a.rank : nullptr, a.rank, q, whole, b[j]);
+    }
+  };
+  uint32_t bq[4][KS][2];
+  constexpr bool AHEAD = KS <= 2;  // the next columns' B as well, where it takes few registers
+  uint32_t bn[4][AHEAD ? KS : 1][2];
+  if constexpr (AHEAD) fetch_b(c0, bq);
   for (int i = threadIdx.x; i < t.count; i += kThreads) token[i] = token_of(a, t.first + i);
-  const int mtiles = (t.count + 15) / 16;
+  const int mtiles = ONE ? 1 : (t.count + 15) / 16;
   if (some) {
     const float scale = a.scales ? a.scales[t.adapter] : 1.f;
     for (int m = warp; m < mtiles; m += kWarps) {
@@ -315,23 +409,11 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
     }
   }
   __syncthreads();
-  const bool whole = a.rank % (KS == 1 ? 4 : 8) == 0 && misalign(a.b) == 0;
-  const T* b0 = some ? static_cast<const T*>(a.b) + int64_t(t.adapter) * a.n * a.rank : nullptr;
-  const int64_t cend = min(a.n, (int64_t(blockIdx.x) + 1) * a.run);
-  const int64_t c0 = int64_t(blockIdx.x) * a.run + warp * 32;
   if (c0 >= cend) return;
   const int items = int((cend - c0 + kWarps * 32 - 1) / (kWarps * 32)) * mtiles;
-  auto fetch_b = [&](int64_t at, uint32_t (&b)[4][KS][2]) {
-    if (!some) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = at + 8 * (r / 2) + 2 * j + (r & 1);
-      load_b<T, KS>(c < cend ? b0 + c * a.rank : nullptr, a.rank, q, whole, b[j]);
-    }
-  };
   // the base rows of the coming items, on their way
   constexpr int W = int(sizeof(O)) / 2;
-  constexpr int D = VEC ? (W == 1 ? 4 : 2) : 1;
+  constexpr int D = VEC ? 2 : 1;
   uint4 raw[D][2][W];
   int fm = 0;
   int64_t fc = c0;  // the next item to fetch
@@ -351,10 +433,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
       fc += kWarps * 32;
     }
   };
-  uint32_t bq[4][KS][2];
-  constexpr bool AHEAD = KS <= 2;  // the next columns' B as well, where it takes few registers
-  uint32_t bn[4][AHEAD ? KS : 1][2];
-  fetch_b(c0, bq);
+  if constexpr (!AHEAD) fetch_b(c0, bq);
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(raw[d]);
   int m = 0;
@@ -494,8 +573,8 @@ int launch(K kern, dim3 grid, int threads, size_t smem, const AdapterArgs& a, bo
 
 template <class T, int NT>
 int launch_shrink(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  return launch(adapter_shrink_kernel<T, NT>, grid_of(a.splits, tiles), kThreads, 0, a,
-                a.tiles != nullptr, a.splits, s);
+  return launch(adapter_shrink_kernel<T, NT>, grid_of(a.splits, tiles), kThreads, 0, a, false,
+                a.splits, s);
 }
 template <class T>
 int launch_shrink_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
@@ -508,25 +587,26 @@ int launch_shrink_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
   }
 }
 template <class T, class O, int KS>
-int launch_expand(const AdapterArgs& a, int64_t tiles, bool vec, cudaStream_t s) {
+int launch_expand(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
   constexpr int TERMS =
       std::is_same<T, __nv_bfloat16>::value && std::is_same<O, float>::value ? 3 : 2;
   const size_t smem = size_t((a.tile + 15) / 16) * KS * TERMS * 512;
   const dim3 grid = grid_of(ceil_div(a.n, a.run), tiles);
-  return vec ? launch(adapter_expand_kernel<T, O, KS, TERMS, true>, grid, kThreads, smem, a, true,
-                      1, s)
-             : launch(adapter_expand_kernel<T, O, KS, TERMS, false>, grid, kThreads, smem, a, true,
-                      1, s);
+  const bool vec = whole_rows<O>(a);
+  auto kern = a.tile > 16 ? (vec ? adapter_expand_kernel<T, O, KS, TERMS, true, false>
+                                 : adapter_expand_kernel<T, O, KS, TERMS, false, false>)
+                          : (vec ? adapter_expand_kernel<T, O, KS, TERMS, true, true>
+                                 : adapter_expand_kernel<T, O, KS, TERMS, false, true>);
+  return launch(kern, grid, kThreads, smem, a, true, 1, s);
 }
 template <class T, class O>
 int launch_expand_rank(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  const bool vec = whole_rows<O>(a);
   switch (a.pitch / 8) {
     case 1:
-    case 2: return launch_expand<T, O, 1>(a, tiles, vec, s);
-    case 4: return launch_expand<T, O, 2>(a, tiles, vec, s);
-    case 8: return launch_expand<T, O, 4>(a, tiles, vec, s);
-    default: return launch_expand<T, O, 8>(a, tiles, vec, s);
+    case 2: return launch_expand<T, O, 1>(a, tiles, s);
+    case 4: return launch_expand<T, O, 2>(a, tiles, s);
+    case 8: return launch_expand<T, O, 4>(a, tiles, s);
+    default: return launch_expand<T, O, 8>(a, tiles, s);
   }
 }
 template <class T>
@@ -592,32 +672,31 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   p.ldo = ldo;
   p.pitch = 8;
   while (p.pitch < rank) p.pitch *= 2;
-  const bool planned = tokens > 16;
-  p.tile = !planned ? 1 : tokens <= 256 ? 16 : kMaxTile;
-  const int64_t some = std::min<int64_t>(tokens, int64_t(adapters) + 1);
-  const int64_t tiles = planned ? tokens / p.tile + some : tokens;
-  const bool wide = p.tile == kMaxTile;
+  const bool wide = tokens > kFew;
+  p.tile = wide ? kMaxTile : kFewTile;
+  const int64_t tiles =
+      tokens / p.tile + std::min<int64_t>(tokens, int64_t(adapters) + 1);  // at most
   // parts of K until there are blocks for every SM, of some steps each
-  const int64_t items = wide ? ceil_div(tokens, kMaxTile) : tiles;
+  const int64_t items = wide ? 2 * ceil_div(tokens, kMaxTile) : ceil_div(tiles, 2);
   const int64_t least = wide ? 256 : 128;
   p.splits = 1;
-  while (p.splits < 8 && items * p.splits * (wide ? 2 : 1) < (wide ? 1 : 2) * num_sms() &&
-         cols > least * p.splits)
-    p.splits *= 2;
+  while (p.splits < 8 && items * p.splits < num_sms() && cols > least * p.splits) p.splits *= 2;
   p.kpart = int(ceil_div(ceil_div(cols, p.splits), 64) * 64);
-  // runs of columns, long where there are many tiles
+  // runs of columns, long where there are many tiles (77 tokens of 64 adapters, rank 16,
+  // 4096 x 16384: 21 us at this length, 23 to 25 us at twice and half of it)
   p.run = 128;
-  while (p.run < 1024 && ceil_div(n, p.run) * tiles > 8 * num_sms()) p.run *= 2;
+  while (p.run < 2048 && ceil_div(n, p.run) * tiles > 16 * num_sms()) p.run *= 2;
+  // the sums, and behind them the tiles
+  const int64_t slots = wide ? tokens : tiles * kFewTile;
+  const size_t h = size_t(slots) * size_t(p.pitch) / 4;
   Workspace ws(s);
-  // the sums, and behind them the plan
-  const size_t h = size_t(tokens) * size_t(p.pitch) / 4;
   float4* w = nullptr;
-  IVFPQ_TRY(ws.alloc(&w, h + (planned ? size_t(tiles) + size_t(ceil_div(tokens + 1, 4)) : 0)));
+  IVFPQ_TRY(ws.alloc(&w, h + size_t(tiles) + size_t(ceil_div(slots + 1, 4))));
   p.h = reinterpret_cast<float*>(w);
-  if (planned) {
-    p.tiles = reinterpret_cast<int4*>(w + h);
-    p.order = reinterpret_cast<int32_t*>(p.tiles + tiles);
-    p.ntiles = p.order + tokens;
+  p.tiles = reinterpret_cast<int4*>(w + h);
+  p.order = reinterpret_cast<int32_t*>(p.tiles + tiles);
+  if (wide) {
+    p.ntiles = p.order + slots;
     IVFPQ_TRY(launch(adapter_plan_kernel, dim3(1), kPlanThreads, size_t(adapters + 1) * 4, p, false,
                      1, s));
   }

@@ -45,7 +45,7 @@ def test_reorder_refusals(lib):
         f = dict(src=256, dst=512, src_row=64, dst_row=64, outer=1, src_outer=0, dst_outer=0,
                  inner=64, unit=0)
         f.update(kw)
-        a = (B._State * 1)(B._State(*f.values()))
+        a = (C.c_int64 * B._STATE)(*(v or 0 for v in f.values()))
         return lib.beam_reorder(a if states else None, count, beams, groups, width, n, lengths, None)
     _bad(lib, [lambda: call(n=0), lambda: call(n=65), lambda: call(width=0), lambda: call(width=65),
                lambda: call(groups=-1), lambda: call(groups=1 << 26), lambda: call(count=-1),
