@@ -21,6 +21,8 @@
 // What was measured at 8192 x 16384 bf16, rank 64: registers instead of shared memory (a
 // warp's 32 columns of 16 rows, fetched four steps ahead) 176 us; rows by bulk copies of
 // 256 bytes, which the copy engine takes one every 30 clocks or so, 250 us.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "adapter.cuh"
@@ -470,57 +472,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- h into A, then accumulators and base rows into output rows ----
     const int group = (warp - 2) / kGroupWarps, lg = warp & 3, row = 32 * lg + lane;
     const int e = threadIdx.x - 64;  // 0 .. kEpiThreads - 1
+    const bool works = group < C::GROUPS;
     // 32 rows of kRowBytes; the 16-byte pieces of row r are swapped around by r mod 8
-    uint8_t* mine = buf + (group < C::GROUPS ? (group * kGroupWarps + lg) * 32 * kRowBytes : 0);
+    uint8_t* mine = buf + (works ? (group * kGroupWarps + lg) * 32 * kRowBytes : 0);
     auto piece = [&](int r, int c) { return mine + r * kRowBytes + ((c ^ (r & 7)) * 16); };
     const O* base = static_cast<const O*>(a.base);
+    // copies: this lane has piece ch of rows sub, sub + 2, ..
     const int sub = lane >> 4, ch = lane & 15;
-    // this warp's rows of the coming unit of its group
+    uint8_t* copy = mine + sub * kRowBytes;
+    int swap[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) swap[j] = (ch ^ (2 * j + sub)) * 16;
+    const uint32_t base_pitch = uint32_t(a.ldb * int64_t(sizeof(O)));  // VEC: below 2^32
+    const uint32_t out_pitch = uint32_t(a.ldo * int64_t(sizeof(O)));
+    auto token_here = [&](const Segment& g) {
+      return g.units > 0 && row < g.tile.count ? uint32_t(token_of(a, g.tile.first + row)) : 0u;
+    };
+    // the coming unit of this group: segment, unit in it, and the token of this lane's row
     int64_t fu = u0;
-    int fit = 0, fk = 0;
-    Segment fg = next(fu);
-    int64_t ftok = 0;
-    auto seek = [&](Segment& g, int64_t& at, int& k, int& i) {
-      // to the next unit that is this group's
-      while (g.units > 0 && i % C::GROUPS != group) {
-        ++i;
-        if (++k == g.units) {
-          g = next(at);
-          k = 0;
+    Segment fg;
+    fg.units = 0;
+    int fk = works ? group : INT_MAX;
+    uint32_t ftok = 0;
+    auto settle = [&]() {  // fk may have passed the segment's end
+      while (works && fk >= fg.units) {
+        fk -= fg.units;
+        fg = next(fu);
+        if (fg.units == 0) {
+          fk = INT_MAX;
+          return;
         }
+        ftok = token_here(fg);
       }
     };
-    auto token_here = [&](const Segment& g) {
-      return g.units > 0 && row < g.tile.count ? token_of(a, g.tile.first + row) : int64_t(0);
-    };
     auto fetch = [&]() {
-      const int tile = fg.tile.first;
-      seek(fg, fu, fk, fit);
-      if (fg.units == 0) return;
-      if (fg.tile.first != tile || fit < C::GROUPS) ftok = token_here(fg);
-      if (VEC && base) {
+      settle();
+      if (VEC && base && works && fk != INT_MAX) {
         const int64_t chunk = fg.chunk + fk;
         const int bytes = row_bytes(chunk), nrows = fg.tile.count - 32 * lg;
-        const O* from = base + chunk * CN + ch * (16 / int(sizeof(O)));
+        const char* from = reinterpret_cast<const char*>(base + chunk * CN) + ch * 16;
+        const uint32_t to = smem_u32(copy);
+        if (nrows >= 32 && bytes == kRowBytes) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = 2 * i + sub;
-          const int64_t t = __shfl_sync(kFullMask, ftok, r);
-          if (r < nrows && ch * 16 < bytes)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(piece(r, ch))),
-                         "l"(from + t * a.ldb)
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t t = __shfl_sync(kFullMask, ftok, 2 * i + sub);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             to + 2 * i * kRowBytes + swap[i & 3]),
+                         "l"(from + uint64_t(t) * base_pitch)
                          : "memory");
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + sub;
+            const uint32_t t = __shfl_sync(kFullMask, ftok, r);
+            if (r < nrows && ch * 16 < bytes)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               smem_u32(piece(r, ch))),
+                           "l"(from + uint64_t(t) * base_pitch)
+                           : "memory");
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      ++fit;
-      if (++fk == fg.units) {
-        fg = next(fu);
-        fk = 0;
-        if (fg.units > 0) ftok = token_here(fg);
-      }
+      if (fk != INT_MAX) fk += C::GROUPS;
     };
-    if (group < C::GROUPS) fetch();
+    fetch();
     for (Segment g = next(u); g.units > 0; g = next(u)) {
       const bool some = g.tile.adapter >= 0;
       if (some) {
@@ -570,14 +587,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         named_barrier(1, kEpiThreads + 32);
       }
-      const int64_t tok = token_here(g);
+      const uint32_t tok = token_here(g);
       const int nrows = min(32, g.tile.count - 32 * lg);
       float f = 1.f;
       if constexpr (std::is_same<T, __half>::value)
         if (some) f = up[row];
-      for (int k = 0; k < g.units; ++k, ++it) {
-        if (it % C::GROUPS != group) continue;
-        const int ab = it % kGroups;
+      // this group's units of the segment: every GROUPS-th of all units
+      const int first = (group + C::GROUPS - it % C::GROUPS) % C::GROUPS;
+      for (int k = works ? first : g.units; k < g.units; k += C::GROUPS) {
+        const int ab = (it + k) % kGroups;
         const int64_t chunk = g.chunk + k;
         const int bytes = row_bytes(chunk);
         if constexpr (VEC) {
@@ -587,33 +605,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int N = Span<O>::N;
 #pragma unroll 8
           for (int i = 0; i < nrows; ++i) {
-            const O* q = base + __shfl_sync(kFullMask, tok, i) * a.ldb + chunk * CN;
+            const O* q = base + int64_t(__shfl_sync(kFullMask, tok, i)) * a.ldb + chunk * CN;
 #pragma unroll
             for (int c = lane; c < CN; c += 32)
               if (c < ncols) reinterpret_cast<O*>(piece(i, c / N))[c % N] = q[c];
           }
         }
-        wait(acc_full(ab), (it / kGroups) & 1);
+        wait(acc_full(ab), ((it + k) / kGroups) & 1);
         __syncwarp();
         tc_fence_after();
+        uint8_t* here = mine + lane * kRowBytes;
+        const int turn = (lane & 7) * 16;
 #pragma unroll
         for (int c = 0; c < CN; c += 32) {
           uint32_t d[32];
           if (some) {
             tmem_ld32_nowait(tmem + (uint32_t(32 * lg) << 16) + uint32_t(ab * CN + c), d);
             tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) d[x] = 0;
           }
           constexpr int N = Span<O>::N;
 #pragma unroll
           for (int q = 0; q < 32 / N; ++q) {
-            uint4* at = reinterpret_cast<uint4*>(piece(lane, c / N + q));
+            uint4* at = reinterpret_cast<uint4*>(here + (((c / N + q) * 16) ^ turn));
             float w[N];
 #pragma unroll
-            for (int x = 0; x < N; ++x) w[x] = 0.f;
-            if (base) unpack_vec<O>(*at, w);
-            if (some) {
+            for (int x = 0; x < N; ++x) w[x] = __uint_as_float(d[q * N + x]);
+            if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
-              for (int x = 0; x < N; ++x) w[x] = fmaf(__uint_as_float(d[q * N + x]), f, w[x]);
+              for (int x = 0; x < N; ++x) w[x] *= f;
+            }
+            if (base) {
+              float v[N];
+              unpack_vec<O>(*at, v);
+#pragma unroll
+              for (int x = 0; x < N; x += 2)
+                unpair(add2(pair(v[x], v[x + 1]), pair(w[x], w[x + 1])), w[x], w[x + 1]);
             }
             *at = pack_vec<O>(w);
           }
@@ -623,20 +652,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(acc_empty(ab));
         if (!__any_sync(kFullMask, *abort_flag)) {
           if constexpr (VEC) {
-            O* to = static_cast<O*>(a.out) + chunk * CN + ch * (16 / int(sizeof(O)));
+            char* to = reinterpret_cast<char*>(static_cast<O*>(a.out) + chunk * CN) + ch * 16;
+            if (nrows == 32 && bytes == kRowBytes) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = 2 * i + sub;
-              const int64_t t = __shfl_sync(kFullMask, tok, r);
-              const uint4 w = *reinterpret_cast<const uint4*>(piece(r, ch));
-              if (r < nrows && ch * 16 < bytes) *reinterpret_cast<uint4*>(to + t * a.ldo) = w;
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t t = __shfl_sync(kFullMask, tok, 2 * i + sub);
+                *reinterpret_cast<uint4*>(to + uint64_t(t) * out_pitch) =
+                    *reinterpret_cast<const uint4*>(copy + 2 * i * kRowBytes + swap[i & 3]);
+              }
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + sub;
+                const uint32_t t = __shfl_sync(kFullMask, tok, r);
+                if (r < nrows && ch * 16 < bytes)
+                  *reinterpret_cast<uint4*>(to + uint64_t(t) * out_pitch) =
+                      *reinterpret_cast<const uint4*>(piece(r, ch));
+              }
             }
           } else {
             const int ncols = bytes / int(sizeof(O));
             constexpr int N = Span<O>::N;
 #pragma unroll 8
             for (int i = 0; i < nrows; ++i) {
-              O* q = static_cast<O*>(a.out) + __shfl_sync(kFullMask, tok, i) * a.ldo + chunk * CN;
+              O* q = static_cast<O*>(a.out) + int64_t(__shfl_sync(kFullMask, tok, i)) * a.ldo +
+                     chunk * CN;
 #pragma unroll
               for (int c = lane; c < CN; c += 32)
                 if (c < ncols) q[c] = reinterpret_cast<const O*>(piece(i, c / N))[c % N];
@@ -646,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fetch();
       }
+      it += g.units;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
@@ -701,7 +742,9 @@ int launch(const AdapterArgs& a, cudaStream_t s) {
 }
 template <class T, class O>
 int launch_rank(const AdapterArgs& a, cudaStream_t s) {
-  if (whole_rows<O>(a))
+  // 32-bit row pitches in bytes for whole rows
+  const int64_t limit = (int64_t(1) << 32) / int64_t(sizeof(O));
+  if (whole_rows<O>(a) && a.ldb < limit && a.ldo < limit)
     return a.rank <= 64 ? launch<T, O, 1, true>(a, s) : launch<T, O, 2, true>(a, s);
   return a.rank <= 64 ? launch<T, O, 1, false>(a, s) : launch<T, O, 2, false>(a, s);
 }
