@@ -982,9 +982,10 @@ def beam_select(scores, totals, k, finished=None, end_id=0, stream=None):
         if finished.dtype is not _late["u8"] and finished.dtype is not _late["bool"]:
             raise TypeError(f"finished must be bool or uint8, got {finished.dtype}")
         fin = _array(finished, finished.dtype, (groups, beams), "finished", at)
-    # one allocation for the three
-    out, which, ids = empty((3, groups, k), dtype=_late["i32"], device=dev).unbind(0)
-    out = out.view(f32)
+    shape, i32 = (groups, k), _late["i32"]
+    out = empty(shape, dtype=f32, device=dev)
+    which = empty(shape, dtype=i32, device=dev)
+    ids = empty(shape, dtype=i32, device=dev)
     rc = (_lib or lib()).beam_select(scores.data_ptr(), code, groups, beams, cols, lds, t, fin,
                                      end_id, k, out.data_ptr(), which.data_ptr(), ids.data_ptr(),
                                      _current(at))

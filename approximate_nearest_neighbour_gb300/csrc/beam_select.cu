@@ -15,9 +15,11 @@
 //     thread, from L2, and their scores at or above it kept.
 //  3. The kept ones are ranked among themselves. Where a cluster of blocks shares a
 //     row, its first block gets the lists of the others and ranks all of them.
-//  4. A second kernel, already waiting, merges the beams' lists of a group, two
-//     at a time. Totals are compared in fp64: they differ by the rounding of
-//     their sums of exponentials, not of the comparison.
+//  4. Totals are compared in fp64: they differ by the rounding of their sums of
+//     exponentials, not of the comparison. Where few beams have few continuations, a
+//     cluster takes a whole group and its first block ranks the beams' lists too (one
+//     kernel, no workspace); else a second kernel, already waiting, merges the
+//     beams' lists of a group, two at a time.
 // Keys hold (score, inverted column), so that no step depends on the order in
 // which threads append and the lowest column of equal scores comes first.
 #include <algorithm>
@@ -32,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxGroup = 16;     // blocks of a cluster that takes a group
 constexpr int kUnroll = 4;         // vectors of a batch
 constexpr int kMaxSteps = 16;      // batches per thread whose maxima are kept apart
 constexpr int kSlack = 8;          // how many threads more than k the bound may let pass
@@ -57,6 +60,11 @@ struct SelectArgs {
   int32_t end_id;
   int k, chunk, shift;
   RowLists o;
+  // a cluster per group
+  int beams, ranks;
+  float* out_totals;  // [groups, k]
+  int32_t* out_beams;
+  int32_t* out_ids;
 };
 
 struct MergeArgs {
@@ -278,6 +286,15 @@ __device__ __forceinline__ void st_cluster64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+// fp64 totals as unsigned integers of the same order.
+__device__ __forceinline__ uint64_t total_key(double v) {
+  const uint64_t u = uint64_t(__double_as_longlong(v + 0.0));
+  return u ^ (uint64_t(int64_t(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_total(uint64_t k) {
+  return __longlong_as_double(int64_t(k ^ (uint64_t(int64_t(~k) >> 63) | 0x8000000000000000ull)));
+}
+
 // A block's statistics and the length of its list.
 struct alignas(16) Part {
   float m, z;
@@ -300,23 +317,94 @@ __device__ __forceinline__ Online join_stats(float m, float z) {
   return o;
 }
 
-template <class T, bool VEC>
+// log Z from its exponent, exactly, and its mantissa in [3/4, 3/2), whose logarithm in
+// fp32 is off by 2^-25 at most.
+__device__ __forceinline__ double log_sum(float z) {
+  const uint32_t u = __float_as_uint(z) - 0x3f400000u;
+  const int ex = int(u) >> 23;
+  const float f = __uint_as_float((u & 0x007fffffu) + 0x3f400000u);
+  return double(ex) * 0.69314718055994530942 + double(logf(f));
+}
+// No softmax: only -inf, or a NaN or +inf among the scores.
+__device__ __forceinline__ bool has_softmax(const Online& o) {
+  return o.z > 0.f && o.z < INFINITY;
+}
+
+// The lists of a group's blocks ([size, k], `ranks` of them per beam), ranked.
+__device__ void rank_group(const SelectArgs& a, int64_t group, int size, const uint64_t* lists,
+                           uint64_t* totals, const Part* all) {
+  __shared__ double base[kMaxGroup];  // t - log Z
+  __shared__ float top[kMaxGroup];
+  __shared__ int len[kMaxGroup];  // of each beam's list, 0 where it has no softmax
+  const int k = a.k;
+  if (threadIdx.x < a.beams) {
+    Online o;
+    int n = 0;
+    for (int p = threadIdx.x * a.ranks; p < int(threadIdx.x + 1) * a.ranks; ++p) {
+      o.join(all[p].m, all[p].z);
+      n += all[p].len;
+    }
+    const bool ok = has_softmax(o);
+    top[threadIdx.x] = o.m;
+    base[threadIdx.x] = ok ? double(a.totals[group * a.beams + threadIdx.x]) - log_sum(o.z) : 0.0;
+    len[threadIdx.x] = ok ? n : 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < size * k; i += kThreads) {
+    const int p = i / k, b = p / a.ranks;
+    const bool ok = len[b] > 0 && i - p * k < all[p].len;
+    const double d = double(key_to_float(uint32_t(lists[i] >> 32))) - double(top[b]);
+    totals[i] = ok ? total_key(d + base[b]) : 0;  // 0 is below every total
+  }
+  __syncthreads();
+  int n = 0;
+  for (int b = 0; b < a.beams; ++b) n += len[b];
+  for (int i = threadIdx.x; i < size * k; i += kThreads) {
+    const uint64_t mine = totals[i], e = lists[i];
+    if (mine == 0) continue;
+    const int beam = i / k / a.ranks;
+    int place = 0;
+    for (int p = 0; p < size; ++p) {
+      const int b = p / a.ranks;
+      // a beam's own entries by score; of equal totals the lower beam's come first
+      const uint64_t* of = (b == beam ? lists : totals) + p * k;
+      const uint64_t than = b == beam ? e : mine - (b < beam);
+#pragma unroll 4
+      for (int j = 0; j < k; ++j) place += of[j] > than;
+    }
+    if (place < k) {
+      a.out_totals[group * k + place] = float(key_total(mine));
+      a.out_beams[group * k + place] = beam;
+      a.out_ids[group * k + place] = int32_t(~uint32_t(e));
+    }
+  }
+  for (int i = n + threadIdx.x; i < k; i += kThreads) {
+    a.out_totals[group * k + i] = -INFINITY;
+    a.out_beams[group * k + i] = -1;
+    a.out_ids[group * k + i] = -1;
+  }
+}
+
+// GROUP: a cluster takes a group, else a row.
+template <class T, bool VEC, bool GROUP>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs a) {
   constexpr int N = Span<T>::N;
   extern __shared__ __align__(16) uint64_t select_smem[];
   uint64_t* kept = select_smem;  // [kCap]
   uint64_t* top = kept + kCap;   // [k]
-  uint64_t* others = top + a.k;  // [ranks, k] where a row has several blocks
+  uint64_t* others = top + a.k;  // [blocks, k] where a cluster has several
   // the peaks (one array with `kept`, which is filled when they have been read)
   uint32_t* peak = reinterpret_cast<uint32_t*>(select_smem);
   __shared__ uint16_t chosen[kMaxSteps * kThreads];
   __shared__ float2 sh[kWarps];
-  __shared__ Part all[kMaxCluster];  // in the first block of a cluster: of all its blocks
+  __shared__ Part all[kMaxGroup];  // in the first block of a cluster: of all its blocks
   __shared__ int nkept, nchosen;
   __shared__ uint32_t keys[kThreads];
-  const int ranks = int(gridDim.x), rank = int(blockIdx.x);
-  const int64_t row = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
-  if (row >= a.rows) return;
+  const int size = int(gridDim.x), block = int(blockIdx.x);  // of the cluster
+  const int ranks = GROUP ? a.ranks : size, rank = GROUP ? block % ranks : block;
+  const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  const int64_t row = GROUP ? item * a.beams + block / ranks : item;
+  if (item >= (GROUP ? a.rows / a.beams : a.rows)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float t = a.totals[row];
   const bool done = a.finished && a.finished[row];
@@ -327,105 +415,114 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
   load_batch(run, 0, r);  // on its way while the total is
   if (threadIdx.x == 0) nkept = nchosen = 0;
   // the blocks of a cluster must have started before one writes to another
-  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const bool alive = fabsf(t) < INFINITY;  // neither infinite nor NaN
+  int n = 0;
+  Online o_block;  // in the last warp
   if (!alive || done) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.o.len[row] = alive ? 1 : 0;
-      a.o.val[row * a.k] = 0.f;
-      a.o.id[row * a.k] = a.end_id;
-      a.o.m[row] = 0.f;
-      a.o.base[row] = double(t);
-    }
-    if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    return;
-  }
-  const int steps = (run.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
-  const int groups = (steps + (1 << a.shift) - 1) >> a.shift;
-  Online o;
-  run_stats(run, steps, a.shift, r, peak, o);
-  grid_go();
-  keys[threadIdx.x] = score_key(o.m);
-  // the block's statistics
-  {
-    const float m = key_to_float(__reduce_max_sync(kFullMask, score_key(o.m)));
-    float z = o.z * exp2_fast(m == -INFINITY ? 0.f : (o.m - m) * kLog2e);
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(kFullMask, z, d);
-    if (lane == 0) sh[warp] = make_float2(m, z);
-  }
-  __syncthreads();
-  const uint32_t bound = kth_bound(keys, a.k);
-  // the batches that reach the bound
-  if (score_key(o.m) >= bound) {
-    for (int g = 0; g < groups; ++g)
-      if (peak[g * kThreads + threadIdx.x] >= bound)
-        chosen[atomicAdd(&nchosen, 1)] = uint16_t(g * kThreads + threadIdx.x);
-  }
-  __syncthreads();  // also: the peaks are read
-  const int per = kUnroll << a.shift, nread = nchosen * per;  // vectors
-  uint64_t bar = uint64_t(bound) << 32;
-  // the same as a score; -inf (and what lies past the end) is no continuation
-  const float least = fmaxf(key_to_float(bound), -3.402823466e38f);
-  for (int v0 = 0; v0 < nread; v0 += kThreads) {
-    const int q = v0 + threadIdx.x;
-    if (q < nread) {
-      const int b = chosen[q / per], e = q % per;
-      const int i = ((b / kThreads) * per + e) * kThreads + b % kThreads;
-      const uint4 w = run.at(i);
-      float v[N];
-      unpack_vec<T>(w, v);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (v[j] >= least) {
-          const uint64_t x = entry(score_key(v[j]), uint32_t(c0) + uint32_t(i * N + j));
-          if (x >= bar) kept[atomicAdd(&nkept, 1)] = x;
-        }
-      }
-    }
-    __syncthreads();
-    const int n = nkept;
-    if (n > kCap - kRound) {
-      sort_entries(kept, n);
-      bar = kept[a.k - 1];
-      if (threadIdx.x == 0) nkept = a.k;
-      __syncthreads();
-    } else if (v0 + kThreads < nread) {
-      __syncthreads();  // n is read before the next round adds to it
-    }
-  }
-  int n = nkept;
-  if (n <= kThreads) {
-    if (threadIdx.x < n) {
-      const uint64_t e = kept[threadIdx.x];
-      int above = 0;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) above += kept[i] > e;
-      if (above < a.k) top[above] = e;
+    // nothing, or the one continuation of a finished beam: its own total
+    if (alive && rank == 0) {
+      n = 1;
+      o_block.m = 0.f;
+      o_block.z = 1.f;
+      if (threadIdx.x == 0) top[0] = entry(score_key(0.f), uint32_t(a.end_id));
     }
   } else {
-    sort_entries(kept, n);
-    for (int i = threadIdx.x; i < min(n, a.k); i += kThreads) top[i] = kept[i];
+    const int steps = (run.nvec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+    const int groups = (steps + (1 << a.shift) - 1) >> a.shift;
+    Online o;
+    run_stats(run, steps, a.shift, r, peak, o);
+    if (!GROUP) grid_go();
+    keys[threadIdx.x] = score_key(o.m);
+    // the block's statistics
+    {
+      const float m = key_to_float(__reduce_max_sync(kFullMask, score_key(o.m)));
+      float z = o.z * exp2_fast(m == -INFINITY ? 0.f : (o.m - m) * kLog2e);
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(kFullMask, z, d);
+      if (lane == 0) sh[warp] = make_float2(m, z);
+    }
+    __syncthreads();
+    const uint32_t bound = kth_bound(keys, a.k);
+    // the batches that reach the bound
+    if (score_key(o.m) >= bound) {
+      for (int g = 0; g < groups; ++g)
+        if (peak[g * kThreads + threadIdx.x] >= bound)
+          chosen[atomicAdd(&nchosen, 1)] = uint16_t(g * kThreads + threadIdx.x);
+    }
+    __syncthreads();  // also: the peaks are read
+    const int per = kUnroll << a.shift, nread = nchosen * per;  // vectors
+    uint64_t bar = uint64_t(bound) << 32;
+    // the same as a score; -inf (and what lies past the end) is no continuation
+    const float least = fmaxf(key_to_float(bound), -3.402823466e38f);
+    for (int v0 = 0; v0 < nread; v0 += kThreads) {
+      const int q = v0 + threadIdx.x;
+      if (q < nread) {
+        const int b = chosen[q / per], e = q % per;
+        const int i = ((b / kThreads) * per + e) * kThreads + b % kThreads;
+        const uint4 w = run.at(i);
+        float v[N];
+        unpack_vec<T>(w, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (v[j] >= least) {
+            const uint64_t x = entry(score_key(v[j]), uint32_t(c0) + uint32_t(i * N + j));
+            if (x >= bar) kept[atomicAdd(&nkept, 1)] = x;
+          }
+        }
+      }
+      __syncthreads();
+      const int n = nkept;
+      if (n > kCap - kRound) {
+        sort_entries(kept, n);
+        bar = kept[a.k - 1];
+        if (threadIdx.x == 0) nkept = a.k;
+        __syncthreads();
+      } else if (v0 + kThreads < nread) {
+        __syncthreads();  // n is read before the next round adds to it
+      }
+    }
+    n = nkept;
+    if (n <= kThreads) {
+      if (threadIdx.x < n) {
+        const uint64_t e = kept[threadIdx.x];
+        int above = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) above += kept[i] > e;
+        if (above < a.k) top[above] = e;
+      }
+    } else {
+      sort_entries(kept, n);
+      for (int i = threadIdx.x; i < min(n, a.k); i += kThreads) top[i] = kept[i];
+    }
+    n = min(n, a.k);
+    if (warp == kWarps - 1) o_block = join_stats(sh[lane % kWarps].x, sh[lane % kWarps].y);
   }
-  n = min(n, a.k);
-  Online o_block;
-  if (warp == kWarps - 1) o_block = join_stats(sh[lane % kWarps].x, sh[lane % kWarps].y);
   __syncthreads();
   int count = n;
   uint64_t* lists = top;
-  if (ranks > 1) {
+  if (size > 1 || GROUP) {
     // to the first block: its `others` and `all`
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (size > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     for (int i = threadIdx.x; i < a.k; i += kThreads)
-      st_cluster64(map_rank(smem_u32(others + rank * a.k + i), 0), i < n ? top[i] : 0);
+      st_cluster64(map_rank(smem_u32(others + block * a.k + i), 0), i < n ? top[i] : 0);
     if (threadIdx.x == kThreads - 1) {
-      const uint32_t at = map_rank(smem_u32(&all[rank]), 0);
+      const uint32_t at = map_rank(smem_u32(&all[block]), 0);
       st_cluster64(at, pair(o_block.m, o_block.z));
       st_cluster64(at + 8, uint64_t(n));
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (rank > 0) return;
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (size > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      if (block > 0) return;
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+    if constexpr (GROUP) {
+      // the totals take the place of the scores that were kept
+      rank_group(a, item, size, others, kept, all);
+      return;
+    }
     lists = others;
     count = 0;
     for (int p = 0; p < ranks; ++p) count += all[p].len;
@@ -464,27 +561,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
     }
   }
   if (threadIdx.x == kThreads - 1) {
-    const Online& j = o_block;
-    // no softmax: only -inf, or a NaN or +inf among the scores
-    const bool ok = j.z > 0.f && j.z < INFINITY;
+    const bool ok = has_softmax(o_block);
     a.o.len[row] = ok ? min(count, a.k) : 0;
-    a.o.m[row] = j.m;
-    // log Z from its exponent, exactly, and its mantissa in [3/4, 3/2), whose
-    // logarithm in fp32 is off by 2^-25 at most
-    const uint32_t u = __float_as_uint(j.z) - 0x3f400000u;
-    const int ex = int(u) >> 23;
-    const float f = __uint_as_float((u & 0x007fffffu) + 0x3f400000u);
-    a.o.base[row] = double(t) - (double(ex) * 0.69314718055994530942 + double(logf(f)));
+    a.o.m[row] = o_block.m;
+    a.o.base[row] = ok ? double(t) - log_sum(o_block.z) : 0.0;
   }
-}
-
-// fp64 totals as unsigned integers of the same order.
-__device__ __forceinline__ uint64_t total_key(double v) {
-  const uint64_t u = uint64_t(__double_as_longlong(v + 0.0));
-  return u ^ (uint64_t(int64_t(u) >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ double key_total(uint64_t k) {
-  return __longlong_as_double(int64_t(k ^ (uint64_t(int64_t(~k) >> 63) | 0x8000000000000000ull)));
 }
 
 // One block per group: the beams' lists merged two neighbours at a time; of equal
@@ -548,32 +629,49 @@ dim3 grid_of(int64_t per_row, int64_t rows) {
   return dim3(unsigned(per_row), unsigned(y), unsigned(ceil_div(rows, y)));
 }
 
-template <class T>
-int launch_rows(SelectArgs a, cudaStream_t s) {
-  // more blocks per row while the rows alone do not fill the device twice, down
-  // to runs of 4,096 columns
+// More blocks per row while the rows alone do not fill the device twice, down to runs
+// of 4,096 columns; at most `most`.
+int ranks_for(int64_t rows, int64_t cols, int most) {
   int ranks = 1;
-  while (ranks < kMaxCluster && a.rows * ranks < 2 * num_sms() && a.cols > 4096 * int64_t(ranks))
+  while (2 * ranks <= most && rows * ranks < 2 * num_sms() && cols > 4096 * int64_t(ranks))
     ranks *= 2;
+  return ranks;
+}
+// Whether a cluster per group does: few entries to rank against each other, and runs
+// that are as long as they would be otherwise or of 16,384 columns at most.
+bool group_fits(const SelectArgs& a, int* ranks) {
+  if (a.beams > kMaxGroup) return false;
+  *ranks = ranks_for(a.rows, a.cols, kMaxGroup / a.beams);
+  return a.beams * *ranks * a.k <= kThreads &&
+         (*ranks == ranks_for(a.rows, a.cols, kMaxCluster) || a.cols <= 16384 * int64_t(*ranks));
+}
+
+template <class T, bool GROUP>
+int launch_rows(SelectArgs a, int ranks, cudaStream_t s) {
+  a.ranks = ranks;
   a.chunk = int(ceil_div(ceil_div(a.cols, ranks), 8) * 8);
   const int64_t steps = ceil_div(a.chunk, int64_t(kThreads) * kUnroll * Span<T>::N);
   a.shift = 0;
   while (ceil_div(steps, int64_t(1) << a.shift) > kMaxSteps) ++a.shift;
-  const size_t smem = (size_t(kCap) + size_t(a.k) * (ranks == 1 ? 1 : 1 + ranks)) * 8;
+  const int size = GROUP ? a.beams * ranks : ranks;
+  const size_t smem = (size_t(kCap) + size_t(a.k) * (size == 1 && !GROUP ? 1 : 1 + size)) * 8;
   constexpr int N = Span<T>::N;
   const bool vec = a.cols % N == 0 && a.lds % N == 0 &&
                    reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
-  auto kern = vec ? beam_rows_kernel<T, true> : beam_rows_kernel<T, false>;
+  auto kern = vec ? beam_rows_kernel<T, true, GROUP> : beam_rows_kernel<T, false, GROUP>;
   // 48 KB with the static part need no leave
   if (smem > 36 * 1024) IVFPQ_TRY(set_dynamic_smem(kern, smem));
+  if (size > kMaxCluster)
+    IVFPQ_CUDA(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid_of(ranks, a.rows);
+  cfg.gridDim = grid_of(size, GROUP ? a.rows / a.beams : a.rows);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(ranks);
+  at[0].val.clusterDim.x = unsigned(size);
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
@@ -629,8 +727,15 @@ extern "C" int beam_select(const void* scores, int dtype, int64_t groups, int be
                 "beam_select: end_id=%d outside [0, %lld)", end_id, (long long)cols);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = groups * beams;
+  SelectArgs a{scores, rows, cols, lds, totals, finished, end_id, k, 0, 0, {}, beams, 1, out_totals,
+               out_beams, out_ids};
+  int ranks = 0;
+  if (group_fits(a, &ranks))
+    return by_dtype(dtype, [&](auto* t) -> int {
+      return launch_rows<std::remove_pointer_t<decltype(t)>, true>(a, ranks, s);
+    });
   Workspace ws(s);
-  RowLists o{};
+  RowLists& o = a.o;
   // one buffer: base, val, id, len, m
   double* w = nullptr;
   const size_t words = size_t(rows) * (size_t(k) * 2 + 2);
@@ -640,9 +745,9 @@ extern "C" int beam_select(const void* scores, int dtype, int64_t groups, int be
   o.id = reinterpret_cast<int32_t*>(o.val + rows * k);
   o.len = o.id + rows * k;
   o.m = reinterpret_cast<float*>(o.len + rows);
-  SelectArgs a{scores, rows, cols, lds, totals, finished, end_id, k, 0, 0, o};
+  ranks = ranks_for(rows, cols, kMaxCluster);
   IVFPQ_TRY(by_dtype(dtype, [&](auto* t) -> int {
-    return launch_rows<std::remove_pointer_t<decltype(t)>>(a, s);
+    return launch_rows<std::remove_pointer_t<decltype(t)>, false>(a, ranks, s);
   }));
   return launch_merge({o, groups, beams, k, out_totals, out_beams, out_ids}, s);
 }

@@ -316,3 +316,14 @@ def test_reorder_refusals_of_the_binding(B):
             pytest.fail(f"case {i} was taken")
     with pytest.raises(TypeError):
         B.beam_reorder(t, beams.long())
+
+
+@pytest.mark.parametrize("beams", range(1, 18))
+def test_every_number_of_beams(B, beams):
+    """A cluster per group up to 16 beams with few continuations, and both ways of ranking."""
+    for groups, cols, k in ((3, 20_000, 3), (2, 5000, 16), (40, 700, 2 * beams)):
+        r = np.random.default_rng(beams)
+        t = -np.abs(r.standard_normal((groups, beams)) * 2).astype(np.float32)
+        t[0, beams // 2] = -np.inf
+        f = (r.random((groups, beams)) < 0.2).astype(np.uint8)
+        _select(B, _scores(groups * beams, cols, "bf16", beams + cols), t, min(k, 128), f, 5)
