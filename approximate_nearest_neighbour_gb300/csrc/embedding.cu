@@ -19,6 +19,8 @@
 //     is many slabs' work, not one block's) leaves a partial sum in every slab.
 //     Further blocks zero the rows without a token.
 //  3. The partial sums of a frequent token are added in slab order.
+// Up to 256 positions one kernel does all of it, without workspace: a block finds the
+// positions of its class, sorts them by rank, and a warp adds each token's rows.
 #include <algorithm>
 
 #include "internal.h"
@@ -625,6 +627,134 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinParts) embedding_join_kerne
   }
 }
 
+// Whether rows of grad and out are whole vectors on 16-byte boundaries.
+template <class T, class O>
+bool whole_vectors(const SumArgs& a) {
+  return a.cols % Span<T>::N == 0 && a.ldg % Span<T>::N == 0 && a.ldo % Span<O>::N == 0 &&
+         reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+}
+
+// ---- gradient of few positions -------------------------------------------------------
+constexpr int kFew = 256;
+constexpr int kFewThreads = 512;
+constexpr int kFewShift = 8;  // 256 classes, one per block
+constexpr int kFewLocal = (1 << 24) >> kFewShift;
+
+struct FewArgs {
+  SumArgs sum;
+  const void* ids;
+  int wide;
+  int64_t padding;
+};
+
+template <class T, class O, bool VEC>
+__global__ void __launch_bounds__(kFewThreads) embedding_few_kernel(const FewArgs f) {
+  constexpr int N = Span<T>::N, U = 8;
+  const SumArgs& a = f.sum;
+  __shared__ int32_t token[kFew], pos[kFew];    // the class's, by position
+  __shared__ int32_t stoken[kFew], spos[kFew];  // sorted by token
+  __shared__ int starts[kFew + 1];              // where tokens begin there
+  __shared__ uint32_t there[kFewLocal / 32];    // tokens of the class that occur
+  __shared__ int found[kFew / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t c = blockIdx.x, mask = (1u << kFewShift) - 1;
+  const int local = int((a.rows - c + mask) >> kFewShift);  // rows of the class
+  // the number of flagged threads before this one among the first kFew; n: of all
+  auto compact = [&](bool flag, int& n) {
+    const unsigned b = __ballot_sync(kFullMask, flag);
+    __syncthreads();
+    if (lane == 0 && warp < kFew / 32) found[warp] = __popc(b);
+    __syncthreads();
+    int at = __popc(b & ((1u << lane) - 1u));
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kFew / 32; ++w) {
+      if (w < warp) at += found[w];
+      n += found[w];
+    }
+    return at;
+  };
+  const int t = threadIdx.x;
+  int64_t id = -1;
+  if (t < a.tokens) id = id_at(f.ids, f.wide, t);
+  for (int i = t; i < (local + 31) / 32; i += kFewThreads) there[i] = 0;
+  const bool mine = t < a.tokens && id >= 0 && id < a.rows && id != f.padding &&
+                    (uint32_t(id) & mask) == c;
+  int n;
+  const int at = compact(mine, n);
+  if (mine) {
+    token[at] = int32_t(id);
+    pos[at] = t;
+    const uint32_t l = uint32_t(id) >> kFewShift;
+    atomicOr(&there[l >> 5], 1u << (l & 31));
+  }
+  __syncthreads();
+  if (t < n) {
+    const int32_t v = token[t];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += token[j] < v || (token[j] == v && j < t);
+    stoken[rank] = v;
+    spos[rank] = pos[t];
+  }
+  __syncthreads();
+  int segments;
+  const bool begins = t < n && (t == 0 || stoken[t - 1] != stoken[t]);
+  const int s_at = compact(begins, segments);
+  if (begins) starts[s_at] = t;
+  if (t == 0) starts[segments] = n;
+  __syncthreads();
+  const int nvec = int((a.cols + N - 1) / N), runs = (nvec + 31) / 32;
+  const T* grad = static_cast<const T*>(a.grad);
+  for (int i = warp; i < segments * runs; i += kFewThreads / 32) {
+    const int g = i / runs, cv = (i - g * runs) * 32 + lane;
+    if (cv >= nvec) continue;
+    float s[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = 0.f;
+    const int end = starts[g + 1];
+    for (int b = starts[g]; b < end; b += U) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b + u < end) {
+          const T* p = grad + spos[b + u] * a.ldg;
+          if constexpr (VEC)
+            r[u] = reinterpret_cast<const uint4*>(p)[cv];
+          else
+            r[u] = load_vec(p, int(a.cols), cv, misalign(p));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b + u < end) {
+          float v[N];
+          unpack_vec<T>(r[u], v);
+#pragma unroll
+          for (int j = 0; j < N; ++j) s[j] += v[j];
+        }
+      }
+    }
+    write_row<T, O, VEC>(a, stoken[starts[g]], cv, s);
+  }
+  if (a.accumulate) return;
+  for (int l = warp; l < local; l += kFewThreads / 32)
+    if (!(there[l >> 5] >> (l & 31) & 1))
+      zero_row(static_cast<O*>(a.out) + ((int64_t(l) << kFewShift) + c) * a.ldo, int(a.cols), lane,
+               32);
+}
+
+template <class T, class O>
+int launch_few(const FewArgs& f, cudaStream_t s) {
+  const unsigned blocks = unsigned(std::min<int64_t>(f.sum.rows, int64_t(1) << kFewShift));
+  if (whole_vectors<T, O>(f.sum))
+    embedding_few_kernel<T, O, true><<<blocks, kFewThreads, 0, s>>>(f);
+  else
+    embedding_few_kernel<T, O, false><<<blocks, kFewThreads, 0, s>>>(f);
+  IVFPQ_LAUNCHED();
+  return IVFPQ_OK;
+}
+
 template <class K, class A>
 int launch_after(K kern, dim3 grid, dim3 threads, const A& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
@@ -648,12 +778,9 @@ int launch_sums(const SumArgs& a, int classes, cudaStream_t s) {
   while (threads < 128 && threads < nvec) threads *= 2;
   const int64_t runs = ceil_div(nvec, threads);
   const int64_t zero = a.accumulate ? 0 : ceil_div(a.rows, kZeroRows);
-  const bool vec = a.cols % Span<T>::N == 0 && a.ldg % Span<T>::N == 0 &&
-                   a.ldo % Span<O>::N == 0 && reinterpret_cast<uintptr_t>(a.grad) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  const bool vec = whole_vectors<T, O>(a);
   IVFPQ_TRY(launch_after(vec ? embedding_sum_kernel<T, O, true> : embedding_sum_kernel<T, O, false>,
                          grid_of(runs, a.slabs + zero), dim3(unsigned(threads)), a, s));
-  if (a.slabs <= 1) return IVFPQ_OK;
   return launch_after(embedding_join_kernel<O>,
                       dim3(unsigned(ceil_div(a.cols, 4 * kJoinThreads)), unsigned(classes)),
                       dim3(kJoinThreads, kJoinParts), a, s);
@@ -713,16 +840,6 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   if (rows == 0 || cols == 0 || (tokens == 0 && accumulate)) return IVFPQ_OK;
   IVFPQ_REQUIRE(out && ((ids && grad) || tokens == 0), "embedding_gradient: null pointer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool wide = ids_bytes == 8;
-  SortArgs o{};
-  o.ids = ids;
-  o.tokens = tokens;
-  o.rows = uint32_t(rows);
-  o.padding = padding >= 0 && padding < rows ? uint32_t(padding) : kNone;
-  // a block per SM or nearly, and more where a class would have too many tokens
-  o.shift = 7;
-  while (ceil_div(rows, int64_t(1) << o.shift) > kMaxLocal) ++o.shift;
-  o.local = int(ceil_div(rows, int64_t(1) << o.shift));
   SumArgs a{};
   a.grad = grad;
   a.cols = cols;
@@ -733,6 +850,23 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.accumulate = accumulate != 0;
   a.out = out;
   a.ldo = ldo;
+  const bool wide = ids_bytes == 8;
+  if (tokens <= kFew) {
+    const FewArgs f{a, ids, wide, padding};
+    return by_dtype(dtype, [&](auto* t) -> int {
+      using T = std::remove_pointer_t<decltype(t)>;
+      return out_dtype == dtype ? launch_few<T, T>(f, s) : launch_few<T, float>(f, s);
+    });
+  }
+  SortArgs o{};
+  o.ids = ids;
+  o.tokens = tokens;
+  o.rows = uint32_t(rows);
+  o.padding = padding >= 0 && padding < rows ? uint32_t(padding) : kNone;
+  // a block per SM or nearly, and more where a class would have too many tokens
+  o.shift = 7;
+  while (ceil_div(rows, int64_t(1) << o.shift) > kMaxLocal) ++o.shift;
+  o.local = int(ceil_div(rows, int64_t(1) << o.shift));
   // short slabs while they are few: a block takes its positions one after the other
   a.slab = 8;
   while (a.slab < kMaxSlab && tokens > int64_t(a.slab) * 512) a.slab *= 2;
@@ -740,7 +874,7 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.pitch = ceil_div(cols, 8) * 8;
   Workspace ws(s);
   // the slabs' partial sums, the frequent tokens and the sorted positions
-  const size_t parts = a.slabs > 1 ? size_t(a.slabs) * 2 * size_t(a.pitch) : 0;
+  const size_t parts = size_t(a.slabs) * 2 * size_t(a.pitch);
   const size_t frequent = size_t(tokens / (a.slab + 1) + 1), classes = size_t(1) << o.shift;
   const size_t words = size_t(tokens) * 5 + size_t(rows) + 1;
   int4* w = nullptr;
