@@ -672,7 +672,9 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   p.ldo = ldo;
   p.pitch = 8;
   while (p.pitch < rank) p.pitch *= 2;
-  const bool wide = tokens > kFew;
+  // tiles of 128 tokens also where few adapters of a high rank have many each: a tile of
+  // 16 reads its adapter's B again
+  const bool wide = tokens > kFew || (rank > 32 && tokens >= 64 && tokens >= 32 * int64_t(adapters));
   p.tile = wide ? kMaxTile : kFewTile;
   const int64_t tiles =
       tokens / p.tile + std::min<int64_t>(tokens, int64_t(adapters) + 1);  // at most

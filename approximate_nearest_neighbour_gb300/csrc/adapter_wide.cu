@@ -199,7 +199,25 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     } else {
       uint4 kept[2][XR + WR];
       auto load = [&](int i, uint4 (&v)[XR + WR]) {
-        const int64_t k = k0 + int64_t(i) * 64 + ch * 8, len = i < steps && k < k1 ? a.cols : 0;
+        const int64_t at = k0 + int64_t(i) * 64, k = at + ch * 8;
+        if (i < steps && at + 72 <= a.cols) {
+          // eight columns more in every row: loads that do not wait for each other; a
+          // row that is not there is another's, made zero
+          const T* some = x[0] ? x[0] : static_cast<const T*>(a.x);
+#pragma unroll
+          for (int j = 0; j < XR; ++j) v[j] = load_across((x[j] ? x[j] : some) + k);
+#pragma unroll
+          for (int j = 0; j < WR; ++j) {
+            const T* p = C::NR % 32 == 0 || r0 + 32 * j < C::NR ? w_row(r0 + 32 * j) : nullptr;
+            v[XR + j] = load_across((p ? p : some) + k);
+            if (!p) v[XR + j] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < XR; ++j)
+            if (!x[j]) v[j] = make_uint4(0, 0, 0, 0);
+          return;
+        }
+        const int64_t len = i < steps && k < k1 ? a.cols : 0;
 #pragma unroll
         for (int j = 0; j < XR; ++j) v[j] = row8(x[j], len, k);
 #pragma unroll
@@ -543,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (some) {
         named_barrier(2, kEpiThreads);  // all groups have seen the last products of the old A
         const float scale = a.scales ? a.scales[g.tile.adapter] : 1.f;
-        constexpr int P = kEpiThreads / kRows;  // threads of a row: chunks of 8 columns p, p + P, ..
+        // threads of a row: chunks of 8 columns p, p + P, ..
+        constexpr int P = kEpiThreads / kRows;
         const int r = e / P, p = e % P;
         const float* h = a.h + int64_t(g.tile.first + r) * a.pitch;
         constexpr int J = 8 * KC / P;

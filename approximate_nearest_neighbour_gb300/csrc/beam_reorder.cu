@@ -36,6 +36,7 @@ struct ReorderArgs {
   const int32_t* lengths;
   int64_t groups, blocks;
   int width, n, count;
+  int run;  // granules of a block's run, a multiple of its threads
   StateArg state[kMaxStates];
 };
 
@@ -106,12 +107,13 @@ __global__ void __launch_bounds__(IN_PLACE ? kInPlaceThreads : kThreads, 4)
     while (block >= a.state[i].blocks) ++i;
     const StateArg& s = a.state[i];
     const int64_t within = block - (i > 0 ? a.state[i - 1].blocks : 0);
-    const int64_t run = int64_t(s.granule) * blockDim.x * (IN_PLACE ? 1 : kUnroll);
+    const int64_t run = int64_t(s.granule) * a.run;
     const int64_t runs = (s.inner + run - 1) / run;
     const int64_t g = within / (s.outer * runs), rest = within - g * (s.outer * runs);
     const int64_t o = rest / runs, at = (rest - o * runs) * run;
     int64_t bytes = s.inner;
-    if (a.lengths && s.unit > 0) bytes = min(bytes, max(int64_t(a.lengths[g]), int64_t(0)) * s.unit);
+    if (a.lengths && s.unit > 0)
+      bytes = min(bytes, max(int64_t(a.lengths[g]), int64_t(0)) * s.unit);
     if (at >= bytes) continue;
     const int valid = sources(a.beams + g * a.n, a.width, a.n, IN_PLACE, to, from);
     const char* src = s.src + g * a.width * s.src_row + o * s.src_outer + at;
@@ -138,15 +140,24 @@ __global__ void __launch_bounds__(IN_PLACE ? kInPlaceThreads : kThreads, 4)
 
 template <bool IN_PLACE>
 int launch(ReorderArgs& a, cudaStream_t s) {
-  if (a.count == 0 || a.blocks == 0) return IVFPQ_OK;
+  if (a.count == 0) return IVFPQ_OK;
   const int threads = IN_PLACE ? kInPlaceThreads : kThreads;
+  // four vectors per thread, one while that leaves blocks for few SMs
+  for (a.run = threads * (IN_PLACE ? 1 : kUnroll);; a.run = threads) {
+    a.blocks = 0;
+    for (int i = 0; i < a.count; ++i) {
+      StateArg& t = a.state[i];
+      a.blocks += a.groups * t.outer * ceil_div(t.inner, int64_t(t.granule) * a.run);
+      t.blocks = a.blocks;
+    }
+    if (a.run == threads || a.blocks >= 4 * num_sms()) break;
+  }
   const size_t smem = IN_PLACE ? size_t(a.n) * threads * 16 : 0;
   if (smem > 40 * 1024) IVFPQ_TRY(set_dynamic_smem(beam_reorder_kernel<IN_PLACE>, smem));
   const unsigned grid = unsigned(std::min<int64_t>(a.blocks, int64_t(1) << 30));
   beam_reorder_kernel<IN_PLACE><<<grid, threads, smem, s>>>(a);
   IVFPQ_LAUNCHED_K(beam_reorder_kernel<IN_PLACE>, smem, threads);
   a.count = 0;
-  a.blocks = 0;
   return IVFPQ_OK;
 }
 
@@ -201,7 +212,6 @@ extern "C" int beam_reorder(const ivfpq_state* states, int count, const int32_t*
     x.width = width;
     x.n = n;
     x.count = 0;
-    x.blocks = 0;
   }
   for (int i = 0; i < count; ++i) {
     const ivfpq_state& t = states[i];
@@ -211,9 +221,6 @@ extern "C" int beam_reorder(const ivfpq_state* states, int count, const int32_t*
     StateArg& y = x.state[x.count];
     y = {static_cast<const char*>(t.src), static_cast<char*>(t.dst), t.src_row, t.dst_row, t.outer,
          t.src_outer, t.dst_outer, t.inner, t.unit, 0, granule_of(t)};
-    const int64_t run = int64_t(y.granule) * (in_place ? kInPlaceThreads : kThreads * kUnroll);
-    x.blocks += groups * t.outer * ceil_div(t.inner, run);
-    y.blocks = x.blocks;
     if (++x.count == kMaxStates)
       IVFPQ_TRY(in_place ? launch<true>(x, s) : launch<false>(x, s));
   }

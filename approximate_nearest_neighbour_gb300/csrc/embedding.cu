@@ -10,8 +10,9 @@
 //     c modulo the number of blocks, so that neighbouring frequent tokens fall to
 //     different blocks; it reads all ids, which are few bytes beside the gradient's
 //     rows, counts its own and those of the lower classes, and so knows where its
-//     tokens go without hearing from the other blocks. One warp places them, 32 in
-//     order at a time.
+//     tokens go without hearing from the other blocks. They are put into their
+//     tokens' places in any order, and then ordered by rank, or by a bitmap of the
+//     positions where a token has many.
 //  2. The sorted positions are cut into slabs of equal length. A block adds a slab's
 //     rows over a run of columns in registers (fp32) and writes a row where the
 //     token changes. A token that goes on beyond its slab is finished by the block in
@@ -92,83 +93,68 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_aligned_kernel(const Lo
   }
 }
 
-// Rows at any offset: vectors that start on a 16-byte boundary of the output, each
-// from two of the table's, and single elements before and after them.
-template <class T, class O>
+// Rows at any offset: a thread has one of every 32 of its warp's 32 N columns, so that
+// loads and stores are whole lines but for their ends.
+template <class T, class O, int U>
 __global__ void __launch_bounds__(kLookupThreads) lookup_any_kernel(const LookupArgs a) {
-  constexpr int N = Span<T>::N, U = 2;
+  constexpr int N = Span<T>::N;
   const int ty = kLookupThreads / a.tx, x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx;
-  const int64_t t = grid_row() * ty + y;
-  if (t >= a.tokens) return;
-  const int cols = int(a.cols), step = int(gridDim.x) * a.tx;
-  int64_t id = id_at(a.ids, a.wide, t);
-  if (id < 0 || id >= a.rows) id = -1;
-  O* dst = static_cast<O*>(a.out) + t * a.ldo;
-  const T* src = static_cast<const T*>(a.table) + (id < 0 ? 0 : id * a.ldt);
-  const int head = min(cols, int((16 - misalign(dst)) & 15) / int(sizeof(O)));
-  const int nvec = (cols - head) / N, rest = cols - nvec * N;
-  const int mis = misalign(src + head);
-  const int first = inner_first(mis), last = inner_last<T>(cols - head, mis);
-  const int x0 = int(blockIdx.x) * a.tx + x;
-  for (int e = x0; e < rest; e += step) {
-    const int c = e < head ? e : nvec * N + e;
-    dst[c] = from_f32<O>((id >= 0 ? to_f32(src[c]) : 0.f) * a.scale);
+  const int64_t t0 = grid_row() * (ty * U) + y;
+  const int cols = int(a.cols), step = int(gridDim.x) * a.tx * N;
+  const T* src[U];
+  O* dst[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * ty;
+    const int64_t id = t < a.tokens ? id_at(a.ids, a.wide, t) : -1;
+    src[u] = id >= 0 && id < a.rows ? static_cast<const T*>(a.table) + id * a.ldt : nullptr;
+    dst[u] = t < a.tokens ? static_cast<O*>(a.out) + t * a.ldo : nullptr;
   }
-  for (int i0 = x0; i0 < nvec; i0 += U * step) {
-    uint4 r[U];
+  const int lane = x & 31;
+  for (int c0 = (int(blockIdx.x) * a.tx + x - lane) * N + lane; c0 < cols; c0 += step) {
+    T r[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * step;
-      r[u] = make_uint4(0, 0, 0, 0);
-      if (id >= 0 && i < nvec)
-        r[u] = i >= first && i <= last ? load_inner(src + head, i, mis)
-                                       : load_edge(src + head, cols - head, i);
-    }
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * step;
-      if (i >= nvec) continue;
-      float v[N];
-      unpack_vec<T>(r[u], v);
+      for (int j = 0; j < N; ++j)
+        r[u][j] = src[u] && c0 + 32 * j < cols ? src[u][c0 + 32 * j] : from_f32<T>(0.f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] *= a.scale;
-      store_vec<O>(dst + head + i * N, v);
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (dst[u] && c0 + 32 * j < cols)
+          dst[u][c0 + 32 * j] = from_f32<O>(to_f32(r[u][j]) * a.scale);
   }
 }
 
 template <class T, class O>
 int launch_lookup(LookupArgs a, cudaStream_t s) {
   constexpr int N = Span<T>::N;
-  const int64_t nvec = std::max<int64_t>(1, a.cols / N);
-  a.tx = 8;
-  while (a.tx < kLookupThreads && a.tx < nvec) a.tx *= 2;
-  const int ty = kLookupThreads / a.tx;
+  const int64_t nvec = ceil_div(a.cols, N);
   const bool aligned = a.cols % N == 0 && a.ldt % N == 0 && a.ldo % N == 0 &&
                        reinterpret_cast<uintptr_t>(a.table) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
-  int64_t runs = std::min<int64_t>(ceil_div(nvec, a.tx), 64);
-  if (!aligned) {
-    lookup_any_kernel<T, O><<<grid_of(runs, ceil_div(a.tokens, ty)), kLookupThreads, 0, s>>>(a);
-  } else if (a.tokens * runs >= int64_t(16) * num_sms() * ty) {
-    // four tokens per thread hide their latency behind each other; one while there
-    // are few, for more blocks
-    lookup_aligned_kernel<T, O, 4>
-        <<<grid_of(runs, ceil_div(a.tokens, 4 * ty)), kLookupThreads, 0, s>>>(a);
-  } else {
-    lookup_aligned_kernel<T, O, 1>
-        <<<grid_of(runs, ceil_div(a.tokens, ty)), kLookupThreads, 0, s>>>(a);
-  }
+  a.tx = aligned ? 8 : 32;
+  while (a.tx < kLookupThreads && a.tx < nvec) a.tx *= 2;
+  const int ty = kLookupThreads / a.tx;
+  const int64_t runs = std::min<int64_t>(ceil_div(nvec, a.tx), 64);
+  // four tokens per thread (two of single columns) hide their latency behind each
+  // other; one while there are few, for more blocks
+  const bool many = a.tokens * runs >= int64_t(16) * num_sms() * ty;
+  const dim3 grid = grid_of(runs, ceil_div(a.tokens, ty * (!many ? 1 : aligned ? 4 : 2)));
+  auto kern = aligned ? (many ? lookup_aligned_kernel<T, O, 4> : lookup_aligned_kernel<T, O, 1>)
+                      : (many ? lookup_any_kernel<T, O, 2> : lookup_any_kernel<T, O, 1>);
+  kern<<<grid, kLookupThreads, 0, s>>>(a);
   IVFPQ_LAUNCHED();
   return IVFPQ_OK;
 }
 
 // ---- gradient: positions by token ----------------------------------------------------
-constexpr int kSortThreads = 512;
 constexpr int kMaxLocal = 16384;  // a block's tokens: 128 KB of counters
 constexpr int kPerThread = 16;    // ids per thread and step
-constexpr int kHot = 64;
-constexpr int kListed = 3584;     // a class's positions kept in shared memory
+constexpr int kMostListed = 8192;  // a class's positions kept in shared memory
+constexpr int kRanked = 128;      // a token's positions that are ordered by rank
+constexpr int kBitmap = 1024;     // words of the bitmap of positions
 
 struct SortArgs {
   const void* ids;
@@ -176,59 +162,54 @@ struct SortArgs {
   uint32_t rows, padding;  // padding: no row where there is none
   int shift;  // 2^shift classes, one per block
   int local;  // tokens of a class
-  int2* list;      // [tokens] scratch: a class's (position, token) in order of position
-  int32_t* bucket; // [tokens] scratch: its positions by token, in any order
+  int2* list;      // [tokens] scratch: a class's (position, token) by token
   int32_t* pos;    // [tokens] positions sorted by (class, token, position)
   int32_t* token;  // [tokens] their tokens; kFrequent marks those with more than `slab`
   int32_t* count;  // [rows] positions of each token
   int32_t* valid;  // [1] positions that hold a token
   int slab;
+  int listed;      // a class's positions that fit shared memory
   int4* frequent;  // (token, first sorted position, positions, 0), by class
   int2* classes;   // [classes] each class's first entry there and how many it has
 };
 
-__device__ __forceinline__ int block_sum(int v, uint64_t* sh) {
+template <int THREADS>
+__device__ __forceinline__ int block_sum(int v, int* sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   v = int(__reduce_add_sync(kFullMask, unsigned(v)));
   __syncthreads();
-  if (lane == 0) sh[warp] = uint64_t(v);
+  if (lane == 0) sh[warp] = v;
   __syncthreads();
-  return int(__reduce_add_sync(kFullMask, lane < kSortThreads / 32 ? unsigned(sh[lane]) : 0u));
+  return int(__reduce_add_sync(kFullMask, lane < THREADS / 32 ? unsigned(sh[lane]) : 0u));
 }
-// The sum of v over the threads before this one; all: over the block. v may hold
-// several counters side by side.
-__device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t* sh, uint64_t* all) {
+// The sum of v over the threads before this one; all: over the block.
+template <int THREADS>
+__device__ __forceinline__ int block_before(int v, int* sh, int* all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int W = kSortThreads / 32;
-  uint64_t in = v;
+  int in = v;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const uint64_t t = __shfl_up_sync(kFullMask, in, d);
+    const int t = __shfl_up_sync(kFullMask, in, d);
     if (lane >= d) in += t;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = in;
   __syncthreads();
-  uint64_t below = 0;
-  *all = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const uint64_t t = sh[w];
-    if (w < warp) below += t;
-    *all += t;
-  }
-  return below + in - v;
+  const int w = lane < THREADS / 32 ? sh[lane] : 0;
+  *all = int(__reduce_add_sync(kFullMask, unsigned(w)));
+  return int(__reduce_add_sync(kFullMask, unsigned(lane < warp ? w : 0))) + in - v;
 }
 
-// The positions of a step that thread x takes: four groups of four, (j kSortThreads + x)
+// The positions of a step that thread x takes: four groups of four, (j THREADS + x)
 // 4 + e, so that a warp's loads are whole lines.
+template <int THREADS>
 __device__ __forceinline__ int64_t position(int64_t t0, int j) {
-  return t0 + (int64_t(j) * kSortThreads + threadIdx.x) * 4;
+  return t0 + (int64_t(j) * THREADS + threadIdx.x) * 4;
 }
 // Their tokens, kNone where there is none to count.
 constexpr uint32_t kNone = 0xffffffffu;
 constexpr int32_t kFrequent = 1 << 30;  // above any token
-template <bool WIDE>
+template <bool WIDE, int THREADS>
 __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0,
                                             uint32_t (&v)[kPerThread]) {
   using Id = std::conditional_t<WIDE, int64_t, int32_t>;
@@ -238,152 +219,151 @@ __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0,
     const bool ok = u < a.rows && u != a.padding && (!WIDE || Id(u) == id);
     return ok ? u : kNone;
   };
-  if (t0 + kSortThreads * kPerThread <= a.tokens && misalign(a.ids) == 0) {
+  if (t0 + THREADS * kPerThread <= a.tokens && misalign(a.ids) == 0) {
     Id w[kPerThread];
     constexpr int V = 16 / int(sizeof(Id));  // ids of a load
 #pragma unroll
     for (int j = 0; j < kPerThread / V; ++j)
       *reinterpret_cast<uint4*>(w + j * V) =
-          reinterpret_cast<const uint4*>(ids + position(t0, j * V / 4))[j % (4 / V)];
+          reinterpret_cast<const uint4*>(ids + position<THREADS>(t0, j * V / 4))[j % (4 / V)];
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) v[j] = token(w[j]);
     return;
   }
 #pragma unroll 4
   for (int j = 0; j < kPerThread; ++j) {
-    const int64_t t = position(t0, j / 4) + j % 4;
+    const int64_t t = position<THREADS>(t0, j / 4) + j % 4;
     v[j] = t < a.tokens ? token(ids[t]) : kNone;
   }
 }
 
-template <bool WIDE>
-__global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const SortArgs a) {
+template <bool WIDE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortArgs a) {
   extern __shared__ int sort_smem[];
-  int* start = sort_smem;         // [local + 1]: counts, then where a token's positions start
+  int* start = sort_smem;  // [local + 1]: counts, then where a token's positions start
   int* fill = start + a.local + 1;  // [local]: how many of them have a place
-  __shared__ int2 list_smem[kListed];
-  __shared__ int bucket_smem[kListed];
-  __shared__ int hot[kHot];  // frequent tokens
-  __shared__ uint64_t sh[kSortThreads / 32];
-  __shared__ int nfrequent;
+  int2* list_smem = reinterpret_cast<int2*>(start + (2 * a.local + 2) / 2 * 2);  // [listed]
+  int2* met = list_smem + a.listed;  // [listed] the class's positions as they were met
+  __shared__ uint32_t bitmap[kBitmap];
+  __shared__ int sh[THREADS / 32];
+  __shared__ int nfrequent, nmet;
   const uint32_t c = blockIdx.x, mask = (1u << a.shift) - 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int64_t step = int64_t(kSortThreads) * kPerThread;
-  constexpr int G = kPerThread / 4;
+  constexpr int64_t step = int64_t(THREADS) * kPerThread;
   grid_go();
   int before = 0;
   uint32_t v[kPerThread];
-  read_tokens<WIDE>(a, 0, v);
-  if (threadIdx.x == 0) nfrequent = 0;
-  for (int i = threadIdx.x; i < 2 * a.local + 1; i += kSortThreads) start[i] = 0;
+  read_tokens<WIDE, THREADS>(a, 0, v);
+  if (threadIdx.x == 0) nfrequent = nmet = 0;
+  for (int i = threadIdx.x; i < 2 * a.local + 1; i += THREADS) start[i] = 0;
   __syncthreads();
+  // (kNone's class is the last: it counts as before none)
   for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
-    if (t0 > 0) read_tokens<WIDE>(a, t0, v);
+    if (t0 > 0) read_tokens<WIDE, THREADS>(a, t0, v);
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const uint32_t cls = v[j] & mask;
-      if (v[j] != kNone) {
-        before += cls < c;
-        if (cls == c) atomicAdd(&start[v[j] >> a.shift], 1);
+      before += cls < c;
+      if (cls == c && v[j] != kNone) {
+        atomicAdd(&start[v[j] >> a.shift], 1);
+        const int i = atomicAdd(&nmet, 1);
+        if (i < a.listed)
+          met[i] = make_int2(int(position<THREADS>(t0, j / 4)) + j % 4, int(v[j]));
       }
     }
   }
-  const int base = block_sum(before, sh);
+  const int base = block_sum<THREADS>(before, sh);
   // counts out; their running sums stay
   int n = 0;
-  for (int i0 = 0; i0 < a.local; i0 += kSortThreads) {
+  for (int i0 = 0; i0 < a.local; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
     const int64_t token = (int64_t(i) << a.shift) + c;
     const int k = i < a.local ? start[i] : 0;
     if (i < a.local && token < a.rows) a.count[token] = k;
-    uint64_t all;
-    const int at = n + int(block_before(uint64_t(k), sh, &all));
+    int all;
+    const int at = n + block_before<THREADS>(k, sh, &all);
     if (i < a.local) start[i] = at;
     if (k > a.slab) {
       // a class of n positions has at most n / (slab + 1) frequent tokens, so that no
       // two classes' entries meet
       const int j = atomicAdd(&nfrequent, 1);
       a.frequent[base / (a.slab + 1) + j] = make_int4(int(token), base + at, k, 0);
-      if (j < kHot) hot[j] = int(token);
     }
-    n += int(all);
+    n += all;
   }
   if (threadIdx.x == 0) start[a.local] = n;
   if (c == mask && threadIdx.x == 0) *a.valid = base + n;
   __syncthreads();
   if (threadIdx.x == 0) a.classes[c] = make_int2(base / (a.slab + 1), nfrequent);
   if (n == 0) return;
-  // the class's positions in order
-  const bool fits = n <= kListed;
+  // positions to their tokens' places, in any order
+  const bool fits = n <= a.listed;
   int2* list = fits ? list_smem : a.list + base;
-  int* bucket = fits ? bucket_smem : a.bucket + base;
-  int found = 0;
-  for (int64_t t0 = 0; found < n && t0 < a.tokens; t0 += step) {
-    if (a.tokens > step) read_tokens<WIDE>(a, t0, v);
-    // a 16-bit counter per group of four: a group has 4 kSortThreads at most
-    uint64_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j)
-      mine += uint64_t(v[j] != kNone && (v[j] & mask) == c) << (16 * (j / 4));
-    uint64_t all;
-    const uint64_t at = block_before(mine, sh, &all);
-    if (mine) {
-      int before_group = found;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        int place = before_group + int(at >> (16 * g) & 0xffff);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (v[4 * g + e] != kNone && (v[4 * g + e] & mask) == c)
-            list[place++] = make_int2(int(position(t0, g)) + e, int(v[4 * g + e]));
-        before_group += int(all >> (16 * g) & 0xffff);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) found += int(all >> (16 * g) & 0xffff);
-  }
-  __syncthreads();
-  // tokens that are not frequent: their positions into a bucket, in any order, ...
-  auto size_of = [&](int l) { return start[l + 1] - start[l]; };
-  for (int i = threadIdx.x; i < n; i += kSortThreads) {
-    const int2 e = list[i];
+  auto put = [&](const int2& e) {
     const int l = e.y >> a.shift;
-    if (size_of(l) <= a.slab) bucket[start[l] + atomicAdd(&fill[l], 1)] = e.x;
+    list[start[l] + atomicAdd(&fill[l], 1)] = e;
+  };
+  if (fits) {
+    for (int i = threadIdx.x; i < n; i += THREADS) put(met[i]);
+  } else {
+    for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
+      read_tokens<WIDE, THREADS>(a, t0, v);
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j)
+        if ((v[j] & mask) == c && v[j] != kNone)
+          put(make_int2(int(position<THREADS>(t0, j / 4)) + j % 4, int(v[j])));
+    }
   }
   __syncthreads();
-  // ... and each to its rank among them
-  for (int i = threadIdx.x; i < n; i += kSortThreads) {
+  // few of a token: each by its rank among them
+  for (int i = threadIdx.x; i < n; i += THREADS) {
     const int2 e = list[i];
-    const int l = e.y >> a.shift, k = size_of(l);
-    if (k > a.slab) continue;
-    const int* of = bucket + start[l];
+    const int l = e.y >> a.shift, from = start[l], k = start[l + 1] - from;
+    if (k > kRanked) continue;
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < k; ++j) rank += of[j] < e.x;
-    a.pos[base + start[l] + rank] = e.x;
-    a.token[base + start[l] + rank] = e.y;
+    for (int j = 0; j < k; ++j) rank += list[from + j].x < e.x;
+    a.pos[base + from + rank] = e.x;
+    a.token[base + from + rank] = e.y | (k > a.slab ? kFrequent : 0);
   }
-  // a frequent token's in order, by a warp that goes through the list
-  const int4* frequent = a.frequent + base / (a.slab + 1);
-  for (int f = warp; f < nfrequent; f += kSortThreads / 32) {
-    const int id = f < kHot ? hot[f] : frequent[f].x;
-    int at = base + start[id >> a.shift];
-    constexpr int U = 4;
-    for (int i0 = 0; i0 < n; i0 += 32 * U) {
-      int2 e[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        e[u] = i0 + 32 * u + lane < n ? list[i0 + 32 * u + lane] : make_int2(-1, -1);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const unsigned same = __ballot_sync(kFullMask, e[u].y == id);
-        if (e[u].y == id) {
-          const int to = at + __popc(same & ((1u << lane) - 1u));
-          a.pos[to] = e[u].x;
-          a.token[to] = id | kFrequent;
-        }
-        at += __popc(same);
+  // many: a bitmap of the positions, a range of them at a time
+  const int lane = threadIdx.x & 31;
+  unsigned more = 0;  // of 32 tokens from l0 on, the same in every warp
+  for (int l0 = -32;;) {
+    while (more == 0 && (l0 += 32) < a.local)
+      more = __ballot_sync(kFullMask, l0 + lane < a.local &&
+                                          start[min(l0 + lane + 1, a.local)] -
+                                                  start[min(l0 + lane, a.local)] > kRanked);
+    if (more == 0) break;
+    const int l = l0 + __ffs(more) - 1, from = start[l], k = start[l + 1] - from;
+    more &= more - 1;
+    const int id = int((uint32_t(l) << a.shift) + c) | (k > a.slab ? kFrequent : 0);
+    int at = base + from;
+    for (int64_t t0 = 0; t0 < a.tokens; t0 += kBitmap * 32) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kBitmap; i += THREADS) bitmap[i] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < k; i += THREADS) {
+        const int64_t p = int64_t(list[from + i].x) - t0;
+        if (p >= 0 && p < kBitmap * 32) atomicOr(&bitmap[p >> 5], 1u << (p & 31));
       }
+      __syncthreads();
+      constexpr int W = kBitmap / THREADS;  // words of a thread
+      uint32_t bits[W];
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        bits[i] = bitmap[threadIdx.x * W + i];
+        mine += __popc(bits[i]);
+      }
+      int all, to = at + block_before<THREADS>(mine, sh, &all);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        for (; bits[i]; bits[i] &= bits[i] - 1) {
+          a.pos[to] = int(t0) + (int(threadIdx.x) * W + i) * 32 + __ffs(bits[i]) - 1;
+          a.token[to++] = id;
+        }
+      }
+      at += all;
     }
   }
 }
@@ -412,14 +392,21 @@ struct SumArgs {
   int64_t ldo;
 };
 
-// VEC: rows of grad and out are whole vectors on 16-byte boundaries.
-// Row values of columns N cv .. N cv + N - 1 of token v.
+// A thread has N columns of a row. VEC (rows of grad and out are whole vectors on
+// 16-byte boundaries): a vector, N cv and following. Else one of every 32 in its warp's
+// 32 N columns: whole lines whatever the offset, and nothing at the ends.
+template <int N, bool VEC>
+__device__ __forceinline__ int column(int cv, int j) {
+  const int lane = threadIdx.x & 31;
+  return VEC ? cv * N + j : (cv - lane) * N + j * 32 + lane;
+}
+// The row of token v.
 template <class T, class O, bool VEC>
 __device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int cv,
                                           const float (&s)[Span<T>::N]) {
   constexpr int N = Span<T>::N, M = Span<O>::N;
-  O* dst = static_cast<O*>(a.out) + v * a.ldo + int64_t(cv) * N;
   if constexpr (VEC) {
+    O* dst = static_cast<O*>(a.out) + v * a.ldo + int64_t(cv) * N;
 #pragma unroll
     for (int q = 0; q < N / M; ++q) {
       float w[M];
@@ -434,20 +421,77 @@ __device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int cv,
       reinterpret_cast<uint4*>(dst)[q] = pack_vec<O>(w);
     }
   } else {
-    const int have = int(min(int64_t(N), a.cols - int64_t(cv) * N));
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (j < have) {
+      const int c = column<N, VEC>(cv, j);
+      if (c < a.cols) {
+        O* dst = static_cast<O*>(a.out) + v * a.ldo + c;
         float w = s[j] * a.scale;
-        if (a.accumulate) w += to_f32(dst[j]);
-        dst[j] = from_f32<O>(w);
+        if (a.accumulate) w += to_f32(*dst);
+        *dst = from_f32<O>(w);
       }
     }
   }
 }
-template <int N>
-__device__ __forceinline__ float* part_at(const SumArgs& a, int64_t slab, int which, int cv) {
-  return a.part + (slab * 2 + which) * a.pitch + int64_t(cv) * N;
+// Adds the rows pos[b], pos[b + 1], .. before `end`, U of them at most: add(u, values).
+template <class T, bool VEC, int U, class F>
+__device__ __forceinline__ void take_rows(const SumArgs& a, const int32_t* pos, int b, int end,
+                                          int cv, F&& add) {
+  constexpr int N = Span<T>::N;
+  const T* grad = static_cast<const T*>(a.grad);
+  if constexpr (VEC) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u < end) r[u] = reinterpret_cast<const uint4*>(grad + pos[b + u] * a.ldg)[cv];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u < end) {
+        float v[N];
+        unpack_vec<T>(r[u], v);
+        add(b + u, v);
+      }
+    }
+  } else {
+    T r[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u < end) {
+        const T* p = grad + pos[b + u] * a.ldg;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int c = column<N, VEC>(cv, j);
+          r[u][j] = c < a.cols ? p[c] : from_f32<T>(0.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u < end) {
+        float v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = to_f32(r[u][j]);
+        add(b + u, v);
+      }
+    }
+  }
+}
+// The partial sums of a slab's token.
+template <int N, bool VEC>
+__device__ __forceinline__ void write_part(const SumArgs& a, int64_t slab, int which, int cv,
+                                           const float (&s)[N]) {
+  float* q = a.part + (slab * 2 + which) * a.pitch;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4)
+      *reinterpret_cast<float4*>(q + cv * N + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = column<N, VEC>(cv, j);
+      if (c < a.cols) q[c] = s[j];
+    }
+  }
 }
 
 template <class O>
@@ -459,8 +503,8 @@ __device__ __forceinline__ void zero_row(O* p, int len, int x, int step) {
 }
 
 template <class T, class O, bool VEC>
-__global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
-  constexpr int N = Span<T>::N, U = 8;
+__global__ void __launch_bounds__(128) embedding_sum_kernel(const SumArgs a) {
+  constexpr int N = Span<T>::N, U = VEC ? 8 : 4;
   __shared__ int32_t pos[2 * kMaxSlab], token[2 * kMaxSlab + 1];
   const int64_t slab = grid_row();
   grid_wait();
@@ -524,47 +568,24 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs a) {
       end = run_end(n, 2 * a.slab + 1) - 1;
   }
   const int cv = int(blockIdx.x * blockDim.x + threadIdx.x);
-  if (int64_t(cv) * N >= a.cols) return;
-  const T* grad = static_cast<const T*>(a.grad);
-  [[maybe_unused]] const int cols = int(a.cols);
+  if (column<N, VEC>(cv, 0) >= a.cols) return;
   float s[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) s[j] = 0.f;
-  for (int b = begin; b < end; b += U) {
-    uint4 r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b + u < end) {
-        const T* p = grad + pos[b + u] * a.ldg;
-        if constexpr (VEC)
-          r[u] = reinterpret_cast<const uint4*>(p)[cv];
-        else
-          r[u] = load_vec(p, cols, cv, misalign(p));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = b + u;
-      if (i >= end) break;
-      float v[N];
-      unpack_vec<T>(r[u], v);
+  for (int b = begin; b < end; b += U)
+    take_rows<T, VEC, U>(a, pos, b, end, cv, [&](int i, const float (&v)[N]) {
 #pragma unroll
       for (int j = 0; j < N; ++j) s[j] += v[j];
       if (i == end - 1 || token[i + 2] != token[i + 1]) {
-        if (first || (last && i == end - 1)) {
-          float* q = part_at<N>(a, slab, first ? 0 : 1, cv);
-#pragma unroll
-          for (int j = 0; j < N; j += 4)
-            *reinterpret_cast<float4*>(q + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-        } else {
+        if (first || (last && i == end - 1))
+          write_part<N, VEC>(a, slab, first ? 0 : 1, cv, s);
+        else
           write_row<T, O, VEC>(a, token[i + 1] & ~kFrequent, cv, s);
-        }
         first = false;
 #pragma unroll
         for (int j = 0; j < N; ++j) s[j] = 0.f;
       }
-    }
-  }
+    });
 }
 
 // The frequent tokens, a class per row of blocks.
@@ -575,7 +596,7 @@ __global__ void __launch_bounds__(kJoinThreads* kJoinParts) embedding_join_kerne
   grid_wait();
   const int2 mine = a.classes[blockIdx.y];
   const int c = int(blockIdx.x * kJoinThreads + threadIdx.x) * 4;
-  for (int i = 0; i < mine.y; ++i) {
+  for (int i = blockIdx.z; i < mine.y; i += gridDim.z) {
     const int4 token = a.frequent[mine.x + i];
     const int64_t slab = token.y / a.slab;
     const int more = int((int64_t(token.y) + token.z - 1) / a.slab - slab);
@@ -650,7 +671,7 @@ struct FewArgs {
 
 template <class T, class O, bool VEC>
 __global__ void __launch_bounds__(kFewThreads) embedding_few_kernel(const FewArgs f) {
-  constexpr int N = Span<T>::N, U = 8;
+  constexpr int N = Span<T>::N, U = VEC ? 8 : 4;
   const SumArgs& a = f.sum;
   __shared__ int32_t token[kFew], pos[kFew];    // the class's, by position
   __shared__ int32_t stoken[kFew], spos[kFew];  // sorted by token
@@ -705,36 +726,17 @@ __global__ void __launch_bounds__(kFewThreads) embedding_few_kernel(const FewArg
   if (t == 0) starts[segments] = n;
   __syncthreads();
   const int nvec = int((a.cols + N - 1) / N), runs = (nvec + 31) / 32;
-  const T* grad = static_cast<const T*>(a.grad);
   for (int i = warp; i < segments * runs; i += kFewThreads / 32) {
-    const int g = i / runs, cv = (i - g * runs) * 32 + lane;
-    if (cv >= nvec) continue;
+    const int g = i / runs, cv = (i - g * runs) * 32 + lane, end = starts[g + 1];
+    if (column<N, VEC>(cv, 0) >= a.cols) continue;
     float s[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) s[j] = 0.f;
-    const int end = starts[g + 1];
-    for (int b = starts[g]; b < end; b += U) {
-      uint4 r[U];
+    for (int b = starts[g]; b < end; b += U)
+      take_rows<T, VEC, U>(a, spos, b, end, cv, [&](int, const float (&v)[N]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (b + u < end) {
-          const T* p = grad + spos[b + u] * a.ldg;
-          if constexpr (VEC)
-            r[u] = reinterpret_cast<const uint4*>(p)[cv];
-          else
-            r[u] = load_vec(p, int(a.cols), cv, misalign(p));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (b + u < end) {
-          float v[N];
-          unpack_vec<T>(r[u], v);
-#pragma unroll
-          for (int j = 0; j < N; ++j) s[j] += v[j];
-        }
-      }
-    }
+        for (int j = 0; j < N; ++j) s[j] += v[j];
+      });
     write_row<T, O, VEC>(a, stoken[starts[g]], cv, s);
   }
   if (a.accumulate) return;
@@ -782,7 +784,7 @@ int launch_sums(const SumArgs& a, int classes, cudaStream_t s) {
   IVFPQ_TRY(launch_after(vec ? embedding_sum_kernel<T, O, true> : embedding_sum_kernel<T, O, false>,
                          grid_of(runs, a.slabs + zero), dim3(unsigned(threads)), a, s));
   return launch_after(embedding_join_kernel<O>,
-                      dim3(unsigned(ceil_div(a.cols, 4 * kJoinThreads)), unsigned(classes)),
+                      dim3(unsigned(ceil_div(a.cols, 4 * kJoinThreads)), unsigned(classes), 4),
                       dim3(kJoinThreads, kJoinParts), a, s);
 }
 
@@ -868,23 +870,23 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   while (ceil_div(rows, int64_t(1) << o.shift) > kMaxLocal) ++o.shift;
   o.local = int(ceil_div(rows, int64_t(1) << o.shift));
   // short slabs while they are few: a block takes its positions one after the other
+  const int64_t runs = ceil_div(cols, 128 * (16 / dtype_size(dtype)));
   a.slab = 8;
-  while (a.slab < kMaxSlab && tokens > int64_t(a.slab) * 512) a.slab *= 2;
+  while (a.slab < kMaxSlab && tokens * runs > int64_t(a.slab) * 4096) a.slab *= 2;
   a.slabs = ceil_div(tokens, a.slab);
   a.pitch = ceil_div(cols, 8) * 8;
   Workspace ws(s);
   // the slabs' partial sums, the frequent tokens and the sorted positions
   const size_t parts = size_t(a.slabs) * 2 * size_t(a.pitch);
   const size_t frequent = size_t(tokens / (a.slab + 1) + 1), classes = size_t(1) << o.shift;
-  const size_t words = size_t(tokens) * 5 + size_t(rows) + 1;
+  const size_t words = size_t(tokens) * 4 + size_t(rows) + 1;
   int4* w = nullptr;
   IVFPQ_TRY(ws.alloc(&w, parts / 4 + frequent + (classes + 1) / 2 + (words + 3) / 4));
   a.part = reinterpret_cast<float*>(w);
   o.frequent = w + parts / 4;
   o.classes = reinterpret_cast<int2*>(o.frequent + frequent);
   o.list = o.classes + 2 * ((classes + 1) / 2);
-  o.bucket = reinterpret_cast<int32_t*>(o.list + tokens);
-  o.pos = o.bucket + tokens;
+  o.pos = reinterpret_cast<int32_t*>(o.list + tokens);
   o.token = o.pos + tokens;
   o.count = o.token + tokens;
   o.valid = o.count + rows;
@@ -895,11 +897,17 @@ extern "C" int embedding_gradient(const void* grad, int dtype, int64_t tokens, i
   a.token = o.token;
   a.count = o.count;
   a.valid = o.valid;
-  const size_t smem = (size_t(o.local) * 2 + 1) * 4;
-  auto sort = wide ? embedding_sort_kernel<true> : embedding_sort_kernel<false>;
+  // counters, and what else fits of positions, as they are met and by token
+  const int64_t counters = (int64_t(o.local) * 2 + 2) / 2 * 8;
+  o.listed = int(std::min<int64_t>({tokens, kMostListed, (216 * 1024 - counters) / 16}));
+  const size_t smem = size_t(counters) + size_t(o.listed) * 16;
+  // more threads where each has several steps of ids
+  const bool many = tokens > 16384;
+  auto sort = wide ? (many ? embedding_sort_kernel<true, 1024> : embedding_sort_kernel<true, 512>)
+                   : (many ? embedding_sort_kernel<false, 1024> : embedding_sort_kernel<false, 512>);
   IVFPQ_TRY(set_dynamic_smem(sort, smem));
-  sort<<<1u << o.shift, kSortThreads, smem, s>>>(o);
-  IVFPQ_LAUNCHED_K(sort, smem, kSortThreads);
+  sort<<<1u << o.shift, many ? 1024 : 512, smem, s>>>(o);
+  IVFPQ_LAUNCHED_K(sort, smem, many ? 1024 : 512);
   return by_dtype(dtype, [&](auto* t) -> int {
     using T = std::remove_pointer_t<decltype(t)>;
     return out_dtype == dtype ? launch_sums<T, T>(a, 1 << o.shift, s)

@@ -133,6 +133,18 @@ def test_gradient_of_many_tokens(B):
         _check_gradient(B.embedding_gradient(g, ids, 70_000), g, ids, 70_000, 1.0)
 
 
+def test_gradient_of_many_frequent_tokens(B):
+    """Hundreds of tokens of one class, each with more positions than are sorted by rank,
+    with fewer, and with more than one block's list holds."""
+    import torch
+    g = _rand(60_000, 12, "f32", 3)
+    r = np.random.default_rng(5)
+    for step in (128, 1):
+        for kinds in (300, 9):
+            ids = torch.from_numpy((r.integers(0, kinds, 60_000) * step).astype(np.int32)).cuda()
+            _check_gradient(B.embedding_gradient(g, ids, kinds * step), g, ids, kinds * step, 1.0)
+
+
 def test_gradient_of_a_large_table(B):
     """More tokens per class than fit one block's counters at 128 classes."""
     import torch
