@@ -9,6 +9,9 @@ they are used together:
 * decode(): one token at a time, fp4_linear makes the scores of every row of a batch,
   score_adjust applies repetition penalties, a temperature and a mask of allowed rows
   and negates them, kselect takes the best, which become the next tokens;
+* search(): the same with beams and requests' own adapters: embedding_lookup takes the
+  tokens' states, adapter_linear adds each request's low-rank adapter to the shared scores,
+  beam_select takes the best continuations, beam_reorder moves the histories to them;
 * distill(): the teacher's top list of each state (kselect's values and ids) trains a
   student head with topk_distill.
 """
@@ -68,6 +71,41 @@ def decode(head, states, x_scale, batch=8, steps=16, k=4):
     return history[:, 1:]
 
 
+def adapters(head, width, count=3, rank=8, seed=1):
+    """Low-rank adapters [count, rank, width] and [count, rows, rank], and their scales."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    a = torch.randn((count, rank, width), generator=gen, device="cuda") * width ** -0.5
+    b = torch.randn((count, head.rows, rank), generator=gen, device="cuda") * 0.2
+    return a.bfloat16(), b.bfloat16(), torch.full((count,), 0.5, device="cuda")
+
+
+def search(head, states, x_scale, low_rank, requests=3, beams=4, steps=8, end=0):
+    """(tokens [requests, beams, steps], totals [requests, beams]), best beams first;
+    request i has adapter i - 1, the first one none; a beam ends with the token `end`."""
+    device = states.device
+    a, b, scales = low_rank
+    rows = requests * beams
+    which = (torch.arange(rows, device=device) // beams - 1).int()
+    history = torch.zeros((rows, steps + 1), dtype=torch.int32, device=device)
+    history[:, 0] = (torch.arange(rows, device=device) // beams * 7 + 3).int()
+    totals = torch.full((requests, beams), -float("inf"), device=device)
+    totals[:, 0] = 0.0  # all beams are alike at first: one is enough
+    finished = torch.zeros((requests, beams), dtype=torch.bool, device=device)
+    length = torch.ones((requests,), dtype=torch.int32, device=device)
+    heat = torch.full((rows,), 0.7, device=device)
+    for t in range(steps):
+        x = B.embedding_lookup(states, history[:, t].contiguous())
+        scores = head.scores(x, x_scale)
+        B.adapter_linear(x, a, b, which, scales=scales, base=scores, out=scores)
+        B.score_adjust(scores, temperature=heat, out=scores)
+        totals, of, ids = B.beam_select(scores, totals, beams, finished=finished, end_id=end)
+        B.beam_reorder(history, of, lengths=length)
+        finished = finished.gather(1, of.clamp(min=0).long()) | (ids == end)
+        history[:, t + 1] = ids.view(-1)
+        length += 1
+    return history[:, 1:].view(requests, beams, steps), totals
+
+
 def distill(head, states, x_scale, steps=60, batch=512, k=32, tau=2.0, rate=30.0):
     """The mean loss before each step of a student head learning the teacher's lists."""
     student = torch.zeros((head.rows, states.shape[1]), device=states.device)
@@ -88,8 +126,10 @@ def main():
     head, states, x_scale = setup()
     tokens = decode(head, states, x_scale)
     losses = distill(head, states, x_scale)
+    beams, totals = search(head, states, x_scale, adapters(head, states.shape[1]))
     B.device_check()
     print("tokens of the first rows:", tokens[:2].tolist())
+    print("best beam of each request:", beams[:, 0].tolist(), totals[:, 0].tolist())
     print("distillation loss: %.4f -> %.4f" % (float(losses[0]), float(losses[-1])))
 
 
