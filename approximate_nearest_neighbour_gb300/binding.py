@@ -982,6 +982,8 @@ def beam_select(scores, totals, k, finished=None, end_id=0, stream=None):
         if finished.dtype is not _late["u8"] and finished.dtype is not _late["bool"]:
             raise TypeError(f"finished must be bool or uint8, got {finished.dtype}")
         fin = _array(finished, finished.dtype, (groups, beams), "finished", at)
+        if not 0 <= end_id < cols:
+            raise ValueError(f"end_id={end_id} outside [0, {cols})")
     shape, i32 = (groups, k), _late["i32"]
     out = empty(shape, dtype=f32, device=dev)
     which = empty(shape, dtype=i32, device=dev)

@@ -677,7 +677,8 @@ int embedding_lookup(const void* table, int dtype, int64_t rows, int64_t cols, i
  *  grad     device [tokens, cols] of dtype, row stride ldg (0: one row for all)
  *  ids      as above; ids outside [0, rows), and the id `padding`, have no gradient
  *  out      device [rows, cols] of out_dtype (dtype or IVFPQ_F32), row stride ldo:
- *           every row is written; with accumulate only those of tokens that occur
+ *           every row is written; with accumulate only those of tokens that occur.
+ *           Not grad's memory
  * Errors: INVALID_ARG, OOM, CUDA.
  */
 int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols, int64_t ldg,
@@ -689,8 +690,9 @@ int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols
  * they share (fp4_linear's, for instance):
  *   out[t] = base[t] + scales[i] (x[t] a[i]^T) b[i]^T,  i = ids[t]
  * x[t] a[i]^T is held in fp32 and enters the second product with a relative error
- * of at most 2^-16 per element (2^-22 where the output is fp32); sums are fp32, the
- * result is rounded once.
+ * of at most 2^-16 per element (2^-22 where the output is fp32; for fp16 operands at
+ * least 2^-36 of the token's largest); sums are fp32, the result is rounded once.
+ * Results repeat bit for bit.
  *  x       device [tokens, cols] of dtype (IVFPQ_F16 or IVFPQ_BF16), row stride ldx
  *          (0 repeats a row)
  *  a       device [adapters, rank, cols], b device [adapters, n, rank] of dtype,

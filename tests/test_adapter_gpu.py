@@ -55,7 +55,8 @@ def _check(got, x, a, b, ids, scales, base):
     (1, 1, 1, 1, 1), (1, 4096, 300, 16, 3), (3, 64, 40, 8, 2), (16, 512, 129, 4, 5),
     (17, 512, 129, 4, 5), (5, 77, 33, 3, 2), (40, 1001, 65, 24, 6), (77, 256, 512, 16, 64),
     (33, 96, 64, 64, 1), (70, 200, 250, 128, 3), (30, 136, 1000, 100, 2), (300, 128, 200, 32, 4),
-    (520, 160, 320, 16, 3), (9, 40, 31, 17, 2)])
+    (520, 160, 320, 16, 3), (9, 40, 31, 17, 2), (300, 96, 200, 4, 2), (300, 96, 201, 100, 2),
+    (100, 96, 72, 100, 2), (130, 64, 72, 128, 1), (64, 200, 136, 40, 2), (257, 72, 1030, 9, 3)])
 def test_against_the_definition(B, dtype, out, tokens, cols, n, rank, adapters):
     import torch
     c = _case(tokens, cols, n, rank, adapters, dtype, out, tokens + cols + n)
@@ -163,3 +164,35 @@ def test_streams_and_captured(B):
         torch.cuda.synchronize()
         for c, o in zip(cs[1:], outs):
             assert torch.equal(o, B.adapter_linear(**c))
+
+
+def test_operands_at_any_offset(B):
+    """Adapters that start off the 16-byte boundaries give the same results, but where
+    tiles of 128 tokens then take another product: there within its error."""
+    import torch
+    for tokens, rank in ((30, 16), (30, 24), (300, 16), (100, 64)):
+        c = _case(tokens, 136, 72, rank, 2, "bf16", "f32", 4)
+        want = B.adapter_linear(**c)
+        for off in (1, 3, 8):
+            d = dict(c)
+            for name in ("a", "b"):
+                flat = torch.zeros(c[name].numel() + off, dtype=torch.bfloat16, device="cuda")
+                d[name] = flat[off:].view(c[name].shape)
+                d[name].copy_(c[name])
+            got = B.adapter_linear(**d)
+            _check(got, **d)
+            if tokens < 64:
+                assert torch.equal(got, want)
+
+
+def test_rows_of_one_value(B):
+    """Every token the same: every result the same, whatever its place in a tile."""
+    import torch
+    for tokens in (1, 2, 15, 16, 17, 255, 256, 257, 384, 385):
+        c = _case(tokens, 64, 40, 8, 1, "f16", "f32", 3)
+        c["ids"].zero_()
+        c["x"].copy_(c["x"][:1].expand(tokens, 64).clone())
+        c["base"].copy_(c["base"][:1].expand(tokens, 40).clone())
+        got = B.adapter_linear(**c)
+        assert torch.equal(got, got[:1].expand(tokens, 40))
+        _check(got, **c)

@@ -157,6 +157,24 @@ def test_empty_and_streams(B):
     assert all(torch.equal(a, b) for o in got for a, b in zip(o, want))
 
 
+def test_captured_with_a_second_kernel(B):
+    """More entries than one cluster ranks: two kernels and workspace in a graph."""
+    import torch
+    s = _scores(40, 9000, "bf16", 20)
+    t = torch.from_numpy(_totals(2, 20, 1)).cuda()
+    B.beam_select(s, t, 40)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = B.beam_select(s, t, 40)
+    for i in range(3):
+        s.copy_(_scores(40, 9000, "bf16", 30 + i))
+        g.replay()
+        want = B.beam_select(s, t, 40)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
 def test_captured(B):
     """Selection and in-place reordering captured; two graphs replayed in turn."""
     import torch
@@ -327,3 +345,15 @@ def test_every_number_of_beams(B, beams):
         t[0, beams // 2] = -np.inf
         f = (r.random((groups, beams)) < 0.2).astype(np.uint8)
         _select(B, _scores(groups * beams, cols, "bf16", beams + cols), t, min(k, 128), f, 5)
+
+
+def test_the_two_ways_agree(B):
+    """A selection of few continuations is the beginning of one of many: one cluster
+    ranks the first, two kernels the second."""
+    import torch
+    for dtype in ("f32", "bf16"):
+        s = _scores(24, 6001, dtype, 2)
+        s[3] = s[2]  # equal rows: the lower beam comes first
+        t = torch.zeros((6, 4), device="cuda")
+        few, many = B.beam_select(s, t, 8), B.beam_select(s, t, 128)
+        assert all(torch.equal(a, b[:, :8]) for a, b in zip(few, many))

@@ -226,3 +226,28 @@ def test_captured_with_an_eager_one(B):
         eager = [B.embedding_gradient(g, v, 200) for v in ids]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, eager))
+
+
+@pytest.mark.parametrize("tokens", [200, 9000, 20_000])
+@pytest.mark.parametrize("wide", [False, True])
+def test_ids_at_any_offset(B, tokens, wide):
+    """Ids that start off the 16-byte boundaries."""
+    import torch
+    g = _rand(tokens, 24, "f32", 1)
+    ids = _ids(tokens, 300, 2, wide)
+    want = B.embedding_gradient(g, ids, 300)
+    table = _rand(300, 24, "f32", 3)
+    rows = B.embedding_lookup(table, ids)
+    for off in (1, 2, 3):
+        room = torch.zeros(tokens + off, dtype=ids.dtype, device="cuda")
+        room[off:] = ids
+        assert torch.equal(B.embedding_gradient(g, room[off:], 300), want)
+        assert torch.equal(B.embedding_lookup(table, room[off:]), rows)
+
+
+def test_one_id(B):
+    import torch
+    table = _rand(9, 33, "f16", 1)
+    i = torch.tensor(4, device="cuda")
+    assert torch.equal(B.embedding_lookup(table, i), table[4])
+    assert (B.embedding_lookup(table, i + 5) == 0).all()
