@@ -61,8 +61,8 @@ struct SelectArgs {
   int k, chunk, shift;
   RowLists o;
   // a cluster per group
-  int beams, ranks;
-  float* out_totals;  // [groups, k]
+  int beams, rank_shift;  // 2^rank_shift blocks per beam
+  float* out_totals;      // [groups, k]
   int32_t* out_beams;
   int32_t* out_ids;
 };
@@ -298,7 +298,8 @@ __device__ __forceinline__ double key_total(uint64_t k) {
 // A block's statistics and the length of its list.
 struct alignas(16) Part {
   float m, z;
-  int len, pad;
+  int len;
+  float t;  // the beam's running total
 };
 // The statistics of `parts` parts (at most 8), in every lane of a warp.
 __device__ __forceinline__ Online join_stats(float m, float z) {
@@ -330,47 +331,55 @@ __device__ __forceinline__ bool has_softmax(const Online& o) {
   return o.z > 0.f && o.z < INFINITY;
 }
 
-// The lists of a group's blocks ([size, k], `ranks` of them per beam), ranked.
+// Entries of a list where a cluster ranks several: whole 16-byte vectors, zeros at the end.
+__host__ __device__ inline int list_stride(int k) { return (k + 1) & ~1; }
+
+// The lists of a group's blocks ([size, stride], 2^rank_shift of them per beam), ranked.
 __device__ void rank_group(const SelectArgs& a, int64_t group, int size, const uint64_t* lists,
                            uint64_t* totals, const Part* all) {
   __shared__ double base[kMaxGroup];  // t - log Z
   __shared__ float top[kMaxGroup];
   __shared__ int len[kMaxGroup];  // of each beam's list, 0 where it has no softmax
-  const int k = a.k;
+  const int k = a.k, stride = list_stride(k), shift = a.rank_shift;
   if (threadIdx.x < a.beams) {
     Online o;
     int n = 0;
-    for (int p = threadIdx.x * a.ranks; p < int(threadIdx.x + 1) * a.ranks; ++p) {
+    const int p0 = int(threadIdx.x) << shift;
+    for (int p = p0; p < p0 + (1 << shift); ++p) {
       o.join(all[p].m, all[p].z);
       n += all[p].len;
     }
     const bool ok = has_softmax(o);
     top[threadIdx.x] = o.m;
-    base[threadIdx.x] = ok ? double(a.totals[group * a.beams + threadIdx.x]) - log_sum(o.z) : 0.0;
+    base[threadIdx.x] = ok ? double(all[p0].t) - log_sum(o.z) : 0.0;
     len[threadIdx.x] = ok ? n : 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < size * k; i += kThreads) {
-    const int p = i / k, b = p / a.ranks;
-    const bool ok = len[b] > 0 && i - p * k < all[p].len;
-    const double d = double(key_to_float(uint32_t(lists[i] >> 32))) - double(top[b]);
-    totals[i] = ok ? total_key(d + base[b]) : 0;  // 0 is below every total
+  // size * stride entries, one per thread at most
+  const int i = threadIdx.x, p = i / stride, beam = p >> shift;
+  uint64_t mine = 0, e = 0;
+  if (p < size) {
+    e = lists[i];
+    if (len[beam] > 0 && i - p * stride < all[p].len)
+      mine = total_key(double(key_to_float(uint32_t(e >> 32))) - double(top[beam]) + base[beam]);
+    totals[i] = mine;  // 0 is below every total
   }
   __syncthreads();
   int n = 0;
   for (int b = 0; b < a.beams; ++b) n += len[b];
-  for (int i = threadIdx.x; i < size * k; i += kThreads) {
-    const uint64_t mine = totals[i], e = lists[i];
-    if (mine == 0) continue;
-    const int beam = i / k / a.ranks;
+  if (mine != 0) {
     int place = 0;
-    for (int p = 0; p < size; ++p) {
-      const int b = p / a.ranks;
+    for (int q = 0; q < size; ++q) {
+      const int b = q >> shift;
       // a beam's own entries by score; of equal totals the lower beam's come first
-      const uint64_t* of = (b == beam ? lists : totals) + p * k;
+      const ulonglong2* of =
+          reinterpret_cast<const ulonglong2*>((b == beam ? lists : totals) + q * stride);
       const uint64_t than = b == beam ? e : mine - (b < beam);
 #pragma unroll 4
-      for (int j = 0; j < k; ++j) place += of[j] > than;
+      for (int j = 0; j < stride / 2; ++j) {
+        const ulonglong2 v = of[j];
+        place += (v.x > than) + (v.y > than);
+      }
     }
     if (place < k) {
       a.out_totals[group * k + place] = float(key_total(mine));
@@ -378,10 +387,10 @@ __device__ void rank_group(const SelectArgs& a, int64_t group, int size, const u
       a.out_ids[group * k + place] = int32_t(~uint32_t(e));
     }
   }
-  for (int i = n + threadIdx.x; i < k; i += kThreads) {
-    a.out_totals[group * k + i] = -INFINITY;
-    a.out_beams[group * k + i] = -1;
-    a.out_ids[group * k + i] = -1;
+  for (int j = n + threadIdx.x; j < k; j += kThreads) {
+    a.out_totals[group * k + j] = -INFINITY;
+    a.out_beams[group * k + j] = -1;
+    a.out_ids[group * k + j] = -1;
   }
 }
 
@@ -390,9 +399,10 @@ template <class T, bool VEC, bool GROUP>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs a) {
   constexpr int N = Span<T>::N;
   extern __shared__ __align__(16) uint64_t select_smem[];
+  const int stride = list_stride(a.k);
   uint64_t* kept = select_smem;  // [kCap]
   uint64_t* top = kept + kCap;   // [k]
-  uint64_t* others = top + a.k;  // [blocks, k] where a cluster has several
+  uint64_t* others = top + stride;  // [blocks, stride] where a cluster has several
   // the peaks (one array with `kept`, which is filled when they have been read)
   uint32_t* peak = reinterpret_cast<uint32_t*>(select_smem);
   __shared__ uint16_t chosen[kMaxSteps * kThreads];
@@ -401,9 +411,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
   __shared__ int nkept, nchosen;
   __shared__ uint32_t keys[kThreads];
   const int size = int(gridDim.x), block = int(blockIdx.x);  // of the cluster
-  const int ranks = GROUP ? a.ranks : size, rank = GROUP ? block % ranks : block;
+  const int ranks = GROUP ? 1 << a.rank_shift : size, rank = GROUP ? block & (ranks - 1) : block;
   const int64_t item = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
-  const int64_t row = GROUP ? item * a.beams + block / ranks : item;
+  const int64_t row = GROUP ? item * a.beams + (block >> a.rank_shift) : item;
   if (item >= (GROUP ? a.rows / a.beams : a.rows)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float t = a.totals[row];
@@ -504,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
   if (size > 1 || GROUP) {
     // to the first block: its `others` and `all`
     if (size > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    for (int i = threadIdx.x; i < a.k; i += kThreads)
-      st_cluster64(map_rank(smem_u32(others + block * a.k + i), 0), i < n ? top[i] : 0);
+    for (int i = threadIdx.x; i < stride; i += kThreads)
+      st_cluster64(map_rank(smem_u32(others + block * stride + i), 0), i < n ? top[i] : 0);
     if (threadIdx.x == kThreads - 1) {
       const uint32_t at = map_rank(smem_u32(&all[block]), 0);
       st_cluster64(at, pair(o_block.m, o_block.z));
-      st_cluster64(at + 8, uint64_t(n));
+      st_cluster64(at + 8, uint64_t(n) | uint64_t(__float_as_uint(t)) << 32);
     }
     if (size > 1) {
       asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -532,23 +542,23 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const SelectArgs
                            lane % kMaxCluster < ranks ? p.z : 0.f);
     }
   }
-  for (int i = threadIdx.x; i < ranks * a.k; i += kThreads) {
-    const int mine = i / a.k, at = i - mine * a.k;
+  for (int i = threadIdx.x; i < ranks * stride; i += kThreads) {
+    const int mine = i / stride, at = i - mine * stride;
     if (at >= (ranks > 1 ? all[mine].len : n)) continue;
     const uint64_t e = lists[i];
     int place = at;
-    if (ranks > 1 && ranks * a.k <= kThreads) {
+    if (ranks > 1 && ranks * stride <= kThreads) {
       // few: those above this one, counted (nothing is below every entry)
       place = 0;
 #pragma unroll 4
-      for (int j = 0; j < ranks * a.k; ++j) place += lists[j] > e;
+      for (int j = 0; j < ranks * stride; ++j) place += lists[j] > e;
     }
-    for (int p = 0; p < ranks && ranks * a.k > kThreads; ++p) {
+    for (int p = 0; p < ranks && ranks * stride > kThreads; ++p) {
       if (p == mine) continue;
       int lo = 0, hi = all[p].len;  // entries of that list above mine
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (lists[p * a.k + mid] > e)
+        if (lists[p * stride + mid] > e)
           lo = mid + 1;
         else
           hi = mid;
@@ -642,19 +652,21 @@ int ranks_for(int64_t rows, int64_t cols, int most) {
 bool group_fits(const SelectArgs& a, int* ranks) {
   if (a.beams > kMaxGroup) return false;
   *ranks = ranks_for(a.rows, a.cols, kMaxGroup / a.beams);
-  return a.beams * *ranks * a.k <= kThreads &&
+  return a.beams * *ranks * list_stride(a.k) <= kThreads &&
          (*ranks == ranks_for(a.rows, a.cols, kMaxCluster) || a.cols <= 16384 * int64_t(*ranks));
 }
 
 template <class T, bool GROUP>
 int launch_rows(SelectArgs a, int ranks, cudaStream_t s) {
-  a.ranks = ranks;
+  a.rank_shift = 0;
+  while (1 << a.rank_shift < ranks) ++a.rank_shift;  // ranks are powers of two
   a.chunk = int(ceil_div(ceil_div(a.cols, ranks), 8) * 8);
   const int64_t steps = ceil_div(a.chunk, int64_t(kThreads) * kUnroll * Span<T>::N);
   a.shift = 0;
   while (ceil_div(steps, int64_t(1) << a.shift) > kMaxSteps) ++a.shift;
   const int size = GROUP ? a.beams * ranks : ranks;
-  const size_t smem = (size_t(kCap) + size_t(a.k) * (size == 1 && !GROUP ? 1 : 1 + size)) * 8;
+  const size_t smem =
+      (size_t(kCap) + size_t(list_stride(a.k)) * (size == 1 && !GROUP ? 1 : 1 + size)) * 8;
   constexpr int N = Span<T>::N;
   const bool vec = a.cols % N == 0 && a.lds % N == 0 &&
                    reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
@@ -727,7 +739,7 @@ extern "C" int beam_select(const void* scores, int dtype, int64_t groups, int be
                 "beam_select: end_id=%d outside [0, %lld)", end_id, (long long)cols);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = groups * beams;
-  SelectArgs a{scores, rows, cols, lds, totals, finished, end_id, k, 0, 0, {}, beams, 1, out_totals,
+  SelectArgs a{scores, rows, cols, lds, totals, finished, end_id, k, 0, 0, {}, beams, 0, out_totals,
                out_beams, out_ids};
   int ranks = 0;
   if (group_fits(a, &ranks))
