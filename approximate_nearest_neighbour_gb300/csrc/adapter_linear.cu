@@ -22,6 +22,14 @@
 //     over columns. h is fp32: it is cut into two terms of the operands' type
 //     (three, if bf16 operands make an fp32 output), each exact to the next, so
 //     that nothing of it is rounded away beyond 2^-17 (2^-22 for fp16, 2^-25 for three).
+// Many tokens go through kernels of their own (adapter_wide.cu), but for the second
+// product where an adapter's rows of B are not multiples of 16 bytes.
+//
+// Measured: 77 tokens of 64 adapters, rank 16, 4096 x 16384 bf16 (35 MB): 7.9 us for h and
+// 13.4 us for the output with cold caches, which overlap to 21.4 to 23.1 us as a program
+// calls it; 5.3 us are the bytes. Each block of the second product waits for h, its tile's
+// B and its base rows one after the other, and a wave is all there is. One token,
+// 4096 x 16384: 5.9 and 4.3 us, two starts of a kernel.
 #include <algorithm>
 
 #include "adapter.cuh"
@@ -673,7 +681,8 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   p.pitch = 8;
   while (p.pitch < rank) p.pitch *= 2;
   // tiles of 128 tokens also where few adapters of a high rank have many each: a tile of
-  // 16 reads its adapter's B again
+  // 16 reads its adapter's B again (256 tokens of one adapter, 4096 x 16384: rank 128 44 us
+  // in tiles of 16 and 29 us in tiles of 128, rank 16 21.5 us, and 26 us for 257 tokens)
   const bool wide = tokens > kFew || (rank > 32 && tokens >= 64 && tokens >= 32 * int64_t(adapters));
   p.tile = wide ? kMaxTile : kFewTile;
   const int64_t tiles =

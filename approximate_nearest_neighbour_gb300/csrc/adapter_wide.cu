@@ -18,9 +18,11 @@
 //  - four groups of four warps take units in turn. A warp brings its 32 base rows into
 //    a place of its own in shared memory, adds the accumulator to them there, a row
 //    per thread, writes them in whole lines, and asks for those of its next unit.
-// What was measured at 8192 x 16384 bf16, rank 64: registers instead of shared memory (a
-// warp's 32 columns of 16 rows, fetched four steps ahead) 176 us; rows by bulk copies of
-// 256 bytes, which the copy engine takes one every 30 clocks or so, 250 us.
+// Measured at 8192 tokens, 4096 x 16384 bf16, rank 64, 6 adapters: h 22 us (67 MB, 3.0 TB/s:
+// few blocks, each a chain of copies and products), the output 93 us (537 MB, 5.8 TB/s).
+// The output through registers instead of shared memory (a warp's 32 columns of 16 rows,
+// fetched four steps ahead) took 176 us; with rows by bulk copies of 256 bytes, which the
+// copy engine takes one every 30 clocks or so, 250 us.
 #include <limits.h>
 
 #include <algorithm>
@@ -341,8 +343,10 @@ struct Segment {
   int units;
 };
 
-// VEC: rows of base and out are whole vectors on 16-byte boundaries. Others are
-// loaded and stored a column per lane.
+// VEC: rows of base and out are whole vectors on 16-byte boundaries. Others are copied
+// in words, from the word that a row's first column lies in: a 16-bit row that starts
+// between two words lies half a word further on in shared memory, too, and its thread
+// moves the columns while it adds.
 template <class T, class O, int KC, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     adapter_expand_wide_kernel(const __grid_constant__ CUtensorMap map_b, const AdapterArgs a,
@@ -501,8 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int swap[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) swap[j] = (ch ^ (2 * j + sub)) * 16;
-    const uint32_t base_pitch = uint32_t(a.ldb * int64_t(sizeof(O)));  // VEC: below 2^32
-    const uint32_t out_pitch = uint32_t(a.ldo * int64_t(sizeof(O)));
+    using Pitch = std::conditional_t<VEC, uint32_t, uint64_t>;  // VEC: below 2^32
+    const Pitch base_pitch = Pitch(a.ldb * int64_t(sizeof(O)));
+    const Pitch out_pitch = Pitch(a.ldo * int64_t(sizeof(O)));
+    // not VEC: this lane's words of row i are here and 128 bytes on; `beyond` is the word
+    // behind a unit's 64 of the lane's own row, where its columns end in there
+    auto word = [&](int i) {
+      return mine + i * kRowBytes + (((lane >> 2) ^ (i & 7)) * 16) + (lane & 3) * 4;
+    };
+    constexpr bool kHalves = !VEC && sizeof(O) == 2;
+    uint32_t beyond = 0;
     auto token_here = [&](const Segment& g) {
       return g.units > 0 && row < g.tile.count ? uint32_t(token_of(a, g.tile.first + row)) : 0u;
     };
@@ -525,6 +537,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto fetch = [&]() {
       settle();
+      if (!VEC && base && works && fk != INT_MAX) {
+        const int64_t chunk = fg.chunk + fk;
+        const int bytes = row_bytes(chunk), nrows = fg.tile.count - 32 * lg;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(base + chunk * CN);
+        auto copy_word = [](uint8_t* to, uintptr_t p) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)),
+                       "l"(reinterpret_cast<const void*>(p))
+                       : "memory");
+        };
+        if (nrows >= 32 && bytes == kRowBytes) {
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) {
+            const uintptr_t p = from + __shfl_sync(kFullMask, ftok, i) * base_pitch;
+            const uintptr_t w = (p & ~uintptr_t(3)) + 4 * lane;
+            copy_word(word(i), w);
+            copy_word(word(i) + 128, w + 128);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < min(32, nrows); ++i) {
+            const uintptr_t p = from + __shfl_sync(kFullMask, ftok, i) * base_pitch;
+            const uintptr_t w = (p & ~uintptr_t(3)) + 4 * lane;
+            const int end = bytes + int(p & 3);  // words that begin before are asked for
+            if (4 * lane < end) copy_word(word(i), w);
+            if (4 * lane + 128 < end) copy_word(word(i) + 128, w + 128);
+          }
+        }
+        if constexpr (kHalves) {
+          const uintptr_t p = from + ftok * base_pitch;
+          if (lane < nrows && (p & 2) && bytes == kRowBytes)
+            beyond = *reinterpret_cast<const uint32_t*>(p - 2 + kRowBytes);
+        }
+      }
       if (VEC && base && works && fk != INT_MAX) {
         const int64_t chunk = fg.chunk + fk;
         const int bytes = row_bytes(chunk), nrows = fg.tile.count - 32 * lg;
@@ -617,24 +662,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ab = (it + k) % kGroups;
         const int64_t chunk = g.chunk + k;
         const int bytes = row_bytes(chunk);
-        if constexpr (VEC) {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        } else if (base) {
-          const int ncols = bytes / int(sizeof(O));
-          constexpr int N = Span<O>::N;
-#pragma unroll 8
-          for (int i = 0; i < nrows; ++i) {
-            const O* q = base + int64_t(__shfl_sync(kFullMask, tok, i)) * a.ldb + chunk * CN;
-#pragma unroll
-            for (int c = lane; c < CN; c += 32)
-              if (c < ncols) reinterpret_cast<O*>(piece(i, c / N))[c % N] = q[c];
-          }
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         wait(acc_full(ab), ((it + k) / kGroups) & 1);
         __syncwarp();
         tc_fence_after();
         uint8_t* here = mine + lane * kRowBytes;
         const int turn = (lane & 7) * 16;
+        // bits by which the row's words are off its columns, read and written
+        const uintptr_t out_row = reinterpret_cast<uintptr_t>(static_cast<O*>(a.out) + chunk * CN) +
+                                  tok * out_pitch;
+        const uint32_t in_off =
+            kHalves ? uint32_t((reinterpret_cast<uintptr_t>(base) + tok * base_pitch) & 2) * 8 : 0;
+        const uint32_t out_off = kHalves ? uint32_t(out_row & 2) * 8 : 0;
+        uint32_t first = 0, before = 0;  // the first two columns, the last two so far
+        uint4 ahead;
+        if (kHalves && base) ahead = *reinterpret_cast<const uint4*>(here + turn);
 #pragma unroll
         for (int c = 0; c < CN; c += 32) {
           uint32_t d[32];
@@ -658,12 +700,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (base) {
               float v[N];
-              unpack_vec<O>(*at, v);
+              if constexpr (kHalves) {
+                const int next = c / N + q + 1;
+                uint4 h = ahead;
+                ahead = next * 16 < kRowBytes
+                            ? *reinterpret_cast<const uint4*>(here + ((next * 16) ^ turn))
+                            : make_uint4(beyond, 0, 0, 0);
+                h.x = __funnelshift_r(h.x, h.y, in_off);
+                h.y = __funnelshift_r(h.y, h.z, in_off);
+                h.z = __funnelshift_r(h.z, h.w, in_off);
+                h.w = __funnelshift_r(h.w, ahead.x, in_off);
+                unpack_vec<O>(h, v);
+              } else {
+                unpack_vec<O>(*at, v);
+              }
 #pragma unroll
               for (int x = 0; x < N; x += 2)
                 unpair(add2(pair(v[x], v[x + 1]), pair(w[x], w[x + 1])), w[x], w[x + 1]);
             }
-            *at = pack_vec<O>(w);
+            uint4 o = pack_vec<O>(w);
+            if constexpr (kHalves) {
+              if (c + q == 0) first = o.x;
+              const uint32_t last = o.w;
+              o.w = __funnelshift_l(o.z, o.w, out_off);
+              o.z = __funnelshift_l(o.y, o.z, out_off);
+              o.y = __funnelshift_l(o.x, o.y, out_off);
+              o.x = __funnelshift_l(before, o.x, out_off);
+              before = last;
+            }
+            *at = o;
           }
         }
         tc_fence_before();
@@ -690,15 +755,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           } else {
-            const int ncols = bytes / int(sizeof(O));
-            constexpr int N = Span<O>::N;
+            const uintptr_t to = reinterpret_cast<uintptr_t>(static_cast<O*>(a.out) + chunk * CN);
+            if (nrows == 32 && bytes == kRowBytes) {
 #pragma unroll 8
-            for (int i = 0; i < nrows; ++i) {
-              O* q = static_cast<O*>(a.out) + int64_t(__shfl_sync(kFullMask, tok, i)) * a.ldo +
-                     chunk * CN;
-#pragma unroll
-              for (int c = lane; c < CN; c += 32)
-                if (c < ncols) q[c] = reinterpret_cast<const O*>(piece(i, c / N))[c % N];
+              for (int i = 0; i < 32; ++i) {
+                const uintptr_t p = to + __shfl_sync(kFullMask, tok, i) * out_pitch;
+                uint32_t* w = reinterpret_cast<uint32_t*>((p & ~uintptr_t(3)) + 4 * lane);
+                if (!kHalves || lane > 0 || !(p & 2))
+                  *w = *reinterpret_cast<const uint32_t*>(word(i));
+                w[32] = *reinterpret_cast<const uint32_t*>(word(i) + 128);
+              }
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < nrows; ++i) {
+                const uintptr_t p = to + __shfl_sync(kFullMask, tok, i) * out_pitch;
+                uint32_t* w = reinterpret_cast<uint32_t*>((p & ~uintptr_t(3)) + 4 * lane);
+                const int end = bytes + int(p & 3);  // whole words of the row
+                if (4 * lane + 4 <= end && (lane > 0 || !(p & 3)))
+                  *w = *reinterpret_cast<const uint32_t*>(word(i));
+                if (4 * lane + 132 <= end) w[32] = *reinterpret_cast<const uint32_t*>(word(i) + 128);
+              }
+            }
+            if constexpr (kHalves) {  // a row's first and last column in a word with others
+              const int end = bytes + int(out_row & 2);
+              if (lane < nrows && (out_row & 2))
+                *reinterpret_cast<uint16_t*>(out_row) = uint16_t(first);
+              if (lane < nrows && (end & 2)) {
+                const uint32_t w = end / 4 * 4 == kRowBytes
+                                       ? before >> 16
+                                       : *reinterpret_cast<const uint32_t*>(
+                                             piece(lane, end / 16) + end % 16 / 4 * 4);
+                *reinterpret_cast<uint16_t*>(out_row + bytes - 2) = uint16_t(w);
+              }
             }
           }
         }

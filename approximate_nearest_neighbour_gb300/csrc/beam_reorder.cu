@@ -12,6 +12,11 @@
 // sources, and a thread loads its part when the source changes. In place, a
 // thread first keeps its part of every source that moves in shared memory, and
 // then writes: its bytes are its own, so no barrier is needed.
+//
+// Measured: 16 x 4 rows of two states of 8 x 4096 x 128 bf16 and their histories, lengths
+// from a quarter to all, not in place: 153 to 163 us; as many bytes at the copy rate take
+// 163 us. 4 rows of four states of 8 x 200 x 128: 5.8 us on the device, the launch and one
+// dependent chain (ids, lengths, rows).
 #include <algorithm>
 
 #include "common.cuh"
@@ -142,7 +147,8 @@ template <bool IN_PLACE>
 int launch(ReorderArgs& a, cudaStream_t s) {
   if (a.count == 0) return IVFPQ_OK;
   const int threads = IN_PLACE ? kInPlaceThreads : kThreads;
-  // four vectors per thread, one while that leaves blocks for few SMs
+  // four vectors per thread, one while that leaves blocks for few SMs: a thread takes a
+  // source's vectors one row after the other, and few blocks have nothing to hide it
   for (a.run = threads * (IN_PLACE ? 1 : kUnroll);; a.run = threads) {
     a.blocks = 0;
     for (int i = 0; i < a.count; ++i) {

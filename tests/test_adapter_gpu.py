@@ -196,3 +196,27 @@ def test_rows_of_one_value(B):
         got = B.adapter_linear(**c)
         assert torch.equal(got, got[:1].expand(tokens, 40))
         _check(got, **c)
+
+
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("bf16", "bf16"), ("f16", "f32"),
+                                       ("bf16", "f32")])
+@pytest.mark.parametrize("rank", [24, 72])
+def test_rows_at_any_offset(B, dtype, out, rank):
+    """Base rows and output rows that start anywhere, each at its own offset, of full and
+    of last units: the same results to the bit, and nothing beside them is written."""
+    import torch
+    for n in (1, 2, 3, 63, 64, 127, 128, 129, 255, 257, 386):
+        c = _case(300, 64, n, rank, 2, dtype, out, n, runs=True)
+        want = B.adapter_linear(**c)
+        _check(want, **c)
+        for i, o, wide in ((0, 1, 1), (1, 0, 1), (1, 1, 2), (2, 3, 2), (3, 2, 4), (7, 8, 8)):
+            base = torch.full((300 * (n + wide) + i,), 7.0, dtype=_dt(out), device="cuda")
+            base = base[i:].view(300, n + wide)[:, :n]
+            base.copy_(c["base"])
+            room = torch.full((1 + o + 300 * (n + wide),), 3.0, dtype=_dt(out), device="cuda")
+            rows = room[1 + o:].view(300, n + wide)
+            B.adapter_linear(**dict(c, base=base, out=rows[:, :n]))
+            assert torch.equal(rows[:, :n], want), (n, i, o, wide)
+            assert (room[:1 + o] == 3).all() and (rows[:, n:] == 3).all()
+            B.adapter_linear(**dict(c, base=base, out=base))
+            assert torch.equal(base, want), (n, i, o, wide)
