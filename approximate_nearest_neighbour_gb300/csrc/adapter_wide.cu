@@ -84,31 +84,40 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 
 // ---- h = x A^T ------------------------------------------------------------------------
 constexpr int kLoadWarps = 8, kShrinkThreads = (kLoadWarps + 1) * 32;
-template <int R>
+template <int R, bool ALIGNED>
 struct ShrinkCfg {
   static constexpr int NR = R < 16 ? 16 : R;  // the instruction's least width is 16
   static constexpr int kStage = (kRows + NR) * 128;
-  static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
-  static constexpr int kTotal = kStages * kStage + 8 * (2 * kStages + 1) + 16 + 1024;
+  static constexpr int kFit = ALIGNED ? 200 * 1024 / kStage : 2;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  // not ALIGNED: steps as they lie in memory
+  static constexpr int kRawRow = 128 + 16, kRaw = (kRows + NR) * kRawRow;
+  static constexpr int kRawFit = ALIGNED ? 0 : (220 * 1024 - kStages * kStage) / kRaw;
+  static constexpr int kRaws = kRawFit < 8 ? kRawFit : 8;
+  static constexpr int kTotal =
+      kStages * kStage + kRaws * kRaw + 8 * (2 * kStages + 1) + 16 + 1024;
   static constexpr int kTmem = NR < 32 ? 32 : NR;
   static_assert(kTotal <= 227 * 1024, "fits shared memory");
 };
 
-// ALIGNED: rows of x and A are multiples of 16 bytes and start on one. Others go through
-// registers instead of asynchronous copies; the sums are the same.
+// ALIGNED: rows of x and A are multiples of 16 bytes and start on one. Others are copied as
+// they lie, in whole vectors, and shifted into the operands' place; the sums are the same.
+// (Shifted on their way through registers, 8192 rows of 4097 columns at rank 128 took
+// 108 us: the loads of a step's rows waited for each other.)
 template <class T, int R, bool ALIGNED>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
     adapter_shrink_wide_kernel(const AdapterArgs a, int* err) {
-  using C = ShrinkCfg<R>;
+  using C = ShrinkCfg<R, ALIGNED>;
   extern __shared__ uint8_t shrink_raw[];
   const uint32_t raw = smem_u32(shrink_raw);
   const uint32_t base_addr = (raw + 1023u) & ~1023u;
   uint8_t* mem = shrink_raw + (base_addr - raw);
-  const uint32_t bars = base_addr + C::kStages * C::kStage;
+  constexpr int kOperands = C::kStages * C::kStage + C::kRaws * C::kRaw;
+  const uint32_t bars = base_addr + kOperands;
   auto full = [&](int i) { return bars + 8 * i; };
   auto empty = [&](int i) { return bars + 8 * (C::kStages + i); };
   const uint32_t done = bars + 8 * 2 * C::kStages;
-  uint8_t* tail = mem + C::kStages * C::kStage + 8 * (2 * C::kStages + 1);
+  uint8_t* tail = mem + kOperands + 8 * (2 * C::kStages + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -199,53 +208,55 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         }
       }
     } else {
-      uint4 kept[2][XR + WR];
-      auto load = [&](int i, uint4 (&v)[XR + WR]) {
-        const int64_t at = k0 + int64_t(i) * 64, k = at + ch * 8;
-        if (i < steps && at + 72 <= a.cols) {
-          // eight columns more in every row: loads that do not wait for each other; a
-          // row that is not there is another's, made zero
-          const T* some = x[0] ? x[0] : static_cast<const T*>(a.x);
+      // the 16-byte vectors that the columns lie in, eight and one more of every row
+      constexpr int P = XR + WR, L = C::kRaws - 1;  // steps on their way
+      const int bytes = int(k1 - k0) * 2;
+      uintptr_t from[P];
+      int mis[P];
 #pragma unroll
-          for (int j = 0; j < XR; ++j) v[j] = load_across((x[j] ? x[j] : some) + k);
-#pragma unroll
-          for (int j = 0; j < WR; ++j) {
-            const T* p = C::NR % 32 == 0 || r0 + 32 * j < C::NR ? w_row(r0 + 32 * j) : nullptr;
-            v[XR + j] = load_across((p ? p : some) + k);
-            if (!p) v[XR + j] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int j = 0; j < XR; ++j)
-            if (!x[j]) v[j] = make_uint4(0, 0, 0, 0);
-          return;
-        }
-        const int64_t len = i < steps && k < k1 ? a.cols : 0;
-#pragma unroll
-        for (int j = 0; j < XR; ++j) v[j] = row8(x[j], len, k);
-#pragma unroll
-        for (int j = 0; j < WR; ++j)
-          v[XR + j] = row8(C::NR % 32 == 0 || r0 + 32 * j < C::NR ? w_row(r0 + 32 * j) : nullptr,
-                           len, k);
+      for (int j = 0; j < P; ++j) {
+        const int row = r0 + 32 * (j - XR);
+        const T* p = j < XR ? x[j < XR ? j : 0] : row < C::NR ? w_row(row) : nullptr;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p + k0);
+        mis[j] = int(at & 15);
+        from[j] = p ? at - mis[j] + ch * 16 : 0;
+      }
+      const uintptr_t some = reinterpret_cast<uintptr_t>(a.a) & ~uintptr_t(15);
+      auto copy = [&](uint32_t to, uintptr_t row, int at, int left) {  // zeros past the row
+        const bool live = row && left > 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                     "l"(reinterpret_cast<const void*>(live ? row + at : some)),
+                     "r"(live ? min(left, 16) : 0)
+                     : "memory");
       };
-      auto put = [&](int i, const uint4 (&v)[XR + WR]) {
-        if (i >= steps) return;
-        const int s = i % C::kStages;
-        wait(empty(s), ((i / C::kStages) & 1) ^ 1);
+      auto here = [&](int j) { return j < XR || C::NR % 32 == 0 || r0 + 32 * (j - XR) < C::NR; };
+      const uint32_t raws = uint32_t(C::kStages * C::kStage) + r0 * C::kRawRow + ch * 16;
+      for (int i = 0; i < steps + L; ++i) {
+        if (i < steps) {
+          const uint32_t to = base_addr + raws + i % C::kRaws * C::kRaw;
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            if (!here(j)) continue;
+            const int left = bytes + mis[j] - i * 128 - ch * 16;
+            copy(to + 32 * j * C::kRawRow, from[j], i * 128, left);
+            if (ch == 7) copy(to + 32 * j * C::kRawRow + 16, from[j], i * 128 + 16, left - 16);
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (i < L) continue;
+        const int n = i - L, s = n % C::kStages;
+        asm volatile("cp.async.wait_group %0;" ::"n"(L) : "memory");
+        __syncwarp();  // a row's nine vectors are one warp's
+        wait(empty(s), ((n / C::kStages) & 1) ^ 1);
+        const uint8_t* raw = mem + raws + n % C::kRaws * C::kRaw;
         uint8_t* at = mem + s * C::kStage + place;
 #pragma unroll
-        for (int j = 0; j < XR; ++j) *reinterpret_cast<uint4*>(at + 32 * j * 128) = v[j];
-#pragma unroll
-        for (int j = 0; j < WR; ++j)
-          if (C::NR % 32 == 0 || r0 + 32 * j < C::NR)
-            *reinterpret_cast<uint4*>(at + (kRows + 32 * j) * 128) = v[XR + j];
-        give(i);
-      };
-      load(0, kept[0]);
-      for (int i = 0; i < steps; i += 2) {
-        load(i + 1, kept[1]);
-        put(i, kept[0]);
-        load(i + 2, kept[0]);
-        put(i + 1, kept[1]);
+        for (int j = 0; j < P; ++j) {
+          if (!here(j)) continue;
+          const uint4* v = reinterpret_cast<const uint4*>(raw + 32 * j * C::kRawRow);
+          *reinterpret_cast<uint4*>(at + 32 * j * 128) = shift_across(v[0], v[1], mis[j]);
+        }
+        give(n);
       }
     }
   } else {
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 
 template <class T, int R, bool ALIGNED>
 int launch_shrink(const AdapterArgs& a, int64_t tiles, cudaStream_t s) {
-  using C = ShrinkCfg<R>;
+  using C = ShrinkCfg<R, ALIGNED>;
   int* err = nullptr;
   IVFPQ_TRY(device_status_word(&err));
   auto kern = adapter_shrink_wide_kernel<T, R, ALIGNED>;

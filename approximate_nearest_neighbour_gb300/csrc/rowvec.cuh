@@ -150,15 +150,8 @@ __device__ __forceinline__ uint4 load_inner(const T* p, int i, int mis) {
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
-// The 16 bytes at p, whatever its alignment, as two loads without a branch, so that
-// several do not wait for each other: the 32 bytes from the 16-byte boundary at or
-// before p on belong to the row or, before its start, to its allocation.
-template <class T>
-__device__ __forceinline__ uint4 load_across(const T* p) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const uint4* b = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
-  const uint4 x = b[0], y = b[1];
-  const int mis = int(at & 15);
+// The 16 bytes from byte `mis` of x and y on, without a branch.
+__device__ __forceinline__ uint4 shift_across(const uint4& x, const uint4& y, int mis) {
   uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int j = 0; j < 6; ++j) w[j] = mis & 8 ? w[j + 2] : w[j];

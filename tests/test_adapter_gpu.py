@@ -220,3 +220,24 @@ def test_rows_at_any_offset(B, dtype, out, rank):
             assert (room[:1 + o] == 3).all() and (rows[:, n:] == 3).all()
             B.adapter_linear(**dict(c, base=base, out=base))
             assert torch.equal(base, want), (n, i, o, wide)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [8, 24, 128])
+def test_odd_columns(B, dtype, rank):
+    """Rows of x and of the adapters that start anywhere and end inside a vector: to the
+    bit what the same rows with zeros behind them give."""
+    import torch
+    for cols in (1, 7, 63, 65, 71, 127, 129, 1001):
+        c = _case(300, cols, 96, rank, 2, dtype, "f32", cols, runs=True)
+        got = B.adapter_linear(**c)
+        _check(got, **c)
+        more = -cols % 8
+        d = dict(c, **{k: torch.nn.functional.pad(c[k], (0, more)) for k in ("x", "a")})
+        assert torch.equal(B.adapter_linear(**d), got), cols
+        # what lies beside the rows, infinities even, is not looked at
+        room = torch.full((300, cols + 9), float("inf"), dtype=_dt(dtype), device="cuda")
+        for off in (1, 4, 9):
+            room.fill_(float("inf"))
+            room[:, off:off + cols] = c["x"]
+            assert torch.equal(B.adapter_linear(**dict(c, x=room[:, off:off + cols])), got), cols
