@@ -1036,12 +1036,14 @@ def _state(t, o, axis, groups, width, n, lengths, at, index):
     shape, so, size = t.shape, o.shape, t.element_size()
     dims = len(shape)
     if dims < 1 or shape[0] != groups * width:
-        raise ValueError(f"states[{index}] must have {groups * width} rows, got shape {tuple(shape)}")
+        raise ValueError(f"states[{index}] must have {groups * width} rows, got shape "
+                         f"{tuple(shape)}")
     if o is not t and (o.dtype != t.dtype or so[0] != groups * n or so[1:] != shape[1:]):
-        raise ValueError(f"the output of states[{index}] must be {t.dtype} with {groups * n} rows of its "
-                         f"shape, got {o.dtype} {tuple(so)}")
+        raise ValueError(f"the output of states[{index}] must be {t.dtype} with {groups * n} "
+                         f"rows of its shape, got {o.dtype} {tuple(so)}")
     if lengths and not 1 <= axis < dims:
-        raise ValueError(f"states[{index}]: positions must be one of its dimensions 1 to {dims - 1}")
+        raise ValueError(f"states[{index}]: positions must be one of its dimensions 1 to "
+                         f"{dims - 1}")
     st = t.stride()
     sto = st if o is t else o.stride()
     if lengths:
@@ -1056,7 +1058,7 @@ def _state(t, o, axis, groups, width, n, lengths, at, index):
         if not lengths:
             return (t.data_ptr(), o.data_ptr(), row, row, 1, 0, 0, row, 0)
         return (t.data_ptr(), o.data_ptr(), row, row, row // inner if inner else 0, inner,
-                      inner, inner, unit)
+                inner, inner, unit)
     first = max(_dense_tail(shape, st), _dense_tail(shape, sto))
     if lengths:
         if first > axis:
@@ -1071,7 +1073,7 @@ def _state(t, o, axis, groups, width, n, lengths, at, index):
     src_row = st[0] if shape[0] > 1 else 0
     dst_row = sto[0] if so[0] > 1 else 0
     return (t.data_ptr(), o.data_ptr(), src_row * size, dst_row * size, outer,
-                  src_outer * size, dst_outer * size, inner, unit)
+            src_outer * size, dst_outer * size, inner, unit)
 
 
 def beam_reorder(states, beams, lengths=None, axis=1, out=None, stream=None):

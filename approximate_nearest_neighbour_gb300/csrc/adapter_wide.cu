@@ -102,8 +102,9 @@ struct ShrinkCfg {
 
 // ALIGNED: rows of x and A are multiples of 16 bytes and start on one. Others are copied as
 // they lie, in whole vectors, and shifted into the operands' place; the sums are the same.
-// (Shifted on their way through registers, 8192 rows of 4097 columns at rank 128 took
-// 108 us: the loads of a step's rows waited for each other.)
+// (8192 rows at rank 128: 27 us with 4096 columns, 50 us with 4097; shifted on their way
+// through registers they took 108 us, since the loads of a step's rows waited for each
+// other.)
 template <class T, int R, bool ALIGNED>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
     adapter_shrink_wide_kernel(const AdapterArgs a, int* err) {
@@ -357,7 +358,7 @@ struct Segment {
 // VEC: rows of base and out are whole vectors on 16-byte boundaries. Others are copied
 // in words, from the word that a row's first column lies in: a 16-bit row that starts
 // between two words lies half a word further on in shared memory, too, and its thread
-// moves the columns while it adds.
+// moves the columns while it adds. (7199 x 6040 fp16, rank 24: 38 us; 6038 or 6037: 54 us.)
 template <class T, class O, int KC, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     adapter_expand_wide_kernel(const __grid_constant__ CUtensorMap map_b, const AdapterArgs a,
