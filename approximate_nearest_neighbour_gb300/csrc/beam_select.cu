@@ -24,8 +24,8 @@
 // which threads append and the lowest column of equal scores comes first.
 //
 // Measured on the device: 64 x 8 rows of 131072 bf16, k = 16 (134 MB) 28.9 us, 4.6 TB/s
-// (the copy rate would be 20.1 us): reading ends at 24 us, the rest is the second look and
-// the ranking, which later blocks hide only in part. 4 rows of 32000 fp32,
+// (at the copy rate 20.1 us): the rest is the second look and the ranking with
+// their barriers, which the SM's other blocks hide only in part. 4 rows of 32000 fp32,
 // k = 8: 9.3 us, nearly all of it one block's chain of barriers and exchanges.
 #include <algorithm>
 
