@@ -244,6 +244,18 @@ __device__ __forceinline__ void read_tokens(const SortArgs& a, int64_t t0,
   }
 }
 
+// counter[i] of every lane with i >= 0 grows by one; returns what it was before the lane.
+// One addition per counter and warp: a frequent token is most of its class.
+__device__ __forceinline__ int take_place(int* counter, int i) {
+  const int lane = threadIdx.x & 31;
+  const unsigned same = __match_any_sync(kFullMask, i);
+  const int first = __ffs(same) - 1;
+  int at = 0;
+  if (i >= 0 && lane == first) at = atomicAdd(&counter[i], __popc(same));
+  at = __shfl_sync(kFullMask, at, first);
+  return at + __popc(same & ((1u << lane) - 1u));
+}
+
 template <bool WIDE, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortArgs a) {
   extern __shared__ int sort_smem[];
@@ -264,21 +276,53 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
   for (int i = threadIdx.x; i < 2 * a.local + 1; i += THREADS) start[i] = 0;
   __syncthreads();
   // (kNone's class is the last: it counts as before none)
+  const int lane = threadIdx.x & 31;
   for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
     if (t0 > 0) read_tokens<WIDE, THREADS>(a, t0, v);
+    uint32_t hits = 0;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const uint32_t cls = v[j] & mask;
       before += cls < c;
-      if (cls == c && v[j] != kNone) {
-        atomicAdd(&start[v[j] >> a.shift], 1);
-        const int i = atomicAdd(&nmet, 1);
+      hits |= uint32_t(cls == c && v[j] != kNone) << j;
+    }
+    if (!__any_sync(kFullMask, hits != 0)) continue;
+    int in = __popc(hits);
+    const int own = in;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int t = __shfl_up_sync(kFullMask, in, d);
+      if (lane >= d) in += t;
+    }
+    int i = 0;
+    if (lane == 31) i = atomicAdd(&nmet, in);
+    i = __shfl_sync(kFullMask, i, 31) + in - own;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      if (hits >> j & 1) {
         if (i < a.listed)
           met[i] = make_int2(int(position<THREADS>(t0, j / 4)) + j % 4, int(v[j]));
+        ++i;
       }
     }
   }
   const int base = block_sum<THREADS>(before, sh);
+  const int found = nmet;
+  const bool fits = found <= a.listed;
+  if (fits) {
+    for (int i0 = 0; i0 < found; i0 += THREADS) {
+      const int i = i0 + threadIdx.x;
+      take_place(start, i < found ? met[i].y >> a.shift : -1);
+    }
+  } else {
+    for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
+      read_tokens<WIDE, THREADS>(a, t0, v);
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j)
+        if ((v[j] & mask) == c && v[j] != kNone) atomicAdd(&start[v[j] >> a.shift], 1);
+    }
+  }
+  __syncthreads();
   // counts out; their running sums stay
   int n = 0;
   for (int i0 = 0; i0 < a.local; i0 += THREADS) {
@@ -303,15 +347,19 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
   if (threadIdx.x == 0) a.classes[c] = make_int2(base / (a.slab + 1), nfrequent);
   if (n == 0) return;
   // positions to their tokens' places, in any order
-  const bool fits = n <= a.listed;
   int2* list = fits ? list_smem : a.list + base;
-  auto put = [&](const int2& e) {
-    const int l = e.y >> a.shift;
-    list[start[l] + atomicAdd(&fill[l], 1)] = e;
-  };
   if (fits) {
-    for (int i = threadIdx.x; i < n; i += THREADS) put(met[i]);
+    for (int i0 = 0; i0 < n; i0 += THREADS) {
+      const int i = i0 + threadIdx.x;
+      const int2 e = i < n ? met[i] : make_int2(0, 0);
+      const int l = i < n ? e.y >> a.shift : -1, at = take_place(fill, l);
+      if (i < n) list[start[l] + at] = e;
+    }
   } else {
+    auto put = [&](const int2& e) {
+      const int l = e.y >> a.shift;
+      list[start[l] + atomicAdd(&fill[l], 1)] = e;
+    };
     for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
       read_tokens<WIDE, THREADS>(a, t0, v);
 #pragma unroll
@@ -333,7 +381,6 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
     a.token[base + from + rank] = e.y | (k > a.slab ? kFrequent : 0);
   }
   // many: a bitmap of the positions, a range of them at a time
-  const int lane = threadIdx.x & 31;
   unsigned more = 0;  // of 32 tokens from l0 on, the same in every warp
   for (int l0 = -32;;) {
     while (more == 0 && (l0 += 32) < a.local)
