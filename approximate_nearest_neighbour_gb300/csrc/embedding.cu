@@ -26,7 +26,7 @@
 // Measured: lookup of 8192 x 4096 bf16 17.5 us on the device, 6.7 TB/s, the copy rate;
 // with 4095 columns 28.8 us as a program calls it (20.7 us with 4096), two bytes per lane
 // and access. Gradient of 16384 x 4096 bf16 into 32000 rows (396 MB) 55.3 us for the sums,
-// 6.0 TB/s, behind 11.2 us of sorting, which reads all ids once per class, and before
+// 6.0 TB/s, behind 10.7 us of sorting, which reads all ids once per class, and before
 // 8.9 us of joining the frequent tokens (all with cold caches). Bulk copies for the rows
 // and a prefetch of them into L2 were slower than plain loads of eight rows at a time.
 #include <algorithm>
