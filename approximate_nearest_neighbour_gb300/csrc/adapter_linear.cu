@@ -683,7 +683,8 @@ extern "C" int adapter_linear(const void* x, int dtype, int64_t tokens, int64_t 
   // tiles of 128 tokens also where few adapters of a high rank have many each: a tile of
   // 16 reads its adapter's B again (256 tokens of one adapter, 4096 x 16384: rank 128 44 us
   // in tiles of 16 and 29 us in tiles of 128, rank 16 21.5 us, and 26 us for 257 tokens)
-  const bool wide = tokens > kFew || (rank > 32 && tokens >= 64 && tokens >= 32 * int64_t(adapters));
+  const bool wide =
+      tokens > kFew || (rank > 32 && tokens >= 64 && tokens >= 32 * int64_t(adapters));
   p.tile = wide ? kMaxTile : kFewTile;
   const int64_t tiles =
       tokens / p.tile + std::min<int64_t>(tokens, int64_t(adapters) + 1);  // at most

@@ -785,7 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int end = bytes + int(p & 3);  // whole words of the row
                 if (4 * lane + 4 <= end && (lane > 0 || !(p & 3)))
                   *w = *reinterpret_cast<const uint32_t*>(word(i));
-                if (4 * lane + 132 <= end) w[32] = *reinterpret_cast<const uint32_t*>(word(i) + 128);
+                if (4 * lane + 132 <= end)
+                  w[32] = *reinterpret_cast<const uint32_t*>(word(i) + 128);
               }
             }
             if constexpr (kHalves) {  // a row's first and last column in a word with others
