@@ -157,7 +157,7 @@ __device__ __forceinline__ void load_batch(const Run<T, VEC>& run, int step, uin
 }
 
 // The sum of a vector's exponentials relative to m where there is nothing yet (m = 0), or
-// where the products of scores pass fp32.
+// where m is too large for add_batch's rounded product.
 template <class T>
 __device__ __noinline__ float far_vec(uint4 r, float m) {
   constexpr int N = Span<T>::N;
@@ -175,9 +175,12 @@ __device__ __forceinline__ void add_batch(const uint4 (&r)[kUnroll], Online& o) 
   const uint64_t scale = pair(kLog2e, kLog2e);
   uint64_t z = pair(0.f, 0.f);
   float z0, z1;
-  if (fabsf(o.m) < 1e38f) {
+  if (fabsf(o.m) < 0x1p30f) {
     // exp2(s c - b) with b = m c rounded, one operation per score; what the
-    // rounding of b does to all of them alike is taken back below
+    // rounding of b does to all of them alike is taken back below: a factor of 2^64 at
+    // most, as b is below 2^31 and a step there 2^7. (Further on one of the two factors
+    // would be infinite and the other 0: scores are subtracted first, as for masks of
+    // -1e10 and beyond.)
     const float b = o.m * kLog2e;
     const uint64_t minus = pair(-b, -b);
 #pragma unroll
