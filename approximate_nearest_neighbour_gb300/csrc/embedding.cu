@@ -12,7 +12,9 @@
 //     rows, counts its own and those of the lower classes, and so knows where its
 //     tokens go without hearing from the other blocks. They are put into their
 //     tokens' places in any order, and then ordered by rank, or by a bitmap of the
-//     positions where a token has many.
+//     positions where a token has many: a range of positions at a time, only those that
+//     hold one. A class that does not fit shared memory is put in place a range after the
+//     other, so that each looks at its own part of the list alone.
 //  2. The sorted positions are cut into slabs of equal length. A block adds a slab's
 //     rows over a run of columns in registers (fp32) and writes a row where the
 //     token changes. A token that goes on beyond its slab is finished by the block in
@@ -29,6 +31,10 @@
 // 6.0 TB/s, behind 10.7 us of sorting, which reads all ids once per class, and before
 // 8.9 us of joining the frequent tokens (all with cold caches). Bulk copies for the rows
 // and a prefetch of them into L2 were slower than plain loads of eight rows at a time.
+// Positions of one token throughout, one block's work, take time as they are many: 65536 x 8
+// fp32 0.28 ms, 2^20 3.1 ms, 2^23 28 ms.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "internal.h"
@@ -162,6 +168,7 @@ constexpr int kPerThread = 16;    // ids per thread and step
 constexpr int kMostListed = 8192;  // a class's positions kept in shared memory
 constexpr int kRanked = 128;      // a token's positions that are ordered by rank
 constexpr int kBitmap = 1024;     // words of the bitmap of positions
+constexpr int kRange = kBitmap * 32;  // positions of a bitmap
 
 struct SortArgs {
   const void* ids;
@@ -309,6 +316,34 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
   const int base = block_sum<THREADS>(before, sh);
   const int found = nmet;
   const bool fits = found <= a.listed;
+  // Calls f(j, token, place) for this thread's ids of the class among v: their places among
+  // the token's that `counter` counts. An addition per id, unless many are of the class
+  // and so perhaps of one token.
+  auto count_step = [&](int* counter, auto&& f) {
+    unsigned hits = 0;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      hits |= unsigned((v[j] & mask) == c && v[j] != kNone) << j;
+    if (__reduce_add_sync(kFullMask, unsigned(__popc(hits))) > 4 * kPerThread) {
+      // (four copies of the code: all sixteen slow the other branch, too)
+#pragma unroll 1
+      for (int q = 0; q < kPerThread; q += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t t = v[e];
+#pragma unroll
+          for (int j = 4; j < kPerThread; j += 4) t = q == j ? v[j + e] : t;
+          const bool hit = hits >> (q + e) & 1;
+          const int at = take_place(counter, hit ? int(t >> a.shift) : -1);
+          if (hit) f(q + e, t, at);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j)
+        if (hits >> j & 1) f(j, v[j], atomicAdd(&counter[v[j] >> a.shift], 1));
+    }
+  };
   if (fits) {
     for (int i0 = 0; i0 < found; i0 += THREADS) {
       const int i = i0 + threadIdx.x;
@@ -317,9 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
   } else {
     for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
       read_tokens<WIDE, THREADS>(a, t0, v);
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j)
-        if ((v[j] & mask) == c && v[j] != kNone) atomicAdd(&start[v[j] >> a.shift], 1);
+      count_step(start, [](int, uint32_t, int) {});
     }
   }
   __syncthreads();
@@ -356,16 +389,17 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
       if (i < n) list[start[l] + at] = e;
     }
   } else {
-    auto put = [&](const int2& e) {
-      const int l = e.y >> a.shift;
-      list[start[l] + atomicAdd(&fill[l], 1)] = e;
-    };
+    read_tokens<WIDE, THREADS>(a, 0, v);
     for (int64_t t0 = 0; t0 < a.tokens; t0 += step) {
-      read_tokens<WIDE, THREADS>(a, t0, v);
+      uint32_t next[kPerThread];
+      if (t0 + step < a.tokens) read_tokens<WIDE, THREADS>(a, t0 + step, next);
+      count_step(fill, [&](int j, uint32_t t, int at) {
+        list[start[t >> a.shift] + at] =
+            make_int2(int(position<THREADS>(t0, j / 4)) + j % 4, int(t));
+      });
+      if ((t0 + step) % kRange == 0) __syncthreads();  // these lie before the next range's
 #pragma unroll
-      for (int j = 0; j < kPerThread; ++j)
-        if ((v[j] & mask) == c && v[j] != kNone)
-          put(make_int2(int(position<THREADS>(t0, j / 4)) + j % 4, int(v[j])));
+      for (int j = 0; j < kPerThread; ++j) v[j] = next[j];
     }
   }
   __syncthreads();
@@ -380,7 +414,10 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
     a.pos[base + from + rank] = e.x;
     a.token[base + from + rank] = e.y | (k > a.slab ? kFrequent : 0);
   }
-  // many: a bitmap of the positions, a range of them at a time
+  // many: a bitmap of the positions, a range of them at a time. `later`: a position
+  // in the next range that holds one.
+  static_assert(kRange % step == 0, "whole steps");
+  __shared__ int later;
   unsigned more = 0;  // of 32 tokens from l0 on, the same in every warp
   for (int l0 = -32;;) {
     while (more == 0 && (l0 += 32) < a.local)
@@ -391,16 +428,27 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
     const int l = l0 + __ffs(more) - 1, from = start[l], k = start[l + 1] - from;
     more &= more - 1;
     const int id = int((uint32_t(l) << a.shift) + c) | (k > a.slab ? kFrequent : 0);
-    int at = base + from;
-    for (int64_t t0 = 0; t0 < a.tokens; t0 += kBitmap * 32) {
+    int done = 0;  // positions of the token that have their place
+    for (int64_t t0 = 0; t0 < a.tokens;) {
       __syncthreads();
       for (int i = threadIdx.x; i < kBitmap; i += THREADS) bitmap[i] = 0;
+      if (threadIdx.x == 0) later = INT_MAX;
       __syncthreads();
-      for (int i = threadIdx.x; i < k; i += THREADS) {
-        const int64_t p = int64_t(list[from + i].x) - t0;
-        if (p >= 0 && p < kBitmap * 32) atomicOr(&bitmap[p >> 5], 1u << (p & 31));
+      int behind = INT_MAX;
+      for (int i = (fits ? 0 : done) + threadIdx.x; i < k; i += THREADS) {
+        const int x = list[from + i].x;
+        const int64_t p = x - t0;
+        if (p >= kRange) {
+          behind = min(behind, x);
+          if (!fits) break;  // so are all that follow
+        } else if (p >= 0) {
+          atomicOr(&bitmap[p >> 5], 1u << (p & 31));
+        }
       }
+      behind = __reduce_min_sync(kFullMask, behind);
+      if (lane == 0 && behind != INT_MAX) atomicMin(&later, behind);
       __syncthreads();
+      const int next = later;
       constexpr int W = kBitmap / THREADS;  // words of a thread
       uint32_t bits[W];
       int mine = 0;
@@ -409,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
         bits[i] = bitmap[threadIdx.x * W + i];
         mine += __popc(bits[i]);
       }
-      int all, to = at + block_before<THREADS>(mine, sh, &all);
+      int all, to = base + from + done + block_before<THREADS>(mine, sh, &all);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         for (; bits[i]; bits[i] &= bits[i] - 1) {
@@ -417,7 +465,9 @@ __global__ void __launch_bounds__(THREADS, 1) embedding_sort_kernel(const SortAr
           a.token[to++] = id;
         }
       }
-      at += all;
+      done += all;
+      if (next == INT_MAX) break;
+      t0 = int64_t(next / kRange) * kRange;
     }
   }
 }
