@@ -101,10 +101,12 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_aligned_kernel(const Lo
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * ty;
       if (t >= a.tokens) continue;
+      // an id outside the table: zeros, whatever the scale
+      const float scale = id[u] >= 0 && id[u] < a.rows ? a.scale : 0.f;
       float v[N];
       unpack_vec<T>(r[u], v);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] *= a.scale;
+      for (int j = 0; j < N; ++j) v[j] *= scale;
       store_vec<O>(static_cast<O*>(a.out) + t * a.ldo + int64_t(i) * N, v);
     }
   }
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_any_kernel(const Lookup
 #pragma unroll
       for (int j = 0; j < N; ++j)
         if (dst[u] && c0 + 32 * j < cols)
-          dst[u][c0 + 32 * j] = from_f32<O>(to_f32(r[u][j]) * a.scale);
+          dst[u][c0 + 32 * j] = from_f32<O>(to_f32(r[u][j]) * (src[u] ? a.scale : 0.f));
   }
 }
 
