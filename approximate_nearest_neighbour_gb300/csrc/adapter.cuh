@@ -55,11 +55,20 @@ __device__ __forceinline__ float term(float& v) {
   return t;
 }
 
-// fp16's range: the power of two that takes a row's largest magnitude to [2^14, 2^15),
-// and its inverse (1 for a row of zeros, or with an infinity or a NaN).
+// Element k of a row of h, 0 past the rank: there h has the products of x with zeros, which
+// an infinity or a NaN in x makes a NaN.
+__device__ __forceinline__ float within_rank(const AdapterArgs& a, int k, float h) {
+  return k < a.rank ? h : 0.f;
+}
+// |v| where it is finite, else 0.
+__device__ __forceinline__ float magnitude(float v) {
+  return fabsf(v) < INFINITY ? fabsf(v) : 0.f;
+}
+// fp16's range: the power of two that takes a row's largest finite magnitude to
+// [2^14, 2^15), and its inverse (1 for a row without one that is not 0).
 __device__ __forceinline__ float2 fp16_range(float top) {
   const int ex = int(__float_as_uint(top) >> 23);  // 127 + its exponent
-  const int by = top > 0.f && top < INFINITY ? min(141 - ex, 126) : 0;
+  const int by = top > 0.f ? min(141 - ex, 126) : 0;
   return make_float2(__uint_as_float(uint32_t(127 + by) << 23),
                      __uint_as_float(uint32_t(127 - by) << 23));
 }

@@ -380,16 +380,16 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
             if (k >= a.pitch) continue;
             const float4 f =
                 *reinterpret_cast<const float4*>(a.h + int64_t(t.first + i) * a.pitch + k);
-            v[e][4 * s] = f.x;
-            v[e][4 * s + 1] = f.y;
-            v[e][4 * s + 2] = f.z;
-            v[e][4 * s + 3] = f.w;
+            v[e][4 * s] = within_rank(a, k, f.x);
+            v[e][4 * s + 1] = within_rank(a, k + 1, f.y);
+            v[e][4 * s + 2] = within_rank(a, k + 2, f.z);
+            v[e][4 * s + 3] = within_rank(a, k + 3, f.w);
           }
         }
 #pragma unroll
         for (int k = 0; k < 4 * KS; ++k) {
           v[e][k] *= scale;
-          top = fmaxf(top, fabsf(v[e][k]));
+          top = fmaxf(top, magnitude(v[e][k]));
         }
         if constexpr (std::is_same<T, __half>::value) {
           // fp16's range: the row's largest value to [2^14, 2^15)

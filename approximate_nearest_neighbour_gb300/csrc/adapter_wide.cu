@@ -635,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
-            v[j][x] = w[x] * scale;
-            top = fmaxf(top, fabsf(v[j][x]));
+            v[j][x] = within_rank(a, k + x, w[x]) * scale;
+            top = fmaxf(top, magnitude(v[j][x]));
           }
         }
         if constexpr (std::is_same<T, __half>::value) {

@@ -692,7 +692,8 @@ int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols
  * x[t] a[i]^T is held in fp32 and enters the second product with a relative error
  * of at most 2^-16 per element (2^-22 where the output is fp32; for fp16 operands at
  * least 2^-36 of the token's largest); sums are fp32, the result is rounded once.
- * Results repeat bit for bit.
+ * Results repeat bit for bit. Infinities and NaN of x, a, scales and base are the
+ * formula's; an element of b that is infinite may give NaN instead.
  *  x       device [tokens, cols] of dtype (IVFPQ_F16 or IVFPQ_BF16), row stride ldx
  *          (0 repeats a row)
  *  a       device [adapters, rank, cols], b device [adapters, n, rank] of dtype,
