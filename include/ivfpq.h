@@ -615,8 +615,8 @@ int topk_distill(const void* scores, int dtype, int64_t rows, int64_t cols, int6
  *  totals     device fp32 [groups, beams]: a beam whose total is not finite has
  *             none (-inf: a beam that is not alive yet)
  *  finished   device uint8 [groups, beams] or NULL: a beam that is nonzero has
- *             one continuation, (b, end_id), with its own total; its scores are
- *             not read
+ *             one continuation, (b, end_id), with its own total; its scores do
+ *             not count (they are loaded before it is known, so the row is there)
  *  end_id     in [0, cols) where finished is given
  *  out_totals device fp32 [groups, k], out_beams, out_ids device int32
  *             [groups, k]; where there are fewer than k, (-inf, -1, -1). A total
@@ -692,8 +692,8 @@ int embedding_gradient(const void* grad, int dtype, int64_t tokens, int64_t cols
  * x[t] a[i]^T is held in fp32 and enters the second product with a relative error
  * of at most 2^-16 per element (2^-22 where the output is fp32; for fp16 operands at
  * least 2^-36 of the token's largest); sums are fp32, the result is rounded once.
- * Results repeat bit for bit. Infinities and NaN of x, a, scales and base are the
- * formula's; an element of b that is infinite may give NaN instead.
+ * Results repeat bit for bit. Infinities and NaN of x, a and base are the formula's;
+ * an infinite scale or element of b may give NaN instead.
  *  x       device [tokens, cols] of dtype (IVFPQ_F16 or IVFPQ_BF16), row stride ldx
  *          (0 repeats a row)
  *  a       device [adapters, rank, cols], b device [adapters, n, rank] of dtype,
