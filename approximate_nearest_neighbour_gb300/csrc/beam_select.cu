@@ -735,7 +735,7 @@ extern "C" int beam_select(const void* scores, int dtype, int64_t groups, int be
   IVFPQ_REQUIRE(known_dtype(dtype), "beam_select: unknown element type %d", dtype);
   IVFPQ_REQUIRE(beams >= 1 && beams <= IVFPQ_MAX_BEAMS, "beam_select: beams=%d outside [1, %d]",
                 beams, IVFPQ_MAX_BEAMS);
-  IVFPQ_REQUIRE(groups >= 0 && groups * beams < (int64_t(1) << 31) && groups < (int64_t(1) << 31),
+  IVFPQ_REQUIRE(groups >= 0 && groups < (int64_t(1) << 31) && groups * beams < (int64_t(1) << 31),
                 "beam_select: groups=%lld of %d beams outside [0, 2^31)", (long long)groups, beams);
   IVFPQ_REQUIRE(cols >= 1 && cols <= (int64_t(1) << 28), "beam_select: cols=%lld outside [1, 2^28]",
                 (long long)cols);
