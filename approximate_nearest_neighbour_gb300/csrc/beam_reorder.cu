@@ -18,6 +18,7 @@
 // 163 us. 4 rows of four states of 8 x 200 x 128: 5.8 us on the device, the launch and one
 // dependent chain (ids, lengths, rows).
 #include <algorithm>
+#include <utility>
 
 #include "common.cuh"
 
@@ -173,6 +174,32 @@ int granule_of(const ivfpq_state& t) {
   return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
 }
 
+// Whether no two of rows * outer runs of `inner` bytes meet, `row` and `step` bytes from
+// one to the next.
+bool apart(int64_t rows, int64_t row, int64_t outer, int64_t step, int64_t inner) {
+  if (outer > rows) {
+    std::swap(rows, outer);
+    std::swap(row, step);
+  }
+  if ((rows > 1 && row < inner) || (outer > 1 && step < inner)) return false;
+  if (outer == 1) return true;
+  // one within the other's gaps, as in every view of a dense tensor
+  if ((row - inner) / step >= outer - 1 || (step - inner) / row >= rows - 1) return true;
+  // run o of the first row lies `rest` behind the start of row q
+  int64_t q = 0, rest = 0;
+  for (int64_t o = 1; o < outer; ++o) {
+    q += step / row;
+    rest += step % row;
+    if (rest >= row) {
+      rest -= row;
+      ++q;
+    }
+    if (q >= rows) break;
+    if (rest < inner || (q + 1 < rows && row - rest < inner)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace ivfpq
 
@@ -199,8 +226,9 @@ extern "C" int beam_reorder(const ivfpq_state* states, int count, const int32_t*
                   "beam_reorder: state %d is too large", i);
     if (t.outer == 0 || t.inner == 0) continue;
     IVFPQ_REQUIRE(t.src && t.dst, "beam_reorder: null pointer in state %d", i);
-    IVFPQ_REQUIRE((groups * n == 1 || t.dst_row >= t.inner) &&
-                      (t.outer == 1 || t.dst_outer >= t.inner),
+    IVFPQ_REQUIRE(t.dst_row < (int64_t(1) << 56) && t.dst_outer < (int64_t(1) << 56),
+                  "beam_reorder: state %d is too large", i);
+    IVFPQ_REQUIRE(apart(groups * n, t.dst_row, t.outer, t.dst_outer, t.inner),
                   "beam_reorder: state %d's written rows or segments overlap", i);
     IVFPQ_REQUIRE(t.src != t.dst || (width == n && t.src_row == t.dst_row &&
                                      (t.outer == 1 || t.src_outer == t.dst_outer)),

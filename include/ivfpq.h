@@ -629,8 +629,9 @@ int beam_select(const void* scores, int dtype, int64_t groups, int beams, int64_
                 float* out_totals, int32_t* out_beams, int32_t* out_ids, void* stream);
 
 /* A state of the beams (a cache, a history): rows of `outer` segments of `inner`
- * bytes. Strides are in bytes, none negative; the rows and segments of dst do not
- * overlap, and dst is src (in place, with the same strides) or does not overlap it. */
+ * bytes. Strides are in bytes, none negative and those of dst below 2^56; a dst whose
+ * rows and segments overlap one another is refused. dst is src (in place, with the
+ * same strides) or does not overlap it. */
 typedef struct {
   const void* src;
   void* dst;
