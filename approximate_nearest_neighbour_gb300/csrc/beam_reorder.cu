@@ -118,8 +118,11 @@ __global__ void __launch_bounds__(IN_PLACE ? kInPlaceThreads : kThreads, 4)
     const int64_t g = within / (s.outer * runs), rest = within - g * (s.outer * runs);
     const int64_t o = rest / runs, at = (rest - o * runs) * run;
     int64_t bytes = s.inner;
-    if (a.lengths && s.unit > 0)
-      bytes = min(bytes, max(int64_t(a.lengths[g]), int64_t(0)) * s.unit);
+    if (a.lengths && s.unit > 0) {
+      // (the product may pass 63 bits: a length is any number, a position any size)
+      const uint64_t n = uint64_t(max(a.lengths[g], 0)), unit = uint64_t(s.unit);
+      if (__umul64hi(n, unit) == 0) bytes = int64_t(min(uint64_t(bytes), n * unit));
+    }
     if (at >= bytes) continue;
     const int valid = sources(a.beams + g * a.n, a.width, a.n, IN_PLACE, to, from);
     const char* src = s.src + g * a.width * s.src_row + o * s.src_outer + at;
