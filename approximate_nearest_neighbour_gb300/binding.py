@@ -1124,7 +1124,7 @@ def beam_reorder(states, beams, lengths=None, axis=1, out=None, stream=None):
     seen = set()
     for i, (t, o, d) in enumerate(zip(src, dst, axes)):
         st = _state(t, o, d, groups, width, n, length is not None, at, i)
-        if st[1] in seen and st[7]:
+        if st[1] in seen and st[4] and st[7]:  # (empty ones may share an address)
             raise ValueError(f"states[{i}] is written twice")
         seen.add(st[1])
         numbers += st
