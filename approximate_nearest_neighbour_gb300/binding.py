@@ -1149,7 +1149,7 @@ def embedding_lookup(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     """scale * table[ids], [*ids.shape, cols] in dtype (the table's if not given,
     or float32); zeros where an id is outside the table. table: [rows, cols],
     rows may be strided; ids: int32 or int64, any shape; out: 2-d with strided
-    rows for 1-d ids, contiguous otherwise."""
+    rows for 1-d ids, contiguous otherwise, in memory of its own."""
     if stream is not None:
         return _on_stream(embedding_lookup, stream, (table, ids, scale, dtype, out), {})
     code, rows, cols, ldt = _rows(table, "table")
@@ -1165,8 +1165,11 @@ def embedding_lookup(table, ids, scale=1.0, dtype=None, out=None, stream=None):
         ldo = _out_rows(out, (tokens, cols), dtype, "out", table.device)
     else:
         out = _out(out, (*ids.shape, cols), dtype, "out", table.device)
+    to = out.data_ptr()
+    if to == table.data_ptr() and tokens and rows and cols:
+        raise ValueError("out must not be the table's memory")
     rc = (_lib or lib()).embedding_lookup(table.data_ptr(), code, rows, cols, ldt, p, size, tokens,
-                                          scale, out.data_ptr(), ocode, ldo, _current(at))
+                                          scale, to, ocode, ldo, _current(at))
     if rc:
         _check("embedding_lookup", rc)
     return out
@@ -1178,7 +1181,8 @@ def embedding_gradient(grad, ids, rows, scale=1.0, padding=None, accumulate=Fals
     cols] (rows may be strided or one repeated) and ids, int32 or int64 of as many
     elements: scale times the sums by token, in dtype (grad's if not given, or
     float32). Ids outside the table and the id `padding` have none. accumulate:
-    the sums are added to out, which must be given; rows without a token stay."""
+    the sums are added to out, which must be given; rows without a token stay. out
+    has memory of its own."""
     if stream is not None:
         return _on_stream(embedding_gradient, stream,
                           (grad, ids, rows, scale, padding, accumulate, dtype, out), {})
@@ -1196,10 +1200,12 @@ def embedding_gradient(grad, ids, rows, scale=1.0, padding=None, accumulate=Fals
         out, ldo = _late["empty"]((rows, cols), dtype=dtype, device=grad.device), cols
     else:
         ldo = _out_rows(out, (rows, cols), dtype, "out", grad.device)
+    to = out.data_ptr()
+    if to == grad.data_ptr() and tokens and rows and cols:
+        raise ValueError("out must not be grad's memory")
     rc = (_lib or lib()).embedding_gradient(
         grad.data_ptr(), code, tokens, cols, ldg, p, size, rows, scale,
-        -1 if padding is None else padding, 1 if accumulate else 0, out.data_ptr(), ocode, ldo,
-        _current(at))
+        -1 if padding is None else padding, 1 if accumulate else 0, to, ocode, ldo, _current(at))
     if rc:
         _check("embedding_gradient", rc)
     return out

@@ -663,7 +663,8 @@ int beam_reorder(const ivfpq_state* states, int count, const int32_t* beams, int
  * and then to out_dtype; zeros where the id is outside [0, rows).
  *  table  device [rows, cols] of dtype, row stride ldt (0 repeats a row)
  *  ids    device int32 or int64 (ids_bytes 4 or 8) [tokens]
- *  out    device [tokens, cols] of out_dtype (dtype or IVFPQ_F32), row stride ldo
+ *  out    device [tokens, cols] of out_dtype (dtype or IVFPQ_F32), row stride ldo;
+ *         not table's memory
  * rows <= 2^24, cols <= 2^20, tokens < 2^30. Errors: INVALID_ARG, CUDA.
  */
 int embedding_lookup(const void* table, int dtype, int64_t rows, int64_t cols, int64_t ldt,
