@@ -27,8 +27,9 @@
 //
 // Measured: 77 tokens of 64 adapters, rank 16, 4096 x 16384 bf16 (35 MB): 7.9 us for h and
 // 13.4 us for the output with cold caches, which overlap to 21.4 to 23.1 us as a program
-// calls it; 5.3 us are the bytes. Each block of the second product waits for h, its tile's
-// B and its base rows one after the other, and a wave is all there is. One token,
+// calls it; 5.3 us are the bytes. Each block of the second product waits for the kernel that
+// makes h, then for its tile and B, h and its base rows, and a wave is all there is. (B and the
+// base rows could be on their way before h is there; the tile that names them is not.) One token,
 // 4096 x 16384: 5.9 and 4.3 us, two starts of a kernel.
 #include <algorithm>
 
@@ -344,7 +345,8 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const AdapterA
   const O* base = static_cast<const O*>(a.base);
   O* out = static_cast<O*>(a.out);
   if (!some && base == out) return;  // in place: nothing changes
-  // B's first columns are asked for before h is looked at
+  // B's first columns are asked for before h is, both after the wait for the kernel that
+  // makes h and the tiles
   const bool whole = a.rank % (KS == 1 ? 4 : 8) == 0 && misalign(a.b) == 0;
   const T* b0 = some ? static_cast<const T*>(a.b) + int64_t(t.adapter) * a.n * a.rank : nullptr;
   const int64_t cend = min(a.n, (int64_t(blockIdx.x) + 1) * a.run);

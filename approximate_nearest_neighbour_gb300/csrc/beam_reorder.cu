@@ -4,19 +4,21 @@
 // where rows whose beam is outside [0, width) and positions past the length stay
 // as they were.
 //
-// Bound by memory: each source row that is taken is read once, whatever the
-// number of its continuations, and each row written once; in place, rows that
-// stay where they are are not touched. All states of a call go through one launch
-// (a decoder has two per layer). A block takes a run of one segment for all rows
-// of a group. Elsewhere than in place, the rows are visited in the order of their
-// sources, and a thread loads its part when the source changes. In place, a
-// thread first keeps its part of every source that moves in shared memory, and
-// then writes: its bytes are its own, so no barrier is needed.
+// Bound by memory: each row is written once, and each source row that is taken is
+// read once, whatever the number of its continuations, but in place, where it is
+// read for each of them and rows that stay where they are are not touched. Up to 32
+// states of a call go through one launch (a decoder has two per layer). A block takes
+// a run of one segment for all rows of a group. Elsewhere than in place, the rows are
+// visited in the order of their sources, and a thread loads its part when the source
+// changes. In place, a thread first keeps its part of the source of every row that
+// moves in shared memory, and then writes: its bytes are its own, so no barrier is
+// needed.
 //
 // Measured: 16 x 4 rows of two states of 8 x 4096 x 128 bf16 and their histories, lengths
 // from a quarter to all, not in place: 153 to 163 us; as many bytes at the copy rate take
 // 163 us. 4 rows of four states of 8 x 200 x 128: 5.8 us on the device, the launch and one
-// dependent chain (ids, lengths, rows).
+// dependent chain (ids, lengths, rows). In place the large batch takes 272 us and its bytes
+// 123: blocks of one vector per thread and row, each of which finds the order of the rows.
 #include <algorithm>
 #include <utility>
 
