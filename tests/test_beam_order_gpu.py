@@ -18,8 +18,8 @@ def _expected(scores, groups, beams, k):
 
 
 @pytest.mark.parametrize("name", ["float32", "float16", "bfloat16"])
-@pytest.mark.parametrize("groups,beams,cols,k", [(2, 4, 4001, 10), (2, 4, 4000, 100), (1, 8, 64, 40),
-                                                 (3, 16, 33, 128), (1, 3, 70_000, 33)])
+@pytest.mark.parametrize("groups,beams,cols,k", [
+    (2, 4, 4001, 10), (2, 4, 4000, 100), (1, 8, 64, 40), (3, 16, 33, 128), (1, 3, 70_000, 33)])
 @pytest.mark.parametrize("repeated", [True, False])
 def test_beams_that_share_a_row(name, groups, beams, cols, k, repeated):
     """One row for all (by a stride of 0, or copied): every score is in the list as often as
